@@ -352,6 +352,151 @@ MODA_API moda_status moda_decode_strided(const void* q, const void* k_cache, con
                                          size_t workspace_bytes, moda_stream_t stream);
 
 /*
+ * Paged KV cache: the sequence keys and values of many requests in one pool of
+ * pages, so that a batch of requests of any lengths is served without moving
+ * rows. A sequence's rows p*page_size .. (p+1)*page_size - 1 lie in page
+ * block_table[s][p]; inside a page the rows of one KV head are contiguous.
+ *
+ *   MODA_KV_BF16  k, v [num_pages, Hk, page_size, d] bf16; k_scale, v_scale NULL
+ *   MODA_KV_MX4   k, v [num_pages, Hk, page_size, d/2] bytes, two e2m1 codes
+ *                 (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3,
+ *                 4, 6) each, the even element in the low half;
+ *                 k_scale, v_scale [num_pages, Hk, page_size, d/32] bytes, one
+ *                 for each block of 32 elements along d: the block's codes
+ *                 stand for code * 2^(byte - 127); byte 255 stands for NaN, and
+ *                 its codes are 0. (The microscaling format of 4-bit floating
+ *                 point with blocks of 32: 4.25 bits an element.)
+ *
+ * page_size is 16, 32, 64 or 128; d is 64 or 128; num_pages * Hk * page_size
+ * is at most 2^31 - 1, max_pages * page_size at most 2^30. k, v, k_scale and
+ * v_scale are 16-byte aligned, block_table 4-byte aligned. The struct is read
+ * during the call; the buffers it names belong to the caller.
+ *
+ * Indexes that live in device memory (block_table, seq, pos, seq_lens) cannot
+ * be checked by the host. A kernel that meets one outside its range reads and
+ * writes nothing there and latches MODA_ERR_INVALID_ARG in the device error
+ * word (moda_get_device_error).
+ */
+typedef enum { MODA_KV_BF16 = 0, MODA_KV_MX4 = 1 } moda_kv_format;
+
+typedef struct {
+  int format;     /* a moda_kv_format */
+  int num_pages;  /* pages of the pool, >= 1 */
+  int page_size;  /* rows of a page */
+  int Hk, d;
+  int B;          /* sequences: rows of block_table, >= 0 */
+  int max_pages;  /* columns of block_table, >= 1 */
+  void *k, *v;
+  void *k_scale, *v_scale;
+  const int* block_table; /* [B, max_pages] int32, device memory */
+} moda_paged_kv;
+
+/*
+ * moda_kv_append -- one step's rows for the cache: the queries and keys are
+ * turned by their positions, and keys and values are written into the pages.
+ * Token n is row pos[n] of sequence seq[n]:
+ *
+ *   q_out[n,h,:] = bf16( R(pos[n]) q[n,h,:] )
+ *   k_out[n,hk,:] = bf16( R(pos[n]) k[n,hk,:] )
+ *   page row of (seq[n], pos[n]), KV head hk:  K = R(pos[n]) k[n,hk,:],  V = v[n,hk,:]
+ *
+ * R(p) turns the first `rot` elements in pairs (a, b) by row p of the table
+ * rope[p] = [ cos_0 .. cos_{rot/2-1} | sin_0 .. sin_{rot/2-1} ]: pair i becomes
+ * (a cos_i - b sin_i, b cos_i + a sin_i). Pair i is elements (i, i + rot/2), or
+ * (2i, 2i+1) when interleaved is not 0. The other elements stay.
+ *   bf16 pages hold K rounded once (the bits of k_out) and the bits of V.
+ *   MX4 pages hold each block of 32 elements under the smallest power of two
+ *   2^E with max|x| <= 7 * 2^E (-126 <= E <= 125), and x / 2^E rounded to the
+ *   nearest e2m1 value, ties to the even code (magnitudes over 6 become 6: up
+ *   to 7 that is no further off than the format's rounding elsewhere in that
+ *   binade). K is rounded from the exact rotation, not from k_out. A block
+ *   with an infinity or a NaN in it is stored as NaN.
+ *
+ *   q      [N, Hq, d] bf16, consecutive tokens q_stride elements apart (a view
+ *          of a fused projection's output); NULL when Hq == 0
+ *   k, v   [N, Hk, d] bf16, k_stride and v_stride elements apart
+ *          strides: multiples of 8, at least Hq*d (Hk*d); unused when N == 1
+ *   rope   [rope_rows, rot] fp32; NULL when rot == 0 (nothing is turned)
+ *   rot    0, or a multiple of 16 up to d
+ *   seq    [N] int32; -1 marks a row of padding, for which nothing is written
+ *   pos    [N] int32, 0 <= pos < max_pages * page_size, < rope_rows if rot > 0
+ *   q_out  [N, Hq, d] bf16, dense; NULL when Hq == 0
+ *   k_out  [N, Hk, d] bf16, dense, or NULL if not wanted. It is what the
+ *          prompt's own attention (moda_fwd) and the depth stream
+ *          (moda_depth_write) read.
+ * A token with an index outside its range is left out like padding, and
+ * latched (see above). Name each (seq, pos) at most once in a call: of two
+ * tokens for one row either may be found there, or parts of both. Outputs and
+ * pages must not overlap the inputs or each other. N <= 2^24, Hq <= 4096.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. N == 0 is a no-op.
+ */
+MODA_API moda_status moda_kv_append(const void* q, const void* k, const void* v,
+                                    long long q_stride, long long k_stride, long long v_stride,
+                                    const float* rope, int rope_rows, int rot, int interleaved,
+                                    const int* seq, const int* pos, int N, int Hq,
+                                    const moda_paged_kv* cache, void* q_out, void* k_out,
+                                    moda_stream_t stream);
+
+/*
+ * moda_kv_gather -- rows of the pages as dense bf16: k[n,hk,:] and v[n,hk,:]
+ * are the row of (seq[n], pos[n]). For bf16 pages the stored bits, for MX4
+ * pages the values that the codes stand for, which bf16 holds exactly. A pass
+ * over the next piece of a prompt gathers the rows cached before it. Rows may
+ * be named any number of times, in any order.
+ *   seq, pos  [N] int32 as in moda_kv_append; a row whose seq is -1 (or whose
+ *             index is out of range, which is latched) is left as it was
+ *   k, v      [N, Hk, d] bf16 outputs; must not overlap the pages or each other
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. N == 0 is a no-op.
+ */
+MODA_API moda_status moda_kv_gather(const moda_paged_kv* cache, const int* seq, const int* pos,
+                                    int N, void* k, void* v, moda_stream_t stream);
+
+/*
+ * moda_decode_paged -- moda_decode for a batch over the paged cache: the new
+ * token of sequence b attends, under one softmax, to the seq_lens[b] rows of
+ * its pages (its own row among them, appended before) and to its L depth
+ * slots:
+ *   z = [ scale * q[b,h,:].K[b,j,hk,:]  for j < seq_lens[b]
+ *       | scale * q[b,h,:].kd[b,hk,l,:] for l < L ]
+ *   o[b,h,:] = sum softmax(z) * [ V[b,j,hk,:] | vd[b,hk,l,:] ],  lse = ln(sum exp(z))
+ *
+ *   q         [B, Hq, d] bf16, turned by its position (q_out of moda_kv_append)
+ *   seq_lens  [B] int32, device memory: 0 <= seq_lens[b] <= max_pages *
+ *             page_size; one outside is taken as the nearer end, and latched.
+ *             Entries of block_table past a sequence's last page are not read;
+ *             rows past its length have no influence, whatever they hold.
+ *   kd, vd    the depth slots: slot l of KV head hk of sequence b is the d
+ *             bf16 values at b*depth_b_stride + hk*depth_hk_stride +
+ *             l*depth_slot_stride (elements, multiples of 8, at least d; one
+ *             that steps along an axis of length 1 is unused). NULL when L == 0
+ *   o         [B, Hq, d] bf16; lse [B, Hq] fp32 (natural log) or NULL. A
+ *             sequence with nothing to attend to (seq_lens[b] == 0, L == 0)
+ *             gets o = 0, lse = -infinity.
+ *   workspace caller-owned device scratch, 16-byte aligned, of at least
+ *             moda_decode_paged_workspace_bytes(Hq, Hk, d) bytes; holds nothing
+ *             between calls. Calls that may run at the same time need one each.
+ * A page index outside [0, num_pages) makes its sequence's result unspecified
+ * and is latched.
+ * Arithmetic: bf16 pages as moda_decode. MX4 pages: the codes' exact values
+ * against q in fp16 (scaled per head, so that its 8 bits stay), fp32
+ * accumulation, block scales applied in fp32, softmax in fp32, probabilities
+ * times V's block scales rounded to fp16 under a running scale. (Scale byte 0,
+ * which moda_kv_append never writes, is read as 0 here.)
+ * Supported: G = Hq/Hk from 1 to 16, B*Hq <= 2^24, 0 <= L <= 1024.
+ * The result depends on how the batch is split over the SMs only by the order
+ * of fp32 sums; the same call on the same device gives the same bits.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA; TIMEOUT via
+ * moda_get_device_error. B == 0 is a no-op.
+ */
+MODA_API size_t moda_decode_paged_workspace_bytes(int Hq, int Hk, int d);
+MODA_API moda_status moda_decode_paged(const void* q, const moda_paged_kv* cache,
+                                       const int* seq_lens, const void* kd, const void* vd,
+                                       long long depth_b_stride, long long depth_hk_stride,
+                                       long long depth_slot_stride, int Hq, int L, float scale,
+                                       void* o, float* lse, float* workspace,
+                                       size_t workspace_bytes, moda_stream_t stream);
+
+/*
  * moda_bwd -- gradients of moda_fwd with respect to all of its inputs. The
  * pages time the fused operator forward + backward (Table 2, Table 7) without
  * writing the backward out; this is the chain rule through the joint softmax

@@ -29,8 +29,20 @@ EXPORTS = ("moda_pack_depth", "moda_depth_write", "moda_depth_write_at", "moda_d
            "moda_fwd", "moda_fwd_layer_major", "moda_fwd_layer_major_host",
            "moda_fwd_host_workspace_bytes", "moda_fwd_depth_cc", "moda_decode",
            "moda_decode_strided",
-           "moda_decode_workspace_bytes", "moda_bwd", "moda_bwd_layer_major", "moda_bwd_noalloc", "moda_get_device_error",
+           "moda_decode_workspace_bytes", "moda_kv_append", "moda_kv_gather", "moda_decode_paged",
+           "moda_decode_paged_workspace_bytes",
+           "moda_bwd", "moda_bwd_layer_major", "moda_bwd_noalloc", "moda_get_device_error",
            "moda_selftest_wait_timeout", "moda_status_string", "moda_last_error_detail")
+
+MODA_KV_BF16, MODA_KV_MX4 = 0, 1
+
+
+class _PagedKv(ctypes.Structure):
+    """moda_paged_kv of include/moda.h."""
+    _fields_ = ([(n, ctypes.c_int) for n in ("format", "num_pages", "page_size", "Hk", "d", "B",
+                                             "max_pages")] +
+                [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "block_table")])
+
 
 _lock = threading.Lock()
 _lib = None
@@ -80,6 +92,17 @@ def load():
         lib.moda_decode_strided.argtypes = [vp] * 5 + [ctypes.c_longlong] * 2 + [i] * 5 + [
             f, vp, vp, vp, ctypes.c_size_t, vp]
         lib.moda_decode_strided.restype = i
+        cache, ll = ctypes.POINTER(_PagedKv), ctypes.c_longlong
+        lib.moda_kv_append.argtypes = [vp] * 3 + [ll] * 3 + [vp, i, i, i, vp, vp, i, i, cache, vp,
+                                                             vp, vp]
+        lib.moda_kv_append.restype = i
+        lib.moda_kv_gather.argtypes = [cache, vp, vp, i, vp, vp, vp]
+        lib.moda_kv_gather.restype = i
+        lib.moda_decode_paged_workspace_bytes.argtypes = [i, i, i]
+        lib.moda_decode_paged_workspace_bytes.restype = ctypes.c_size_t
+        lib.moda_decode_paged.argtypes = [vp, cache, vp, vp, vp] + [ll] * 3 + [
+            i, i, f, vp, vp, vp, ctypes.c_size_t, vp]
+        lib.moda_decode_paged.restype = i
         lib.moda_fwd.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, vp, vp, vp]
         lib.moda_fwd_depth_cc.restype = i
         lib.moda_fwd_depth_cc.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, vp, vp, vp]
@@ -433,6 +456,180 @@ def moda_decode(q, k_cache, v_cache, kd_tok, vd_tok, scale: float, o=None, lse=N
                                         d, L, float(scale), _ptr(o), _ptr(lse), _ptr(workspace),
                                         ws_bytes, _stream(stream))
         _check(st, "moda_decode_strided")
+    return o, lse
+
+
+def _here(*tensors):
+    """The calls launch on the current device: every tensor must live there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def _paged_cache(k_pages, v_pages, block_table, k_scales, v_scales):
+    """moda_paged_kv for the tensors of a cache."""
+    mx4 = k_scales is not None or v_scales is not None
+    dtype = torch.uint8 if mx4 else torch.bfloat16
+    _need(k_pages, "k_pages", dtype), _need(v_pages, "v_pages", dtype)
+    _need(block_table, "block_table", torch.int32)
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must both be [num_pages,Hk,page_size,d"
+                         + ("/2]" if mx4 else "]"))
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B,max_pages]")
+    num_pages, Hk, page_size, w = k_pages.shape
+    d = 2 * w if mx4 else w
+    if mx4:
+        for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            _need(t, n, torch.uint8)
+            if tuple(t.shape) != (num_pages, Hk, page_size, d // 32):
+                raise ValueError(f"{n} must be [num_pages,Hk,page_size,d/32] = "
+                                 f"{(num_pages, Hk, page_size, d // 32)}")
+    B, max_pages = block_table.shape
+    return _PagedKv(MODA_KV_MX4 if mx4 else MODA_KV_BF16, num_pages, page_size, Hk, d, B, max_pages,
+                    k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr() if mx4 else None,
+                    v_scales.data_ptr() if mx4 else None, block_table.data_ptr())
+
+
+def _need_rows(t, name, N, H, d):
+    """A bf16 CUDA tensor [N,H,d] whose tokens are dense, at any distance; returns the distance."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != N or t.shape[1] != H or t.shape[2] != d:
+        raise ValueError(f"{name}: expected shape {(N, H, d)}, got {tuple(t.shape)}")
+    if N and ((t.stride(2) != 1) or (H > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the [H,d] rows of a token must be dense")
+    return t.stride(0) if N > 1 else H * d
+
+
+def _need_index(seq, pos):
+    _need(seq, "seq", torch.int32), _need(pos, "pos", torch.int32)
+    if seq.dim() != 1 or seq.shape != pos.shape:
+        raise ValueError("seq and pos must both be [N]")
+    return seq.shape[0]
+
+
+def moda_kv_append(q, k, v, k_pages, v_pages, block_table, seq, pos, rope=None, interleaved=False,
+                   k_scales=None, v_scales=None, q_out=None, k_out=None, stream=None,
+                   want_k_out: bool = True):
+    """One step's rows for the paged cache. q[N,Hq,d] (or None), k/v[N,Hk,d]
+    bf16, views with dense tokens allowed; token n is row pos[n] of sequence
+    seq[n] (int32; seq -1: padding, left out). q and k are turned by row
+    pos[n] of rope[P,rot] (fp32: cosines, then sines; None: not at all), in
+    pairs (i, i+rot/2), or (2i, 2i+1) if interleaved; k and v are written into
+    the pages: k_pages/v_pages[num_pages,Hk,page_size,d] bf16, or uint8
+    [...,d/2] with k_scales/v_scales[...,d/32] for the 4-bit format.
+    Returns (q_out[N,Hq,d], k_out[N,Hk,d]), the turned q and k in bf16 (rows
+    of padding are left as they were, in new tensors undefined)."""
+    cache = _paged_cache(k_pages, v_pages, block_table, k_scales, v_scales)
+    N = _need_index(seq, pos)
+    Hk, d = cache.Hk, cache.d
+    Hq = 0 if q is None else q.shape[1]
+    qs = _need_rows(q, "q", N, Hq, d) if q is not None else 0
+    ks, vs = _need_rows(k, "k", N, Hk, d), _need_rows(v, "v", N, Hk, d)
+    rows = rot = 0
+    if rope is not None:
+        _need(rope, "rope", torch.float32)
+        if rope.dim() != 2:
+            raise ValueError("rope must be [P,rot]")
+        rows, rot = rope.shape
+    if q is not None and q_out is None:
+        q_out = torch.empty((N, Hq, d), dtype=torch.bfloat16, device=q.device)
+    if want_k_out and k_out is None:
+        k_out = torch.empty((N, Hk, d), dtype=torch.bfloat16, device=k.device)
+    for t, n, H in ((q_out, "q_out", Hq), (k_out, "k_out", Hk)):
+        if t is not None:
+            _need(t, n)
+            if tuple(t.shape) != (N, H, d):
+                raise ValueError(f"{n}: expected shape {(N, H, d)}, got {tuple(t.shape)}")
+    _here(q, k, v, k_pages, v_pages, block_table, k_scales, v_scales, seq, pos, rope, q_out, k_out)
+    st = load().moda_kv_append(_ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(rope), rows, rot,
+                               int(bool(interleaved)), _ptr(seq), _ptr(pos), N, Hq, cache,
+                               _ptr(q_out), _ptr(k_out), _stream(stream))
+    _check(st, "moda_kv_append")
+    return q_out, k_out
+
+
+def moda_kv_gather(k_pages, v_pages, block_table, seq, pos, k_scales=None, v_scales=None, k=None,
+                   v=None, stream=None):
+    """Rows (seq[n], pos[n]) of the paged cache as dense bf16 k, v [N,Hk,d]
+    (see moda_kv_append for the cache; rows with seq -1 are left as they
+    were, in new tensors undefined)."""
+    cache = _paged_cache(k_pages, v_pages, block_table, k_scales, v_scales)
+    N = _need_index(seq, pos)
+    shape = (N, cache.Hk, cache.d)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
+    for t, n in ((k, "k"), (v, "v")):
+        _need(t, n)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{n}: expected shape {shape}, got {tuple(t.shape)}")
+    _here(k_pages, v_pages, block_table, k_scales, v_scales, seq, pos, k, v)
+    st = load().moda_kv_gather(cache, _ptr(seq), _ptr(pos), N, _ptr(k), _ptr(v), _stream(stream))
+    _check(st, "moda_kv_gather")
+    return k, v
+
+
+def moda_decode_paged_workspace_bytes(Hq: int, Hk: int, d: int) -> int:
+    return int(load().moda_decode_paged_workspace_bytes(int(Hq), int(Hk), int(d)))
+
+
+def moda_decode_paged(q, k_pages, v_pages, block_table, seq_lens, scale: float, kd=None, vd=None,
+                      k_scales=None, v_scales=None, o=None, lse=None, workspace=None, stream=None,
+                      want_lse: bool = True):
+    """One decoding step of a batch over the paged cache (see moda_kv_append).
+    q[B,Hq,d] bf16, block_table[B,max_pages] and seq_lens[B] int32, kd/vd
+    [B,Hk,L,d] bf16 views with contiguous rows of d values (None when L == 0).
+    Returns (o[B,Hq,d] bf16, lse[B,Hq] fp32 or None)."""
+    cache = _paged_cache(k_pages, v_pages, block_table, k_scales, v_scales)
+    B, Hk, d = cache.B, cache.Hk, cache.d
+    _need(q, "q"), _need(seq_lens, "seq_lens", torch.int32)
+    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d:
+        raise ValueError(f"q must be [B,Hq,d] with B={B}, d={d}")
+    if tuple(seq_lens.shape) != (B,):
+        raise ValueError(f"seq_lens must be [B] with B={B}")
+    Hq = q.shape[1]
+    L, strides = 0, (0, 0, 0)
+    if (kd is None) != (vd is None):
+        raise ValueError("kd and vd come together")
+    if kd is not None:
+        if kd.dim() != 4 or kd.shape[0] != B or kd.shape[1] != Hk or kd.shape[3] != d:
+            raise ValueError(f"kd must be [B,Hk,L,d] with B={B}, Hk={Hk}, d={d}")
+        L = kd.shape[2]
+        if L == 0 or B == 0:
+            kd = vd = None
+        else:
+            for t, n in ((kd, "kd"), (vd, "vd")):
+                if not t.is_cuda or t.dtype != torch.bfloat16 or t.shape != kd.shape or t.stride(3) != 1:
+                    raise ValueError(f"{n}: expected a bf16 CUDA view [B,Hk,L,d] with contiguous rows")
+            strides = kd.stride()[:3]
+            if any(kd.shape[i] > 1 and kd.stride(i) != vd.stride(i) for i in range(3)):
+                raise ValueError("kd and vd must have the same strides")
+    if o is None:
+        o = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=q.device)
+    _need(o, "o")
+    if want_lse and lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _need(lse, "lse", torch.float32)
+    if tuple(o.shape) != (B, Hq, d) or (lse is not None and tuple(lse.shape) != (B, Hq)):
+        raise ValueError(f"o must be {(B, Hq, d)} and lse {(B, Hq)}")
+    if workspace is None:
+        need = moda_decode_paged_workspace_bytes(Hq, Hk, d)
+        workspace = torch.empty(max(4, need // 4), dtype=torch.float32, device=q.device)
+    _need(workspace, "workspace", torch.float32)
+    _here(q, k_pages, v_pages, block_table, k_scales, v_scales, seq_lens, kd, vd, o, lse, workspace)
+    st = load().moda_decode_paged(_ptr(q), cache, _ptr(seq_lens), _ptr(kd), _ptr(vd), *strides, Hq, L,
+                                  float(scale), _ptr(o), _ptr(lse), _ptr(workspace),
+                                  workspace.numel() * 4, _stream(stream))
+    _check(st, "moda_decode_paged")
     return o, lse
 
 

@@ -128,6 +128,10 @@ moda_status checked_device(int* dev) {
   return device_state(dev, &err, &sms);
 }
 
+moda_status device_info(int* dev, unsigned int** err, int* num_sms) {
+  return device_state(dev, err, num_sms);
+}
+
 moda_status report(moda_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);

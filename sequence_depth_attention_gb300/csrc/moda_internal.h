@@ -76,6 +76,9 @@ void* current_context();
 // MODA_ERR_NO_DEVICE (or MODA_ERR_CUDA) with the detail set.
 moda_status checked_device(int* dev);
 
+// The same with the device error word's address and the SM count.
+moda_status device_info(int* dev, unsigned int** err, int* num_sms);
+
 // Sets the calling thread's last-error detail (see moda_last_error_detail)
 // and returns s.
 moda_status report(moda_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
@@ -115,6 +118,46 @@ size_t depth_mass_workspace_floats(int T, int Hk, int L);
 cudaError_t launch_depth_mass(const DepthMassArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_admit(int* ages, const float* mass, int Hk, int S, int recent,
                                int new_age, int* slot_out, cudaStream_t stream);
+// The paged cache of a call, with the device error word its kernels latch into.
+struct PagedKv {
+  int format, num_pages, page_size, Hk, d, B, max_pages;
+  void *k, *v, *k_scale, *v_scale;
+  const int* table;  // [B, max_pages]
+  unsigned int* err;
+};
+
+// Arguments of one append to the paged cache after validation on the host.
+struct KvAppendArgs {
+  const void *q, *k, *v;  // [N, H, d] bf16, rows of a token dense, tokens *_stride elements apart
+  int64_t q_stride, k_stride, v_stride;
+  const float* rope;  // [rope_rows, rot]
+  int rope_rows, rot, interleaved;
+  const int *seq, *pos;  // [N]
+  int N, Hq;
+  PagedKv c;
+  void *q_out, *k_out;  // dense; k_out may be nullptr
+  int num_sms;
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_gather(const PagedKv& c, const int* seq, const int* pos, int N, void* k,
+                             void* v, int num_sms, cudaStream_t stream);
+
+// Arguments of one paged decode call after validation on the host.
+struct DecodePagedArgs {
+  const void *q, *kd, *vd;  // q [B,Hq,d]; depth slots at the strides below (nullptr when L == 0)
+  PagedKv c;
+  const int* seq_lens;  // [B]
+  int64_t depth_b_stride, depth_hk_stride, depth_slot_stride;
+  int Hq, G, L;
+  float scale;
+  void* o;     // [B,Hq,d] bf16
+  float* lse;  // [B,Hq] or nullptr
+  float* work;
+  int num_sms;
+};
+size_t decode_paged_workspace_bytes(int Hq, int Hk, int d);
+cudaError_t launch_decode_paged(const DecodePagedArgs& a, cudaStream_t stream);
+
 cudaError_t launch_selftest_wait(unsigned int* err, int timeout_ms, cudaStream_t stream);
 
 }  // namespace moda
