@@ -1,0 +1,334 @@
+// What the two paged decode kernels (bf16 pages, 4-bit pages) share: the line
+// of units and its division over the CTAs, a warp's softmax state, and the way
+// a segment's result leaves a CTA.
+//
+// The batch is cut into units (some rows of one KV head of one sequence, or
+// some of its depth slots), all units of the batch lie in one line, and CTA i
+// of P takes the i-th P-th of them, whatever sequences it crosses: each CTA
+// streams the same number of bytes, for one long context as for a ragged
+// batch, and the lengths stay on the device. The units of one (sequence, KV
+// head) are a segment. A segment inside one CTA's share is written out there;
+// one that is cut leaves a partial state (m, l, unnormalised o) per CTA, and a
+// dependent kernel joins them.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "moda_internal.h"
+#include "sm103.cuh"
+#include "warp_mma.cuh"
+
+namespace moda {
+namespace paged {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxCtas = 608;  // four per SM of 152; sizes the workspace
+
+// The workspace: for each CTA the segment that it opens and does not finish
+// (-1: none) with the number of its partials, and the partials of CTA i: slot
+// 2i for a segment opened by an earlier CTA, 2i + 1 for the one that it opens.
+struct Work {
+  int2* opened;
+  float* o;   // [2 * kMaxCtas][G][D]
+  float* ml;  // [2 * kMaxCtas][G][2]
+};
+__host__ __device__ inline Work work_of(float* w, int G, int D) {
+  Work k;
+  k.opened = reinterpret_cast<int2*>(w);
+  k.o = w + 2 * kMaxCtas;
+  k.ml = k.o + (int64_t)2 * kMaxCtas * G * D;
+  return k;
+}
+
+struct Params {
+  const __nv_bfloat16* q;
+  const int* lens;
+  const int* table;
+  int num_pages, page_size, max_pages, B, Hk, G, L;
+  float scale_log2;
+  __nv_bfloat16* o;
+  float* lse;
+  float* work;
+  unsigned int* err;
+};
+inline Params params_of(const DecodePagedArgs& a) {
+  const PagedKv& c = a.c;
+  return {(const __nv_bfloat16*)a.q, a.seq_lens, c.table, c.num_pages, c.page_size, c.max_pages, c.B,
+          c.Hk, a.G, a.L, a.scale * kLog2e, (__nv_bfloat16*)a.o, a.lse, a.work, c.err};
+}
+
+// Sequence b's rows, within what its table can name.
+__device__ __forceinline__ int rows_of(const Params& p, int b) {
+  return min(max(__ldg(p.lens + b), 0), p.max_pages * p.page_size);
+}
+
+// A place in the line of units: depth units first, then units of KEYS rows.
+template <int KEYS>
+struct Place {
+  int b, hk, off, n, len;  // unit off of the n units of segment (b, hk); len rows
+  __device__ __forceinline__ void enter(const Params& p, int depth_units) {
+    len = rows_of(p, b);
+    n = depth_units + (len + KEYS - 1) / KEYS;
+  }
+  // the first unit of the next segment that has any; only where there is one
+  __device__ __forceinline__ void next_segment(const Params& p, int depth_units) {
+    off = 0;
+    if (++hk < p.Hk) return;
+    hk = 0;
+    do {
+      ++b;
+      enter(p, depth_units);
+    } while (n == 0);
+  }
+};
+
+// A CTA's share [u0, u1) of the `total` units, and the place it begins at.
+template <int KEYS>
+struct Share {
+  long long u0, u1, total;
+  int shares;  // CTAs that have any
+  Place<KEYS> at;
+};
+template <int WARPS>
+struct ShareSmem {
+  long long warp_sum[WARPS];
+  int start[3];
+};
+template <int KEYS, int WARPS>
+__device__ __forceinline__ Share<KEYS> share_of(const Params& p, int depth_units,
+                                                ShareSmem<WARPS>& sm) {
+  constexpr int THREADS = WARPS * 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // units before each thread's run of sequences, and in all
+  const int per = (p.B + THREADS - 1) / THREADS;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int raw = __ldg(p.lens + b);
+    if (raw < 0 || raw > p.max_pages * p.page_size)
+      atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
+    mine += depth_units + (rows_of(p, b) + KEYS - 1) / KEYS;
+  }
+  long long before = mine;  // inclusive scan of the warp
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, before, off);
+    if (lane >= off) before += x;
+  }
+  if (lane == 31) sm.warp_sum[warp] = before;
+  __syncthreads();
+  Share<KEYS> s;
+  s.total = 0;
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) before += sm.warp_sum[w];
+    s.total += sm.warp_sum[w];
+  }
+  before = (before - mine) * p.Hk;
+  s.total *= p.Hk;
+  s.shares = (int)min((long long)gridDim.x, s.total);
+  const int cta = blockIdx.x;
+  s.u0 = cta < s.shares ? s.total * cta / s.shares : 0;
+  s.u1 = cta < s.shares ? s.total * (cta + 1) / s.shares : 0;
+  if (s.u0 < s.u1 && s.u0 >= before && s.u0 < before + mine * p.Hk) {
+    long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      const int n = depth_units + (rows_of(p, b) + KEYS - 1) / KEYS;
+      if (s.u0 < at + (long long)n * p.Hk) {
+        sm.start[0] = b;
+        sm.start[1] = (int)((s.u0 - at) / n);
+        sm.start[2] = (int)((s.u0 - at) % n);
+        break;
+      }
+      at += (long long)n * p.Hk;
+    }
+  }
+  __syncthreads();
+  if (s.u0 < s.u1) {
+    s.at.b = sm.start[0];
+    s.at.hk = sm.start[1];
+    s.at.off = sm.start[2];
+    s.at.enter(p, depth_units);
+  }
+  return s;
+}
+
+// The CTA that owns unit u.
+template <int KEYS>
+__device__ __forceinline__ int owner_of(const Share<KEYS>& s, long long u) {
+  return (int)(((u + 1) * s.shares + s.total - 1) / s.total) - 1;
+}
+
+// o = 0 and lse = -infinity for the sequences with nothing to attend to.
+template <int D>
+__device__ __forceinline__ void write_empty(const Params& p) {
+  const int Hq = p.Hk * p.G;
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (rows_of(p, b) != 0) continue;
+    uint32_t* o = reinterpret_cast<uint32_t*>(p.o + (int64_t)b * Hq * D);
+    for (int i = threadIdx.x; i < Hq * D / 2; i += blockDim.x) o[i] = 0u;
+    if (p.lse)
+      for (int i = threadIdx.x; i < Hq; i += blockDim.x) p.lse[(int64_t)b * Hq + i] = -INFINITY;
+  }
+}
+
+// Byte offset of (row, col) in a bf16 tile of ROWS rows: 64-column boxes,
+// 16-byte chunks XORed with the row's low bits (the 128-byte TMA swizzle).
+template <int ROWS>
+__device__ __forceinline__ uint32_t at_bf16(int row, int col) {
+  return (uint32_t)((col >> 6) * (ROWS * 128) + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4) +
+                    ((col & 7) << 1));
+}
+
+// One warp's softmax state of a segment: for head pair (2c, 2c + 1) of each
+// 8-head tile the running maximum m (log2 units), this lane's share of the
+// sum l, and O^T.
+template <int D, int NT>
+struct State {
+  float m[NT][2], l[NT][2];
+  float o[NT][D / 16][4];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+    }
+  }
+  // Raises m of tile t to cover z (the scores plus the exponents that their
+  // values carry), and brings l and o to it. z: rows r0 and r0 + 8, heads 2c
+  // and 2c + 1. Most tiles bring no new maximum: one vote tells.
+  __device__ __forceinline__ void raise(int t, const float* z) {
+    const bool up = z[0] > m[t][0] || z[2] > m[t][0] || z[1] > m[t][1] || z[3] > m[t][1];
+    if (!__any_sync(0xffffffffu, up)) return;
+    float x0 = fmaxf(fmaxf(z[0], z[2]), m[t][0]), x1 = fmaxf(fmaxf(z[1], z[3]), m[t][1]);
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
+      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+    }
+    const float a0 = m[t][0] == x0 ? 1.f : sm103::ex2_approx(m[t][0] - x0);
+    const float a1 = m[t][1] == x1 ? 1.f : sm103::ex2_approx(m[t][1] - x1);
+    m[t][0] = x0;
+    m[t][1] = x1;
+    l[t][0] *= a0;
+    l[t][1] *= a1;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      o[t][i][0] *= a0; o[t][i][1] *= a1; o[t][i][2] *= a0; o[t][i][3] *= a1;
+    }
+  }
+  // p = 2^(s - m), added to l
+  __device__ __forceinline__ void weigh(int t, const float* s, float* p) {
+    const float r0 = m[t][0] == -INFINITY ? 0.f : m[t][0], r1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+    p[0] = sm103::ex2_approx(s[0] - r0);
+    p[1] = sm103::ex2_approx(s[1] - r1);
+    p[2] = sm103::ex2_approx(s[2] - r0);
+    p[3] = sm103::ex2_approx(s[3] - r1);
+    l[t][0] += p[0] + p[2];
+    l[t][1] += p[1] + p[3];
+  }
+};
+
+// bf16 queries of KV head hk as B tiles of S^T = K Q^T: k = the head
+// dimension, n = the head. Heads G and above are 0.
+template <int D, int NT>
+__device__ __forceinline__ void load_q_bf16(uint32_t (&qb)[NT][D / 16][2], const __nv_bfloat16* q,
+                                            int G, int lane) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int h = t * 8 + (lane >> 2);
+    const uint32_t* row = reinterpret_cast<const uint32_t*>(q + (int64_t)h * D) + (lane & 3);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      qb[t][ks][0] = h < G ? __ldg(row + ks * 8) : 0u;
+      qb[t][ks][1] = h < G ? __ldg(row + ks * 8 + 4) : 0u;
+    }
+  }
+}
+
+// The merge buffer: O of kCols columns of 8 heads for each warp, and (m, l).
+constexpr int kCols = 64;
+constexpr int kRowPad = kCols + 4;  // floats; the lanes of a quad land in different banks
+template <int WARPS>
+struct MergeSmem {
+  float o[WARPS][8][kRowPad];
+  float ml[WARPS][8][2];
+};
+
+// The state of WARPS warps (threads 0 .. 32 * WARPS - 1, which meet at named
+// barrier 1) as the segment's result, or as a partial in `slot` when the
+// segment is cut. put(m0, m1, t, half) stores the warp's columns 64 * half ..
+// + 63 of tile t for its heads 2c and 2c + 1. row0: the segment's first row of
+// o and lse.
+template <int D, int NT, int WARPS, class Put>
+__device__ __forceinline__ void leave(const Params& p, const Work& wk, MergeSmem<WARPS>& sm,
+                                      State<D, NT>& st, bool cut, int slot, int64_t row0, Put put) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane & 3;
+  auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory"); };
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int sh = 4; sh < 32; sh <<= 1) {
+      st.l[t][0] += __shfl_xor_sync(0xffffffffu, st.l[t][0], sh);
+      st.l[t][1] += __shfl_xor_sync(0xffffffffu, st.l[t][1], sh);
+    }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int heads = min(8, p.G - t * 8);
+#pragma unroll
+    for (int half = 0; half < D / kCols; ++half) {
+      meet();  // the buffer is free
+      put(sm.o[warp][2 * c], sm.o[warp][2 * c + 1], t, half);
+      if (lane < 4) {
+        sm.ml[warp][2 * c][0] = st.m[t][0];
+        sm.ml[warp][2 * c][1] = st.l[t][0];
+        sm.ml[warp][2 * c + 1][0] = st.m[t][1];
+        sm.ml[warp][2 * c + 1][1] = st.l[t][1];
+      }
+      meet();
+      // four columns of one head per thread
+      for (int i = tid; i < heads * (kCols / 4); i += WARPS * 32) {
+        const int h = i / (kCols / 4), d = (i % (kCols / 4)) * 4;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm.ml[w][h][0]);
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+          const float mw = sm.ml[w][h][0];
+          // a state that has met no key is (-infinity, 0, 0); one that has met
+          // only NaN scores has -infinity too, and its NaN must go on
+          const float a = mw == -INFINITY ? 1.f : sm103::ex2_approx(mw - M);
+          const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][h][d]);
+          L = fmaf(a, sm.ml[w][h][1], L);
+          acc.x = fmaf(a, x.x, acc.x); acc.y = fmaf(a, x.y, acc.y);
+          acc.z = fmaf(a, x.z, acc.z); acc.w = fmaf(a, x.w, acc.w);
+        }
+        const int g = t * 8 + h, col = half * kCols + d;
+        if (cut) {
+          *reinterpret_cast<float4*>(wk.o + ((int64_t)slot * p.G + g) * D + col) = acc;
+          if (col == 0) {
+            wk.ml[((int64_t)slot * p.G + g) * 2] = M;
+            wk.ml[((int64_t)slot * p.G + g) * 2 + 1] = L;
+          }
+        } else {
+          const float inv = 1.f / L;
+          const int64_t r = row0 + g;
+          *reinterpret_cast<uint2*>(p.o + r * D + col) =
+              make_uint2(wmma16::pack_bf16(acc.x * inv, acc.y * inv),
+                         wmma16::pack_bf16(acc.z * inv, acc.w * inv));
+          if (col == 0 && p.lse) p.lse[r] = (M + log2f(L)) * kLn2;
+        }
+      }
+    }
+  }
+}
+
+cudaError_t launch_join(const DecodePagedArgs& a, int grid, cudaStream_t stream);
+cudaError_t launch_mx4(const DecodePagedArgs& a, cudaStream_t stream);
+
+}  // namespace paged
+}  // namespace moda
