@@ -368,7 +368,8 @@ MODA_API moda_status moda_decode_strided(const void* q, const void* k_cache, con
  *                 point with blocks of 32: 4.25 bits an element.)
  *
  * page_size is 16, 32, 64 or 128; d is 64 or 128; num_pages * Hk * page_size
- * is at most 2^31 - 1, max_pages * page_size at most 2^30. k, v, k_scale and
+ * is at most 2^31 - 1, max_pages * page_size at most 2^30, B * Hk * max_pages *
+ * page_size at most 2^40. k, v, k_scale and
  * v_scale are 16-byte aligned, block_table 4-byte aligned. The struct is read
  * during the call; the buffers it names belong to the caller.
  *

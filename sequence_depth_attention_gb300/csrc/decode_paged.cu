@@ -20,6 +20,7 @@ namespace {
 constexpr int kCW = 4;                // consumer warps
 constexpr int kWarps = kCW + 1;       // and the producer
 constexpr int kKeys = 64;             // cached rows, or depth slots, of a unit
+constexpr int kCols = 64;             // columns of O merged at a time
 constexpr int kCtasPerSm = 2;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
@@ -28,7 +29,7 @@ struct Smem {
   static constexpr int kNS = D == 128 ? 3 : 6;      // stages
   static constexpr int kTile = kKeys * D * 2;
   uint8_t ring[kNS][2][kTile];  // [stage][K or V], 1024-byte aligned
-  MergeSmem<kCW> merge;
+  MergeSmem<kCW, kCols> merge;
   uint64_t full[kNS], empty[kNS];
   ShareSmem<kWarps> share;
   int abort;
@@ -60,7 +61,7 @@ __device__ __forceinline__ void tile_bf16(State<D, NT>& st, const uint32_t (&qb)
     s[t][1] = k0 ? s[t][1] * scale_log2 : -INFINITY;
     s[t][2] = k1 ? s[t][2] * scale_log2 : -INFINITY;
     s[t][3] = k1 ? s[t][3] * scale_log2 : -INFINITY;
-    st.raise(t, s[t]);
+    st.template raise<4>(t, s[t]);
     float p[4];
     st.weigh(t, s[t], p);
     // P^T (rows = keys, columns = heads) transposed into the B tile
@@ -126,18 +127,18 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
       if (x.off < depth_units) return 0;
       const int key = (x.off - depth_units) * kKeys + lane * box;
       if (lane * box >= kKeys || key >= x.len) return 0;
-      return __ldg(p.table + (int64_t)x.b * p.max_pages + key / p.page_size);
+      return __ldg(p.table + (int64_t)x.b * p.max_pages + (key >> p.page_shift));
     };
-    const long long n = sh.u1 - sh.u0;
+    const int n = (int)(sh.u1 - sh.u0);
     int page = page_of(at);
-    for (long long k = 0; k < n; ++k) {
+    for (int k = 0; k < n; ++k) {
       const Place<kKeys> cur = at;
       int pg = page;
       if (k + 1 < n) {
         if (++at.off == at.n) at.next_segment(p, depth_units);
         page = page_of(at);
       }
-      const int s = (int)(k % NS);
+      const int s = k % NS;
       const uint32_t bar = sm103::smem_u32(&sm.full[s]);
       if (k >= NS)
         sm103::mbar_wait_bounded(sm103::smem_u32(&sm.empty[s]), (uint32_t)((k / NS - 1) & 1), &sm.abort,
@@ -166,7 +167,7 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
             pg = 0;
           }
-          const int row = (key0 + lane * box) % p.page_size;
+          const int row = (key0 + lane * box) & ((1 << p.page_shift) - 1);
           const int head = pg * p.Hk + cur.hk;
 #pragma unroll
           for (int x = 0; x < D / 64; ++x) {
@@ -194,10 +195,10 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
   // arithmetic, so that they meet at the same barriers.
   const int r0 = lane >> 2;
   State<D, NT> st;
-  long long k = 0, left = sh.u1 - sh.u0;
+  int k = 0, left = (int)(sh.u1 - sh.u0);
   bool opened = false;
   while (left > 0) {
-    const int cnt = (int)min(left, (long long)(at.n - at.off));
+    const int cnt = min(left, at.n - at.off);
     const int end = at.off + cnt;
     const bool cut_before = at.off > 0, cut_after = end < at.n;
     const __nv_bfloat16* q = p.q + ((int64_t)at.b * p.Hk + at.hk) * p.G * D;
@@ -216,7 +217,7 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     uint32_t qb[NT][D / 16][2];
     load_q_bf16<D, NT>(qb, q, p.G, lane);
     for (; off < end; ++off) {
-      const int s = (int)(k % NS);
+      const int s = k % NS;
       const bool ok = take(s);
       const int there = (off < depth_units ? p.L - off * kKeys
                                            : at.len - (off - depth_units) * kKeys) - warp * 16;
@@ -226,12 +227,12 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                                 lane);
       give(s);
     }
-    leave<D, NT, kCW>(p, wk, sm.merge, st, cut_before || cut_after,
+    leave<D, NT>(p, wk, sm.merge, st, cut_before || cut_after,
                       2 * blockIdx.x + (cut_before ? 0 : 1),
-                      ((int64_t)at.b * p.Hk + at.hk) * p.G, [&](float* m0, float* m1, int t, int half) {
+                      ((int64_t)at.b * p.Hk + at.hk) * p.G, [&](float* m0, float* m1, int t, int part) {
 #pragma unroll
                         for (int i = 0; i < kCols / 16; ++i) {
-                          const float(&x)[4] = st.o[t][half * 4 + i];
+                          const float(&x)[4] = st.o[t][part * 4 + i];
                           m0[i * 16 + r0] = x[0];
                           m1[i * 16 + r0] = x[1];
                           m0[i * 16 + r0 + 8] = x[2];

@@ -45,7 +45,7 @@ struct Params {
   const __nv_bfloat16* q;
   const int* lens;
   const int* table;
-  int num_pages, page_size, max_pages, B, Hk, G, L;
+  int num_pages, page_shift, max_pages, B, Hk, G, L;  // pages of 1 << page_shift rows
   float scale_log2;
   __nv_bfloat16* o;
   float* lse;
@@ -54,13 +54,13 @@ struct Params {
 };
 inline Params params_of(const DecodePagedArgs& a) {
   const PagedKv& c = a.c;
-  return {(const __nv_bfloat16*)a.q, a.seq_lens, c.table, c.num_pages, c.page_size, c.max_pages, c.B,
-          c.Hk, a.G, a.L, a.scale * kLog2e, (__nv_bfloat16*)a.o, a.lse, a.work, c.err};
+  return {(const __nv_bfloat16*)a.q, a.seq_lens, c.table, c.num_pages, __builtin_ctz((unsigned)c.page_size),
+          c.max_pages, c.B, c.Hk, a.G, a.L, a.scale * kLog2e, (__nv_bfloat16*)a.o, a.lse, a.work, c.err};
 }
 
 // Sequence b's rows, within what its table can name.
 __device__ __forceinline__ int rows_of(const Params& p, int b) {
-  return min(max(__ldg(p.lens + b), 0), p.max_pages * p.page_size);
+  return min(max(__ldg(p.lens + b), 0), p.max_pages << p.page_shift);
 }
 
 // A place in the line of units: depth units first, then units of KEYS rows.
@@ -106,7 +106,7 @@ __device__ __forceinline__ Share<KEYS> share_of(const Params& p, int depth_units
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
     const int raw = __ldg(p.lens + b);
-    if (raw < 0 || raw > p.max_pages * p.page_size)
+    if (raw < 0 || raw > p.max_pages << p.page_shift)
       atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
     mine += depth_units + (rows_of(p, b) + KEYS - 1) / KEYS;
   }
@@ -196,13 +196,20 @@ struct State {
       for (int i = 0; i < D / 16; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
     }
   }
-  // Raises m of tile t to cover z (the scores plus the exponents that their
-  // values carry), and brings l and o to it. z: rows r0 and r0 + 8, heads 2c
-  // and 2c + 1. Most tiles bring no new maximum: one vote tells.
-  __device__ __forceinline__ void raise(int t, const float* z) {
-    const bool up = z[0] > m[t][0] || z[2] > m[t][0] || z[1] > m[t][1] || z[3] > m[t][1];
-    if (!__any_sync(0xffffffffu, up)) return;
-    float x0 = fmaxf(fmaxf(z[0], z[2]), m[t][0]), x1 = fmaxf(fmaxf(z[1], z[3]), m[t][1]);
+  // Raises m of tile t to cover z, N scores (for the 4-bit path plus what
+  // their values carry) of head 2c at even and 2c + 1 at odd places, and brings
+  // l and o to it. Most tiles bring no new maximum: one vote tells.
+  template <int N>
+  __device__ __forceinline__ void raise(int t, const float (&z)[N]) {
+    float x0 = z[0], x1 = z[1];
+#pragma unroll
+    for (int i = 2; i < N; i += 2) {
+      x0 = fmaxf(x0, z[i]);
+      x1 = fmaxf(x1, z[i + 1]);
+    }
+    if (!__any_sync(0xffffffffu, x0 > m[t][0] || x1 > m[t][1])) return;
+    x0 = fmaxf(x0, m[t][0]);
+    x1 = fmaxf(x1, m[t][1]);
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
       x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
@@ -248,22 +255,20 @@ __device__ __forceinline__ void load_q_bf16(uint32_t (&qb)[NT][D / 16][2], const
   }
 }
 
-// The merge buffer: O of kCols columns of 8 heads for each warp, and (m, l).
-constexpr int kCols = 64;
-constexpr int kRowPad = kCols + 4;  // floats; the lanes of a quad land in different banks
-template <int WARPS>
+// The merge buffer: O of COLS columns of 8 heads for each warp, and (m, l).
+template <int WARPS, int COLS>
 struct MergeSmem {
-  float o[WARPS][8][kRowPad];
+  float o[WARPS][8][COLS + 4];  // the lanes of a quad land in different banks
   float ml[WARPS][8][2];
 };
 
 // The state of WARPS warps (threads 0 .. 32 * WARPS - 1, which meet at named
 // barrier 1) as the segment's result, or as a partial in `slot` when the
-// segment is cut. put(m0, m1, t, half) stores the warp's columns 64 * half ..
-// + 63 of tile t for its heads 2c and 2c + 1. row0: the segment's first row of
+// segment is cut. put(m0, m1, t, part) stores the warp's columns COLS * part
+// .. of tile t for its heads 2c and 2c + 1. row0: the segment's first row of
 // o and lse.
-template <int D, int NT, int WARPS, class Put>
-__device__ __forceinline__ void leave(const Params& p, const Work& wk, MergeSmem<WARPS>& sm,
+template <int D, int NT, int WARPS, int COLS, class Put>
+__device__ __forceinline__ void leave(const Params& p, const Work& wk, MergeSmem<WARPS, COLS>& sm,
                                       State<D, NT>& st, bool cut, int slot, int64_t row0, Put put) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane & 3;
   auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory"); };
@@ -278,9 +283,9 @@ __device__ __forceinline__ void leave(const Params& p, const Work& wk, MergeSmem
   for (int t = 0; t < NT; ++t) {
     const int heads = min(8, p.G - t * 8);
 #pragma unroll
-    for (int half = 0; half < D / kCols; ++half) {
+    for (int part = 0; part < D / COLS; ++part) {
       meet();  // the buffer is free
-      put(sm.o[warp][2 * c], sm.o[warp][2 * c + 1], t, half);
+      put(sm.o[warp][2 * c], sm.o[warp][2 * c + 1], t, part);
       if (lane < 4) {
         sm.ml[warp][2 * c][0] = st.m[t][0];
         sm.ml[warp][2 * c][1] = st.l[t][0];
@@ -289,8 +294,8 @@ __device__ __forceinline__ void leave(const Params& p, const Work& wk, MergeSmem
       }
       meet();
       // four columns of one head per thread
-      for (int i = tid; i < heads * (kCols / 4); i += WARPS * 32) {
-        const int h = i / (kCols / 4), d = (i % (kCols / 4)) * 4;
+      for (int i = tid; i < heads * (COLS / 4); i += WARPS * 32) {
+        const int h = i / (COLS / 4), d = (i % (COLS / 4)) * 4;
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm.ml[w][h][0]);
@@ -307,7 +312,7 @@ __device__ __forceinline__ void leave(const Params& p, const Work& wk, MergeSmem
           acc.x = fmaf(a, x.x, acc.x); acc.y = fmaf(a, x.y, acc.y);
           acc.z = fmaf(a, x.z, acc.z); acc.w = fmaf(a, x.w, acc.w);
         }
-        const int g = t * 8 + h, col = half * kCols + d;
+        const int g = t * 8 + h, col = part * COLS + d;
         if (cut) {
           *reinterpret_cast<float4*>(wk.o + ((int64_t)slot * p.G + g) * D + col) = acc;
           if (col == 0) {

@@ -27,14 +27,23 @@ constexpr int kWarps = 4;
 constexpr int kKeys = 32;       // cached rows of a unit
 constexpr int kDepthKeys = 16;  // depth slots of a unit; their K and V take a stage each
 constexpr int kNS = 3;          // stages of a warp
+constexpr int kCols = 32;       // columns of O merged at a time
 template <int NT>
 constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
 
+// A stage: codes of K and of V (or kDepthKeys bf16 rows of one of the two),
+// then their scales.
+template <int D>
+struct Stage {
+  static constexpr uint32_t kRow = D / 2, kBlocks = D / 32;  // bytes of a row
+  static constexpr uint32_t kV = kKeys * kRow;
+  static constexpr uint32_t kKs = 2 * kV, kVs = kKs + kKeys * kBlocks;
+  static constexpr uint32_t kBytes = kVs + kKeys * kBlocks;
+};
 template <int D>
 struct Smem {
-  uint8_t codes[kWarps][kNS][2 * kKeys * D / 2];  // 1024-byte aligned stages
-  uint8_t scales[kWarps][kNS][2][kKeys * D / 32];
-  MergeSmem<kWarps> merge;
+  uint8_t ring[kWarps][kNS][Stage<D>::kBytes];
+  MergeSmem<kWarps, kCols> merge;
   ShareSmem<kWarps> share;
 };
 
@@ -49,33 +58,34 @@ struct Mx4Pages {
 // 2^-29 of it.
 constexpr float kHeadroom = 15.f;
 
-// Byte offset of 16-byte chunk `chunk` of a 4-bit row: rows of D/2 bytes whose
-// chunks are XORed with bits of the row, so that neither the words that a warp
-// reads of 8 keys of K nor the half words of 4 keys of V meet in a bank.
+// Byte offset of 16-byte vector `v` (block v of 32 codes) of row r, placed so
+// that none of these meet in a bank: whole rows side by side (the copies), 8
+// rows in a row (V's transposing loads), rows 4i and 4i + 1, or 4i + 2 and
+// 4i + 3, of 16 (K's words).
 template <int D>
-__device__ __forceinline__ uint32_t at_mx4(int row, int chunk) {
-  return D == 128 ? (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4))
-                  : (uint32_t)(row * 32 + ((chunk ^ ((row >> 2) & 1)) << 4));
+__device__ __forceinline__ uint32_t at_mx4(int r, int v) {
+  return D == 128 ? (uint32_t)(r * 64 + ((v ^ ((r >> 1) & 3) ^ ((r >> 3) & 1)) << 4))
+                  : (uint32_t)((r ^ ((r >> 2) & 2)) * 32 + ((v ^ ((r >> 2) & 1)) << 4));
 }
 // The key that MMA index i (a row of K, a column of V^T) of a 16-key tile
-// stands for in the 4-bit path: bits 0 and 1 change places, so that the four
-// rows that the lanes of a quad read V from at once lie in different banks.
-__device__ __forceinline__ int key_of(int i) { return (i & 12) | ((i & 1) << 1) | ((i >> 1) & 1); }
+// stands for: a lane's columns 2c, 2c + 1, 2c + 8, 2c + 9 of V^T are the four
+// keys in a row that the transposing load gives it.
+__device__ __forceinline__ int key_of(int i) {
+  return ((i & 6) << 1) | ((i & 8) >> 2) | (i & 1);
+}
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
+// Two 16x16 byte matrices (16 rows of 16 bytes at the addresses of lanes 0-15
+// and 16-31) transposed: lane (r0, c) gets of each matrix the bytes of rows
+// 4c .. 4c + 3 in column r0 (first register) and r0 + 8 (second).
+__device__ __forceinline__ void ldsm_t_bytes(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
 }
 
 // The eight e2m1 codes of w as fp16 pairs: byte i gives r[i], low half first.
@@ -87,14 +97,23 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& r0, uint32_t&
       : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
       : "r"(w));
 }
-// Two scale bytes as powers of two (255: NaN).
-__device__ __forceinline__ void scales_to_f32(uint32_t two, float& a, float& b) {
-  uint32_t r;
-  asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.bf16x2.ue8m0x2 %0, t;\n}\n"
-      : "=r"(r)
-      : "r"(two));
-  a = __uint_as_float(r << 16);
-  b = __uint_as_float(r & 0xffff0000u);
+// Those of bytes 1 and 3 alone.
+__device__ __forceinline__ void odd_codes_to_f16(uint32_t w, uint32_t& r1, uint32_t& r3) {
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %2;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b;\n cvt.rn.f16x2.e2m1x2 %1, d;\n}\n"
+      : "=r"(r1), "=r"(r3)
+      : "r"(w));
+}
+// The scale bytes of a row's blocks as powers of two (255: infinity). A byte
+// at a time: the load unit and the multiplier have room, the ALU has not.
+template <int NB>
+__device__ __forceinline__ void load_scales(uint32_t addr, float (&f)[NB]) {
+#pragma unroll
+  for (int g = 0; g < NB; ++g) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr + g));
+    f[g] = __uint_as_float(v * (1u << 23));
+  }
 }
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -102,6 +121,13 @@ __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0
       "{%0,%1,%2,%3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_first(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};\n"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
@@ -145,7 +171,8 @@ __device__ __forceinline__ void load_q_f16(uint32_t (&qb)[NT][D / 32][4], float 
         qb[t][g][i] = pack_f16(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
     }
     // heads 2c and 2c + 1 of this tile belong to lanes 8c and 8c + 4
-    const float mine = scale_log2 * __uint_as_float((uint32_t)(127 - 14 + max(e, -112)) << 23);
+    // (never 0: the rows that do not exist carry -infinity times it)
+    const float mine = fmaxf(scale_log2 * __uint_as_float((uint32_t)(127 - 14 + e) << 23), 0x1p-126f);
     back[t][0] = __shfl_sync(0xffffffffu, mine, c * 8);
     back[t][1] = __shfl_sync(0xffffffffu, mine, c * 8 + 4);
   }
@@ -172,13 +199,13 @@ __device__ __forceinline__ void depth_scores(State<D, NT>& st, const uint32_t (&
 #pragma unroll
   for (int ks = 0; ks < D / 16; ++ks) {
     uint32_t a[4];
-    wmma16::ldsm_x4(kb + at_bf16<16>((lm & 1) * 8 + key_of(lr), ks * 16 + (lm >> 1) * 8), a[0], a[1],
+    wmma16::ldsm_x4(kb + at_bf16<16>(key_of((lm & 1) * 8 + lr), ks * 16 + (lm >> 1) * 8), a[0], a[1],
                     a[2], a[3]);
 #pragma unroll
     for (int t = 0; t < NT; ++t) wmma16::mma_bf16(s[t], a, qb[t][ks][0], qb[t][ks][1]);
   }
   const int ka = key_of(lane >> 2);
-  const bool k0 = ka < there, k1 = ka + 8 < there;
+  const bool k0 = ka < there, k1 = ka + 2 < there;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     s[t][0] = k0 ? s[t][0] * scale_log2 : -INFINITY;
@@ -187,7 +214,7 @@ __device__ __forceinline__ void depth_scores(State<D, NT>& st, const uint32_t (&
     s[t][3] = k1 ? s[t][3] * scale_log2 : -INFINITY;
     const float z[4] = {s[t][0] - kHeadroom, s[t][1] - kHeadroom, s[t][2] - kHeadroom,
                         s[t][3] - kHeadroom};
-    st.raise(t, z);
+    st.template raise<4>(t, z);
     float p[4];
     st.weigh(t, s[t], p);
     pb[t][0] = wmma16::movmatrix_t(wmma16::pack_bf16(p[0], p[1]));
@@ -195,22 +222,26 @@ __device__ __forceinline__ void depth_scores(State<D, NT>& st, const uint32_t (&
   }
 }
 
-// Their values, in this kernel's order of O's rows: tile 2g + t of block g
-// holds d = 32 g + 4 r0 + 2 t in row r0 and the next one in r0 + 8. Rows past
-// L are zeros.
+// Their values, in this kernel's order of O's rows: of block g, tile 2g holds
+// d = 32 g + 2 r0 in row r0 and 32 g + 16 + 2 r0 in r0 + 8, tile 2g + 1 the
+// elements after them. Rows past L are zeros.
 template <int D, int NT>
 __device__ __forceinline__ void depth_values(State<D, NT>& st, const uint32_t (&pb)[NT][2], uint32_t vb,
                                              int lane) {
-  const int r0 = lane >> 2, v0 = key_of(2 * (lane & 3));
+  const int r0 = lane >> 2, v0 = 4 * (lane & 3);
 #pragma unroll
   for (int g = 0; g < D / 32; ++g) {
-    const int col = g * 32 + r0 * 4;
-    const uint2 x0 = lds64(vb + at_bf16<16>(v0, col)), x1 = lds64(vb + at_bf16<16>(v0 + 2, col));
-    const uint2 x2 = lds64(vb + at_bf16<16>(v0 + 8, col)), x3 = lds64(vb + at_bf16<16>(v0 + 10, col));
-    const uint32_t a[4] = {__byte_perm(x0.x, x1.x, 0x5410), __byte_perm(x0.x, x1.x, 0x7632),
-                           __byte_perm(x2.x, x3.x, 0x5410), __byte_perm(x2.x, x3.x, 0x7632)};
-    const uint32_t b[4] = {__byte_perm(x0.y, x1.y, 0x5410), __byte_perm(x0.y, x1.y, 0x7632),
-                           __byte_perm(x2.y, x3.y, 0x5410), __byte_perm(x2.y, x3.y, 0x7632)};
+    uint32_t a[4], b[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int col = g * 32 + h * 16 + r0 * 2;
+      const uint32_t x0 = lds32(vb + at_bf16<16>(v0, col)), x1 = lds32(vb + at_bf16<16>(v0 + 1, col));
+      const uint32_t x2 = lds32(vb + at_bf16<16>(v0 + 2, col)), x3 = lds32(vb + at_bf16<16>(v0 + 3, col));
+      a[h] = __byte_perm(x0, x1, 0x5410);
+      a[h + 2] = __byte_perm(x2, x3, 0x5410);
+      b[h] = __byte_perm(x0, x1, 0x7632);
+      b[h + 2] = __byte_perm(x2, x3, 0x7632);
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       wmma16::mma_bf16(st.o[t][2 * g], a, pb[t][0], pb[t][1]);
@@ -219,136 +250,201 @@ __device__ __forceinline__ void depth_values(State<D, NT>& st, const uint32_t (&
   }
 }
 
-// The 32 rows of a unit into the state, two tiles of 16 keys side by side.
-// TAIL: only `there` of them exist.
+// The 32 rows of a unit (in the stage at `sb`) into the state, two tiles of 16
+// keys side by side. TAIL: only `there` of them exist.
 template <int D, int NT, bool TAIL>
 __device__ __forceinline__ void unit_mx4(State<D, NT>& st, const uint32_t (&qb)[NT][D / 32][4],
-                                         const float (&back)[NT][2], uint32_t kb, uint32_t vb,
-                                         uint32_t ksb, uint32_t vsb, int there, int lane) {
-  constexpr int NB = D / 32;  // blocks of a row
-  constexpr int ROW = D / 2;  // bytes
+                                         const float (&back)[NT][2], uint32_t sb, int there, int lane) {
+  using S = Stage<D>;
+  constexpr int NB = S::kBlocks;
   const int r0 = lane >> 2, c = lane & 3;
-  const int ka = key_of(r0);  // this lane's keys: ka + 8 i, i = 0 .. 3
-  auto scale_word = [&](uint32_t base, int i) -> uint32_t {
-    const uint32_t a = base + (ka + 8 * i) * NB;
-    return NB == 4 ? lds32(a) : lds16(a);
-  };
+  // this lane's keys: ka + 16 j + 2 i, rows r0 + 8 i of tile j
+  const int ka = key_of(r0);
+  auto key = [&](int n) { return ka + 16 * (n >> 1) + 2 * (n & 1); };
+  uint32_t kw[2][NB];  // block g of rows ka and ka + 2
+#pragma unroll
+  for (int g = 0; g < NB; ++g) {
+    kw[0][g] = at_mx4<D>(ka, g) + c * 4;
+    kw[1][g] = at_mx4<D>(ka + 2, g) + c * 4;
+  }
   float s[2][NT][4];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     float f[2][NB];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t w = scale_word(ksb, 2 * j + i);
-#pragma unroll
-      for (int g = 0; g < NB; g += 2) scales_to_f32(w >> (8 * g), f[i][g], f[i][g + 1]);
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) s[j][t][0] = s[j][t][1] = s[j][t][2] = s[j][t][3] = 0.f;
+    load_scales<NB>(sb + S::kKs + key(2 * j) * NB, f[0]);
+    load_scales<NB>(sb + S::kKs + key(2 * j + 1) * NB, f[1]);
 #pragma unroll
     for (int g = 0; g < NB; ++g) {
       uint32_t a[4], b[4];  // two k-steps of 16
-      const uint32_t w = kb + at_mx4<D>(ka, g) + c * 4 + j * 16 * ROW;
-      codes_to_f16(lds32(w), a[0], a[2], b[0], b[2]);
-      codes_to_f16(lds32(w + 8 * ROW), a[1], a[3], b[1], b[3]);
+      const uint32_t tile = sb + j * 16 * S::kRow;
+      codes_to_f16(lds32(tile + kw[0][g]), a[0], a[2], b[0], b[2]);
+      codes_to_f16(lds32(tile + kw[1][g]), a[1], a[3], b[1], b[3]);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16(x, a, qb[t][g][0], qb[t][g][1]);
+        float x[4];
+        mma_f16_first(x, a, qb[t][g][0], qb[t][g][1]);
         mma_f16(x, b, qb[t][g][2], qb[t][g][3]);
-        s[j][t][0] = fmaf(x[0], f[0][g], s[j][t][0]);
-        s[j][t][1] = fmaf(x[1], f[0][g], s[j][t][1]);
-        s[j][t][2] = fmaf(x[2], f[1][g], s[j][t][2]);
-        s[j][t][3] = fmaf(x[3], f[1][g], s[j][t][3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          s[j][t][i] = g == 0 ? x[i] * f[i >> 1][g] : fmaf(x[i], f[i >> 1][g], s[j][t][i]);
       }
     }
   }
+  // V's scales, and the exponent of each row's largest, from -80 so that the
+  // sum of 2^(score - m) stays in range. A block stored as NaN (its codes are
+  // 0, and 0 times infinity is NaN) leaves the other blocks' alone.
+  float f[4][NB], e[4];
+  uint32_t dead = 0;  // bit n: this lane's key n does not exist
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    // V's scales, and the exponent of each row's largest (NaN aside), from -80
-    // so that the sum of 2^(score - m) stays in range
-    float f[2][NB], e[2];
+  for (int n = 0; n < 4; ++n) {
+    load_scales<NB>(sb + S::kVs + key(n) * NB, f[n]);
+    if (TAIL && key(n) >= there) {
+      dead |= 1u << n;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t w = scale_word(vsb, 2 * j + i);
-      // what lies behind the last row may be any byte: weight 0 times a power of two
-      if (TAIL && ka + 8 * (2 * j + i) >= there) w = 0x7f7f7f7fu;
-#pragma unroll
-      for (int g = 0; g < NB; g += 2) scales_to_f32(w >> (8 * g), f[i][g], f[i][g + 1]);
-      float big = 0x1p-80f;
-#pragma unroll
-      for (int g = 0; g < NB; ++g) big = fmaxf(big, f[i][g]);
-      e[i] = (float)((int)(__float_as_uint(big) >> 23) - 127) - kHeadroom;
+      for (int g = 0; g < NB; ++g) f[n][g] = 1.f;  // it may be any byte: weight 0 times 1
     }
-    float p[NT][4];
+    e[n] = 0x1p-80f;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float x[4];
+    for (int g = 0; g < NB; ++g) e[n] = fmaxf(e[n], f[n][g]);
+  }
+  if (__any_sync(0xffffffffu, fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) == INFINITY)) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = s[j][t][i] * back[t][i & 1];
-        if (TAIL && ka + 8 * (2 * j + (i >> 1)) >= there) x[i] = -INFINITY;
-      }
-      const float z[4] = {x[0] + e[0], x[1] + e[0], x[2] + e[1], x[3] + e[1]};
-      st.raise(t, z);
-      st.weigh(t, x, p[t]);
-    }
-    const int v0 = key_of(2 * c);
-    const uint32_t r2 = r0 * 2 + j * 16 * ROW;
+    for (int n = 0; n < 4; ++n) {
+      e[n] = 0x1p-80f;
 #pragma unroll
-    for (int g = 0; g < NB; ++g) {
-      // 4 codes (d = 32 g + 4 r0 .. + 3) of each of the lane's 4 keys; the same
-      // code of a pair of keys side by side in a byte
-      const uint32_t w0 = vb + at_mx4<D>(v0, g) + r2, w1 = vb + at_mx4<D>(v0 + 2, g) + r2;
-      const uint32_t x = lds16(w0) | (lds16(w0 + 8 * ROW) << 16);
-      const uint32_t y = lds16(w1) | (lds16(w1 + 8 * ROW) << 16);
-      uint32_t a[4], b[4];
-      codes_to_f16((x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u), a[0], b[0], a[2], b[2]);
-      codes_to_f16(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), a[1], b[1], a[3], b[3]);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const uint32_t pb0 = wmma16::movmatrix_t(pack_f16(p[t][0] * f[0][g], p[t][1] * f[0][g]));
-        const uint32_t pb1 = wmma16::movmatrix_t(pack_f16(p[t][2] * f[1][g], p[t][3] * f[1][g]));
-        mma_f16(st.o[t][2 * g], a, pb0, pb1);
-        mma_f16(st.o[t][2 * g + 1], b, pb0, pb1);
-      }
+      for (int g = 0; g < NB; ++g)
+        if (f[n][g] < INFINITY) e[n] = fmaxf(e[n], f[n][g]);
     }
   }
+#pragma unroll
+  for (int n = 0; n < 4; ++n)  // as a float, by way of 2^23 + its biased form
+    e[n] = __uint_as_float(0x4b000000u | (__float_as_uint(e[n]) >> 23)) - (8388608.f + 127.f + kHeadroom);
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    float z[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float& x = s[i >> 2][t][i & 3];
+      if (TAIL && (dead >> (i >> 1) & 1u)) x = -INFINITY;
+      z[i] = fmaf(x, back[t][i & 1], e[i >> 1]);
+    }
+    st.template raise<8>(t, z);
+    // p = 2^(score - m); a row of no finite score so far keeps m = -infinity
+    const float n0 = st.m[t][0] == -INFINITY ? 0.f : -st.m[t][0];
+    const float n1 = st.m[t][1] == -INFINITY ? 0.f : -st.m[t][1];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float& x = s[i >> 2][t][i & 3];
+      x = sm103::ex2_approx(fmaf(x, back[t][i & 1], i & 1 ? n1 : n0));
+    }
+    st.l[t][0] += (s[0][t][0] + s[0][t][2]) + (s[1][t][0] + s[1][t][2]);
+    st.l[t][1] += (s[0][t][1] + s[0][t][3]) + (s[1][t][1] + s[1][t][3]);
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int g2 = 0; g2 < NB; g2 += 2) {
+      uint32_t raw[4];  // blocks g2 and g2 + 1: bytes of 4 keys, columns r0 and r0 + 8
+      ldsm_t_bytes(sb + S::kV + j * 16 * S::kRow + at_mx4<D>(lane & 15, g2 + (lane >> 4)), raw);
+#pragma unroll
+      for (int gi = 0; gi < 2; ++gi) {
+        const int g = g2 + gi;
+        // a byte holds elements 2r and 2r + 1 of one key: put the same element
+        // of keys 0, 1 into byte 1 and of keys 2, 3 into byte 3 (left shifts
+        // only, which the multiplier does)
+        uint32_t a[4], b[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t x = raw[2 * gi + h], x4 = x * 16u, x8 = x * 256u;
+          odd_codes_to_f16((x8 & 0x0f000f00u) | (x4 & ~0x0f000f00u), a[h], a[h + 2]);
+          odd_codes_to_f16((x4 & 0x0f000f00u) | (x & ~0x0f000f00u), b[h], b[h + 2]);
+        }
+        const float f0 = f[2 * j][g], f1 = f[2 * j + 1][g];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float(&p)[4] = s[j][t];
+          const uint32_t pb0 = wmma16::movmatrix_t(pack_f16(p[0] * f0, p[1] * f0));
+          const uint32_t pb1 = wmma16::movmatrix_t(pack_f16(p[2] * f1, p[3] * f1));
+          mma_f16(st.o[t][2 * g], a, pb0, pb1);
+          mma_f16(st.o[t][2 * g + 1], b, pb0, pb1);
+        }
+      }
+    }
 }
 
-// What a warp copies next: its units, W apart in the CTA's share; a depth unit
-// is two entries of the ring (K, then V), a unit of rows one.
+// What a warp copies next: its units, kWarps apart in the CTA's share; a depth
+// unit is two entries of the ring (K, then V), a unit of rows one.
 template <int D>
 struct Feed {
-  static constexpr int ROW = D / 2, NB = D / 32;
+  using S = Stage<D>;
+  static constexpr int ROW = S::kRow, NB = S::kBlocks;
   Place<kKeys> at;
-  long long left;  // units of the CTA's share from `at` on
-  int part;        // of a depth unit
+  int left;  // units of the CTA's share from `at` on
+  int part;  // of a depth unit
+  const int* pages;  // of the sequence
   int page0, page1;  // pages of the unit's first and second 16 rows
 
   __device__ __forceinline__ void look_up(const Params& p, int depth_units) {
     page0 = page1 = 0;
     if (left <= 0 || at.off < depth_units) return;
     const int key = (at.off - depth_units) * kKeys;
-    const int* row = p.table + (int64_t)at.b * p.max_pages;
-    page0 = __ldg(row + key / p.page_size);
-    page1 = p.page_size > 16 ? page0 : key + 16 < at.len ? __ldg(row + key / p.page_size + 1) : 0;
+    page0 = __ldg(pages + (key >> p.page_shift));
+    page1 = p.page_shift > 4 ? page0 : key + 16 < at.len ? __ldg(pages + (key >> 4) + 1) : 0;
+  }
+  __device__ __forceinline__ void begin(const Params& p, int depth_units, const Share<kKeys>& sh,
+                                        int first) {
+    at = sh.at;
+    left = (int)(sh.u1 - sh.u0);
+    part = 0;
+    pages = p.table + (int64_t)at.b * p.max_pages;
+    skip(p, depth_units, first);
+    look_up(p, depth_units);
   }
   // n units on
   __device__ __forceinline__ void skip(const Params& p, int depth_units, int n) {
     left -= n;
-    if (left <= 0) return;
-    int off = at.off + n;
-    while (off >= at.n) {
+    at.off += n;
+    if (at.off < at.n || left <= 0) return;
+    int off = at.off;
+    do {
       off -= at.n;
       at.next_segment(p, depth_units);
-    }
+    } while (off >= at.n);
     at.off = off;
+    pages = p.table + (int64_t)at.b * p.max_pages;
+  }
+  // Rows row0 .. + 15 and row1 .. + 15 of the pool; TAIL: only `rows` of them
+  // are read, the others become zeros.
+  template <bool TAIL>
+  __device__ __forceinline__ void copy_rows(const Mx4Pages& pg, uint32_t stage, uint32_t row0,
+                                            uint32_t row1, int rows, int lane) {
+    constexpr int RPI = 512 / ROW;  // rows of one copy instruction of a warp
+    const int r = lane / NB, v = lane % NB;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int64_t from = (int64_t)(half ? row1 : row0) * ROW + lane * 16;
+#pragma unroll
+      for (int i = 0; i < 16 / RPI; ++i) {
+        const int to = half * 16 + i * RPI + r;
+        const bool there = !TAIL || to < rows;
+        const int64_t src = there ? from + i * 512 : 0;
+        cp16(stage + at_mx4<D>(to, v), pg.k + src, there);
+        cp16(stage + S::kV + at_mx4<D>(to, v), pg.v + src, there);
+      }
+    }
+    // scales: 16-byte vectors of 16 / NB rows
+    constexpr int SV = kKeys * NB / 16;  // vectors of the unit, of K or of V
+    if (lane < 2 * SV) {
+      const int first = lane % SV * (16 / NB);
+      const bool there = !TAIL || first < rows;
+      const int64_t src = there ? (int64_t)(first < 16 ? row0 + first : row1 + first - 16) * NB : 0;
+      cp16(stage + S::kKs + lane * 16, (lane < SV ? pg.k_scale : pg.v_scale) + src, there);
+    }
   }
   // Starts the next entry's copies into a stage (or nothing at the end); one
   // group of asynchronous copies in any case.
   __device__ __forceinline__ void start(const Params& p, const Mx4Pages& pg, int depth_units,
-                                        uint32_t codes, uint32_t scales, int lane) {
+                                        uint32_t stage, int lane) {
     if (left > 0) {
       if (at.off < depth_units) {
         const int l0 = at.off * kDepthKeys;
@@ -359,7 +455,7 @@ struct Feed {
         for (int i = 0; i < kDepthKeys * VPR / 32; ++i) {
           const int r = (i * 32 + lane) / VPR, v = lane % VPR;
           const bool there = l0 + r < p.L;
-          cp16(codes + at_bf16<16>(r, v * 8), there ? src + r * pg.depth_slot + v * 16 : src, there);
+          cp16(stage + at_bf16<16>(r, v * 8), there ? src + r * pg.depth_slot + v * 16 : src, there);
         }
         if (part == 0) {
           part = 1;
@@ -370,36 +466,20 @@ struct Feed {
         }
       } else {
         const int key = (at.off - depth_units) * kKeys, rows = at.len - key;
-        if (page0 < 0 || page0 >= p.num_pages || page1 < 0 || page1 >= p.num_pages) {
+        if ((unsigned)page0 >= (unsigned)p.num_pages || (unsigned)page1 >= (unsigned)p.num_pages) {
           if (lane == 0) atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
           page0 = min(max(page0, 0), p.num_pages - 1);
           page1 = min(max(page1, 0), p.num_pages - 1);
         }
-        const int in0 = key % p.page_size;
-        const int in1 = p.page_size > 16 ? in0 + 16 : 0;
-        const int64_t row[2] = {((int64_t)page0 * p.Hk + at.hk) * p.page_size + in0,
-                                ((int64_t)page1 * p.Hk + at.hk) * p.page_size + in1};
-        constexpr int RPI = 512 / ROW;  // rows of one copy instruction of a warp
-        const int r = lane / (ROW / 16), v = lane % (ROW / 16);
-        const uint32_t dst = codes + at_mx4<D>(r, v);
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-          for (int i = 0; i < 16 / RPI; ++i) {
-            const bool there = half * 16 + i * RPI + r < rows;
-            const int64_t from = there ? row[half] * ROW + i * 512 + lane * 16 : 0;
-            const uint32_t to = dst + (half * 16 + i * RPI) * ROW;
-            cp16(to, pg.k + from, there);
-            cp16(to + kKeys * ROW, pg.v + from, there);
-          }
-        // scales: 16-byte vectors of 16 / NB rows
-        constexpr int SV = kKeys * NB / 16;  // vectors of the unit, of K or of V
-        if (lane < 2 * SV) {
-          const int x = lane % SV, first = x * (16 / NB);
-          const bool there = first < rows;
-          const int64_t from = there ? (first < 16 ? row[0] + first : row[1] + first - 16) * NB : 0;
-          cp16(scales + lane * 16, (lane < SV ? pg.k_scale : pg.v_scale) + from, there);
-        }
+        // row numbers in the pool fit 31 bits
+        const uint32_t in0 = key & ((1u << p.page_shift) - 1);
+        const uint32_t row0 = (((uint32_t)page0 * p.Hk + at.hk) << p.page_shift) + in0;
+        const uint32_t row1 =
+            p.page_shift > 4 ? row0 + 16 : ((uint32_t)page1 * p.Hk + at.hk) << p.page_shift;
+        if (rows >= kKeys)
+          copy_rows<false>(pg, stage, row0, row1, rows, lane);
+        else
+          copy_rows<true>(pg, stage, row0, row1, rows, lane);
         skip(p, depth_units, kWarps);
         look_up(p, depth_units);
       }
@@ -425,40 +505,35 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
     if (tid == 0) wk.opened[blockIdx.x] = make_int2(-1, 0);
     return;
   }
-  const uint32_t codes0 = sm103::smem_u32(&sm.codes[warp][0][0]);
-  const uint32_t scales0 = sm103::smem_u32(&sm.scales[warp][0][0][0]);
-  constexpr uint32_t kCodes = 2 * kKeys * D / 2, kScales = 2 * kKeys * D / 32;
+  const uint32_t ring = sm103::smem_u32(&sm.ring[warp][0][0]);
+  constexpr uint32_t kRing = kNS * Stage<D>::kBytes;
 
   Feed<D> feed;
-  feed.at = sh.at;
-  feed.left = sh.u1 - sh.u0;
-  feed.part = 0;
-  feed.skip(p, depth_units, warp);
-  feed.look_up(p, depth_units);
-  int in = 0, out = 0;  // stages to fill and to read next
+  feed.begin(p, depth_units, sh, warp);
+  uint32_t in = 0, out = 0;  // stages to fill and to read next
   auto fill = [&] {
-    feed.start(p, pg, depth_units, codes0 + in * kCodes, scales0 + in * kScales, lane);
-    in = in + 1 == kNS ? 0 : in + 1;
+    feed.start(p, pg, depth_units, ring + in, lane);
+    in = in + Stage<D>::kBytes == kRing ? 0 : in + Stage<D>::kBytes;
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < kNS - 1; ++i) fill();
   // the oldest entry has landed, and the stage read before it is filled again
-  auto next = [&]() -> int {
+  auto next = [&]() -> uint32_t {
     cp_wait<kNS - 2>();
     __syncwarp();
     fill();
-    const int s = out;
-    out = out + 1 == kNS ? 0 : out + 1;
+    const uint32_t s = ring + out;
+    out = out + Stage<D>::kBytes == kRing ? 0 : out + Stage<D>::kBytes;
     return s;
   };
 
   Place<kKeys> at = sh.at;
   State<D, NT> st;
-  long long left = sh.u1 - sh.u0;
+  int left = (int)(sh.u1 - sh.u0);
   int turn = 0;  // the warp that takes the unit at `at`
   bool opened = false;
   while (left > 0) {
-    const int cnt = (int)min(left, (long long)(at.n - at.off));
+    const int cnt = min(left, at.n - at.off);
     const int end = at.off + cnt;
     const bool cut_before = at.off > 0, cut_after = end < at.n;
     const __nv_bfloat16* q = p.q + ((int64_t)at.b * p.Hk + at.hk) * p.G * D;
@@ -468,10 +543,10 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
       uint32_t qb[NT][D / 16][2], pb[NT][2];
       load_q_bf16<D, NT>(qb, q, p.G, lane);
       for (; off < min(end, depth_units); off += kWarps) {
-        int s = next();
-        depth_scores<D, NT>(st, qb, codes0 + s * kCodes, p.L - off * kDepthKeys, p.scale_log2, lane, pb);
+        uint32_t s = next();
+        depth_scores<D, NT>(st, qb, s, p.L - off * kDepthKeys, p.scale_log2, lane, pb);
         s = next();
-        depth_values<D, NT>(st, pb, codes0 + s * kCodes, lane);
+        depth_values<D, NT>(st, pb, s, lane);
       }
     }
     if (off < end) {
@@ -479,26 +554,27 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
       float back[NT][2];
       load_q_f16<D, NT>(qb, back, q, p.G, p.scale_log2, lane);
       for (; off < end; off += kWarps) {
-        const int s = next();
+        const uint32_t s = next();
         const int there = at.len - (off - depth_units) * kKeys;
-        const uint32_t kb = codes0 + s * kCodes, ks = scales0 + s * kScales;
         if (there >= kKeys)
-          unit_mx4<D, NT, false>(st, qb, back, kb, kb + kCodes / 2, ks, ks + kScales / 2, there, lane);
+          unit_mx4<D, NT, false>(st, qb, back, s, there, lane);
         else
-          unit_mx4<D, NT, true>(st, qb, back, kb, kb + kCodes / 2, ks, ks + kScales / 2, there, lane);
+          unit_mx4<D, NT, true>(st, qb, back, s, there, lane);
       }
     }
-    leave<D, NT, kWarps>(p, wk, sm.merge, st, cut_before || cut_after,
+    leave<D, NT>(p, wk, sm.merge, st, cut_before || cut_after,
                          2 * blockIdx.x + (cut_before ? 0 : 1),
                          ((int64_t)at.b * p.Hk + at.hk) * p.G,
-                         [&](float* m0, float* m1, int t, int half) {
+                         [&](float* m0, float* m1, int t, int part) {
 #pragma unroll
                            for (int g = 0; g < kCols / 32; ++g) {
-                             const float(&x)[4] = st.o[t][half * 4 + 2 * g];
-                             const float(&y)[4] = st.o[t][half * 4 + 2 * g + 1];
-                             const int d = g * 32 + (lane >> 2) * 4;
-                             *reinterpret_cast<float4*>(m0 + d) = make_float4(x[0], x[2], y[0], y[2]);
-                             *reinterpret_cast<float4*>(m1 + d) = make_float4(x[1], x[3], y[1], y[3]);
+                             const float(&x)[4] = st.o[t][part * (kCols / 16) + 2 * g];
+                             const float(&y)[4] = st.o[t][part * (kCols / 16) + 2 * g + 1];
+                             const int d = g * 32 + (lane >> 2) * 2;
+                             *reinterpret_cast<float2*>(m0 + d) = make_float2(x[0], y[0]);
+                             *reinterpret_cast<float2*>(m1 + d) = make_float2(x[1], y[1]);
+                             *reinterpret_cast<float2*>(m0 + d + 16) = make_float2(x[2], y[2]);
+                             *reinterpret_cast<float2*>(m1 + d + 16) = make_float2(x[3], y[3]);
                            }
                          });
     if (cut_after && !cut_before) {

@@ -47,6 +47,9 @@ moda_status check_cache(const moda_paged_kv* c, moda::PagedKv* out, CacheRanges*
   if ((int64_t)c->max_pages * P > (1 << 30))
     return report(MODA_ERR_UNSUPPORTED, "max_pages * page_size = %lld > 2^30",
                   (long long)c->max_pages * P);
+  // a CTA's share of a decode's units is counted in 32 bits
+  if ((int64_t)c->max_pages * P > (1LL << 40) / c->Hk / (c->B > 0 ? c->B : 1))
+    return report(MODA_ERR_UNSUPPORTED, "B * Hk * max_pages * page_size exceeds 2^40 rows");
   const bool mx4 = c->format == MODA_KV_MX4;
   if (!c->k || !c->v || (c->B > 0 && !c->block_table) || (mx4 && (!c->k_scale || !c->v_scale)))
     return report(MODA_ERR_INVALID_ARG, "NULL pages, scales or block table");
