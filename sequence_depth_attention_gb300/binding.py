@@ -459,59 +459,101 @@ def moda_decode(q, k_cache, v_cache, kd_tok, vd_tok, scale: float, o=None, lse=N
     return o, lse
 
 
-def _here(*tensors):
-    """The calls launch on the current device: every tensor must live there."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+# The paged calls are made once a layer and step, often on small inputs, where
+# this module's own time counts: quick checks first and their messages only
+# after a refusal, plain integers for pointers, the stream's handle without its
+# Python object (an append of one token 21.7 -> 12.9 us, 3.7 of them the library).
+_bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _paged_cache(k_pages, v_pages, block_table, k_scales, v_scales):
+def _current_device():
+    """The current device's index; without a GPU one that no tensor is on, so
+    that the arguments' own checks speak first."""
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _here(t, dtype, dev):
+    """A contiguous tensor on the current device, where the calls launch?"""
+    try:
+        return t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+    except AttributeError:
+        return False
+
+
+def _refuse(dev, *tensors):
+    """Raises for the first of (t, name, dtype) that is not as _here wants it;
+    None is skipped."""
+    for t, name, dtype in tensors:
+        if t is not None and not _here(t, dtype, dev):
+            _need(t, name, dtype)
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales):
     """moda_paged_kv for the tensors of a cache."""
-    mx4 = k_scales is not None or v_scales is not None
-    dtype = torch.uint8 if mx4 else torch.bfloat16
-    _need(k_pages, "k_pages", dtype), _need(v_pages, "v_pages", dtype)
-    _need(block_table, "block_table", torch.int32)
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
-        raise ValueError("k_pages and v_pages must both be [num_pages,Hk,page_size,d"
-                         + ("/2]" if mx4 else "]"))
-    if block_table.dim() != 2:
+    if k_scales is None and v_scales is None:
+        if not (_here(k_pages, _bf16, dev) and _here(v_pages, _bf16, dev) and _here(block_table, _i32, dev)):
+            _refuse(dev, (k_pages, "k_pages", _bf16), (v_pages, "v_pages", _bf16),
+                    (block_table, "block_table", _i32))
+        shape = k_pages.shape
+        if len(shape) != 4 or shape != v_pages.shape:
+            raise ValueError("k_pages and v_pages must both be [num_pages,Hk,page_size,d]")
+        num_pages, Hk, page_size, d = shape
+        fmt, ks, vs = MODA_KV_BF16, None, None
+    else:
+        if k_scales is None or v_scales is None:
+            raise ValueError("k_scales and v_scales come together")
+        if not (_here(k_pages, _u8, dev) and _here(v_pages, _u8, dev) and _here(block_table, _i32, dev)
+                and _here(k_scales, _u8, dev) and _here(v_scales, _u8, dev)):
+            _refuse(dev, (k_pages, "k_pages", _u8), (v_pages, "v_pages", _u8),
+                    (block_table, "block_table", _i32), (k_scales, "k_scales", _u8),
+                    (v_scales, "v_scales", _u8))
+        shape = k_pages.shape
+        if len(shape) != 4 or shape != v_pages.shape:
+            raise ValueError("k_pages and v_pages must both be [num_pages,Hk,page_size,d/2]")
+        num_pages, Hk, page_size, d = shape
+        d *= 2
+        want = (num_pages, Hk, page_size, d // 32)
+        if k_scales.shape != want or v_scales.shape != want:
+            raise ValueError(f"k_scales and v_scales must be [num_pages,Hk,page_size,d/32] = {want}")
+        fmt, ks, vs = MODA_KV_MX4, k_scales.data_ptr(), v_scales.data_ptr()
+    table = block_table.shape
+    if len(table) != 2:
         raise ValueError("block_table must be [B,max_pages]")
-    num_pages, Hk, page_size, w = k_pages.shape
-    d = 2 * w if mx4 else w
-    if mx4:
-        for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-            _need(t, n, torch.uint8)
-            if tuple(t.shape) != (num_pages, Hk, page_size, d // 32):
-                raise ValueError(f"{n} must be [num_pages,Hk,page_size,d/32] = "
-                                 f"{(num_pages, Hk, page_size, d // 32)}")
-    B, max_pages = block_table.shape
-    return _PagedKv(MODA_KV_MX4 if mx4 else MODA_KV_BF16, num_pages, page_size, Hk, d, B, max_pages,
-                    k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr() if mx4 else None,
-                    v_scales.data_ptr() if mx4 else None, block_table.data_ptr())
+    return _PagedKv(fmt, num_pages, page_size, Hk, d, table[0], table[1], k_pages.data_ptr(),
+                    v_pages.data_ptr(), ks, vs, block_table.data_ptr()), Hk, d, table[0]
 
 
-def _need_rows(t, name, N, H, d):
-    """A bf16 CUDA tensor [N,H,d] whose tokens are dense, at any distance; returns the distance."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != N or t.shape[1] != H or t.shape[2] != d:
+def _rows_stride(dev, t, name, N, H, d):
+    """The distance of the tokens of t[N,H,d], bf16 with dense tokens."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _bf16:
+        raise TypeError(f"{name}: expected a torch.bfloat16 torch.Tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: must be a CUDA tensor on the current device cuda:{dev}")
+    if t.shape != (N, H, d):
         raise ValueError(f"{name}: expected shape {(N, H, d)}, got {tuple(t.shape)}")
-    if N and ((t.stride(2) != 1) or (H > 1 and t.stride(1) != d)):
+    s = t.stride()
+    if N and (s[2] != 1 or (s[1] != d and H > 1)):
         raise ValueError(f"{name}: the [H,d] rows of a token must be dense")
-    return t.stride(0) if N > 1 else H * d
+    return s[0] if N > 1 else H * d
 
 
-def _need_index(seq, pos):
-    _need(seq, "seq", torch.int32), _need(pos, "pos", torch.int32)
-    if seq.dim() != 1 or seq.shape != pos.shape:
+def _tokens(dev, seq, pos):
+    if not (_here(seq, _i32, dev) and _here(pos, _i32, dev)):
+        _refuse(dev, (seq, "seq", _i32), (pos, "pos", _i32))
+    shape = seq.shape
+    if len(shape) != 1 or shape != pos.shape:
         raise ValueError("seq and pos must both be [N]")
-    return seq.shape[0]
+    return shape[0]
 
 
 def moda_kv_append(q, k, v, k_pages, v_pages, block_table, seq, pos, rope=None, interleaved=False,
@@ -526,32 +568,36 @@ def moda_kv_append(q, k, v, k_pages, v_pages, block_table, seq, pos, rope=None, 
     [...,d/2] with k_scales/v_scales[...,d/32] for the 4-bit format.
     Returns (q_out[N,Hq,d], k_out[N,Hk,d]), the turned q and k in bf16 (rows
     of padding are left as they were, in new tensors undefined)."""
-    cache = _paged_cache(k_pages, v_pages, block_table, k_scales, v_scales)
-    N = _need_index(seq, pos)
-    Hk, d = cache.Hk, cache.d
-    Hq = 0 if q is None else q.shape[1]
-    qs = _need_rows(q, "q", N, Hq, d) if q is not None else 0
-    ks, vs = _need_rows(k, "k", N, Hk, d), _need_rows(v, "v", N, Hk, d)
-    rows = rot = 0
+    dev = _current_device()
+    cache, Hk, d, _ = _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales)
+    N = _tokens(dev, seq, pos)
+    Hq = qs = qp = rows = rot = rp = 0
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        qs, qp = _rows_stride(dev, q, "q", N, Hq, d), q.data_ptr()
+    ks, vs = _rows_stride(dev, k, "k", N, Hk, d), _rows_stride(dev, v, "v", N, Hk, d)
     if rope is not None:
-        _need(rope, "rope", torch.float32)
         if rope.dim() != 2:
             raise ValueError("rope must be [P,rot]")
         rows, rot = rope.shape
+        rp = rope.data_ptr()
     if q is not None and q_out is None:
-        q_out = torch.empty((N, Hq, d), dtype=torch.bfloat16, device=q.device)
+        q_out = torch.empty((N, Hq, d), dtype=_bf16, device=q.device)
     if want_k_out and k_out is None:
-        k_out = torch.empty((N, Hk, d), dtype=torch.bfloat16, device=k.device)
-    for t, n, H in ((q_out, "q_out", Hq), (k_out, "k_out", Hk)):
-        if t is not None:
-            _need(t, n)
-            if tuple(t.shape) != (N, H, d):
-                raise ValueError(f"{n}: expected shape {(N, H, d)}, got {tuple(t.shape)}")
-    _here(q, k, v, k_pages, v_pages, block_table, k_scales, v_scales, seq, pos, rope, q_out, k_out)
-    st = load().moda_kv_append(_ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(rope), rows, rot,
-                               int(bool(interleaved)), _ptr(seq), _ptr(pos), N, Hq, cache,
-                               _ptr(q_out), _ptr(k_out), _stream(stream))
-    _check(st, "moda_kv_append")
+        k_out = torch.empty((N, Hk, d), dtype=_bf16, device=k.device)
+    if not ((rope is None or _here(rope, _f32, dev)) and (q_out is None or _here(q_out, _bf16, dev))
+            and (k_out is None or _here(k_out, _bf16, dev))):
+        _refuse(dev, (rope, "rope", _f32), (q_out, "q_out", _bf16), (k_out, "k_out", _bf16))
+    if q_out is not None and q_out.shape != (N, Hq, d):
+        raise ValueError(f"q_out: expected shape {(N, Hq, d)}, got {tuple(q_out.shape)}")
+    if k_out is not None and k_out.shape != (N, Hk, d):
+        raise ValueError(f"k_out: expected shape {(N, Hk, d)}, got {tuple(k_out.shape)}")
+    st = (_lib or load()).moda_kv_append(
+        qp, k.data_ptr(), v.data_ptr(), qs, ks, vs, rp, rows, rot, 1 if interleaved else 0,
+        seq.data_ptr(), pos.data_ptr(), N, Hq, cache, q_out.data_ptr() if q_out is not None else None,
+        k_out.data_ptr() if k_out is not None else None, _raw_stream(stream, dev))
+    if st:
+        _check(st, "moda_kv_append")
     return q_out, k_out
 
 
@@ -560,20 +606,22 @@ def moda_kv_gather(k_pages, v_pages, block_table, seq, pos, k_scales=None, v_sca
     """Rows (seq[n], pos[n]) of the paged cache as dense bf16 k, v [N,Hk,d]
     (see moda_kv_append for the cache; rows with seq -1 are left as they
     were, in new tensors undefined)."""
-    cache = _paged_cache(k_pages, v_pages, block_table, k_scales, v_scales)
-    N = _need_index(seq, pos)
-    shape = (N, cache.Hk, cache.d)
+    dev = _current_device()
+    cache, Hk, d, _ = _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales)
+    N = _tokens(dev, seq, pos)
+    shape = (N, Hk, d)
     if k is None:
-        k = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
+        k = torch.empty(shape, dtype=_bf16, device=k_pages.device)
     if v is None:
-        v = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
-    for t, n in ((k, "k"), (v, "v")):
-        _need(t, n)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{n}: expected shape {shape}, got {tuple(t.shape)}")
-    _here(k_pages, v_pages, block_table, k_scales, v_scales, seq, pos, k, v)
-    st = load().moda_kv_gather(cache, _ptr(seq), _ptr(pos), N, _ptr(k), _ptr(v), _stream(stream))
-    _check(st, "moda_kv_gather")
+        v = torch.empty(shape, dtype=_bf16, device=k_pages.device)
+    if not (_here(k, _bf16, dev) and _here(v, _bf16, dev)):
+        _refuse(dev, (k, "k", _bf16), (v, "v", _bf16))
+    if k.shape != shape or v.shape != shape:
+        raise ValueError(f"k and v: expected shape {shape}, got {tuple(k.shape)}, {tuple(v.shape)}")
+    st = (_lib or load()).moda_kv_gather(cache, seq.data_ptr(), pos.data_ptr(), N, k.data_ptr(),
+                                         v.data_ptr(), _raw_stream(stream, dev))
+    if st:
+        _check(st, "moda_kv_gather")
     return k, v
 
 
@@ -588,48 +636,52 @@ def moda_decode_paged(q, k_pages, v_pages, block_table, seq_lens, scale: float, 
     q[B,Hq,d] bf16, block_table[B,max_pages] and seq_lens[B] int32, kd/vd
     [B,Hk,L,d] bf16 views with contiguous rows of d values (None when L == 0).
     Returns (o[B,Hq,d] bf16, lse[B,Hq] fp32 or None)."""
-    cache = _paged_cache(k_pages, v_pages, block_table, k_scales, v_scales)
-    B, Hk, d = cache.B, cache.Hk, cache.d
-    _need(q, "q"), _need(seq_lens, "seq_lens", torch.int32)
-    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d:
+    dev = _current_device()
+    cache, Hk, d, B = _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales)
+    if not (_here(q, _bf16, dev) and _here(seq_lens, _i32, dev)):
+        _refuse(dev, (q, "q", _bf16), (seq_lens, "seq_lens", _i32))
+    shape = q.shape
+    if len(shape) != 3 or shape[0] != B or shape[2] != d:
         raise ValueError(f"q must be [B,Hq,d] with B={B}, d={d}")
-    if tuple(seq_lens.shape) != (B,):
+    if seq_lens.shape != (B,):
         raise ValueError(f"seq_lens must be [B] with B={B}")
-    Hq = q.shape[1]
-    L, strides = 0, (0, 0, 0)
-    if (kd is None) != (vd is None):
-        raise ValueError("kd and vd come together")
-    if kd is not None:
-        if kd.dim() != 4 or kd.shape[0] != B or kd.shape[1] != Hk or kd.shape[3] != d:
-            raise ValueError(f"kd must be [B,Hk,L,d] with B={B}, Hk={Hk}, d={d}")
-        L = kd.shape[2]
-        if L == 0 or B == 0:
-            kd = vd = None
-        else:
-            for t, n in ((kd, "kd"), (vd, "vd")):
-                if not t.is_cuda or t.dtype != torch.bfloat16 or t.shape != kd.shape or t.stride(3) != 1:
-                    raise ValueError(f"{n}: expected a bf16 CUDA view [B,Hk,L,d] with contiguous rows")
-            strides = kd.stride()[:3]
-            if any(kd.shape[i] > 1 and kd.stride(i) != vd.stride(i) for i in range(3)):
-                raise ValueError("kd and vd must have the same strides")
+    Hq = shape[1]
+    L, kp, vp, strides = 0, None, None, (0, 0, 0)
+    if kd is not None or vd is not None:
+        if kd is None or vd is None:
+            raise ValueError("kd and vd come together")
+        dshape = kd.shape
+        if len(dshape) != 4 or dshape[0] != B or dshape[1] != Hk or dshape[3] != d or vd.shape != dshape:
+            raise ValueError(f"kd and vd must be [B,Hk,L,d] with B={B}, Hk={Hk}, d={d}")
+        L = dshape[2]
+        if L and B:
+            strides = kd.stride()
+            for x, n in ((kd, "kd"), (vd, "vd")):
+                if x.dtype is not _bf16 or x.get_device() != dev or strides[3] != 1:
+                    raise ValueError(f"{n}: expected a bf16 CUDA view [B,Hk,L,d] with contiguous rows "
+                                     f"on the current device cuda:{dev}")
+            if vd.stride() != strides:
+                other = vd.stride()
+                if any(dshape[i] > 1 and other[i] != strides[i] for i in range(4)):
+                    raise ValueError("kd and vd must have the same strides")
+            strides, kp, vp = strides[:3], kd.data_ptr(), vd.data_ptr()
     if o is None:
-        o = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=q.device)
-    _need(o, "o")
+        o = torch.empty(shape, dtype=_bf16, device=q.device)
     if want_lse and lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    if lse is not None:
-        _need(lse, "lse", torch.float32)
-    if tuple(o.shape) != (B, Hq, d) or (lse is not None and tuple(lse.shape) != (B, Hq)):
-        raise ValueError(f"o must be {(B, Hq, d)} and lse {(B, Hq)}")
+        lse = torch.empty((B, Hq), dtype=_f32, device=q.device)
     if workspace is None:
         need = moda_decode_paged_workspace_bytes(Hq, Hk, d)
-        workspace = torch.empty(max(4, need // 4), dtype=torch.float32, device=q.device)
-    _need(workspace, "workspace", torch.float32)
-    _here(q, k_pages, v_pages, block_table, k_scales, v_scales, seq_lens, kd, vd, o, lse, workspace)
-    st = load().moda_decode_paged(_ptr(q), cache, _ptr(seq_lens), _ptr(kd), _ptr(vd), *strides, Hq, L,
-                                  float(scale), _ptr(o), _ptr(lse), _ptr(workspace),
-                                  workspace.numel() * 4, _stream(stream))
-    _check(st, "moda_decode_paged")
+        workspace = torch.empty(max(4, need // 4), dtype=_f32, device=q.device)
+    if not (_here(o, _bf16, dev) and (lse is None or _here(lse, _f32, dev)) and _here(workspace, _f32, dev)):
+        _refuse(dev, (o, "o", _bf16), (lse, "lse", _f32), (workspace, "workspace", _f32))
+    if o.shape != shape or (lse is not None and lse.shape != (B, Hq)):
+        raise ValueError(f"o must be {(B, Hq, d)} and lse {(B, Hq)}")
+    st = (_lib or load()).moda_decode_paged(
+        q.data_ptr(), cache, seq_lens.data_ptr(), kp, vp, *strides, Hq, L, float(scale), o.data_ptr(),
+        lse.data_ptr() if lse is not None else None, workspace.data_ptr(), workspace.numel() * 4,
+        _raw_stream(stream, dev))
+    if st:
+        _check(st, "moda_decode_paged")
     return o, lse
 
 
