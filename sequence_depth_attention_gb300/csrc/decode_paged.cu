@@ -109,11 +109,10 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     }
     sm103::fence_barrier_init();
   }
-  // the joining kernel may be scheduled now; it waits for this grid to finish
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_stream();
   const Share<kKeys> sh = share_of<kKeys, kWarps>(p, depth_units, sm.share);
   if (depth_units == 0) write_empty<D>(p);
-  if (sh.u0 >= sh.u1) {
+  if (sh.n == 0) {
     if (tid == 0) wk.opened[blockIdx.x] = make_int2(-1, 0);
     return;
   }
@@ -127,9 +126,9 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
       if (x.off < depth_units) return 0;
       const int key = (x.off - depth_units) * kKeys + lane * box;
       if (lane * box >= kKeys || key >= x.len) return 0;
-      return __ldg(p.table + (int64_t)x.b * p.max_pages + (key >> p.page_shift));
+      return *(p.table + (int64_t)x.b * p.max_pages + (key >> p.page_shift));
     };
-    const int n = (int)(sh.u1 - sh.u0);
+    const int n = sh.n;
     int page = page_of(at);
     for (int k = 0; k < n; ++k) {
       const Place<kKeys> cur = at;
@@ -195,7 +194,7 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
   // arithmetic, so that they meet at the same barriers.
   const int r0 = lane >> 2;
   State<D, NT> st;
-  int k = 0, left = (int)(sh.u1 - sh.u0);
+  int k = 0, left = sh.n;
   bool opened = false;
   while (left > 0) {
     const int cnt = min(left, at.n - at.off);
@@ -256,42 +255,65 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
   }
 }
 
-// Joins the partials of the segment that split CTA blockIdx.x opened, for head
-// blockIdx.y: 8 warps take them in turn, each lane D/32 columns.
-constexpr int kJoinWarps = 8;
+// Joins the partials of one segment. A batch of fewer segments than split CTAs
+// has a CTA for each segment, which looks among the `shares` split CTAs for the
+// one that opened it; otherwise split CTA blockIdx.x's segment is meant. The 16
+// warps share the heads of the CTA (all G, or head blockIdx.y alone when there
+// are few segments, and so many partials each); a lane takes D/32 columns, a
+// warp every n-th partial.
+constexpr int kJoinWarps = 16;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-decode_paged_join(float* work, int G, __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
+decode_paged_join(float* work, int G, int shares, int by_segment, __nv_bfloat16* o, float* lse) {
   constexpr int E = D / 32;
   constexpr int U = 8;  // partials a warp loads before it adds the first
   __shared__ float sm_o[kJoinWarps][D];
   __shared__ float sm_ml[kJoinWarps][2];
+  __shared__ int sm_opener, sm_parts;
   const Work wk = work_of(work, G, D);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = blockIdx.y;
-  // launched as a programmatic dependent of the split kernel: wait until that
-  // grid has completed and what it wrote is visible
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int2 seg = wk.opened[blockIdx.x];
-  if (seg.x < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int heads = gridDim.y > 1 ? 1 : G;
+  const int each = kJoinWarps / heads;  // warps of a head
+  const int g = gridDim.y > 1 ? (int)blockIdx.y : warp % heads, sub = warp / heads;
+  if (threadIdx.x == 0) sm_opener = -1;
+  wait_for_stream();
+  __syncthreads();
+  if (by_segment) {
+    for (int i = threadIdx.x; i < shares; i += kJoinWarps * 32) {
+      const int2 x = wk.opened[i];
+      if (x.x == (int)blockIdx.x) {
+        sm_opener = i;
+        sm_parts = x.y;
+      }
+    }
+  } else if (threadIdx.x == 0) {
+    const int2 x = wk.opened[blockIdx.x];
+    sm_opener = x.x < 0 ? -1 : (int)blockIdx.x;
+    sm_parts = x.y;
+  }
+  __syncthreads();
+  const int opener = sm_opener, parts = sm_parts;
+  if (opener < 0) return;
+  const int segment = by_segment ? (int)blockIdx.x : wk.opened[opener].x;
   float M = -INFINITY, L = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int i0 = warp; i0 < seg.y; i0 += kJoinWarps * U) {
+  for (int i0 = sub; i0 < parts && sub < each; i0 += each * U) {
     float pm[U], pl[U], po[U][E];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kJoinWarps;
+      const int i = i0 + u * each;
       pm[u] = -INFINITY;
       pl[u] = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) po[u][e] = 0.f;
-      if (i < seg.y) {
-        const int64_t row = (int64_t)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * G + g;
+      if (i < parts) {
+        const int64_t row = (int64_t)(2 * (opener + i) + (i == 0 ? 1 : 0)) * G + g;
         pm[u] = wk.ml[row * 2];
         pl[u] = wk.ml[row * 2 + 1];
 #pragma unroll
-        for (int e = 0; e < E; ++e) po[u][e] = wk.o[row * D + lane * E + e];
+        for (int e = 0; e < E; ++e) po[u][e] = wk.o[row * D + e * 32 + lane];
       }
     }
     float Mn = M;
@@ -311,24 +333,22 @@ decode_paged_join(float* work, int G, __nv_bfloat16* __restrict__ o, float* __re
     }
   }
 #pragma unroll
-  for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = acc[e];
+  for (int e = 0; e < E; ++e) sm_o[warp][e * 32 + lane] = acc[e];
   if (lane == 0) {
     sm_ml[warp][0] = M;
     sm_ml[warp][1] = L;
   }
   __syncthreads();
-  if (threadIdx.x < D) {
-    const int d = threadIdx.x;
+  for (int i = threadIdx.x; i < heads * D; i += kJoinWarps * 32) {
+    const int h = i / D, d = i % D;
     float Mt = -INFINITY, Lt = 0.f, ot = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) Mt = fmaxf(Mt, sm_ml[w][0]);
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
+    for (int w = h; w < each * heads; w += heads) Mt = fmaxf(Mt, sm_ml[w][0]);
+    for (int w = h; w < each * heads; w += heads) {
       const float a = sm_ml[w][0] == -INFINITY ? 1.f : sm103::ex2_approx(sm_ml[w][0] - Mt);
       Lt = fmaf(a, sm_ml[w][1], Lt);
       ot = fmaf(a, sm_o[w][d], ot);
     }
-    const int64_t r = (int64_t)seg.x * G + g;
+    const int64_t r = (int64_t)segment * G + (gridDim.y > 1 ? (int)blockIdx.y : h);
     o[r * D + d] = __float2bfloat16_rn(ot / Lt);
     if (d == 0 && lse) lse[r] = (Mt + log2f(Lt)) * kLn2;
   }
@@ -366,29 +386,22 @@ cudaError_t launch(const DecodePagedArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   int grid = a.num_sms * kCtasPerSm;
   grid = grid < kMaxCtas ? grid : kMaxCtas;
-  decode_paged_split<D, NT><<<grid, kWarps * 32, smem, stream>>>(tk, tv, tkd, tvd, params_of(a), box);
-  e = cudaGetLastError();
+  e = launch_dependent(decode_paged_split<D, NT>, dim3(grid), kWarps * 32, smem, stream, tk, tv, tkd, tvd,
+                       params_of(a), box);
   return e != cudaSuccess ? e : launch_join(a, grid, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_join(const DecodePagedArgs& a, int grid, cudaStream_t stream) {
-  // programmatic dependent launch: the joining CTAs become resident while the
-  // split kernel runs and start as soon as it completes
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, a.G);
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e =
-      a.c.d == 128 ? cudaLaunchKernelEx(&cfg, decode_paged_join<128>, a.work, a.G, (__nv_bfloat16*)a.o, a.lse)
-                   : cudaLaunchKernelEx(&cfg, decode_paged_join<64>, a.work, a.G, (__nv_bfloat16*)a.o, a.lse);
-  return e != cudaSuccess ? e : cudaGetLastError();
+cudaError_t launch_join(const DecodePagedArgs& a, int shares, cudaStream_t stream) {
+  const int64_t segments = (int64_t)a.c.B * a.c.Hk;
+  const bool by_segment = segments <= shares;
+  // a CTA for each head while all of them fit the SMs at once
+  const bool by_head = by_segment && segments * a.G <= a.num_sms * 4;
+  return launch_dependent(a.c.d == 128 ? decode_paged_join<128> : decode_paged_join<64>,
+                          dim3(by_segment ? (unsigned)segments : shares, by_head ? a.G : 1),
+                          kJoinWarps * 32, 0, stream, a.work, a.G, shares, (int)by_segment,
+                          (__nv_bfloat16*)a.o, a.lse);
 }
 
 }  // namespace paged

@@ -60,7 +60,7 @@ inline Params params_of(const DecodePagedArgs& a) {
 
 // Sequence b's rows, within what its table can name.
 __device__ __forceinline__ int rows_of(const Params& p, int b) {
-  return min(max(__ldg(p.lens + b), 0), p.max_pages << p.page_shift);
+  return min(max(p.lens[b], 0), p.max_pages << p.page_shift);
 }
 
 // A place in the line of units: depth units first, then units of KEYS rows.
@@ -83,11 +83,19 @@ struct Place {
   }
 };
 
-// A CTA's share [u0, u1) of the `total` units, and the place it begins at.
+// a / b for what are almost always small numbers
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// A CTA's share of the `total` units, and the place it begins at: the first
+// `rem` of the `shares` CTAs that have any take base + 1 units, the others base.
 template <int KEYS>
 struct Share {
-  long long u0, u1, total;
-  int shares;  // CTAs that have any
+  long long total, base;
+  int shares, rem;
+  long long u0;
+  int n;  // units of this CTA
   Place<KEYS> at;
 };
 template <int WARPS>
@@ -100,12 +108,19 @@ __device__ __forceinline__ Share<KEYS> share_of(const Params& p, int depth_units
                                                 ShareSmem<WARPS>& sm) {
   constexpr int THREADS = WARPS * 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // The block table is needed as soon as the lengths are known: the grid asks
+  // for it meanwhile, a line a thread (up to 5 MB of it).
+  {
+    const int64_t line = (int64_t)blockIdx.x * THREADS + tid;
+    if (line * 32 < (int64_t)p.B * p.max_pages)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + line * 32));
+  }
   // units before each thread's run of sequences, and in all
   const int per = (p.B + THREADS - 1) / THREADS;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
-    const int raw = __ldg(p.lens + b);
+    const int raw = p.lens[b];
     if (raw < 0 || raw > p.max_pages << p.page_shift)
       atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
     mine += depth_units + (rows_of(p, b) + KEYS - 1) / KEYS;
@@ -127,24 +142,33 @@ __device__ __forceinline__ Share<KEYS> share_of(const Params& p, int depth_units
   before = (before - mine) * p.Hk;
   s.total *= p.Hk;
   s.shares = (int)min((long long)gridDim.x, s.total);
+  s.base = s.n = s.rem = 0;
+  s.u0 = 0;
+  if (s.shares > 0) {
+    s.base = divide(s.total, s.shares);
+    s.rem = (int)(s.total - s.base * s.shares);
+  }
   const int cta = blockIdx.x;
-  s.u0 = cta < s.shares ? s.total * cta / s.shares : 0;
-  s.u1 = cta < s.shares ? s.total * (cta + 1) / s.shares : 0;
-  if (s.u0 < s.u1 && s.u0 >= before && s.u0 < before + mine * p.Hk) {
+  if (cta < s.shares) {
+    s.u0 = s.base * cta + min(cta, s.rem);
+    s.n = (int)s.base + (cta < s.rem ? 1 : 0);
+  }
+  if (s.n > 0 && s.u0 >= before && s.u0 < before + mine * p.Hk) {
     long long at = before;
     for (int b = b0; b < b1; ++b) {
       const int n = depth_units + (rows_of(p, b) + KEYS - 1) / KEYS;
       if (s.u0 < at + (long long)n * p.Hk) {
+        const int hk = (int)divide(s.u0 - at, n);
         sm.start[0] = b;
-        sm.start[1] = (int)((s.u0 - at) / n);
-        sm.start[2] = (int)((s.u0 - at) % n);
+        sm.start[1] = hk;
+        sm.start[2] = (int)(s.u0 - at - (long long)hk * n);
         break;
       }
       at += (long long)n * p.Hk;
     }
   }
   __syncthreads();
-  if (s.u0 < s.u1) {
+  if (s.n > 0) {
     s.at.b = sm.start[0];
     s.at.hk = sm.start[1];
     s.at.off = sm.start[2];
@@ -156,7 +180,8 @@ __device__ __forceinline__ Share<KEYS> share_of(const Params& p, int depth_units
 // The CTA that owns unit u.
 template <int KEYS>
 __device__ __forceinline__ int owner_of(const Share<KEYS>& s, long long u) {
-  return (int)(((u + 1) * s.shares + s.total - 1) / s.total) - 1;
+  const long long wide = (s.base + 1) * s.rem;  // units of the CTAs with base + 1
+  return u < wide ? (int)divide(u, s.base + 1) : s.rem + (int)divide(u - wide, s.base);
 }
 
 // o = 0 and lse = -infinity for the sequences with nothing to attend to.
@@ -249,8 +274,8 @@ __device__ __forceinline__ void load_q_bf16(uint32_t (&qb)[NT][D / 16][2], const
     const uint32_t* row = reinterpret_cast<const uint32_t*>(q + (int64_t)h * D) + (lane & 3);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-      qb[t][ks][0] = h < G ? __ldg(row + ks * 8) : 0u;
-      qb[t][ks][1] = h < G ? __ldg(row + ks * 8 + 4) : 0u;
+      qb[t][ks][0] = h < G ? row[ks * 8] : 0u;
+      qb[t][ks][1] = h < G ? row[ks * 8 + 4] : 0u;
     }
   }
 }
@@ -332,7 +357,33 @@ __device__ __forceinline__ void leave(const Params& p, const Work& wk, MergeSmem
   }
 }
 
-cudaError_t launch_join(const DecodePagedArgs& a, int grid, cudaStream_t stream);
+// Every kernel of the paged cache starts as a programmatic dependent: its
+// launch overlaps the end of the kernel before it in the stream, and it waits
+// here, before it touches global memory, until that one has completed. (So
+// what earlier kernels wrote changes while it is resident: it reads by plain
+// loads, never through the non-coherent path.)
+__device__ __forceinline__ void wait_for_stream() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                             cudaStream_t stream, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_join(const DecodePagedArgs& a, int shares, cudaStream_t stream);
 cudaError_t launch_mx4(const DecodePagedArgs& a, cudaStream_t stream);
 
 }  // namespace paged

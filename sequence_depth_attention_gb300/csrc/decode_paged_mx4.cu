@@ -152,7 +152,7 @@ __device__ __forceinline__ void load_q_f16(uint32_t (&qb)[NT][D / 32][4], float 
 #pragma unroll
     for (int g = 0; g < D / 32; ++g) {
       raw[g] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < G) raw[g] = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)h * D + g * 32) + c);
+      if (h < G) raw[g] = *(reinterpret_cast<const uint4*>(q + (int64_t)h * D + g * 32) + c);
       const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) big = max(big, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
@@ -388,13 +388,13 @@ struct Feed {
     page0 = page1 = 0;
     if (left <= 0 || at.off < depth_units) return;
     const int key = (at.off - depth_units) * kKeys;
-    page0 = __ldg(pages + (key >> p.page_shift));
-    page1 = p.page_shift > 4 ? page0 : key + 16 < at.len ? __ldg(pages + (key >> 4) + 1) : 0;
+    page0 = pages[key >> p.page_shift];
+    page1 = p.page_shift > 4 ? page0 : key + 16 < at.len ? pages[(key >> 4) + 1] : 0;
   }
   __device__ __forceinline__ void begin(const Params& p, int depth_units, const Share<kKeys>& sh,
                                         int first) {
     at = sh.at;
-    left = (int)(sh.u1 - sh.u0);
+    left = sh.n;
     part = 0;
     pages = p.table + (int64_t)at.b * p.max_pages;
     skip(p, depth_units, first);
@@ -497,11 +497,10 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
   const int depth_units = (p.L + kDepthKeys - 1) / kDepthKeys;
   const Work wk = work_of(p.work, p.G, D);
 
-  // the joining kernel may be scheduled now; it waits for this grid to finish
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_stream();
   const Share<kKeys> sh = share_of<kKeys, kWarps>(p, depth_units, sm.share);
   if (depth_units == 0) write_empty<D>(p);
-  if (sh.u0 >= sh.u1) {
+  if (sh.n == 0) {
     if (tid == 0) wk.opened[blockIdx.x] = make_int2(-1, 0);
     return;
   }
@@ -529,7 +528,7 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
 
   Place<kKeys> at = sh.at;
   State<D, NT> st;
-  int left = (int)(sh.u1 - sh.u0);
+  int left = sh.n;
   int turn = 0;  // the warp that takes the unit at `at`
   bool opened = false;
   while (left > 0) {
@@ -580,7 +579,7 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
     if (cut_after && !cut_before) {
       opened = true;
       if (tid == 0) {
-        const long long last = sh.u1 - left + (at.n - at.off) - 1;  // of the segment
+        const long long last = sh.u0 + sh.n - left + (at.n - at.off) - 1;  // of the segment
         wk.opened[blockIdx.x] =
             make_int2(at.b * p.Hk + at.hk, owner_of(sh, last) - (int)blockIdx.x + 1);
       }
@@ -605,8 +604,8 @@ cudaError_t launch(const DecodePagedArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   int grid = a.num_sms * kCtasPerSm<NT>;
   grid = grid < kMaxCtas ? grid : kMaxCtas;
-  decode_paged_mx4_split<D, NT><<<grid, kWarps * 32, sizeof(Smem<D>), stream>>>(params_of(a), pg);
-  e = cudaGetLastError();
+  e = launch_dependent(decode_paged_mx4_split<D, NT>, dim3(grid), kWarps * 32, sizeof(Smem<D>), stream,
+                       params_of(a), pg);
   return e != cudaSuccess ? e : launch_join(a, grid, stream);
 }
 

@@ -13,7 +13,7 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
-#include "moda_internal.h"
+#include "decode_paged.cuh"
 
 namespace moda {
 namespace {
@@ -28,7 +28,7 @@ __device__ __forceinline__ int64_t page_row(const PagedKv& c, int s, int p, int 
   if (s == -1) return -1;
   int page = -1;
   if (s >= 0 && s < c.B && p >= 0 && p < pos_limit) {
-    page = __ldg(c.table + (int64_t)s * c.max_pages + p / c.page_size);
+    page = *(c.table + (int64_t)s * c.max_pages + p / c.page_size);
     if (page >= 0 && page < c.num_pages)
       return (int64_t)page * c.Hk * c.page_size + p % c.page_size;
   }
@@ -136,6 +136,7 @@ kv_append_kernel(const KvAppendArgs a, const AppendGrid g) {
   const int lane = threadIdx.x & 31;
   const int j = lane % VPR, sub = lane / VPR;
   const int64_t item = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  paged::wait_for_stream();
   if (item >= g.items) return;
   const int per_group = g.q_chunks + 2 * g.kv_chunks;
   const int64_t group = item / per_group;
@@ -148,7 +149,7 @@ kv_append_kernel(const KvAppendArgs a, const AppendGrid g) {
 
   const int64_t n = group * TPW + sub;
   const bool in = n < a.N;
-  const int s = in ? __ldg(a.seq + n) : -1, p = in ? __ldg(a.pos + n) : 0;
+  const int s = in ? a.seq[n] : -1, p = in ? a.pos[n] : 0;
   int limit = a.c.max_pages * a.c.page_size;
   if (a.rot > 0) limit = min(limit, a.rope_rows);
   const int64_t row0 = page_row(a.c, s, p, limit);
@@ -164,8 +165,8 @@ kv_append_kernel(const KvAppendArgs a, const AppendGrid g) {
   if (turned && on) {
     const float* t = a.rope + (int64_t)p * a.rot;
     if (inter) {
-      const float4 c0 = __ldg(reinterpret_cast<const float4*>(t + j * 4));
-      const float4 s0 = __ldg(reinterpret_cast<const float4*>(t + a.rot / 2 + j * 4));
+      const float4 c0 = *(reinterpret_cast<const float4*>(t + j * 4));
+      const float4 s0 = *(reinterpret_cast<const float4*>(t + a.rot / 2 + j * 4));
       const float cc[4] = {c0.x, c0.y, c0.z, c0.w}, ss[4] = {s0.x, s0.y, s0.z, s0.w};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -177,8 +178,8 @@ kv_append_kernel(const KvAppendArgs a, const AppendGrid g) {
       const float* tc = t + (low ? j : j - half) * 8;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float4 c0 = __ldg(reinterpret_cast<const float4*>(tc) + i);
-        const float4 s0 = __ldg(reinterpret_cast<const float4*>(tc + a.rot / 2) + i);
+        const float4 c0 = *(reinterpret_cast<const float4*>(tc) + i);
+        const float4 s0 = *(reinterpret_cast<const float4*>(tc + a.rot / 2) + i);
         cs[4 * i] = c0.x; cs[4 * i + 1] = c0.y; cs[4 * i + 2] = c0.z; cs[4 * i + 3] = c0.w;
         sn[4 * i] = low ? -s0.x : s0.x; sn[4 * i + 1] = low ? -s0.y : s0.y;
         sn[4 * i + 2] = low ? -s0.z : s0.z; sn[4 * i + 3] = low ? -s0.w : s0.w;
@@ -206,7 +207,7 @@ kv_append_kernel(const KvAppendArgs a, const AppendGrid g) {
 #pragma unroll
     for (int u = 0; u < kInFlight; ++u) {
       raw[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (on && h + u < h1) raw[u] = __ldg(src4 + (int64_t)(h + u) * VPR);
+      if (on && h + u < h1) raw[u] = *(src4 + (int64_t)(h + u) * VPR);
     }
 #pragma unroll
     for (int u = 0; u < kInFlight; ++u) {
@@ -258,17 +259,18 @@ kv_append_kernel(const KvAppendArgs a, const AppendGrid g) {
 // One lane: 8 elements of one row of one head, of k and of v.
 template <int D, bool MX4>
 __global__ void __launch_bounds__(kThreads)
-kv_gather_kernel(const PagedKv c, const int* __restrict__ seq, const int* __restrict__ pos,
-                 int64_t vecs, uint4* __restrict__ k, uint4* __restrict__ v) {
+kv_gather_kernel(const PagedKv c, const int* seq, const int* pos,
+                 int64_t vecs, uint4* k, uint4* v) {
   constexpr int VPR = D / 8;
   const int limit = c.max_pages * c.page_size;
+  paged::wait_for_stream();
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < vecs;
        i += (int64_t)gridDim.x * kThreads) {
     const int j = (int)(i % VPR);
     const int64_t nh = i / VPR;
     const int64_t n = nh / c.Hk;
     const int h = (int)(nh - n * c.Hk);
-    const int64_t row0 = page_row(c, __ldg(seq + n), __ldg(pos + n), limit);
+    const int64_t row0 = page_row(c, seq[n], pos[n], limit);
     if (row0 < 0) continue;
     const int64_t row = row0 + (int64_t)h * c.page_size;
 #pragma unroll
@@ -276,8 +278,8 @@ kv_gather_kernel(const PagedKv c, const int* __restrict__ seq, const int* __rest
       const void* pages = kv ? c.v : c.k;
       uint4 out;
       if constexpr (MX4) {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(pages) + row * VPR + j);
-        const uint32_t b = __ldg(reinterpret_cast<const uint8_t*>(kv ? c.v_scale : c.k_scale) +
+        const uint32_t w = *(reinterpret_cast<const uint32_t*>(pages) + row * VPR + j);
+        const uint32_t b = *(reinterpret_cast<const uint8_t*>(kv ? c.v_scale : c.k_scale) +
                                  row * (VPR / 4) + (j >> 2));
         // 2^(b - 127); 255 is NaN, 0 is 2^-127
         const float sc = __uint_as_float(b == 255 ? 0x7fc00000u : b == 0 ? 0x00400000u : b << 23);
@@ -292,7 +294,7 @@ kv_gather_kernel(const PagedKv c, const int* __restrict__ seq, const int* __rest
         }
         out = pack8(x);
       } else {
-        out = __ldg(reinterpret_cast<const uint4*>(pages) + row * VPR + j);
+        out = *(reinterpret_cast<const uint4*>(pages) + row * VPR + j);
       }
       (kv ? v : k)[i] = out;
     }
@@ -315,11 +317,9 @@ cudaError_t append_d(const KvAppendArgs& a, cudaStream_t stream) {
   g.items = groups * (g.q_chunks + 2 * g.kv_chunks);
   const int64_t blocks = (g.items + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  if (a.c.format == MODA_KV_MX4)
-    kv_append_kernel<D, true><<<(unsigned)blocks, kThreads, 0, stream>>>(a, g);
-  else
-    kv_append_kernel<D, false><<<(unsigned)blocks, kThreads, 0, stream>>>(a, g);
-  return cudaGetLastError();
+  return paged::launch_dependent(
+      a.c.format == MODA_KV_MX4 ? kv_append_kernel<D, true> : kv_append_kernel<D, false>,
+      dim3((unsigned)blocks), kThreads, 0, stream, a, g);
 }
 
 template <int D>
@@ -329,13 +329,9 @@ cudaError_t gather_d(const PagedKv& c, const int* seq, const int* pos, int N, vo
   int64_t blocks = (vecs + kThreads - 1) / kThreads;
   const int64_t cap = (int64_t)num_sms * 16;
   if (blocks > cap) blocks = cap;
-  if (c.format == MODA_KV_MX4)
-    kv_gather_kernel<D, true><<<(unsigned)blocks, kThreads, 0, stream>>>(c, seq, pos, vecs,
-                                                                       (uint4*)k, (uint4*)v);
-  else
-    kv_gather_kernel<D, false><<<(unsigned)blocks, kThreads, 0, stream>>>(c, seq, pos, vecs,
-                                                                        (uint4*)k, (uint4*)v);
-  return cudaGetLastError();
+  return paged::launch_dependent(
+      c.format == MODA_KV_MX4 ? kv_gather_kernel<D, true> : kv_gather_kernel<D, false>,
+      dim3((unsigned)blocks), kThreads, 0, stream, c, seq, pos, vecs, (uint4*)k, (uint4*)v);
 }
 
 }  // namespace
