@@ -22,6 +22,7 @@ constexpr int kWarps = kCW + 1;       // and the producer
 constexpr int kKeys = 64;             // cached rows, or depth slots, of a unit
 constexpr int kCols = 64;             // columns of O merged at a time
 constexpr int kCtasPerSm = 2;
+constexpr float kSlack = 8.f;  // weights up to 2^8: the same 8 bits in bf16
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 template <int D>
@@ -61,7 +62,7 @@ __device__ __forceinline__ void tile_bf16(State<D, NT>& st, const uint32_t (&qb)
     s[t][1] = k0 ? s[t][1] * scale_log2 : -INFINITY;
     s[t][2] = k1 ? s[t][2] * scale_log2 : -INFINITY;
     s[t][3] = k1 ? s[t][3] * scale_log2 : -INFINITY;
-    st.template raise<4>(t, s[t]);
+    st.template raise<4>(t, s[t], kSlack);
     float p[4];
     st.weigh(t, s[t], p);
     // P^T (rows = keys, columns = heads) transposed into the B tile

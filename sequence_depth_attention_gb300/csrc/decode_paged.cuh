@@ -223,16 +223,17 @@ struct State {
   }
   // Raises m of tile t to cover z, N scores (for the 4-bit path plus what
   // their values carry) of head 2c at even and 2c + 1 at odd places, and brings
-  // l and o to it. Most tiles bring no new maximum: one vote tells.
+  // l and o to it. Only when one of them is more than `slack` above m, which
+  // most tiles' are not: one vote tells.
   template <int N>
-  __device__ __forceinline__ void raise(int t, const float (&z)[N]) {
+  __device__ __forceinline__ void raise(int t, const float (&z)[N], float slack) {
     float x0 = z[0], x1 = z[1];
 #pragma unroll
     for (int i = 2; i < N; i += 2) {
       x0 = fmaxf(x0, z[i]);
       x1 = fmaxf(x1, z[i + 1]);
     }
-    if (!__any_sync(0xffffffffu, x0 > m[t][0] || x1 > m[t][1])) return;
+    if (!__any_sync(0xffffffffu, x0 > m[t][0] + slack || x1 > m[t][1] + slack)) return;
     x0 = fmaxf(x0, m[t][0]);
     x1 = fmaxf(x1, m[t][1]);
 #pragma unroll

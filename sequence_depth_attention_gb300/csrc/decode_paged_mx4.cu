@@ -53,10 +53,12 @@ struct Mx4Pages {
   int64_t depth_b, depth_hk, depth_slot;  // bytes
 };
 
-// m is kept 15 below the largest score (with its values' exponent), so that
-// the largest weight is 2^15: in fp16 weights then keep their 11 bits down to
-// 2^-29 of it.
-constexpr float kHeadroom = 15.f;
+// m is kept 7 below the largest score (with its values' exponent) when it is
+// raised, and raised again only when a score is 8 above that: weights stay
+// below 2^15.01 in fp16, the largest is 2^7 at least, so that they keep their
+// 11 bits down to 2^-21 of it and lose at most 2^-32 of it below.
+constexpr float kHeadroom = 7.f;
+constexpr float kSlack = 8.f;
 
 // Byte offset of 16-byte vector `v` (block v of 32 codes) of row r, placed so
 // that none of these meet in a bank: whole rows side by side (the copies), 8
@@ -214,7 +216,7 @@ __device__ __forceinline__ void depth_scores(State<D, NT>& st, const uint32_t (&
     s[t][3] = k1 ? s[t][3] * scale_log2 : -INFINITY;
     const float z[4] = {s[t][0] - kHeadroom, s[t][1] - kHeadroom, s[t][2] - kHeadroom,
                         s[t][3] - kHeadroom};
-    st.template raise<4>(t, z);
+    st.template raise<4>(t, z, kSlack);
     float p[4];
     st.weigh(t, s[t], p);
     pb[t][0] = wmma16::movmatrix_t(wmma16::pack_bf16(p[0], p[1]));
@@ -250,35 +252,53 @@ __device__ __forceinline__ void depth_values(State<D, NT>& st, const uint32_t (&
   }
 }
 
+// A lane's places in a stage, the same for every unit.
+template <int D>
+struct Lane {
+  static constexpr int NB = D / 32;
+  uint32_t k[2][NB];    // codes of block g of its keys in a tile's rows r0 and r0 + 8
+  uint32_t v[NB / 2];   // row of V's transposing load of blocks 2g and 2g + 1
+  uint32_t scale;       // of its first key
+  uint32_t copy, copy8; // of its vector in 8 rows from row 0, and from row 8 (D = 128)
+  __device__ __forceinline__ explicit Lane(int lane) {
+    const int c = lane & 3, ka = key_of(lane >> 2);
+#pragma unroll
+    for (int g = 0; g < NB; ++g) {
+      k[0][g] = at_mx4<D>(ka, g) + c * 4;
+      k[1][g] = at_mx4<D>(ka + 2, g) + c * 4;
+    }
+#pragma unroll
+    for (int g = 0; g < NB; g += 2)
+      v[g / 2] = Stage<D>::kV + at_mx4<D>(lane & 15, g + (lane >> 4));
+    scale = Stage<D>::kKs + ka * NB;
+    copy = at_mx4<D>(lane / NB, lane % NB);
+    copy8 = at_mx4<D>(lane / NB + 8, lane % NB);
+  }
+};
+
 // The 32 rows of a unit (in the stage at `sb`) into the state, two tiles of 16
 // keys side by side. TAIL: only `there` of them exist.
 template <int D, int NT, bool TAIL>
 __device__ __forceinline__ void unit_mx4(State<D, NT>& st, const uint32_t (&qb)[NT][D / 32][4],
-                                         const float (&back)[NT][2], uint32_t sb, int there, int lane) {
+                                         const float (&back)[NT][2], const Lane<D>& at, uint32_t sb, int there,
+                                         int lane) {
   using S = Stage<D>;
   constexpr int NB = S::kBlocks;
-  const int r0 = lane >> 2, c = lane & 3;
   // this lane's keys: ka + 16 j + 2 i, rows r0 + 8 i of tile j
-  const int ka = key_of(r0);
+  const int ka = key_of(lane >> 2);
   auto key = [&](int n) { return ka + 16 * (n >> 1) + 2 * (n & 1); };
-  uint32_t kw[2][NB];  // block g of rows ka and ka + 2
-#pragma unroll
-  for (int g = 0; g < NB; ++g) {
-    kw[0][g] = at_mx4<D>(ka, g) + c * 4;
-    kw[1][g] = at_mx4<D>(ka + 2, g) + c * 4;
-  }
   float s[2][NT][4];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     float f[2][NB];
-    load_scales<NB>(sb + S::kKs + key(2 * j) * NB, f[0]);
-    load_scales<NB>(sb + S::kKs + key(2 * j + 1) * NB, f[1]);
+    load_scales<NB>(sb + at.scale + (16 * j) * NB, f[0]);
+    load_scales<NB>(sb + at.scale + (16 * j + 2) * NB, f[1]);
 #pragma unroll
     for (int g = 0; g < NB; ++g) {
       uint32_t a[4], b[4];  // two k-steps of 16
       const uint32_t tile = sb + j * 16 * S::kRow;
-      codes_to_f16(lds32(tile + kw[0][g]), a[0], a[2], b[0], b[2]);
-      codes_to_f16(lds32(tile + kw[1][g]), a[1], a[3], b[1], b[3]);
+      codes_to_f16(lds32(tile + at.k[0][g]), a[0], a[2], b[0], b[2]);
+      codes_to_f16(lds32(tile + at.k[1][g]), a[1], a[3], b[1], b[3]);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float x[4];
@@ -297,7 +317,7 @@ __device__ __forceinline__ void unit_mx4(State<D, NT>& st, const uint32_t (&qb)[
   uint32_t dead = 0;  // bit n: this lane's key n does not exist
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
-    load_scales<NB>(sb + S::kVs + key(n) * NB, f[n]);
+    load_scales<NB>(sb + at.scale + kKeys * NB + (16 * (n >> 1) + 2 * (n & 1)) * NB, f[n]);
     if (TAIL && key(n) >= there) {
       dead |= 1u << n;
 #pragma unroll
@@ -328,7 +348,7 @@ __device__ __forceinline__ void unit_mx4(State<D, NT>& st, const uint32_t (&qb)[
       if (TAIL && (dead >> (i >> 1) & 1u)) x = -INFINITY;
       z[i] = fmaf(x, back[t][i & 1], e[i >> 1]);
     }
-    st.template raise<8>(t, z);
+    st.template raise<8>(t, z, kSlack);
     // p = 2^(score - m); a row of no finite score so far keeps m = -infinity
     const float n0 = st.m[t][0] == -INFINITY ? 0.f : -st.m[t][0];
     const float n1 = st.m[t][1] == -INFINITY ? 0.f : -st.m[t][1];
@@ -345,7 +365,7 @@ __device__ __forceinline__ void unit_mx4(State<D, NT>& st, const uint32_t (&qb)[
 #pragma unroll
     for (int g2 = 0; g2 < NB; g2 += 2) {
       uint32_t raw[4];  // blocks g2 and g2 + 1: bytes of 4 keys, columns r0 and r0 + 8
-      ldsm_t_bytes(sb + S::kV + j * 16 * S::kRow + at_mx4<D>(lane & 15, g2 + (lane >> 4)), raw);
+      ldsm_t_bytes(sb + j * 16 * S::kRow + at.v[g2 / 2], raw);
 #pragma unroll
       for (int gi = 0; gi < 2; ++gi) {
         const int g = g2 + gi;
@@ -378,27 +398,35 @@ template <int D>
 struct Feed {
   using S = Stage<D>;
   static constexpr int ROW = S::kRow, NB = S::kBlocks;
+  static constexpr int kStep = kWarps * kKeys;  // rows from one unit of a warp to its next
   Place<kKeys> at;
   int left;  // units of the CTA's share from `at` on
   int part;  // of a depth unit
-  const int* pages;  // of the sequence
-  int page0, page1;  // pages of the unit's first and second 16 rows
+  int run;   // units of rows from `at` on, all whole, with another one of the segment after each
+  const int* pages;   // the table's entry of the unit's first 16 rows
+  uint32_t in_page;   // their place in the page: the same for all units of a segment,
+                      // since page sizes divide kStep
+  int page0, page1;   // pages of the unit's first and second 16 rows
 
-  __device__ __forceinline__ void look_up(const Params& p, int depth_units) {
+  // The unit at `at`, from nothing.
+  __device__ __forceinline__ void enter(const Params& p, int depth_units) {
+    run = 0;
     page0 = page1 = 0;
     if (left <= 0 || at.off < depth_units) return;
     const int key = (at.off - depth_units) * kKeys;
-    page0 = pages[key >> p.page_shift];
-    page1 = p.page_shift > 4 ? page0 : key + 16 < at.len ? pages[(key >> 4) + 1] : 0;
+    pages = p.table + (int64_t)at.b * p.max_pages + (key >> p.page_shift);
+    in_page = key & ((1 << p.page_shift) - 1);
+    page0 = pages[0];
+    page1 = p.page_shift > 4 ? page0 : key + 16 < at.len ? pages[1] : 0;
+    run = min((min(at.n, at.off + left) - 1 - at.off) / kWarps, (at.len - key) / kStep);
   }
   __device__ __forceinline__ void begin(const Params& p, int depth_units, const Share<kKeys>& sh,
                                         int first) {
     at = sh.at;
     left = sh.n;
     part = 0;
-    pages = p.table + (int64_t)at.b * p.max_pages;
     skip(p, depth_units, first);
-    look_up(p, depth_units);
+    enter(p, depth_units);
   }
   // n units on
   __device__ __forceinline__ void skip(const Params& p, int depth_units, int n) {
@@ -411,25 +439,31 @@ struct Feed {
       at.next_segment(p, depth_units);
     } while (off >= at.n);
     at.off = off;
-    pages = p.table + (int64_t)at.b * p.max_pages;
   }
-  // Rows row0 .. + 15 and row1 .. + 15 of the pool; TAIL: only `rows` of them
-  // are read, the others become zeros.
+  // The rows of the unit at `at`; TAIL: only `rows` of them are read, the
+  // others become zeros.
   template <bool TAIL>
-  __device__ __forceinline__ void copy_rows(const Mx4Pages& pg, uint32_t stage, uint32_t row0,
-                                            uint32_t row1, int rows, int lane) {
+  __device__ __forceinline__ void copy_rows(const Params& p, const Mx4Pages& pg, const Lane<D>& to,
+                                            uint32_t stage, int rows, int lane) {
+    if ((unsigned)page0 >= (unsigned)p.num_pages || (unsigned)page1 >= (unsigned)p.num_pages) {
+      if (lane == 0) atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
+      page0 = min(max(page0, 0), p.num_pages - 1);
+      page1 = min(max(page1, 0), p.num_pages - 1);
+    }
+    // row numbers in the pool fit 31 bits
+    const uint32_t row0 = (((uint32_t)page0 * p.Hk + at.hk) << p.page_shift) + in_page;
+    const uint32_t row1 = p.page_shift > 4 ? row0 + 16 : ((uint32_t)page1 * p.Hk + at.hk) << 4;
     constexpr int RPI = 512 / ROW;  // rows of one copy instruction of a warp
-    const int r = lane / NB, v = lane % NB;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int64_t from = (int64_t)(half ? row1 : row0) * ROW + lane * 16;
 #pragma unroll
       for (int i = 0; i < 16 / RPI; ++i) {
-        const int to = half * 16 + i * RPI + r;
-        const bool there = !TAIL || to < rows;
+        const bool there = !TAIL || half * 16 + i * RPI + lane / NB < rows;
         const int64_t src = there ? from + i * 512 : 0;
-        cp16(stage + at_mx4<D>(to, v), pg.k + src, there);
-        cp16(stage + S::kV + at_mx4<D>(to, v), pg.v + src, there);
+        const uint32_t dst = stage + half * 16 * ROW + (i ? to.copy8 : to.copy);
+        cp16(dst, pg.k + src, there);
+        cp16(dst + S::kV, pg.v + src, there);
       }
     }
     // scales: 16-byte vectors of 16 / NB rows
@@ -444,8 +478,18 @@ struct Feed {
   // Starts the next entry's copies into a stage (or nothing at the end); one
   // group of asynchronous copies in any case.
   __device__ __forceinline__ void start(const Params& p, const Mx4Pages& pg, int depth_units,
-                                        uint32_t stage, int lane) {
-    if (left > 0) {
+                                        const Lane<D>& to, uint32_t stage, int lane) {
+    if (run > 0) {
+      copy_rows<false>(p, pg, to, stage, kKeys, lane);
+      --run;
+      at.off += kWarps;
+      left -= kWarps;
+      pages += kStep >> p.page_shift;
+      page0 = pages[0];
+      // past the sequence's end there is no page to look up
+      page1 = p.page_shift > 4 ? page0
+              : (at.off - depth_units) * kKeys + 16 < at.len ? pages[1] : 0;
+    } else if (left > 0) {
       if (at.off < depth_units) {
         const int l0 = at.off * kDepthKeys;
         const uint8_t* src = (part ? pg.vd : pg.kd) + at.b * pg.depth_b + at.hk * pg.depth_hk +
@@ -457,31 +501,15 @@ struct Feed {
           const bool there = l0 + r < p.L;
           cp16(stage + at_bf16<16>(r, v * 8), there ? src + r * pg.depth_slot + v * 16 : src, there);
         }
+        part ^= 1;
         if (part == 0) {
-          part = 1;
-        } else {
-          part = 0;
           skip(p, depth_units, kWarps);
-          look_up(p, depth_units);
+          enter(p, depth_units);
         }
       } else {
-        const int key = (at.off - depth_units) * kKeys, rows = at.len - key;
-        if ((unsigned)page0 >= (unsigned)p.num_pages || (unsigned)page1 >= (unsigned)p.num_pages) {
-          if (lane == 0) atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
-          page0 = min(max(page0, 0), p.num_pages - 1);
-          page1 = min(max(page1, 0), p.num_pages - 1);
-        }
-        // row numbers in the pool fit 31 bits
-        const uint32_t in0 = key & ((1u << p.page_shift) - 1);
-        const uint32_t row0 = (((uint32_t)page0 * p.Hk + at.hk) << p.page_shift) + in0;
-        const uint32_t row1 =
-            p.page_shift > 4 ? row0 + 16 : ((uint32_t)page1 * p.Hk + at.hk) << p.page_shift;
-        if (rows >= kKeys)
-          copy_rows<false>(pg, stage, row0, row1, rows, lane);
-        else
-          copy_rows<true>(pg, stage, row0, row1, rows, lane);
+        copy_rows<true>(p, pg, to, stage, at.len - (at.off - depth_units) * kKeys, lane);
         skip(p, depth_units, kWarps);
-        look_up(p, depth_units);
+        enter(p, depth_units);
       }
     }
     cp_commit();
@@ -507,11 +535,12 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
   const uint32_t ring = sm103::smem_u32(&sm.ring[warp][0][0]);
   constexpr uint32_t kRing = kNS * Stage<D>::kBytes;
 
+  const Lane<D> to(lane);
   Feed<D> feed;
   feed.begin(p, depth_units, sh, warp);
   uint32_t in = 0, out = 0;  // stages to fill and to read next
   auto fill = [&] {
-    feed.start(p, pg, depth_units, ring + in, lane);
+    feed.start(p, pg, depth_units, to, ring + in, lane);
     in = in + Stage<D>::kBytes == kRing ? 0 : in + Stage<D>::kBytes;
   };
 #pragma unroll 1
@@ -552,13 +581,13 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
       uint32_t qb[NT][D / 32][4];
       float back[NT][2];
       load_q_f16<D, NT>(qb, back, q, p.G, p.scale_log2, lane);
-      for (; off < end; off += kWarps) {
-        const uint32_t s = next();
-        const int there = at.len - (off - depth_units) * kKeys;
-        if (there >= kKeys)
-          unit_mx4<D, NT, false>(st, qb, back, s, there, lane);
-        else
-          unit_mx4<D, NT, true>(st, qb, back, s, there, lane);
+      // whole units, then the sequence's last one if it is not
+      const int whole = min(end, depth_units + at.len / kKeys);
+      for (; off < whole; off += kWarps)
+        unit_mx4<D, NT, false>(st, qb, back, to, next(), kKeys, lane);
+      if (off < end) {
+        unit_mx4<D, NT, true>(st, qb, back, to, next(), at.len % kKeys, lane);
+        off += kWarps;
       }
     }
     leave<D, NT>(p, wk, sm.merge, st, cut_before || cut_after,

@@ -140,8 +140,8 @@ def decode_reference(cache, q, lens, kd, vd, scale):
     What rounding relative to the value does not cover is underflow. In fp32 a
     weight exp(z - max z) below 2^-126 may become 0: with the sum of weights at
     least 1, o is off by at most n 2^-126 max|v|. Over 4-bit pages a weight
-    times its block scale is held in fp16 with the largest of all at 2^14 or
-    more, so it is off by 2^-25 there, 2^-39 of the largest product of
+    times its block scale is held in fp16 with the largest of all at 2^7 or
+    more, so it is off by 2^-25 there, 2^-32 of the largest product of
     probability and block scale, times codes of at most 6."""
     B, Hq, d = q.shape
     Hk = cache.Hk
@@ -168,7 +168,7 @@ def decode_reference(cache, q, lens, kd, vd, scale):
         tol_o += n * 2.0 ** -126 * v.abs().amax(dim=(1, 2))[:, None, None]
         if cache.fmt == "mx4" and lens[b]:
             w = p[..., : lens[b]] * cache.block_scales("v", b, lens[b])[:, None]
-            tol_o += n * 6 * 2.0 ** -39 * w.amax(-1, keepdim=True)
+            tol_o += n * 6 * 2.0 ** -32 * w.amax(-1, keepdim=True)
         tol_lse = ds + n * 2.0 ** -24 + lse.abs() * 2.0 ** -22 + 2.0 ** -19
         for got, x in zip(out, (o, lse, tol_o, tol_lse)):
             got.append(x.reshape(Hq, -1) if x.dim() == 3 else x.reshape(Hq))
