@@ -395,9 +395,10 @@ cudaError_t launch(const DecodePagedArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_join(const DecodePagedArgs& a, int shares, cudaStream_t stream) {
+  // Eight partials a segment and more: a CTA for each segment and head, while
+  // those fit the SMs at once. Fewer: a CTA for each split CTA.
   const int64_t segments = (int64_t)a.c.B * a.c.Hk;
-  const bool by_segment = segments <= shares;
-  // a CTA for each head while all of them fit the SMs at once
+  const bool by_segment = segments * 8 <= shares;
   const bool by_head = by_segment && segments * a.G <= a.num_sms * 4;
   return launch_dependent(a.c.d == 128 ? decode_paged_join<128> : decode_paged_join<64>,
                           dim3(by_segment ? (unsigned)segments : shares, by_head ? a.G : 1),

@@ -81,6 +81,12 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
+// The bits of a where m has ones, of b elsewhere.
+__device__ __forceinline__ uint32_t choose_bits(uint32_t a, uint32_t b, uint32_t m) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xe4;" : "=r"(r) : "r"(a), "r"(b), "r"(m));
+  return r;
+}
 // Two 16x16 byte matrices (16 rows of 16 bytes at the addresses of lanes 0-15
 // and 16-31) transposed: lane (r0, c) gets of each matrix the bytes of rows
 // 4c .. 4c + 3 in column r0 (first register) and r0 + 8 (second).
@@ -376,8 +382,8 @@ __device__ __forceinline__ void unit_mx4(State<D, NT>& st, const uint32_t (&qb)[
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t x = raw[2 * gi + h], x4 = x * 16u, x8 = x * 256u;
-          odd_codes_to_f16((x8 & 0x0f000f00u) | (x4 & ~0x0f000f00u), a[h], a[h + 2]);
-          odd_codes_to_f16((x4 & 0x0f000f00u) | (x & ~0x0f000f00u), b[h], b[h + 2]);
+          odd_codes_to_f16(choose_bits(x8, x4, 0x0f000f00u), a[h], a[h + 2]);
+          odd_codes_to_f16(choose_bits(x4, x, 0x0f000f00u), b[h], b[h + 2]);
         }
         const float f0 = f[2 * j][g], f1 = f[2 * j + 1][g];
 #pragma unroll
