@@ -21,6 +21,8 @@ constexpr int kCW = 4;                // consumer warps
 constexpr int kWarps = kCW + 1;       // and the producer
 constexpr int kKeys = 64;             // cached rows, or depth slots, of a unit
 constexpr int kCols = 64;             // columns of O merged at a time
+template <int D>
+constexpr int kCost = D == 128 ? 1 : 2;  // entering and leaving a segment, in units
 constexpr int kCtasPerSm = 2;
 constexpr float kSlack = 8.f;  // weights up to 2^8: the same 8 bits in bf16
 constexpr uint64_t kTimeoutNs = 2000000000ull;
@@ -111,7 +113,7 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     sm103::fence_barrier_init();
   }
   wait_for_stream();
-  const Share<kKeys> sh = share_of<kKeys, kWarps>(p, depth_units, sm.share);
+  const Share<kKeys> sh = share_of<kKeys, kWarps, kCost<D>, 1>(p, depth_units, sm.share);
   if (depth_units == 0) write_empty<D>(p);
   if (sh.n == 0) {
     if (tid == 0) wk.opened[blockIdx.x] = make_int2(-1, 0);
@@ -197,6 +199,7 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
   State<D, NT> st;
   int k = 0, left = sh.n;
   bool opened = false;
+  long long seg_end = sh.end;
   while (left > 0) {
     const int cnt = min(left, at.n - at.off);
     const int end = at.off + cnt;
@@ -227,28 +230,35 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                                 lane);
       give(s);
     }
-    leave<D, NT>(p, wk, sm.merge, st, cut_before || cut_after,
-                      2 * blockIdx.x + (cut_before ? 0 : 1),
-                      ((int64_t)at.b * p.Hk + at.hk) * p.G, [&](float* m0, float* m1, int t, int part) {
+    const auto put = [&](float* m0, float* m1, int t, int part, const auto& buf) {
+      constexpr int kTiles = std::remove_reference_t<decltype(buf)>::kCols / 16;
 #pragma unroll
-                        for (int i = 0; i < kCols / 16; ++i) {
-                          const float(&x)[4] = st.o[t][part * 4 + i];
-                          m0[i * 16 + r0] = x[0];
-                          m1[i * 16 + r0] = x[1];
-                          m0[i * 16 + r0 + 8] = x[2];
-                          m1[i * 16 + r0 + 8] = x[3];
-                        }
-                      });
+      for (int i = 0; i < kTiles; ++i) {
+        const float(&x)[4] = st.o[t][part * kTiles + i];
+        m0[i * 16 + r0] = x[0];
+        m1[i * 16 + r0] = x[1];
+        m0[i * 16 + r0 + 8] = x[2];
+        m1[i * 16 + r0 + 8] = x[3];
+      }
+    };
+    const int slot = 2 * blockIdx.x + (cut_before ? 0 : 1);
+    const int64_t row0 = ((int64_t)at.b * p.Hk + at.hk) * p.G;
+    if (left == cnt)  // the last: the ring is free
+      leave<D, NT>(p, wk, *reinterpret_cast<MergeSmem<kCW, D>*>(sm.ring), st, cut_before || cut_after,
+                   slot, row0, put);
+    else
+      leave<D, NT>(p, wk, sm.merge, st, cut_before || cut_after, slot, row0, put);
     if (cut_after && !cut_before) {
       opened = true;
-      if (tid == 0) {
-        const long long last = sh.u0 + (k - cnt) + (at.n - at.off) - 1;  // of the segment
+      if (tid == 0)
         wk.opened[blockIdx.x] =
-            make_int2(at.b * p.Hk + at.hk, owner_of(sh, last) - (int)blockIdx.x + 1);
-      }
+            make_int2(at.b * p.Hk + at.hk, sh.owner_of(seg_end - 1) - (int)blockIdx.x + 1);
     }
     left -= cnt;
-    if (left > 0) at.next_segment(p, depth_units);
+    if (left > 0) {
+      at.next_segment(p, depth_units);
+      seg_end += kCost<D> + at.n;
+    }
   }
   if (tid == 0) {
     if (!opened) wk.opened[blockIdx.x] = make_int2(-1, 0);

@@ -14,6 +14,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "moda_internal.h"
 #include "sm103.cuh"
 #include "warp_mma.cuh"
@@ -88,22 +90,36 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// A CTA's share of the `total` units, and the place it begins at: the first
-// `rem` of the `shares` CTAs that have any take base + 1 units, the others base.
+// A CTA's share of the line, and the place it begins at. Entering and leaving
+// a segment costs about as much as `cost` of its units, so the line that is
+// divided has that many more in front of each segment ("points"): the first
+// `rem` of the `shares` CTAs that have any take base + 1 points, the others
+// base, and a CTA works on the units among its points.
 template <int KEYS>
 struct Share {
-  long long total, base;
+  long long total, base;  // points
   int shares, rem;
-  long long u0;
-  int n;  // units of this CTA
+  long long end;  // the point behind the segment that it begins in
+  int n;          // units of this CTA
   Place<KEYS> at;
+
+  __device__ __forceinline__ long long first_point(int cta) const {
+    return base * cta + min(cta, rem);
+  }
+  // the CTA that owns a point
+  __device__ __forceinline__ int owner_of(long long point) const {
+    const long long wide = (base + 1) * rem;  // points of the CTAs with base + 1
+    return point < wide ? (int)divide(point, base + 1) : rem + (int)divide(point - wide, base);
+  }
 };
 template <int WARPS>
 struct ShareSmem {
-  long long warp_sum[WARPS];
-  int start[3];
+  unsigned long long warp_sum[WARPS];
+  int start[4];       // sequence, KV head, point of the segment, units
+  long long units[2]; // of the line before the share's begin and before its end
 };
-template <int KEYS, int WARPS>
+// COST: see above. LEAST: points that are worth a CTA.
+template <int KEYS, int WARPS, int COST, int LEAST>
 __device__ __forceinline__ Share<KEYS> share_of(const Params& p, int depth_units,
                                                 ShareSmem<WARPS>& sm) {
   constexpr int THREADS = WARPS * 32;
@@ -115,73 +131,85 @@ __device__ __forceinline__ Share<KEYS> share_of(const Params& p, int depth_units
     if (line * 32 < (int64_t)p.B * p.max_pages)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + line * 32));
   }
-  // units before each thread's run of sequences, and in all
+  // Points of one KV head before each thread's run of sequences and in all
+  // (below 2^37), and sequences that have any (at most 2^24), side by side.
   const int per = (p.B + THREADS - 1) / THREADS;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  long long mine = 0;
+  auto units_of = [&](int b) { return depth_units + (rows_of(p, b) + KEYS - 1) / KEYS; };
+  unsigned long long mine = 0;
   for (int b = b0; b < b1; ++b) {
     const int raw = p.lens[b];
     if (raw < 0 || raw > p.max_pages << p.page_shift)
       atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
-    mine += depth_units + (rows_of(p, b) + KEYS - 1) / KEYS;
+    const int n = units_of(b);
+    if (n > 0) mine += ((unsigned long long)(n + COST) << 25) + 1;
   }
-  long long before = mine;  // inclusive scan of the warp
+  unsigned long long before = mine;  // inclusive scan of the warp
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, before, off);
+    const unsigned long long x = __shfl_up_sync(0xffffffffu, before, off);
     if (lane >= off) before += x;
   }
   if (lane == 31) sm.warp_sum[warp] = before;
+  if (tid == 0) sm.units[0] = sm.units[1] = -1;
   __syncthreads();
-  Share<KEYS> s;
-  s.total = 0;
+  unsigned long long all = 0;
+#pragma unroll
   for (int w = 0; w < WARPS; ++w) {
     if (w < warp) before += sm.warp_sum[w];
-    s.total += sm.warp_sum[w];
+    all += sm.warp_sum[w];
   }
-  before = (before - mine) * p.Hk;
-  s.total *= p.Hk;
-  s.shares = (int)min((long long)gridDim.x, s.total);
+  before -= mine;
+  Share<KEYS> s;
+  s.total = (long long)(all >> 25) * p.Hk;
+  s.shares = (int)min((long long)gridDim.x, divide(s.total + LEAST - 1, LEAST));
   s.base = s.n = s.rem = 0;
-  s.u0 = 0;
   if (s.shares > 0) {
     s.base = divide(s.total, s.shares);
     s.rem = (int)(s.total - s.base * s.shares);
   }
   const int cta = blockIdx.x;
   if (cta < s.shares) {
-    s.u0 = s.base * cta + min(cta, s.rem);
-    s.n = (int)s.base + (cta < s.rem ? 1 : 0);
-  }
-  if (s.n > 0 && s.u0 >= before && s.u0 < before + mine * p.Hk) {
-    long long at = before;
-    for (int b = b0; b < b1; ++b) {
-      const int n = depth_units + (rows_of(p, b) + KEYS - 1) / KEYS;
-      if (s.u0 < at + (long long)n * p.Hk) {
-        const int hk = (int)divide(s.u0 - at, n);
-        sm.start[0] = b;
-        sm.start[1] = hk;
-        sm.start[2] = (int)(s.u0 - at - (long long)hk * n);
-        break;
+    // where the share begins and ends, by the threads whose sequences these are
+    const long long from = (long long)(before >> 25) * p.Hk, to = from + (long long)(mine >> 25) * p.Hk;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const long long point = s.first_point(cta + e);
+      if (point < from || point >= to) continue;
+      long long at = from, segments = (long long)(before & 0x1ffffff) * p.Hk;
+      for (int b = b0; b < b1; ++b) {
+        const int n = units_of(b);
+        if (n == 0) continue;
+        const int len = n + COST;
+        if (point < at + (long long)len * p.Hk) {
+          const int hk = (int)divide(point - at, len);
+          const int off = (int)(point - at - (long long)hk * len);
+          sm.units[e] = point - (segments + hk) * COST - min(off, COST);
+          if (e == 0) {
+            sm.start[0] = b;
+            sm.start[1] = hk;
+            sm.start[2] = off;
+            sm.start[3] = n;
+          }
+          break;
+        }
+        at += (long long)len * p.Hk;
+        segments += p.Hk;
       }
-      at += (long long)n * p.Hk;
     }
   }
   __syncthreads();
-  if (s.n > 0) {
+  if (cta < s.shares) {
+    const long long all_units = s.total - (long long)(all & 0x1ffffff) * p.Hk * COST;
+    s.n = (int)((sm.units[1] < 0 ? all_units : sm.units[1]) - sm.units[0]);
     s.at.b = sm.start[0];
     s.at.hk = sm.start[1];
-    s.at.off = sm.start[2];
-    s.at.enter(p, depth_units);
+    s.at.off = max(0, sm.start[2] - COST);
+    s.at.n = sm.start[3];
+    s.at.len = rows_of(p, s.at.b);
+    s.end = s.first_point(cta) - sm.start[2] + COST + s.at.n;
   }
   return s;
-}
-
-// The CTA that owns unit u.
-template <int KEYS>
-__device__ __forceinline__ int owner_of(const Share<KEYS>& s, long long u) {
-  const long long wide = (s.base + 1) * s.rem;  // units of the CTAs with base + 1
-  return u < wide ? (int)divide(u, s.base + 1) : s.rem + (int)divide(u - wide, s.base);
 }
 
 // o = 0 and lse = -infinity for the sequences with nothing to attend to.
@@ -284,13 +312,14 @@ __device__ __forceinline__ void load_q_bf16(uint32_t (&qb)[NT][D / 16][2], const
 // The merge buffer: O of COLS columns of 8 heads for each warp, and (m, l).
 template <int WARPS, int COLS>
 struct MergeSmem {
+  static constexpr int kCols = COLS;
   float o[WARPS][8][COLS + 4];  // the lanes of a quad land in different banks
   float ml[WARPS][8][2];
 };
 
 // The state of WARPS warps (threads 0 .. 32 * WARPS - 1, which meet at named
 // barrier 1) as the segment's result, or as a partial in `slot` when the
-// segment is cut. put(m0, m1, t, part) stores the warp's columns COLS * part
+// segment is cut. put(m0, m1, t, part, sm) stores the warp's columns COLS * part
 // .. of tile t for its heads 2c and 2c + 1. row0: the segment's first row of
 // o and lse.
 template <int D, int NT, int WARPS, int COLS, class Put>
@@ -311,7 +340,7 @@ __device__ __forceinline__ void leave(const Params& p, const Work& wk, MergeSmem
 #pragma unroll
     for (int part = 0; part < D / COLS; ++part) {
       meet();  // the buffer is free
-      put(sm.o[warp][2 * c], sm.o[warp][2 * c + 1], t, part);
+      put(sm.o[warp][2 * c], sm.o[warp][2 * c + 1], t, part, sm);
       if (lane < 4) {
         sm.ml[warp][2 * c][0] = st.m[t][0];
         sm.ml[warp][2 * c][1] = st.l[t][0];

@@ -28,6 +28,8 @@ constexpr int kKeys = 32;       // cached rows of a unit
 constexpr int kDepthKeys = 16;  // depth slots of a unit; their K and V take a stage each
 constexpr int kNS = 3;          // stages of a warp
 constexpr int kCols = 32;       // columns of O merged at a time
+template <int D>
+constexpr int kCost = D == 128 ? 6 : 10;  // entering and leaving a segment, in units
 template <int NT>
 constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
 
@@ -532,7 +534,7 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
   const Work wk = work_of(p.work, p.G, D);
 
   wait_for_stream();
-  const Share<kKeys> sh = share_of<kKeys, kWarps>(p, depth_units, sm.share);
+  const Share<kKeys> sh = share_of<kKeys, kWarps, kCost<D>, kWarps>(p, depth_units, sm.share);
   if (depth_units == 0) write_empty<D>(p);
   if (sh.n == 0) {
     if (tid == 0) wk.opened[blockIdx.x] = make_int2(-1, 0);
@@ -566,6 +568,7 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
   int left = sh.n;
   int turn = 0;  // the warp that takes the unit at `at`
   bool opened = false;
+  long long seg_end = sh.end;
   while (left > 0) {
     const int cnt = min(left, at.n - at.off);
     const int end = at.off + cnt;
@@ -596,32 +599,38 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
         off += kWarps;
       }
     }
-    leave<D, NT>(p, wk, sm.merge, st, cut_before || cut_after,
-                         2 * blockIdx.x + (cut_before ? 0 : 1),
-                         ((int64_t)at.b * p.Hk + at.hk) * p.G,
-                         [&](float* m0, float* m1, int t, int part) {
+    const auto put = [&](float* m0, float* m1, int t, int part, const auto& buf) {
+      constexpr int kBlocks = std::remove_reference_t<decltype(buf)>::kCols / 32;
 #pragma unroll
-                           for (int g = 0; g < kCols / 32; ++g) {
-                             const float(&x)[4] = st.o[t][part * (kCols / 16) + 2 * g];
-                             const float(&y)[4] = st.o[t][part * (kCols / 16) + 2 * g + 1];
-                             const int d = g * 32 + (lane >> 2) * 2;
-                             *reinterpret_cast<float2*>(m0 + d) = make_float2(x[0], y[0]);
-                             *reinterpret_cast<float2*>(m1 + d) = make_float2(x[1], y[1]);
-                             *reinterpret_cast<float2*>(m0 + d + 16) = make_float2(x[2], y[2]);
-                             *reinterpret_cast<float2*>(m1 + d + 16) = make_float2(x[3], y[3]);
-                           }
-                         });
+      for (int g = 0; g < kBlocks; ++g) {
+        const float(&x)[4] = st.o[t][2 * (part * kBlocks + g)];
+        const float(&y)[4] = st.o[t][2 * (part * kBlocks + g) + 1];
+        const int d = g * 32 + (lane >> 2) * 2;
+        *reinterpret_cast<float2*>(m0 + d) = make_float2(x[0], y[0]);
+        *reinterpret_cast<float2*>(m1 + d) = make_float2(x[1], y[1]);
+        *reinterpret_cast<float2*>(m0 + d + 16) = make_float2(x[2], y[2]);
+        *reinterpret_cast<float2*>(m1 + d + 16) = make_float2(x[3], y[3]);
+      }
+    };
+    const int slot = 2 * blockIdx.x + (cut_before ? 0 : 1);
+    const int64_t row0 = ((int64_t)at.b * p.Hk + at.hk) * p.G;
+    if (left == cnt)  // the last: the rings are free
+      leave<D, NT>(p, wk, *reinterpret_cast<MergeSmem<kWarps, D>*>(sm.ring), st, cut_before || cut_after,
+                   slot, row0, put);
+    else
+      leave<D, NT>(p, wk, sm.merge, st, cut_before || cut_after, slot, row0, put);
     if (cut_after && !cut_before) {
       opened = true;
-      if (tid == 0) {
-        const long long last = sh.u0 + sh.n - left + (at.n - at.off) - 1;  // of the segment
+      if (tid == 0)
         wk.opened[blockIdx.x] =
-            make_int2(at.b * p.Hk + at.hk, owner_of(sh, last) - (int)blockIdx.x + 1);
-      }
+            make_int2(at.b * p.Hk + at.hk, sh.owner_of(seg_end - 1) - (int)blockIdx.x + 1);
     }
     left -= cnt;
     turn = (turn + cnt) & (kWarps - 1);
-    if (left > 0) at.next_segment(p, depth_units);
+    if (left > 0) {
+      at.next_segment(p, depth_units);
+      seg_end += kCost<D> + at.n;
+    }
   }
   if (tid == 0 && !opened) wk.opened[blockIdx.x] = make_int2(-1, 0);
 }
