@@ -5,12 +5,17 @@
 //         page row of (sequence, position), as bf16 or as microscaled 4-bit.
 // gather  the rows back as dense bf16.
 //
-// Both are HBM-bound. A lane owns 8 consecutive elements (16 bytes), d/8 lanes
-// a row of one head, so a warp works on 2 (d = 128) or 4 (d = 64) tokens at a
-// time, for one kind (q, k or v) and a chunk of its heads: a lane reads its
-// cosines and sines once and turns every head of the chunk with them, and the
-// pair's other half comes from a lane of the same row by shuffle.
+// Both are HBM-bound, with little arithmetic between a load and its store:
+// what counts is how many warps have their loads on the way. An append's warp
+// takes one token and a handful of its heads, 2 KB of rows, and asks for them
+// before it knows where they go.
+//   Turning: a lane owns two 16-byte vectors of a head, the two halves of 8
+//   pairs (or two vectors of 4 interleaved pairs each), so that 16 values of
+//   the table turn 16 elements and no lane needs another's; d/16 lanes a head.
+//   4-bit rows: a lane owns one 16-byte vector, four lanes a block of 32; the
+//   halves of k's pairs come by shuffle.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 #include "decode_paged.cuh"
@@ -19,18 +24,21 @@ namespace moda {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kInFlight = 4;  // rows a lane loads before it stores the first
+constexpr int kWarpsPerCta = kThreads / 32;
+constexpr int kAppendCtas = 10;  // of an SM, at least
 
 // -------------------------------------------------------------- page rows
 // The row of (s, p) inside its page pool, for KV head 0: page * Hk * page_size
-// + offset; -1 when there is none, which is latched unless s is padding.
-__device__ __forceinline__ int64_t page_row(const PagedKv& c, int s, int p, int pos_limit) {
+// + offset (below 2^31); -1 when there is none, which is latched unless s is
+// padding.
+__device__ __forceinline__ int page_row(const PagedKv& c, int s, int p, int pos_limit) {
   if (s == -1) return -1;
-  int page = -1;
   if (s >= 0 && s < c.B && p >= 0 && p < pos_limit) {
-    page = *(c.table + (int64_t)s * c.max_pages + p / c.page_size);
+    // page sizes are powers of two
+    const int shift = 31 - __clz(c.page_size);
+    const int page = c.table[(int64_t)s * c.max_pages + (p >> shift)];
     if (page >= 0 && page < c.num_pages)
-      return (int64_t)page * c.Hk * c.page_size + p % c.page_size;
+      return ((page * c.Hk) << shift) + (p & (c.page_size - 1));
   }
   atomicCAS(c.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
   return -1;
@@ -123,215 +131,282 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
 
 // ----------------------------------------------------------------- append
 struct AppendGrid {
-  int chunk;                 // heads of one work item
-  int q_chunks, kv_chunks;   // items of a token group: q_chunks, then k's and v's kv_chunks
-  int64_t items;
+  int q_parts, parts;  // of a token: q's heads, then k's and v's
+  int64_t items;       // warps
 };
 
-template <int D, bool MX4>
-__global__ void __launch_bounds__(kThreads)
-kv_append_kernel(const KvAppendArgs a, const AppendGrid g) {
-  constexpr int VPR = D / 8;      // lanes of a row
-  constexpr int TPW = 32 / VPR;   // tokens of a warp
-  const int lane = threadIdx.x & 31;
-  const int j = lane % VPR, sub = lane / VPR;
-  const int64_t item = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  paged::wait_for_stream();
-  if (item >= g.items) return;
-  const int per_group = g.q_chunks + 2 * g.kv_chunks;
-  const int64_t group = item / per_group;
-  int c = (int)(item - group * per_group);
-  // kind 0: q, 1: k, 2: v
-  const int kind = c < g.q_chunks ? 0 : c < g.q_chunks + g.kv_chunks ? 1 : 2;
-  c -= kind == 0 ? 0 : kind == 1 ? g.q_chunks : g.q_chunks + g.kv_chunks;
-  const int H = kind == 0 ? a.Hq : a.c.Hk;
-  const int h0 = c * g.chunk, h1 = min(H, h0 + g.chunk);
+__device__ __forceinline__ void load4(const float* p, float* x) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+}
 
-  const int64_t n = group * TPW + sub;
-  const bool in = n < a.N;
-  const int s = in ? a.seq[n] : -1, p = in ? a.pos[n] : 0;
-  int limit = a.c.max_pages * a.c.page_size;
-  if (a.rot > 0) limit = min(limit, a.rope_rows);
-  const int64_t row0 = page_row(a.c, s, p, limit);
-  const bool on = row0 >= 0;
-
-  // this lane's cosines and signed sines, and the lane that holds its pairs'
-  // other halves (itself when the pairs are interleaved)
-  const int half = a.rot / 16;  // vectors of half the turned part
-  const bool turned = kind != 2 && j < 2 * half;
-  const bool inter = a.interleaved;
-  float cs[8], sn[8];
-  int partner = lane;
-  if (turned && on) {
-    const float* t = a.rope + (int64_t)p * a.rot;
-    if (inter) {
-      const float4 c0 = *(reinterpret_cast<const float4*>(t + j * 4));
-      const float4 s0 = *(reinterpret_cast<const float4*>(t + a.rot / 2 + j * 4));
-      const float cc[4] = {c0.x, c0.y, c0.z, c0.w}, ss[4] = {s0.x, s0.y, s0.z, s0.w};
+// Turns a and b, the halves of 8 pairs (or 4 interleaved pairs each), by the 8
+// cosines at `table` and the sines rot/2 behind them.
+__device__ __forceinline__ void turn_pair(uint4& a, uint4& b, const float* table, int rot,
+                                          bool interleaved) {
+  float c[8], s[8], x[8], y[8];
+  load4(table, c);
+  load4(table + 4, c + 4);
+  load4(table + rot / 2, s);
+  load4(table + rot / 2 + 4, s + 4);
+  unpack8(a, x);
+  unpack8(b, y);
+  if (interleaved) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        cs[i] = cc[i / 2];
-        sn[i] = (i & 1) ? ss[i / 2] : -ss[i / 2];
-      }
-    } else {
-      const bool low = j < half;
-      const float* tc = t + (low ? j : j - half) * 8;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 c0 = *(reinterpret_cast<const float4*>(tc) + i);
-        const float4 s0 = *(reinterpret_cast<const float4*>(tc + a.rot / 2) + i);
-        cs[4 * i] = c0.x; cs[4 * i + 1] = c0.y; cs[4 * i + 2] = c0.z; cs[4 * i + 3] = c0.w;
-        sn[4 * i] = low ? -s0.x : s0.x; sn[4 * i + 1] = low ? -s0.y : s0.y;
-        sn[4 * i + 2] = low ? -s0.z : s0.z; sn[4 * i + 3] = low ? -s0.w : s0.w;
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
+      x[2 * i] = fmaf(x0, c[i], -(x1 * s[i]));
+      x[2 * i + 1] = fmaf(x1, c[i], x0 * s[i]);
+      y[2 * i] = fmaf(y0, c[i + 4], -(y1 * s[i + 4]));
+      y[2 * i + 1] = fmaf(y1, c[i + 4], y0 * s[i + 4]);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      cs[i] = 1.f;
-      sn[i] = 0.f;
+      const float x0 = x[i], y0 = y[i];
+      x[i] = fmaf(x0, c[i], -(y0 * s[i]));
+      y[i] = fmaf(y0, c[i], x0 * s[i]);
     }
   }
-  if (turned && !inter) partner = lane + (j < half ? half : -half);
+  a = pack8(x);
+  b = pack8(y);
+}
 
-  const uint16_t* src = reinterpret_cast<const uint16_t*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
-                        (in ? n : 0) * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride);
-  const uint4* src4 = reinterpret_cast<const uint4*>(src) + j;
-  uint4* dense = reinterpret_cast<uint4*>(kind == 0 ? a.q_out : kind == 1 ? a.k_out : nullptr);
-  if (dense) dense += n * H * VPR + j;
-  void* pages = kind == 1 ? a.c.k : a.c.v;
-  void* scales = kind == 1 ? a.c.k_scale : a.c.v_scale;
-
-  for (int h = h0; h < h1; h += kInFlight) {
-    uint4 raw[kInFlight];
+// One head of k and of v as 4-bit rows, and of k_out. The warp's rows are
+// d/8 lanes each; `on`: the lane's head exists.
+template <int D>
+__device__ __forceinline__ void put_mx4(const KvAppendArgs& a, const uint4& kr, const uint4& vr,
+                                        const float* table, int64_t n, int64_t row, int h, bool on,
+                                        int lane) {
+  constexpr int VPR = D / 8;
+  const int j = lane % VPR, half = a.rot / 16;
+  // cosines and signed sines, and the lane with the pairs' other halves
+  // (itself when they are interleaved)
+  const bool turned = j < 2 * half;
+  float x[8], y[8], z[8];
+  unpack8(kr, x);
+  if (a.interleaved) {
 #pragma unroll
-    for (int u = 0; u < kInFlight; ++u) {
-      raw[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (on && h + u < h1) raw[u] = *(src4 + (int64_t)(h + u) * VPR);
+    for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
+  } else {
+    const int partner = turned ? lane + (j < half ? half : -half) : lane;
+    uint4 o;
+    o.x = __shfl_sync(0xffffffffu, kr.x, partner);
+    o.y = __shfl_sync(0xffffffffu, kr.y, partner);
+    o.z = __shfl_sync(0xffffffffu, kr.z, partner);
+    o.w = __shfl_sync(0xffffffffu, kr.w, partner);
+    unpack8(o, y);
+  }
+  uint4* dense = a.k_out && on
+                     ? reinterpret_cast<uint4*>(a.k_out) + (n * a.c.Hk + h) * VPR + j : nullptr;
+  if (turned) {
+    float cs[8], sn[8];
+    if (a.interleaved) {
+      float c[4], s[4];
+      load4(table + j * 4, c);
+      load4(table + a.rot / 2 + j * 4, s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        cs[i] = c[i / 2];
+        sn[i] = (i & 1) ? s[i / 2] : -s[i / 2];
+      }
+    } else {
+      const bool low = j < half;
+      const float* t = table + (low ? j : j - half) * 8;
+      load4(t, cs);
+      load4(t + 4, cs + 4);
+      load4(t + a.rot / 2, sn);
+      load4(t + a.rot / 2 + 4, sn + 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sn[i] = low ? -sn[i] : sn[i];
     }
 #pragma unroll
-    for (int u = 0; u < kInFlight; ++u) {
-      if (h + u >= h1) break;  // the same for the whole warp
-      uint4 out = raw[u];
-      float x[8], y[8], z[8];
-      if (kind != 2) {
-        unpack8(raw[u], x);
-        if (inter) {
+    for (int i = 0; i < 8; ++i) z[i] = fmaf(x[i], cs[i], y[i] * sn[i]);
+    if (dense) *dense = pack8(z);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
-        } else {
-          uint4 o;
-          o.x = __shfl_sync(0xffffffffu, raw[u].x, partner);
-          o.y = __shfl_sync(0xffffffffu, raw[u].y, partner);
-          o.z = __shfl_sync(0xffffffffu, raw[u].z, partner);
-          o.w = __shfl_sync(0xffffffffu, raw[u].w, partner);
-          unpack8(o, y);
-        }
-        if (turned) {
+    for (int i = 0; i < 8; ++i) z[i] = turn_sticky(x[i], cs[i], y[i], sn[i]);
+  } else {
+    if (dense) *dense = kr;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = fmaf(x[i], cs[i], y[i] * sn[i]);
-          out = pack8(z);
-        }
-        if (dense && on) dense[(int64_t)(h + u) * VPR] = out;
-        if (kind == 0) continue;
-      }
-      const int64_t row = row0 + (int64_t)(h + u) * a.c.page_size;
-      if constexpr (MX4) {
-        if (kind == 2) {
-          unpack8(raw[u], z);
-        } else if (turned) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = turn_sticky(x[i], cs[i], y[i], sn[i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = x[i];
-        }
-        mx4_store(z, reinterpret_cast<uint8_t*>(pages), reinterpret_cast<uint8_t*>(scales), row, j,
-                  VPR, on);
-      } else {
-        if (on) reinterpret_cast<uint4*>(pages)[row * VPR + j] = out;
-      }
+    for (int i = 0; i < 8; ++i) z[i] = x[i];
+  }
+  mx4_store(z, reinterpret_cast<uint8_t*>(a.c.k), reinterpret_cast<uint8_t*>(a.c.k_scale), row, j, VPR, on);
+  unpack8(vr, z);
+  mx4_store(z, reinterpret_cast<uint8_t*>(a.c.v), reinterpret_cast<uint8_t*>(a.c.v_scale), row, j, VPR, on);
+}
+
+template <int D, bool MX4>
+__global__ void __launch_bounds__(kThreads, kAppendCtas)
+kv_append_kernel(const __grid_constant__ KvAppendArgs a, const __grid_constant__ AppendGrid g) {
+  constexpr int VPR = D / 8;
+  const int lane = threadIdx.x & 31;
+  const int64_t item = (int64_t)blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
+  paged::wait_for_stream();
+  if (item >= g.items) return;
+  const int64_t n = g.items >> 31 == 0 ? (uint32_t)item / (uint32_t)g.parts : item / g.parts;
+  const int part = (int)(item - n * g.parts);
+  const int s = a.seq[n], p = a.pos[n];
+  int limit = a.c.max_pages * a.c.page_size;
+  if (a.rot > 0) limit = min(limit, a.rope_rows);
+
+  if (MX4 && part >= g.q_parts) {
+    constexpr int HPI = 32 / VPR;
+    const int h = (part - g.q_parts) * HPI + lane / VPR;
+    const bool on = h < a.c.Hk;
+    uint4 kr = make_uint4(0u, 0u, 0u, 0u), vr = kr;
+    if (on) {
+      const int64_t at = (int64_t)h * D + lane % VPR * 8;
+      kr = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.k) + n * a.k_stride + at);
+      vr = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.v) + n * a.v_stride + at);
     }
+    const int row = page_row(a.c, s, p, limit);
+    if (row < 0) return;
+    put_mx4<D>(a, kr, vr, a.rope + (int64_t)p * a.rot, n, (int64_t)row + (int64_t)h * a.c.page_size, h,
+               on, lane);
+    return;
+  }
+  // this lane's two vectors of a head
+  constexpr int HPI = 64 / VPR;
+  const int slot = lane % (VPR / 2), half = a.rot / 16;
+  const bool turned = slot < half;
+  const int v0 = turned && !a.interleaved ? slot : 2 * slot;
+  const int v1 = turned && !a.interleaved ? slot + half : 2 * slot + 1;
+  const bool is_q = part < g.q_parts;
+  const int h = (is_q ? part : part - g.q_parts) * HPI + lane / (VPR / 2);
+  const bool on = h < (is_q ? a.Hq : a.c.Hk);
+  uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x, vx = x, vy = x;
+  if (on) {
+    const uint16_t* src = is_q ? reinterpret_cast<const uint16_t*>(a.q) + n * a.q_stride
+                               : reinterpret_cast<const uint16_t*>(a.k) + n * a.k_stride;
+    const uint4* u = reinterpret_cast<const uint4*>(src + (int64_t)h * D);
+    x = __ldcs(u + v0);
+    y = __ldcs(u + v1);
+    if (!MX4 && !is_q) {
+      u = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.v) + n * a.v_stride +
+                                         (int64_t)h * D);
+      vx = __ldcs(u + v0);
+      vy = __ldcs(u + v1);
+    }
+  }
+  const int row = page_row(a.c, s, p, limit);
+  if (row < 0 || !on) return;
+  if (turned) turn_pair(x, y, a.rope + (int64_t)p * a.rot + slot * 8, a.rot, a.interleaved);
+  uint16_t* out = reinterpret_cast<uint16_t*>(is_q ? a.q_out : a.k_out);
+  if (out) {
+    uint4* u = reinterpret_cast<uint4*>(out + (n * (is_q ? a.Hq : a.c.Hk) + h) * D);
+    __stcs(u + v0, x);
+    __stcs(u + v1, y);
+  }
+  if (!MX4 && !is_q) {
+    const int64_t r = ((int64_t)row + (int64_t)h * a.c.page_size) * VPR;
+    uint4* u = reinterpret_cast<uint4*>(a.c.k) + r;
+    __stcs(u + v0, x);
+    __stcs(u + v1, y);
+    u = reinterpret_cast<uint4*>(a.c.v) + r;
+    __stcs(u + v0, vx);
+    __stcs(u + v1, vy);
   }
 }
 
 // ----------------------------------------------------------------- gather
-// One lane: 8 elements of one row of one head, of k and of v.
+// A warp: `tokens` tokens, all heads; a lane one 16-byte vector of the output.
 template <int D, bool MX4>
 __global__ void __launch_bounds__(kThreads)
-kv_gather_kernel(const PagedKv c, const int* seq, const int* pos,
-                 int64_t vecs, uint4* k, uint4* v) {
+kv_gather_kernel(const __grid_constant__ PagedKv c, const int* seq, const int* pos, int N, int tokens,
+                 uint4* k, uint4* v) {
   constexpr int VPR = D / 8;
-  const int limit = c.max_pages * c.page_size;
+  constexpr int HPI = 32 / VPR;  // heads at once
+  const int lane = threadIdx.x & 31, j = lane % VPR, sub = lane / VPR;
+  const int64_t n0 = ((int64_t)blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5)) * tokens;
   paged::wait_for_stream();
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < vecs;
-       i += (int64_t)gridDim.x * kThreads) {
-    const int j = (int)(i % VPR);
-    const int64_t nh = i / VPR;
-    const int64_t n = nh / c.Hk;
-    const int h = (int)(nh - n * c.Hk);
-    const int64_t row0 = page_row(c, seq[n], pos[n], limit);
-    if (row0 < 0) continue;
-    const int64_t row = row0 + (int64_t)h * c.page_size;
+  int my_row = -1;
+  if (lane < tokens && n0 + lane < N)
+    my_row = page_row(c, seq[n0 + lane], pos[n0 + lane], c.max_pages * c.page_size);
+  // (token, heads) pairs in one line, U of them in flight
+  constexpr int U = 4;
+  const int per = (c.Hk + HPI - 1) / HPI;
+  for (int i0 = 0; i0 < tokens * per; i0 += U) {
+    uint4 x[U][2];
+    float sc[U][2];
+    int64_t to[U];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const void* pages = kv ? c.v : c.k;
-      uint4 out;
-      if constexpr (MX4) {
-        const uint32_t w = *(reinterpret_cast<const uint32_t*>(pages) + row * VPR + j);
-        const uint32_t b = *(reinterpret_cast<const uint8_t*>(kv ? c.v_scale : c.k_scale) +
-                                 row * (VPR / 4) + (j >> 2));
-        // 2^(b - 127); 255 is NaN, 0 is 2^-127
-        const float sc = __uint_as_float(b == 255 ? 0x7fc00000u : b == 0 ? 0x00400000u : b << 23);
-        float x[8];
+    for (int u = 0; u < U; ++u) {
+      const int t = (i0 + u) / per, h = (i0 + u - t * per) * HPI + sub;
+      const int row0 = __shfl_sync(0xffffffffu, my_row, t & 31);
+      to[u] = -1;
+      if (i0 + u < tokens * per && row0 >= 0 && h < c.Hk) {
+        to[u] = ((n0 + t) * c.Hk + h) * VPR + j;
+        const int64_t row = (int64_t)row0 + (int64_t)h * c.page_size;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t q = w >> (4 * e);
-          // e2m1 as the top of an fp32 pattern: 2^-126 times too small, exactly
-          // (codes 0 and 0.5 are zero and a subnormal there)
-          const float m = __uint_as_float((q & 7u) << 22) * __uint_as_float(253u << 23);
-          x[e] = ((q & 8u) ? -m : m) * sc;
+        for (int e = 0; e < 2; ++e) {
+          const void* pages = e ? c.v : c.k;
+          if constexpr (MX4) {
+            x[u][e].x = reinterpret_cast<const uint32_t*>(pages)[row * VPR + j];
+            const uint32_t b =
+                reinterpret_cast<const uint8_t*>(e ? c.v_scale : c.k_scale)[row * (VPR / 4) + (j >> 2)];
+            // 2^(b - 127); 255 is NaN, 0 is 2^-127
+            sc[u][e] = __uint_as_float(b == 255 ? 0x7fc00000u : b == 0 ? 0x00400000u : b << 23);
+          } else {
+            x[u][e] = reinterpret_cast<const uint4*>(pages)[row * VPR + j];
+          }
         }
-        out = pack8(x);
-      } else {
-        out = *(reinterpret_cast<const uint4*>(pages) + row * VPR + j);
       }
-      (kv ? v : k)[i] = out;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (to[u] < 0) continue;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint4 out = x[u][e];
+        if constexpr (MX4) {
+          uint32_t f16[4];  // code pairs, exact
+          asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+              " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+              " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+              : "=r"(f16[0]), "=r"(f16[1]), "=r"(f16[2]), "=r"(f16[3])
+              : "r"(x[u][e].x));
+          float f[8];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&f16[q]));
+            f[2 * q] = y.x * sc[u][e];
+            f[2 * q + 1] = y.y * sc[u][e];
+          }
+          out = pack8(f);
+        }
+        (e ? v : k)[to[u]] = out;
+      }
     }
   }
 }
 
 template <int D>
 cudaError_t append_d(const KvAppendArgs& a, cudaStream_t stream) {
-  constexpr int TPW = 32 / (D / 8);
-  const int64_t groups = ((int64_t)a.N + TPW - 1) / TPW;
-  // heads per item: up to 8, so that a lane's cosines and sines serve 8 heads,
-  // fewer while that leaves SMs without two warps each
+  const bool mx4 = a.c.format == MODA_KV_MX4;
+  constexpr int VPR = D / 8;
   AppendGrid g;
-  g.chunk = 8;
-  while (g.chunk > 1 &&
-         groups * ((a.Hq + 2 * a.c.Hk + g.chunk - 1) / g.chunk) < (int64_t)a.num_sms * 8)
-    g.chunk >>= 1;
-  g.q_chunks = (a.Hq + g.chunk - 1) / g.chunk;
-  g.kv_chunks = (a.c.Hk + g.chunk - 1) / g.chunk;
-  g.items = groups * (g.q_chunks + 2 * g.kv_chunks);
-  const int64_t blocks = (g.items + kThreads / 32 - 1) / (kThreads / 32);
+  g.q_parts = (a.Hq + 64 / VPR - 1) / (64 / VPR);
+  const int kv_heads = (mx4 ? 32 : 64) / VPR;
+  g.parts = g.q_parts + (a.c.Hk + kv_heads - 1) / kv_heads;
+  g.items = (int64_t)a.N * g.parts;
+  const int64_t blocks = (g.items + kWarpsPerCta - 1) / kWarpsPerCta;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return paged::launch_dependent(
-      a.c.format == MODA_KV_MX4 ? kv_append_kernel<D, true> : kv_append_kernel<D, false>,
-      dim3((unsigned)blocks), kThreads, 0, stream, a, g);
+  return paged::launch_dependent(mx4 ? kv_append_kernel<D, true> : kv_append_kernel<D, false>,
+                                 dim3((unsigned)blocks), kThreads, 0, stream, a, g);
 }
 
 template <int D>
 cudaError_t gather_d(const PagedKv& c, const int* seq, const int* pos, int N, void* k, void* v,
                      int num_sms, cudaStream_t stream) {
-  const int64_t vecs = (int64_t)N * c.Hk * (D / 8);
-  int64_t blocks = (vecs + kThreads - 1) / kThreads;
-  const int64_t cap = (int64_t)num_sms * 16;
-  if (blocks > cap) blocks = cap;
+  // as many tokens a warp as make about one wave of warps: their look-ups are
+  // made once and at once
+  int tokens = 1;
+  while (tokens < 32 && N > num_sms * 32 * (int64_t)tokens) tokens *= 2;
+  const int64_t warps = ((int64_t)N + tokens - 1) / tokens;
   return paged::launch_dependent(
       c.format == MODA_KV_MX4 ? kv_gather_kernel<D, true> : kv_gather_kernel<D, false>,
-      dim3((unsigned)blocks), kThreads, 0, stream, c, seq, pos, vecs, (uint4*)k, (uint4*)v);
+      dim3((unsigned)((warps + kWarpsPerCta - 1) / kWarpsPerCta)), kThreads, 0, stream, c, seq, pos, N,
+      tokens, (uint4*)k, (uint4*)v);
 }
 
 }  // namespace
