@@ -266,55 +266,114 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
   }
 }
 
-// Joins the partials of one segment. A batch of fewer segments than split CTAs
-// has a CTA for each segment, which looks among the `shares` split CTAs for the
-// one that opened it; otherwise split CTA blockIdx.x's segment is meant. The 16
-// warps share the heads of the CTA (all G, or head blockIdx.y alone when there
-// are few segments, and so many partials each); a lane takes D/32 columns, a
-// warp every n-th partial.
-constexpr int kJoinWarps = 16;
+// U partial states (m, l, o) added to the state (M, L, acc). An empty one is
+// (-infinity, 0, 0); one that has met only NaN scores has -infinity too, and
+// its NaN must go on.
+template <int U, int E>
+__device__ __forceinline__ void add_partials(float& M, float& L, float (&acc)[E], const float (&pm)[U],
+                                             const float (&pl)[U], const float (&po)[U][E]) {
+  float Mn = M;
+#pragma unroll
+  for (int u = 0; u < U; ++u) Mn = fmaxf(Mn, pm[u]);
+  const float a = M == -INFINITY ? 1.f : sm103::ex2_approx(M - Mn);
+  M = Mn;
+  L *= a;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] *= a;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float b = pm[u] == -INFINITY ? 1.f : sm103::ex2_approx(pm[u] - M);
+    L = fmaf(b, pl[u], L);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(b, po[u][e], acc[e]);
+  }
+}
+
+// Joining the partials, where segments have few of them: a warp for each split
+// CTA (the segment that it opened) and head, all of its partials' loads in
+// flight at once, a lane D/32 columns. Few small CTAs, because they have to be
+// brought up when the split kernel has ended.
+constexpr int kFewWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32)
-decode_paged_join(float* work, int G, int shares, int by_segment, __nv_bfloat16* o, float* lse) {
+__global__ void __launch_bounds__(kFewWarps * 32)
+decode_paged_join_few(float* work, int G, int shares, __nv_bfloat16* o, float* lse) {
+  constexpr int E = D / 32;
+  constexpr int U = 4;
+  const Work wk = work_of(work, G, D);
+  const int lane = threadIdx.x & 31;
+  const int stride = gridDim.x * kFewWarps;
+  wait_for_stream();
+  for (int item = blockIdx.x * kFewWarps + (threadIdx.x >> 5); item < shares * G; item += stride) {
+    const int opener = item / G, g = item - opener * G;
+    const int2 seg = wk.opened[opener];
+    if (seg.x < 0) continue;
+    float M = -INFINITY, L = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int i0 = 0; i0 < seg.y; i0 += U) {
+      float pm[U], pl[U], po[U][E];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u;
+        pm[u] = -INFINITY;
+        pl[u] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) po[u][e] = 0.f;
+        if (i < seg.y) {
+          const int64_t row = (int64_t)(2 * (opener + i) + (i == 0 ? 1 : 0)) * G + g;
+          pm[u] = wk.ml[row * 2];
+          pl[u] = wk.ml[row * 2 + 1];
+#pragma unroll
+          for (int e = 0; e < E; ++e) po[u][e] = wk.o[row * D + lane * E + e];
+        }
+      }
+      add_partials<U, E>(M, L, acc, pm, pl, po);
+    }
+    const int64_t r = (int64_t)seg.x * G + g;
+    const float inv = 1.f / L;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[r * D + lane * E + e] = __float2bfloat16_rn(acc[e] * inv);
+    if (lane == 0 && lse) lse[r] = (M + log2f(L)) * kLn2;
+  }
+}
+
+// And where they have many: a CTA for each segment (blockIdx.x) and head
+// (blockIdx.y), which looks among the `shares` split CTAs for the one that
+// opened the segment; its 16 warps take the partials in turn.
+constexpr int kManyWarps = 16;
+
+template <int D>
+__global__ void __launch_bounds__(kManyWarps * 32)
+decode_paged_join_many(float* work, int G, int shares, __nv_bfloat16* o, float* lse) {
   constexpr int E = D / 32;
   constexpr int U = 8;  // partials a warp loads before it adds the first
-  __shared__ float sm_o[kJoinWarps][D];
-  __shared__ float sm_ml[kJoinWarps][2];
+  __shared__ float sm_o[kManyWarps][D];
+  __shared__ float sm_ml[kManyWarps][2];
   __shared__ int sm_opener, sm_parts;
   const Work wk = work_of(work, G, D);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int heads = gridDim.y > 1 ? 1 : G;
-  const int each = kJoinWarps / heads;  // warps of a head
-  const int g = gridDim.y > 1 ? (int)blockIdx.y : warp % heads, sub = warp / heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = blockIdx.y;
   if (threadIdx.x == 0) sm_opener = -1;
-  wait_for_stream();
   __syncthreads();
-  if (by_segment) {
-    for (int i = threadIdx.x; i < shares; i += kJoinWarps * 32) {
-      const int2 x = wk.opened[i];
-      if (x.x == (int)blockIdx.x) {
-        sm_opener = i;
-        sm_parts = x.y;
-      }
+  wait_for_stream();
+  for (int i = threadIdx.x; i < shares; i += kManyWarps * 32) {
+    const int2 x = wk.opened[i];
+    if (x.x == (int)blockIdx.x) {
+      sm_opener = i;
+      sm_parts = x.y;
     }
-  } else if (threadIdx.x == 0) {
-    const int2 x = wk.opened[blockIdx.x];
-    sm_opener = x.x < 0 ? -1 : (int)blockIdx.x;
-    sm_parts = x.y;
   }
   __syncthreads();
   const int opener = sm_opener, parts = sm_parts;
   if (opener < 0) return;
-  const int segment = by_segment ? (int)blockIdx.x : wk.opened[opener].x;
   float M = -INFINITY, L = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int i0 = sub; i0 < parts && sub < each; i0 += each * U) {
+  for (int i0 = warp; i0 < parts; i0 += kManyWarps * U) {
     float pm[U], pl[U], po[U][E];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * each;
+      const int i = i0 + u * kManyWarps;
       pm[u] = -INFINITY;
       pl[u] = 0.f;
 #pragma unroll
@@ -327,21 +386,7 @@ decode_paged_join(float* work, int G, int shares, int by_segment, __nv_bfloat16*
         for (int e = 0; e < E; ++e) po[u][e] = wk.o[row * D + e * 32 + lane];
       }
     }
-    float Mn = M;
-#pragma unroll
-    for (int u = 0; u < U; ++u) Mn = fmaxf(Mn, pm[u]);
-    const float a = M == -INFINITY ? 1.f : sm103::ex2_approx(M - Mn);
-    M = Mn;
-    L *= a;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= a;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float b = pm[u] == -INFINITY ? 1.f : sm103::ex2_approx(pm[u] - M);
-      L = fmaf(b, pl[u], L);
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(b, po[u][e], acc[e]);
-    }
+    add_partials<U, E>(M, L, acc, pm, pl, po);
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) sm_o[warp][e * 32 + lane] = acc[e];
@@ -350,18 +395,24 @@ decode_paged_join(float* work, int G, int shares, int by_segment, __nv_bfloat16*
     sm_ml[warp][1] = L;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < heads * D; i += kJoinWarps * 32) {
-    const int h = i / D, d = i % D;
-    float Mt = -INFINITY, Lt = 0.f, ot = 0.f;
-    for (int w = h; w < each * heads; w += heads) Mt = fmaxf(Mt, sm_ml[w][0]);
-    for (int w = h; w < each * heads; w += heads) {
-      const float a = sm_ml[w][0] == -INFINITY ? 1.f : sm103::ex2_approx(sm_ml[w][0] - Mt);
-      Lt = fmaf(a, sm_ml[w][1], Lt);
-      ot = fmaf(a, sm_o[w][d], ot);
-    }
-    const int64_t r = (int64_t)segment * G + (gridDim.y > 1 ? (int)blockIdx.y : h);
-    o[r * D + d] = __float2bfloat16_rn(ot / Lt);
-    if (d == 0 && lse) lse[r] = (Mt + log2f(Lt)) * kLn2;
+  if (warp < E) {  // 32 columns a warp; each lane first weighs one state
+    float m = lane < kManyWarps ? sm_ml[lane][0] : -INFINITY, l = lane < kManyWarps ? sm_ml[lane][1] : 0.f;
+    float Mt = m;
+#pragma unroll
+    for (int sh = 1; sh < kManyWarps; sh <<= 1) Mt = fmaxf(Mt, __shfl_xor_sync(0xffffffffu, Mt, sh));
+    Mt = __shfl_sync(0xffffffffu, Mt, 0);
+    const float a = m == -INFINITY ? 1.f : sm103::ex2_approx(m - Mt);
+    l *= a;
+#pragma unroll
+    for (int sh = 1; sh < kManyWarps; sh <<= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
+    l = __shfl_sync(0xffffffffu, l, 0);
+    const int d = threadIdx.x;
+    float ot = 0.f;
+#pragma unroll
+    for (int w = 0; w < kManyWarps; ++w) ot = fmaf(__shfl_sync(0xffffffffu, a, w), sm_o[w][d], ot);
+    const int64_t r = (int64_t)blockIdx.x * G + g;
+    o[r * D + d] = __float2bfloat16_rn(ot / l);
+    if (d == 0 && lse) lse[r] = (Mt + log2f(l)) * kLn2;
   }
 }
 
@@ -405,15 +456,18 @@ cudaError_t launch(const DecodePagedArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_join(const DecodePagedArgs& a, int shares, cudaStream_t stream) {
-  // Eight partials a segment and more: a CTA for each segment and head, while
-  // those fit the SMs at once. Fewer: a CTA for each split CTA.
+  // Many partials: eight a segment and more, while a CTA for each segment and
+  // head fits the SMs at once.
   const int64_t segments = (int64_t)a.c.B * a.c.Hk;
-  const bool by_segment = segments * 8 <= shares;
-  const bool by_head = by_segment && segments * a.G <= a.num_sms * 4;
-  return launch_dependent(a.c.d == 128 ? decode_paged_join<128> : decode_paged_join<64>,
-                          dim3(by_segment ? (unsigned)segments : shares, by_head ? a.G : 1),
-                          kJoinWarps * 32, 0, stream, a.work, a.G, shares, (int)by_segment,
-                          (__nv_bfloat16*)a.o, a.lse);
+  __nv_bfloat16* o = (__nv_bfloat16*)a.o;
+  if (segments * 8 <= shares && segments * a.G <= a.num_sms * 4)
+    return launch_dependent(a.c.d == 128 ? decode_paged_join_many<128> : decode_paged_join_many<64>,
+                            dim3((unsigned)segments, a.G), kManyWarps * 32, 0, stream, a.work, a.G, shares,
+                            o, a.lse);
+  const int ctas = (shares * a.G + kFewWarps - 1) / kFewWarps;
+  return launch_dependent(a.c.d == 128 ? decode_paged_join_few<128> : decode_paged_join_few<64>,
+                          dim3(ctas < 4 * a.num_sms ? ctas : 4 * a.num_sms), kFewWarps * 32, 0, stream, a.work,
+                          a.G, shares, o, a.lse);
 }
 
 }  // namespace paged
