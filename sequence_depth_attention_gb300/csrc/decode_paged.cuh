@@ -182,8 +182,17 @@ __device__ __forceinline__ Share<KEYS> share_of(const Params& p, int depth_units
         if (n == 0) continue;
         const int len = n + COST;
         if (point < at + (long long)len * p.Hk) {
-          const int hk = (int)divide(point - at, len);
-          const int off = (int)(point - at - (long long)hk * len);
+          // (point - at) / len, at most 4096 or so: a float's quotient is at
+          // most one off
+          int hk = (int)((float)(point - at) / (float)len);
+          int off = (int)(point - at - (long long)hk * len);
+          if (off < 0) {
+            --hk;
+            off += len;
+          } else if (off >= len) {
+            ++hk;
+            off -= len;
+          }
           sm.units[e] = point - (segments + hk) * COST - min(off, COST);
           if (e == 0) {
             sm.start[0] = b;

@@ -25,7 +25,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarpsPerCta = kThreads / 32;
-constexpr int kAppendCtas = 10;  // of an SM, at least
+constexpr int kAppendCtasMx4 = 9;  // of an SM, at least
+constexpr int kAppendCtasBf16 = 8;
 
 // -------------------------------------------------------------- page rows
 // The row of (s, p) inside its page pool, for KV head 0: page * Hk * page_size
@@ -140,37 +141,41 @@ __device__ __forceinline__ void load4(const float* p, float* x) {
   x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
 }
 
-// Turns a and b, the halves of 8 pairs (or 4 interleaved pairs each), by the 8
-// cosines at `table` and the sines rot/2 behind them.
-__device__ __forceinline__ void turn_pair(uint4& a, uint4& b, const float* table, int rot,
-                                          bool interleaved) {
-  float c[8], s[8], x[8], y[8];
-  load4(table, c);
-  load4(table + 4, c + 4);
-  load4(table + rot / 2, s);
-  load4(table + rot / 2 + 4, s + 4);
-  unpack8(a, x);
-  unpack8(b, y);
-  if (interleaved) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
-      x[2 * i] = fmaf(x0, c[i], -(x1 * s[i]));
-      x[2 * i + 1] = fmaf(x1, c[i], x0 * s[i]);
-      y[2 * i] = fmaf(y0, c[i + 4], -(y1 * s[i + 4]));
-      y[2 * i + 1] = fmaf(y1, c[i + 4], y0 * s[i + 4]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x0 = x[i], y0 = y[i];
-      x[i] = fmaf(x0, c[i], -(y0 * s[i]));
-      y[i] = fmaf(y0, c[i], x0 * s[i]);
-    }
+// A lane's 8 cosines and 8 sines, and the turning of a and b, the halves of 8
+// pairs (or 4 interleaved pairs each).
+struct Turn {
+  float c[8], s[8];
+  __device__ __forceinline__ void load(const float* table, int rot) {
+    load4(table, c);
+    load4(table + 4, c + 4);
+    load4(table + rot / 2, s);
+    load4(table + rot / 2 + 4, s + 4);
   }
-  a = pack8(x);
-  b = pack8(y);
-}
+  __device__ __forceinline__ void apply(uint4& a, uint4& b, bool interleaved) const {
+    float x[8], y[8];
+    unpack8(a, x);
+    unpack8(b, y);
+    if (interleaved) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
+        x[2 * i] = fmaf(x0, c[i], -(x1 * s[i]));
+        x[2 * i + 1] = fmaf(x1, c[i], x0 * s[i]);
+        y[2 * i] = fmaf(y0, c[i + 4], -(y1 * s[i + 4]));
+        y[2 * i + 1] = fmaf(y1, c[i + 4], y0 * s[i + 4]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x0 = x[i], y0 = y[i];
+        x[i] = fmaf(x0, c[i], -(y0 * s[i]));
+        y[i] = fmaf(y0, c[i], x0 * s[i]);
+      }
+    }
+    a = pack8(x);
+    b = pack8(y);
+  }
+};
 
 // One head of k and of v as 4-bit rows, and of k_out. The warp's rows are
 // d/8 lanes each; `on`: the lane's head exists.
@@ -236,13 +241,14 @@ __device__ __forceinline__ void put_mx4(const KvAppendArgs& a, const uint4& kr, 
 }
 
 template <int D, bool MX4>
-__global__ void __launch_bounds__(kThreads, kAppendCtas)
+__global__ void __launch_bounds__(kThreads, MX4 ? kAppendCtasMx4 : kAppendCtasBf16)
 kv_append_kernel(const __grid_constant__ KvAppendArgs a, const __grid_constant__ AppendGrid g) {
   constexpr int VPR = D / 8;
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
   paged::wait_for_stream();
   if (item >= g.items) return;
+  // item = token * parts + part, below 2^31 almost always
   const int64_t n = g.items >> 31 == 0 ? (uint32_t)item / (uint32_t)g.parts : item / g.parts;
   const int part = (int)(item - n * g.parts);
   const int s = a.seq[n], p = a.pos[n];
@@ -265,37 +271,49 @@ kv_append_kernel(const __grid_constant__ KvAppendArgs a, const __grid_constant__
                on, lane);
     return;
   }
-  // this lane's two vectors of a head
+  // this lane's two vectors of a head; of two heads of q, or of one of k and v
   constexpr int HPI = 64 / VPR;
   const int slot = lane % (VPR / 2), half = a.rot / 16;
   const bool turned = slot < half;
   const int v0 = turned && !a.interleaved ? slot : 2 * slot;
   const int v1 = turned && !a.interleaved ? slot + half : 2 * slot + 1;
   const bool is_q = part < g.q_parts;
-  const int h = (is_q ? part : part - g.q_parts) * HPI + lane / (VPR / 2);
-  const bool on = h < (is_q ? a.Hq : a.c.Hk);
-  uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x, vx = x, vy = x;
-  if (on) {
+  const int H = is_q ? a.Hq : a.c.Hk;
+  const int h = (is_q ? part * (2 * HPI) : (part - g.q_parts) * HPI) + lane / (VPR / 2);
+  const bool on = h < H, on2 = is_q ? h + HPI < H : on;
+  uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x, x2 = x, y2 = x;
+  {
     const uint16_t* src = is_q ? reinterpret_cast<const uint16_t*>(a.q) + n * a.q_stride
                                : reinterpret_cast<const uint16_t*>(a.k) + n * a.k_stride;
-    const uint4* u = reinterpret_cast<const uint4*>(src + (int64_t)h * D);
-    x = __ldcs(u + v0);
-    y = __ldcs(u + v1);
-    if (!MX4 && !is_q) {
-      u = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.v) + n * a.v_stride +
-                                         (int64_t)h * D);
-      vx = __ldcs(u + v0);
-      vy = __ldcs(u + v1);
+    const uint16_t* src2 = is_q ? src + HPI * D : reinterpret_cast<const uint16_t*>(a.v) + n * a.v_stride;
+    const uint4* u = reinterpret_cast<const uint4*>(src + h * D);
+    const uint4* u2 = reinterpret_cast<const uint4*>(src2 + h * D);
+    if (on) {
+      x = __ldcs(u + v0);
+      y = __ldcs(u + v1);
+    }
+    if (on2) {
+      x2 = __ldcs(u2 + v0);
+      y2 = __ldcs(u2 + v1);
     }
   }
   const int row = page_row(a.c, s, p, limit);
   if (row < 0 || !on) return;
-  if (turned) turn_pair(x, y, a.rope + (int64_t)p * a.rot + slot * 8, a.rot, a.interleaved);
+  if (turned) {
+    Turn turn;
+    turn.load(a.rope + (int64_t)p * a.rot + slot * 8, a.rot);
+    turn.apply(x, y, a.interleaved);
+    if (is_q) turn.apply(x2, y2, a.interleaved);
+  }
   uint16_t* out = reinterpret_cast<uint16_t*>(is_q ? a.q_out : a.k_out);
   if (out) {
-    uint4* u = reinterpret_cast<uint4*>(out + (n * (is_q ? a.Hq : a.c.Hk) + h) * D);
+    uint4* u = reinterpret_cast<uint4*>(out + (n * H + h) * D);
     __stcs(u + v0, x);
     __stcs(u + v1, y);
+    if (is_q && on2) {
+      __stcs(u + HPI * VPR + v0, x2);
+      __stcs(u + HPI * VPR + v1, y2);
+    }
   }
   if (!MX4 && !is_q) {
     const int64_t r = ((int64_t)row + (int64_t)h * a.c.page_size) * VPR;
@@ -303,8 +321,8 @@ kv_append_kernel(const __grid_constant__ KvAppendArgs a, const __grid_constant__
     __stcs(u + v0, x);
     __stcs(u + v1, y);
     u = reinterpret_cast<uint4*>(a.c.v) + r;
-    __stcs(u + v0, vx);
-    __stcs(u + v1, vy);
+    __stcs(u + v0, x2);
+    __stcs(u + v1, y2);
   }
 }
 
@@ -385,7 +403,7 @@ cudaError_t append_d(const KvAppendArgs& a, cudaStream_t stream) {
   const bool mx4 = a.c.format == MODA_KV_MX4;
   constexpr int VPR = D / 8;
   AppendGrid g;
-  g.q_parts = (a.Hq + 64 / VPR - 1) / (64 / VPR);
+  g.q_parts = (a.Hq + 128 / VPR - 1) / (128 / VPR);
   const int kv_heads = (mx4 ? 32 : 64) / VPR;
   g.parts = g.q_parts + (a.c.Hk + kv_heads - 1) / kv_heads;
   g.items = (int64_t)a.N * g.parts;
