@@ -410,8 +410,9 @@ typedef struct {
  *   2^E with max|x| <= 7 * 2^E (-126 <= E <= 125), and x / 2^E rounded to the
  *   nearest e2m1 value, ties to the even code (magnitudes over 6 become 6: up
  *   to 7 that is no further off than the format's rounding elsewhere in that
- *   binade). K is rounded from the exact rotation, not from k_out. A block
- *   with an infinity or a NaN in it is stored as NaN.
+ *   binade). K is rounded from the exact rotation (products below 2^-102
+ *   aside), not from k_out. A block with an infinity or a NaN in it is stored
+ *   as NaN.
  *
  *   q      [N, Hq, d] bf16, consecutive tokens q_stride elements apart (a view
  *          of a fused projection's output); NULL when Hq == 0
@@ -428,7 +429,8 @@ typedef struct {
  * A token with an index outside its range is left out like padding, and
  * latched (see above). Name each (seq, pos) at most once in a call: of two
  * tokens for one row either may be found there, or parts of both. Outputs and
- * pages must not overlap the inputs or each other. N <= 2^24, Hq <= 4096.
+ * pages must not overlap the inputs or each other. N <= 2^24, Hq and Hk <= 4096,
+ * N * (Hq + 2 Hk) <= 2^31 - 1.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. N == 0 is a no-op.
  */
 MODA_API moda_status moda_kv_append(const void* q, const void* k, const void* v,
@@ -441,9 +443,10 @@ MODA_API moda_status moda_kv_append(const void* q, const void* k, const void* v,
 /*
  * moda_kv_gather -- rows of the pages as dense bf16: k[n,hk,:] and v[n,hk,:]
  * are the row of (seq[n], pos[n]). For bf16 pages the stored bits, for MX4
- * pages the values that the codes stand for, which bf16 holds exactly. A pass
- * over the next piece of a prompt gathers the rows cached before it. Rows may
- * be named any number of times, in any order.
+ * pages the values that the codes stand for, which bf16 holds exactly (from
+ * 2^128 on, which moda_kv_append never stores, infinity). A pass over the next
+ * piece of a prompt gathers the rows cached before it. Rows may be named any
+ * number of times, in any order.
  *   seq, pos  [N] int32 as in moda_kv_append; a row whose seq is -1 (or whose
  *             index is out of range, which is latched) is left as it was
  *   k, v      [N, Hk, d] bf16 outputs; must not overlap the pages or each other
@@ -478,11 +481,13 @@ MODA_API moda_status moda_kv_gather(const moda_paged_kv* cache, const int* seq, 
  *             between calls. Calls that may run at the same time need one each.
  * A page index outside [0, num_pages) makes its sequence's result unspecified
  * and is latched.
- * Arithmetic: bf16 pages as moda_decode. MX4 pages: the codes' exact values
- * against q in fp16 (scaled per head, so that its 8 bits stay), fp32
- * accumulation, block scales applied in fp32, softmax in fp32, probabilities
- * times V's block scales rounded to fp16 under a running scale. (Scale byte 0,
- * which moda_kv_append never writes, is read as 0 here.)
+ * Arithmetic: fp32 accumulation, softmax in fp32. bf16 pages: probabilities in
+ * two bf16 parts, so that o is right to its own rounding. MX4 pages: the codes'
+ * exact values against q in fp16 (scaled per head, so that its 8 bits stay),
+ * block scales applied in fp32, probabilities times V's block scales rounded to
+ * fp16 under a running scale: to 11 bits, and to 2^-32 of the largest of them
+ * where that is more. (Scale byte 0, which moda_kv_append never writes, is read
+ * as 0 here, 2^-80 is the least that V's scales count for in the running one.)
  * Supported: G = Hq/Hk from 1 to 16, B*Hq <= 2^24, 0 <= L <= 1024.
  * The result depends on how the batch is split over the SMs only by the order
  * of fp32 sums; the same call on the same device gives the same bits.

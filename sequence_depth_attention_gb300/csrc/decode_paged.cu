@@ -57,7 +57,7 @@ __device__ __forceinline__ void tile_bf16(State<D, NT>& st, const uint32_t (&qb)
     for (int t = 0; t < NT; ++t) wmma16::mma_bf16(s[t], a, qb[t][ks][0], qb[t][ks][1]);
   }
   const bool k0 = r0 < there, k1 = r0 + 8 < there;
-  uint32_t pb[NT][2];
+  uint32_t pb[NT][2], pl[NT][2];  // P^T rounded to bf16, and what that left
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     s[t][0] = k0 ? s[t][0] * scale_log2 : -INFINITY;
@@ -68,8 +68,14 @@ __device__ __forceinline__ void tile_bf16(State<D, NT>& st, const uint32_t (&qb)
     float p[4];
     st.weigh(t, s[t], p);
     // P^T (rows = keys, columns = heads) transposed into the B tile
-    pb[t][0] = wmma16::movmatrix_t(wmma16::pack_bf16(p[0], p[1]));
-    pb[t][1] = wmma16::movmatrix_t(wmma16::pack_bf16(p[2], p[3]));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t hi = wmma16::pack_bf16(p[2 * i], p[2 * i + 1]);
+      const uint32_t lo = wmma16::pack_bf16(p[2 * i] - __uint_as_float(hi << 16),
+                                            p[2 * i + 1] - __uint_as_float(hi & 0xffff0000u));
+      pb[t][i] = wmma16::movmatrix_t(hi);
+      pl[t][i] = wmma16::movmatrix_t(lo);
+    }
   }
   // rows that do not exist weigh 0, but 0 times what they hold may be NaN
   uint32_t lo = 0xffffffffu, hi = 0xffffffffu;
@@ -86,7 +92,10 @@ __device__ __forceinline__ void tile_bf16(State<D, NT>& st, const uint32_t (&qb)
       a[0] &= lo; a[1] &= lo; a[2] &= hi; a[3] &= hi;
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) wmma16::mma_bf16(st.o[t][i], a, pb[t][0], pb[t][1]);
+    for (int t = 0; t < NT; ++t) {
+      wmma16::mma_bf16(st.o[t][i], a, pb[t][0], pb[t][1]);
+      wmma16::mma_bf16(st.o[t][i], a, pl[t][0], pl[t][1]);
+    }
   }
 }
 

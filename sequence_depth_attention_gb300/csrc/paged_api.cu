@@ -100,6 +100,9 @@ moda_status moda_kv_append(const void* q, const void* k, const void* v, long lon
   if (N > kMaxTokens) return report(MODA_ERR_UNSUPPORTED, "N = %d > 2^24", N);
   if (Hq > 4096 || Hk > 4096)
     return report(MODA_ERR_UNSUPPORTED, "Hq = %d, Hk = %d (at most 4096)", Hq, Hk);
+  if ((int64_t)N * ((int64_t)Hq + 2 * Hk) > 0x7fffffffLL)
+    return report(MODA_ERR_UNSUPPORTED, "N * (Hq + 2 Hk) = %lld rows exceed 2^31 - 1",
+                  (long long)N * ((long long)Hq + 2 * Hk));
   if (rot < 0) return report(MODA_ERR_INVALID_ARG, "rot = %d < 0", rot);
   if (rot > d || rot % 16 != 0)
     return report(MODA_ERR_UNSUPPORTED, "rot = %d (a multiple of 16 up to d = %d)", rot, d);

@@ -195,3 +195,8 @@ def test_decode_reference_against_one_softmax(fmt):
             w = torch.softmax(k @ q[b, h].double() * 0.125, 0)
             assert torch.allclose(w @ v, o[b, h])
             assert abs(torch.log(torch.exp(k @ q[b, h].double() * 0.125).sum()) - lse[b, h]) < 1e-12
+
+
+def test_append_rejects_too_many_rows(lib):
+    # N * (Hq + 2 Hk) rows beyond 2^31 - 1
+    assert append(lib, N=1 << 24, Hq=256, qs=256 * 64, ks=1 << 20, vs=1 << 20, Hk=2) == UNSUPPORTED

@@ -568,3 +568,111 @@ def test_prompt_then_steps(fmt):
         want_k = torch.cat([pc.turned(xs[b][1], rope, torch.arange(total[b], device="cuda"), False)
                             for b in range(2)])
         assert torch.equal(kg.double(), pc.mx4_quantised(want_k))
+
+
+# --------------------------------------------------------- wide, many, often
+@pytest.mark.parametrize("fmt", ["bf16", "mx4"])
+@pytest.mark.parametrize("B,Hk,G,L", [(3000, 1, 2, 0), (700, 4, 16, 3), (257, 2, 5, 17)])
+def test_decode_many_sequences(fmt, B, Hk, G, L):
+    """More sequences than threads of a CTA, empty ones among them, segments
+    shorter than a unit and cut anywhere."""
+    d, page = 64, 16
+    g = torch.Generator().manual_seed(100 + B)
+    lens = torch.randint(0, 90, (B,), generator=g)
+    lens[torch.rand(B, generator=g) < 0.3] = 0
+    lens[B // 2] = 2500
+    lens = lens.tolist()
+    c = pc.Cache(fmt, lens, Hk, d, page, seed=101, device="cuda")
+    q = torch.randn(B, Hk * G, d, generator=g).bfloat16().cuda()
+    kd, vd = depth(B, Hk, L, d, 102)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = moda.moda_decode_paged(q, *c.args(), n, 0.125, kd=kd, vd=vd, **c.scales())
+    settled()
+    check_decode(c, q, lens, kd, vd, 0.125, o, lse)
+
+
+def test_decode_paged_against_moda_decode():
+    """One sequence through the dense cache's decode and through pages."""
+    d, Hk, G, L, n = 128, 4, 4, 46, 5000
+    c = pc.Cache("bf16", [n], Hk, d, 64, seed=110, device="cuda")
+    k, v = (c.rows(w, 0, n).transpose(0, 1).contiguous().bfloat16() for w in ("k", "v"))
+    q = torch.randn(1, Hk * G, d, generator=torch.Generator().manual_seed(111)).bfloat16().cuda()
+    kd, vd = depth(1, Hk, L, d, 112)
+    o, lse = moda.moda_decode_paged(q, *c.args(), torch.tensor([n], dtype=torch.int32, device="cuda"),
+                                    d ** -0.5, kd=kd, vd=vd)
+    od, lsed = moda.moda_decode(q[0], k, v, kd[0], vd[0], d ** -0.5)
+    settled()
+    ro, rl, to, tl = pc.decode_reference(c, q, [n], kd, vd, d ** -0.5)
+    # each is within its tolerance of the same values
+    assert ((o - od).abs().double() <= 2 * to).all() and ((lse - lsed).abs().double() <= 2 * tl).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mx4"])
+def test_append_many_heads(fmt):
+    """More heads than a warp's or a CTA's, of odd numbers."""
+    d, Hk, Hq, N = 64, 37, 37 * 3, 70
+    c = pc.Cache(fmt, [N, 3], Hk, d, 32, seed=120, device="cuda")
+    q, k, v = fused_qkv(N, Hq, Hk, d, 121)
+    seq = torch.zeros(N, dtype=torch.int32, device="cuda")
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")
+    rope = pc.rope_table(N, d).cuda()
+    qo, ko = moda.moda_kv_append(q, k, v, *c.args(), seq, pos, rope=rope, **c.scales())
+    kg, vg = moda.moda_kv_gather(*c.args(), seq, pos, **c.scales())
+    settled()
+    for x, out in ((q, qo), (k, ko)):
+        want = pc.turned(x, rope, pos, False)
+        size = x.double().abs().amax(dim=(1, 2), keepdim=True) * 2
+        assert ((out.double() - want).abs() <= pc.HALF_BF16 * want.abs() + 4 * pc.HALF_FP32 * size).all()
+    if fmt == "bf16":
+        assert torch.equal(kg, ko) and torch.equal(vg, v)
+    else:
+        assert torch.equal(kg.double(), pc.mx4_quantised(pc.turned(k, rope, pos, False)))
+        assert torch.equal(vg.double(), pc.mx4_quantised(v.double()))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mx4"])
+def test_calls_follow_one_another_without_waits(fmt):
+    """Every call reads what the one before it in the stream wrote, tensors and
+    workspace used again at once; the bits of the same calls with a
+    synchronisation after each, three times over."""
+    d, Hk, G, L, steps = 128, 4, 4, 24, 30
+    Hq, scale = Hk * G, d ** -0.5
+    total = [400, 33, 1000]
+    rope = pc.rope_table(1000 + steps, d).cuda()
+    q, k, v = fused_qkv(3, Hq, Hk, d, 130)
+    base = q._base
+    seq = torch.arange(3, dtype=torch.int32, device="cuda")
+    ws = torch.empty(moda.moda_decode_paged_workspace_bytes(Hq, Hk, d) // 4, device="cuda")
+    qo = torch.empty(3, Hq, d, dtype=torch.bfloat16, device="cuda")
+    ko = torch.empty(3, Hk, d, dtype=torch.bfloat16, device="cuda")
+    kb, vb = torch.empty_like(ko), torch.empty_like(ko)
+    kd, vd = depth(3, Hk, L, d, 131)
+    start = base.clone()
+
+    def run(wait):
+        c = pc.Cache(fmt, [t + steps for t in total], Hk, d, 16, seed=132, device="cuda")
+        base.copy_(start)
+        n = torch.tensor(total, dtype=torch.int32, device="cuda")
+        got = []
+        o, lse = torch.empty_like(qo), torch.empty(3, Hq, device="cuda")
+        for _ in range(steps):
+            moda.moda_kv_append(q, k, v, *c.args(), seq, n, rope=rope, q_out=qo, k_out=ko, **c.scales())
+            wait()
+            moda.moda_kv_gather(*c.args(), seq, n, k=kb, v=vb, **c.scales())
+            wait()
+            n.add_(1)
+            moda.moda_decode_paged(qo, *c.args(), n, scale, kd=kd, vd=vd, o=o, lse=lse, workspace=ws,
+                                   **c.scales())
+            wait()
+            got += [o.clone(), lse.clone(), kb.clone(), vb.clone()]
+            # the next step's rows depend on this one's result
+            base.view(3, -1)[:, : Hq * d].copy_((o.float() * 3).view(3, -1).bfloat16())
+            base.view(3, -1)[:, Hq * d : (Hq + Hk) * d].copy_(kb.view(3, -1))
+        torch.cuda.synchronize()
+        return got
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(3):
+        for a, b in zip(run(lambda: None), want):
+            assert torch.equal(a, b)
+    settled()
