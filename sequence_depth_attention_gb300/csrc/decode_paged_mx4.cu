@@ -12,6 +12,9 @@
 //   O^T += V^T P^T: a lane pairs the codes of two keys in a byte, one
 //     conversion gives their fp16 pair. V's block scales go into P, one P^T
 //     per block of 32 columns.
+// Measured (d = 128): 64 ragged sequences of up to 32768 rows at G = 8, 584 MB,
+// 123 us, issue 73 % and the ALU 61 % busy in the loop; the same rows in TMA
+// boxes with a producer warp and four codes to a load took 226.
 // Each warp streams units of its own (32 rows, or 16 depth slots) through its
 // own ring of shared-memory stages by asynchronous copies: no barrier between
 // warps but at the end of a segment.
@@ -28,8 +31,10 @@ constexpr int kKeys = 32;       // cached rows of a unit
 constexpr int kDepthKeys = 16;  // depth slots of a unit; their K and V take a stage each
 constexpr int kNS = 3;          // stages of a warp
 constexpr int kCols = 32;       // columns of O merged at a time
+// entering and leaving a segment, in units (about 2 us of a CTA's time)
 template <int D>
-constexpr int kCost = D == 128 ? 6 : 10;  // entering and leaving a segment, in units
+constexpr int kCost = D == 128 ? 6 : 10;
+// 168 registers (two head tiles: 255): four at 128 registers were 6 % slower
 template <int NT>
 constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
 

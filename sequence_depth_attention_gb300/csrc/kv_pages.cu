@@ -14,6 +14,10 @@
 //   the table turn 16 elements and no lane needs another's; d/16 lanes a head.
 //   4-bit rows: a lane owns one 16-byte vector, four lanes a block of 32; the
 //   halves of k's pairs come by shuffle.
+// Measured: a prompt of 16384 tokens (Hq 16, Hk 4, d 128, 227 MB) 35.4 us, 96 %
+// of the copy bandwidth; two vectors a lane on the way instead of four 41 us.
+// 16001 4-bit rows of 4 heads gathered, 42 MB, 11 us; an elementwise kernel over
+// as many bytes takes 10.4.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -25,7 +29,9 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarpsPerCta = kThreads / 32;
-constexpr int kAppendCtasMx4 = 9;  // of an SM, at least
+// CTAs of an SM, at least: 56 and 64 registers (ragged 4-bit prompts at 8, 9,
+// 10, 11: 54.5, 51.7, 51.8, 61 us, from 10 on with spills)
+constexpr int kAppendCtasMx4 = 9;
 constexpr int kAppendCtasBf16 = 8;
 
 // -------------------------------------------------------------- page rows
