@@ -23,9 +23,10 @@ void resolve() {
 
 }  // namespace
 
-static CUresult encode(CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank,
-                       const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
-                       CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion) {
+static CUresult encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
+                            const uint64_t* strides_bytes, const uint32_t* box,
+                            CUtensorMapSwizzle swizzle,
+                            CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   std::call_once(g_once, resolve);
   if (!g_encode) return CUDA_ERROR_NOT_FOUND;
   cuuint64_t gdim[5];
@@ -37,17 +38,9 @@ static CUresult encode(CUtensorMap* m, CUtensorMapDataType type, const void* bas
     estride[i] = 1;
   }
   for (int i = 0; i + 1 < rank; ++i) gstride[i] = strides_bytes[i];
-  return g_encode(m, type, (cuuint32_t)rank, const_cast<void*>(base), gdim, gstride, bdim, estride,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-}
-
-static CUresult encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
-                            const uint64_t* strides_bytes, const uint32_t* box,
-                            CUtensorMapSwizzle swizzle,
-                            CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides_bytes, box, swizzle,
-                promotion);
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base),
+                  gdim, gstride, bdim, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 CUresult encode_bf16_sw128(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
@@ -61,13 +54,6 @@ CUresult encode_bf16_sw128(CUtensorMap* m, const void* base, int rank, const uin
 CUresult encode_bf16_plain(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
                            const uint64_t* strides_bytes, const uint32_t* box) {
   return encode_bf16(m, base, rank, dims, strides_bytes, box, CU_TENSOR_MAP_SWIZZLE_NONE);
-}
-
-CUresult encode_bytes_swizzled(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
-                               const uint64_t* strides_bytes, const uint32_t* box) {
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, rank, dims, strides_bytes, box,
-                box[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 }  // namespace moda

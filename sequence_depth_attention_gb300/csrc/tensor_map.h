@@ -23,9 +23,4 @@ CUresult encode_bf16_sw128(CUtensorMap* m, const void* base, int rank, const uin
 CUresult encode_bf16_plain(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
                            const uint64_t* strides_bytes, const uint32_t* box);
 
-// A tensor map over bytes whose boxes are as wide as a box row (64 or 32
-// bytes), under the swizzle of that width.
-CUresult encode_bytes_swizzled(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
-                               const uint64_t* strides_bytes, const uint32_t* box);
-
 }  // namespace moda
