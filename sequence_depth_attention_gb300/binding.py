@@ -10,6 +10,8 @@ If it is missing, loading raises ``ModaError``: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -17,6 +19,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = os.path.join(_HERE, "_build", "libmoda.so")
+_EXT = os.path.join(_HERE, "_build", "paged_py.so")
 
 MODA_OK = 0
 _STATUS = {0: "MODA_OK", 1: "MODA_ERR_INVALID_ARG", 2: "MODA_ERR_UNSUPPORTED",
@@ -46,6 +49,21 @@ class _PagedKv(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
+_paged = None  # the extension module that marshals the paged calls' arguments
+
+
+def _load_paged(lib):
+    if not os.path.exists(_EXT):
+        raise ModaError(6, "load", f"{_EXT} is missing; build it with "
+                        "`python -m sequence_depth_attention_gb300.build`")
+    loader = importlib.machinery.ExtensionFileLoader("paged_py", _EXT)
+    ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("paged_py", loader))
+    loader.exec_module(ext)
+    address = (ctypes.cast(f, ctypes.c_void_p).value
+               for f in (lib.moda_kv_append, lib.moda_kv_gather, lib.moda_decode_paged))
+    ext.setup(torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.uint8,
+              torch.cuda.current_device, torch._C._cuda_getCurrentRawStream, *address)
+    return ext
 
 
 class ModaError(RuntimeError):
@@ -61,7 +79,7 @@ def library_path() -> str:
 
 def load():
     """Load libmoda.so once; raises ModaError if it has not been built."""
-    global _lib
+    global _lib, _paged
     with _lock:
         if _lib is not None:
             return _lib
@@ -128,6 +146,8 @@ def load():
         lib.moda_status_string.restype = ctypes.c_char_p
         lib.moda_last_error_detail.argtypes = []
         lib.moda_last_error_detail.restype = ctypes.c_char_p
+        if torch.backends.cuda.is_built():
+            _paged = _load_paged(lib)
         _lib = lib
         return lib
 
@@ -460,9 +480,9 @@ def moda_decode(q, k_cache, v_cache, kd_tok, vd_tok, scale: float, o=None, lse=N
 
 
 # The paged calls are made once a layer and step, often on small inputs, where
-# this module's own time counts: quick checks first and their messages only
-# after a refusal, plain integers for pointers, the stream's handle without its
-# Python object (an append of one token 21.7 -> 12.9 us, 3.7 of them the library).
+# this module's own time counts. A call whose tensors are all there and as they
+# should be goes through the extension module; what is below checks again,
+# allocates what is missing, and says what is wrong.
 _bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
@@ -568,6 +588,13 @@ def moda_kv_append(q, k, v, k_pages, v_pages, block_table, seq, pos, rope=None, 
     [...,d/2] with k_scales/v_scales[...,d/32] for the 4-bit format.
     Returns (q_out[N,Hq,d], k_out[N,Hk,d]), the turned q and k in bf16 (rows
     of padding are left as they were, in new tensors undefined)."""
+    if stream is None and _paged is not None and (k_out is not None or not want_k_out):
+        st = _paged.append(q, k, v, k_pages, v_pages, block_table, seq, pos, rope, interleaved,
+                           k_scales, v_scales, q_out, k_out)
+        if st is not None:
+            if st:
+                _check(st, "moda_kv_append")
+            return q_out, k_out
     dev = _current_device()
     cache, Hk, d, _ = _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales)
     N = _tokens(dev, seq, pos)
@@ -606,6 +633,12 @@ def moda_kv_gather(k_pages, v_pages, block_table, seq, pos, k_scales=None, v_sca
     """Rows (seq[n], pos[n]) of the paged cache as dense bf16 k, v [N,Hk,d]
     (see moda_kv_append for the cache; rows with seq -1 are left as they
     were, in new tensors undefined)."""
+    if stream is None and _paged is not None:
+        st = _paged.gather(k_pages, v_pages, block_table, seq, pos, k_scales, v_scales, k, v)
+        if st is not None:
+            if st:
+                _check(st, "moda_kv_gather")
+            return k, v
     dev = _current_device()
     cache, Hk, d, _ = _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales)
     N = _tokens(dev, seq, pos)
@@ -636,6 +669,13 @@ def moda_decode_paged(q, k_pages, v_pages, block_table, seq_lens, scale: float, 
     q[B,Hq,d] bf16, block_table[B,max_pages] and seq_lens[B] int32, kd/vd
     [B,Hk,L,d] bf16 views with contiguous rows of d values (None when L == 0).
     Returns (o[B,Hq,d] bf16, lse[B,Hq] fp32 or None)."""
+    if stream is None and _paged is not None and (lse is not None or not want_lse):
+        st = _paged.decode(q, k_pages, v_pages, block_table, seq_lens, scale, kd, vd, k_scales,
+                           v_scales, o, lse, workspace)
+        if st is not None:
+            if st:
+                _check(st, "moda_decode_paged")
+            return o, lse
     dev = _current_device()
     cache, Hk, d, B = _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales)
     if not (_here(q, _bf16, dev) and _here(seq_lens, _i32, dev)):

@@ -5,7 +5,8 @@
 Each .cu under csrc/ is compiled in parallel to an object, then linked into
 ``_build/libmoda.so`` with the CUDA runtime linked statically, so the library
 depends only on the driver. Objects are rebuilt when a source or header is
-newer than them.
+newer than them. csrc/paged_py.c becomes the Python extension module
+``_build/paged_py.so`` (gcc, no CUDA).
 """
 from __future__ import annotations
 
@@ -15,6 +16,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -22,6 +24,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(BUILD, "libmoda.so")
+EXT = os.path.join(BUILD, "paged_py.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -38,8 +41,25 @@ def _flags(extra=()):
             "--expt-relaxed-constexpr", *extra]
 
 
+def build_extension(force: bool = False) -> str:
+    """The extension module that marshals the paged calls' arguments."""
+    src = os.path.join(CSRC, "paged_py.c")
+    newest = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "moda.h")))
+    if not force and os.path.exists(EXT) and os.path.getmtime(EXT) >= newest:
+        return EXT
+    tmp = EXT + f".tmp{os.getpid()}"
+    cmd = [shutil.which("gcc") or "gcc", "-O2", "-shared", "-fPIC", "-Wall", "-I", INCLUDE, "-I",
+           sysconfig.get_paths()["include"], src, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on {os.path.basename(src)}:\n{r.stderr}")
+    os.replace(tmp, EXT)
+    return EXT
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
+    build_extension(force)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     headers = (glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
                glob.glob(os.path.join(INCLUDE, "*.h")))
