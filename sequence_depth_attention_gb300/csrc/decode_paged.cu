@@ -74,13 +74,7 @@ __device__ __forceinline__ void tile_bf16(State<D, NT>& st, const uint32_t (&qb)
     st.weigh(t, s[t], p);
     // P^T (rows = keys, columns = heads) transposed into the B tile
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t hi = wmma16::pack_bf16(p[2 * i], p[2 * i + 1]);
-      const uint32_t lo = wmma16::pack_bf16(p[2 * i] - __uint_as_float(hi << 16),
-                                            p[2 * i + 1] - __uint_as_float(hi & 0xffff0000u));
-      pb[t][i] = wmma16::movmatrix_t(hi);
-      pl[t][i] = wmma16::movmatrix_t(lo);
-    }
+    for (int i = 0; i < 2; ++i) weights_bf16(p[2 * i], p[2 * i + 1], pb[t][i], pl[t][i]);
   }
   // rows that do not exist weigh 0, but 0 times what they hold may be NaN
   uint32_t lo = 0xffffffffu, hi = 0xffffffffu;

@@ -182,8 +182,8 @@ __device__ __forceinline__ Share<KEYS> share_of(const Params& p, int depth_units
         if (n == 0) continue;
         const int len = n + COST;
         if (point < at + (long long)len * p.Hk) {
-          // (point - at) / len, at most 4096 or so: a float's quotient is at
-          // most one off
+          // (point - at) / len is below Hk, at most 4096: a float's quotient is
+          // at most one off
           int hk = (int)((float)(point - at) / (float)len);
           int off = (int)(point - at - (long long)hk * len);
           if (off < 0) {
@@ -316,6 +316,16 @@ __device__ __forceinline__ void load_q_bf16(uint32_t (&qb)[NT][D / 16][2], const
       qb[t][ks][1] = h < G ? row[ks * 8 + 4] : 0u;
     }
   }
+}
+
+// Weights of two keys for heads 2c and 2c + 1 as a register of the B tile of
+// O^T += V^T P^T: rounded to bf16, and what that left, for a second product.
+__device__ __forceinline__ void weights_bf16(float p0, float p1, uint32_t& head, uint32_t& rest) {
+  const uint32_t hi = wmma16::pack_bf16(p0, p1);
+  const uint32_t lo =
+      wmma16::pack_bf16(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
+  head = wmma16::movmatrix_t(hi);
+  rest = wmma16::movmatrix_t(lo);
 }
 
 // The merge buffer: O of COLS columns of 8 heads for each warp, and (m, l).

@@ -202,11 +202,11 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Weights of 16 depth slots: p, as B tiles of O^T += V^T P^T.
+// Weights of 16 depth slots, as B tiles of O^T += V^T P^T: bf16 and the rest.
 template <int D, int NT>
 __device__ __forceinline__ void depth_scores(State<D, NT>& st, const uint32_t (&qb)[NT][D / 16][2],
                                              uint32_t kb, int there, float scale_log2, int lane,
-                                             uint32_t (&pb)[NT][2]) {
+                                             uint32_t (&pb)[NT][2], uint32_t (&pl)[NT][2]) {
   const int lr = lane & 7, lm = lane >> 3;
   float s[NT][4];
 #pragma unroll
@@ -232,8 +232,8 @@ __device__ __forceinline__ void depth_scores(State<D, NT>& st, const uint32_t (&
     st.template raise<4>(t, z, kSlack);
     float p[4];
     st.weigh(t, s[t], p);
-    pb[t][0] = wmma16::movmatrix_t(wmma16::pack_bf16(p[0], p[1]));
-    pb[t][1] = wmma16::movmatrix_t(wmma16::pack_bf16(p[2], p[3]));
+    weights_bf16(p[0], p[1], pb[t][0], pl[t][0]);
+    weights_bf16(p[2], p[3], pb[t][1], pl[t][1]);
   }
 }
 
@@ -241,8 +241,8 @@ __device__ __forceinline__ void depth_scores(State<D, NT>& st, const uint32_t (&
 // d = 32 g + 2 r0 in row r0 and 32 g + 16 + 2 r0 in r0 + 8, tile 2g + 1 the
 // elements after them. Rows past L are zeros.
 template <int D, int NT>
-__device__ __forceinline__ void depth_values(State<D, NT>& st, const uint32_t (&pb)[NT][2], uint32_t vb,
-                                             int lane) {
+__device__ __forceinline__ void depth_values(State<D, NT>& st, const uint32_t (&pb)[NT][2],
+                                             const uint32_t (&pl)[NT][2], uint32_t vb, int lane) {
   const int r0 = lane >> 2, v0 = 4 * (lane & 3);
 #pragma unroll
   for (int g = 0; g < D / 32; ++g) {
@@ -260,7 +260,9 @@ __device__ __forceinline__ void depth_values(State<D, NT>& st, const uint32_t (&
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       wmma16::mma_bf16(st.o[t][2 * g], a, pb[t][0], pb[t][1]);
+      wmma16::mma_bf16(st.o[t][2 * g], a, pl[t][0], pl[t][1]);
       wmma16::mma_bf16(st.o[t][2 * g + 1], b, pb[t][0], pb[t][1]);
+      wmma16::mma_bf16(st.o[t][2 * g + 1], b, pl[t][0], pl[t][1]);
     }
   }
 }
@@ -582,13 +584,13 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
     st.clear();
     int off = at.off + ((warp - turn) & (kWarps - 1));
     if (off < min(end, depth_units)) {
-      uint32_t qb[NT][D / 16][2], pb[NT][2];
+      uint32_t qb[NT][D / 16][2], pb[NT][2], pl[NT][2];
       load_q_bf16<D, NT>(qb, q, p.G, lane);
       for (; off < min(end, depth_units); off += kWarps) {
         uint32_t s = next();
-        depth_scores<D, NT>(st, qb, s, p.L - off * kDepthKeys, p.scale_log2, lane, pb);
+        depth_scores<D, NT>(st, qb, s, p.L - off * kDepthKeys, p.scale_log2, lane, pb, pl);
         s = next();
-        depth_values<D, NT>(st, pb, s, lane);
+        depth_values<D, NT>(st, pb, pl, s, lane);
       }
     }
     if (off < end) {
