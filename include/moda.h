@@ -367,9 +367,9 @@ MODA_API moda_status moda_decode_strided(const void* q, const void* k_cache, con
  *                 its codes are 0. (The microscaling format of 4-bit floating
  *                 point with blocks of 32: 4.25 bits an element.)
  *
- * page_size is 16, 32, 64 or 128; d is 64 or 128; num_pages * Hk * page_size
- * is at most 2^31 - 1, max_pages * page_size at most 2^30, B * Hk * max_pages *
- * page_size at most 2^40. k, v, k_scale and
+ * page_size is 16, 32, 64 or 128; d is 64 or 128; Hk is at most 4096, num_pages
+ * * Hk * page_size at most 2^31 - 1, max_pages * page_size at most 2^30, B * Hk *
+ * max_pages * page_size at most 2^40. k, v, k_scale and
  * v_scale are 16-byte aligned, block_table 4-byte aligned. The struct is read
  * during the call; the buffers it names belong to the caller.
  *
@@ -429,7 +429,7 @@ typedef struct {
  * A token with an index outside its range is left out like padding, and
  * latched (see above). Name each (seq, pos) at most once in a call: of two
  * tokens for one row either may be found there, or parts of both. Outputs and
- * pages must not overlap the inputs or each other. N <= 2^24, Hq and Hk <= 4096,
+ * pages must not overlap the inputs or each other. N <= 2^24, Hq <= 4096,
  * N * (Hq + 2 Hk) <= 2^31 - 1.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. N == 0 is a no-op.
  */
@@ -481,14 +481,18 @@ MODA_API moda_status moda_kv_gather(const moda_paged_kv* cache, const int* seq, 
  *             between calls. Calls that may run at the same time need one each.
  * A page index outside [0, num_pages) makes its sequence's result unspecified
  * and is latched.
- * Arithmetic: fp32 accumulation, softmax in fp32. bf16 pages: probabilities in
- * two bf16 parts, so that o is right to its own rounding. MX4 pages: the codes'
+ * Arithmetic: fp32 accumulation, softmax in fp32. bf16 pages and the depth
+ * slots: probabilities in two bf16 parts, so that o is right to its own
+ * rounding. MX4 pages: the codes'
  * exact values against q in fp16 (scaled per head, so that its 8 bits stay),
  * block scales applied in fp32, probabilities times V's block scales rounded to
  * fp16 under a running scale: to 11 bits, and to 2^-32 of the largest of them
  * where that is more. (Scale byte 0, which moda_kv_append never writes, is read
- * as 0 here, 2^-80 is the least that V's scales count for in the running one.)
- * Supported: G = Hq/Hk from 1 to 16, B*Hq <= 2^24, 0 <= L <= 1024.
+ * as 0 here, 2^-80 is the least that V's scales count for in the running one.
+ * K's values below 2^100 cannot overflow a score's fp32 sum, and scale times a
+ * head's largest |q| counts for 2^-112 at least.)
+ * Supported: G = Hq/Hk from 1 to 16, B*Hq <= 2^24, 0 <= L <= 1024, scale > 0
+ * and at most 2e38.
  * The result depends on how the batch is split over the SMs only by the order
  * of fp32 sums; the same call on the same device gives the same bits.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA; TIMEOUT via

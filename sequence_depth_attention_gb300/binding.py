@@ -9,6 +9,7 @@ If it is missing, loading raises ``ModaError``: there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.machinery
 import importlib.util
@@ -482,7 +483,7 @@ def moda_decode(q, k_cache, v_cache, kd_tok, vd_tok, scale: float, o=None, lse=N
 # The paged calls are made once a layer and step, often on small inputs, where
 # this module's own time counts. A call whose tensors are all there and as they
 # should be goes through the extension module; what is below checks again,
-# allocates what is missing, and says what is wrong.
+# allocates what is missing (on the call's stream), and says what is wrong.
 _bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
@@ -499,6 +500,17 @@ def _raw_stream(stream, dev):
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _allocating(stream, dev):
+    """The context to allocate in for a call on `stream`: on that stream, since
+    memory of the current one may still be in use there, and a workspace goes
+    back to its pool when the call returns."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_raw_stream(stream, dev), device=dev)
+    return torch.cuda.stream(stream)
 
 
 def _here(t, dtype, dev):
@@ -608,10 +620,11 @@ def moda_kv_append(q, k, v, k_pages, v_pages, block_table, seq, pos, rope=None, 
             raise ValueError("rope must be [P,rot]")
         rows, rot = rope.shape
         rp = rope.data_ptr()
-    if q is not None and q_out is None:
-        q_out = torch.empty((N, Hq, d), dtype=_bf16, device=q.device)
-    if want_k_out and k_out is None:
-        k_out = torch.empty((N, Hk, d), dtype=_bf16, device=k.device)
+    with _allocating(stream, dev):
+        if q is not None and q_out is None:
+            q_out = torch.empty((N, Hq, d), dtype=_bf16, device=q.device)
+        if want_k_out and k_out is None:
+            k_out = torch.empty((N, Hk, d), dtype=_bf16, device=k.device)
     if not ((rope is None or _here(rope, _f32, dev)) and (q_out is None or _here(q_out, _bf16, dev))
             and (k_out is None or _here(k_out, _bf16, dev))):
         _refuse(dev, (rope, "rope", _f32), (q_out, "q_out", _bf16), (k_out, "k_out", _bf16))
@@ -643,10 +656,11 @@ def moda_kv_gather(k_pages, v_pages, block_table, seq, pos, k_scales=None, v_sca
     cache, Hk, d, _ = _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales)
     N = _tokens(dev, seq, pos)
     shape = (N, Hk, d)
-    if k is None:
-        k = torch.empty(shape, dtype=_bf16, device=k_pages.device)
-    if v is None:
-        v = torch.empty(shape, dtype=_bf16, device=k_pages.device)
+    with _allocating(stream, dev):
+        if k is None:
+            k = torch.empty(shape, dtype=_bf16, device=k_pages.device)
+        if v is None:
+            v = torch.empty(shape, dtype=_bf16, device=k_pages.device)
     if not (_here(k, _bf16, dev) and _here(v, _bf16, dev)):
         _refuse(dev, (k, "k", _bf16), (v, "v", _bf16))
     if k.shape != shape or v.shape != shape:
@@ -705,13 +719,14 @@ def moda_decode_paged(q, k_pages, v_pages, block_table, seq_lens, scale: float, 
                 if any(dshape[i] > 1 and other[i] != strides[i] for i in range(4)):
                     raise ValueError("kd and vd must have the same strides")
             strides, kp, vp = strides[:3], kd.data_ptr(), vd.data_ptr()
-    if o is None:
-        o = torch.empty(shape, dtype=_bf16, device=q.device)
-    if want_lse and lse is None:
-        lse = torch.empty((B, Hq), dtype=_f32, device=q.device)
-    if workspace is None:
-        need = moda_decode_paged_workspace_bytes(Hq, Hk, d)
-        workspace = torch.empty(max(4, need // 4), dtype=_f32, device=q.device)
+    with _allocating(stream, dev):
+        if o is None:
+            o = torch.empty(shape, dtype=_bf16, device=q.device)
+        if want_lse and lse is None:
+            lse = torch.empty((B, Hq), dtype=_f32, device=q.device)
+        if workspace is None:
+            need = moda_decode_paged_workspace_bytes(Hq, Hk, d)
+            workspace = torch.empty(max(4, need // 4), dtype=_f32, device=q.device)
     if not (_here(o, _bf16, dev) and (lse is None or _here(lse, _f32, dev)) and _here(workspace, _f32, dev)):
         _refuse(dev, (o, "o", _bf16), (lse, "lse", _f32), (workspace, "workspace", _f32))
     if o.shape != shape or (lse is not None and lse.shape != (B, Hq)):

@@ -139,7 +139,7 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
 // ----------------------------------------------------------------- append
 struct AppendGrid {
   int q_parts, parts;  // of a token: q's heads, then k's and v's
-  int64_t items;       // warps
+  uint32_t items;      // warps: no more than rows, which are below 2^31
 };
 
 __device__ __forceinline__ void load4(const float* p, float* x) {
@@ -251,12 +251,11 @@ __global__ void __launch_bounds__(kThreads, MX4 ? kAppendCtasMx4 : kAppendCtasBf
 kv_append_kernel(const __grid_constant__ KvAppendArgs a, const __grid_constant__ AppendGrid g) {
   constexpr int VPR = D / 8;
   const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
+  const uint32_t item = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
   paged::wait_for_stream();
   if (item >= g.items) return;
-  // item = token * parts + part, below 2^31 almost always
-  const int64_t n = g.items >> 31 == 0 ? (uint32_t)item / (uint32_t)g.parts : item / g.parts;
-  const int part = (int)(item - n * g.parts);
+  const int64_t n = item / (uint32_t)g.parts;  // item = token * parts + part
+  const int part = (int)(item - (uint32_t)n * g.parts);
   const int s = a.seq[n], p = a.pos[n];
   int limit = a.c.max_pages * a.c.page_size;
   if (a.rot > 0) limit = min(limit, a.rope_rows);
@@ -412,11 +411,10 @@ cudaError_t append_d(const KvAppendArgs& a, cudaStream_t stream) {
   g.q_parts = (a.Hq + 128 / VPR - 1) / (128 / VPR);
   const int kv_heads = (mx4 ? 32 : 64) / VPR;
   g.parts = g.q_parts + (a.c.Hk + kv_heads - 1) / kv_heads;
-  g.items = (int64_t)a.N * g.parts;
-  const int64_t blocks = (g.items + kWarpsPerCta - 1) / kWarpsPerCta;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  g.items = (uint32_t)a.N * g.parts;
+  const unsigned blocks = (g.items + kWarpsPerCta - 1) / kWarpsPerCta;
   return paged::launch_dependent(mx4 ? kv_append_kernel<D, true> : kv_append_kernel<D, false>,
-                                 dim3((unsigned)blocks), kThreads, 0, stream, a, g);
+                                 dim3(blocks), kThreads, 0, stream, a, g);
 }
 
 template <int D>

@@ -42,6 +42,7 @@ moda_status check_cache(const moda_paged_kv* c, moda::PagedKv* out, CacheRanges*
     return report(MODA_ERR_UNSUPPORTED, "page_size = %d (supported: 16, 32, 64, 128)", P);
   if (c->d != 64 && c->d != 128)
     return report(MODA_ERR_UNSUPPORTED, "d = %d (supported: 64, 128)", c->d);
+  if (c->Hk > 4096) return report(MODA_ERR_UNSUPPORTED, "Hk = %d > 4096", c->Hk);
   if ((int64_t)c->num_pages * c->Hk > 0x7fffffffLL / P)
     return report(MODA_ERR_UNSUPPORTED, "num_pages * Hk * page_size exceeds 2^31 - 1 rows");
   if ((int64_t)c->max_pages * P > (1 << 30))
@@ -98,8 +99,7 @@ moda_status moda_kv_append(const void* q, const void* k, const void* v, long lon
   if (N < 0) return report(MODA_ERR_INVALID_ARG, "N = %d < 0", N);
   if (Hq < 0) return report(MODA_ERR_INVALID_ARG, "Hq = %d < 0", Hq);
   if (N > kMaxTokens) return report(MODA_ERR_UNSUPPORTED, "N = %d > 2^24", N);
-  if (Hq > 4096 || Hk > 4096)
-    return report(MODA_ERR_UNSUPPORTED, "Hq = %d, Hk = %d (at most 4096)", Hq, Hk);
+  if (Hq > 4096) return report(MODA_ERR_UNSUPPORTED, "Hq = %d > 4096", Hq);
   if ((int64_t)N * ((int64_t)Hq + 2 * Hk) > 0x7fffffffLL)
     return report(MODA_ERR_UNSUPPORTED, "N * (Hq + 2 Hk) = %lld rows exceed 2^31 - 1",
                   (long long)N * ((long long)Hq + 2 * Hk));
@@ -163,7 +163,6 @@ moda_status moda_kv_gather(const moda_paged_kv* cache, const int* seq, const int
   if (st != MODA_OK) return st;
   if (N < 0) return report(MODA_ERR_INVALID_ARG, "N = %d < 0", N);
   if (N > kMaxTokens) return report(MODA_ERR_UNSUPPORTED, "N = %d > 2^24", N);
-  if (c.Hk > 4096) return report(MODA_ERR_UNSUPPORTED, "Hk = %d > 4096", c.Hk);
   if (N == 0) return ok();
   if (!seq || !pos || !k || !v) return report(MODA_ERR_INVALID_ARG, "NULL input or output");
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(seq, 4) || !aligned(pos, 4))
@@ -202,8 +201,9 @@ moda_status moda_decode_paged(const void* q, const moda_paged_kv* cache, const i
   if (Hq < 1) return report(MODA_ERR_INVALID_ARG, "Hq = %d < 1", Hq);
   if (Hq % Hk != 0) return report(MODA_ERR_INVALID_ARG, "Hq = %d not a multiple of Hk = %d", Hq, Hk);
   if (L < 0) return report(MODA_ERR_INVALID_ARG, "L = %d < 0", L);
-  if (!(scale > 0.f) || scale == __builtin_inff())
-    return report(MODA_ERR_INVALID_ARG, "scale must be positive and finite");
+  // the kernels work with scale * log2(e)
+  if (!(scale > 0.f) || scale > 2e38f)
+    return report(MODA_ERR_INVALID_ARG, "scale must be positive and at most 2e38");
   const int G = Hq / Hk;
   if (G > 16) return report(MODA_ERR_UNSUPPORTED, "G = Hq/Hk = %d (supported: 1 to 16)", G);
   if (L > 1024) return report(MODA_ERR_UNSUPPORTED, "L = %d > 1024", L);

@@ -200,3 +200,13 @@ def test_decode_reference_against_one_softmax(fmt):
 def test_append_rejects_too_many_rows(lib):
     # N * (Hq + 2 Hk) rows beyond 2^31 - 1
     assert append(lib, N=1 << 24, Hq=256, qs=256 * 64, ks=1 << 20, vs=1 << 20, Hk=2) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("call", [append, gather, decode])
+def test_more_kv_heads_than_supported(lib, call):
+    assert call(lib, Hk=4097, num_pages=1) == UNSUPPORTED
+    assert "4097" in lib.moda_last_error_detail().decode()
+
+
+def test_decode_rejects_a_scale_whose_log2_form_overflows(lib):
+    assert decode(lib, scale=2.4e38) == INVALID

@@ -676,3 +676,109 @@ def test_calls_follow_one_another_without_waits(fmt):
         for a, b in zip(run(lambda: None), want):
             assert torch.equal(a, b)
     settled()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mx4"])
+def test_what_a_call_allocates_belongs_to_its_stream(fmt, monkeypatch):
+    """Outputs and workspace of a call on a stream of its own come from that
+    stream's memory: what the current stream's pool hands out may still be in
+    use there, and would be handed out again while the call runs."""
+    d, Hk, lens = 64, 2, [70, 5]
+    c = pc.Cache(fmt, lens, Hk, d, 16, seed=3, device="cuda")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    seq = torch.arange(2, dtype=torch.int32, device="cuda")
+    q, k, v = fused_qkv(2, 8, Hk, d, 4)
+    want = (moda.moda_kv_append(q, k, v, *c.args(), seq, n - 1, **c.scales()),
+            moda.moda_kv_gather(*c.args(), seq, n - 1, **c.scales()),
+            moda.moda_decode_paged(q.contiguous(), *c.args(), n, 0.1, **c.scales()))
+    qc, pos = q.contiguous(), n - 1
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    on, empty = [], torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: (on.append(torch.cuda.current_stream()), empty(*a, **kw))[1])
+    for stream in (side, side.cuda_stream):
+        on.clear()
+        got = (moda.moda_kv_append(q, k, v, *c.args(), seq, pos, stream=stream, **c.scales()),
+               moda.moda_kv_gather(*c.args(), seq, pos, stream=stream, **c.scales()),
+               moda.moda_decode_paged(qc, *c.args(), n, 0.1, stream=stream, **c.scales()))
+        assert len(on) == 7 and {s.cuda_stream for s in on} == {side.cuda_stream}
+        settled()
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mx4"])
+def test_captured_among_copies_and_other_streams(fmt):
+    """A step captured where what comes before each call is not a kernel (a
+    copy, a fill) or is two streams that meet; replayed on new inputs."""
+    d, Hk, lens = 64, 2, [130, 17, 1]
+    c = pc.Cache(fmt, lens, Hk, d, 16, seed=13, device="cuda")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    seq, pos, scale = torch.arange(3, dtype=torch.int32, device="cuda"), n - 1, d ** -0.5
+    q, k, v = (torch.zeros(3, h, d, dtype=torch.bfloat16, device="cuda") for h in (4, Hk, Hk))
+    new = [torch.zeros_like(t) for t in (q, k, v)]
+    qo, o, kg, vg = torch.empty_like(q), torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ko, lse = torch.empty_like(k), torch.empty(3, 4, device="cuda")
+    ws = torch.empty(moda.moda_decode_paged_workspace_bytes(4, Hk, d) // 4, device="cuda")
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step():
+        for t, x in zip((q, k, v), new):
+            t.copy_(x)  # the append's predecessor is a copy
+        moda.moda_kv_append(q, k, v, *c.args(), seq, pos, q_out=qo, k_out=ko, **c.scales())
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            kg.zero_()
+            moda.moda_kv_gather(*c.args(), seq, pos, k=kg, v=vg, **c.scales())
+        o.zero_()
+        moda.moda_decode_paged(qo, *c.args(), n, scale, o=o, lse=lse, workspace=ws, **c.scales())
+        torch.cuda.current_stream().wait_stream(side)
+        # two streams end here, and the next call waits for both
+        moda.moda_kv_append(None, kg, vg, *c.args(), seq, pos, k_out=ko, **c.scales())
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(main):
+        step()
+        main.synchronize()
+        with torch.cuda.graph(graph, stream=main):
+            step()
+    for rep in range(3):
+        for i, t in enumerate(new):
+            t.copy_(torch.randn(t.shape, generator=torch.Generator().manual_seed(5 * rep + i)).bfloat16())
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        held = [t.clone() for t in (o, lse, kg, vg, ko)]
+        with torch.cuda.stream(main):
+            step()
+        torch.cuda.synchronize()
+        for a, b in zip(held, (o, lse, kg, vg, ko)):
+            assert torch.equal(a, b)
+        if fmt == "bf16":
+            assert torch.equal(kg, new[1]) and torch.equal(vg, new[2])
+        check_decode(c, new[0], lens, None, None, scale, o, lse)
+    settled()
+
+
+@pytest.mark.parametrize("G", [1, 8, 16])
+def test_depth_slots_weigh_in_two_parts_over_4_bit_pages(G):
+    """Where the depth slots hold nearly all of the weight, o is right to its
+    own rounding and the sums' (pc.decode_reference without the rounding of a
+    probability: two bf16 parts leave 2^-16 of it)."""
+    d, Hk, L = 128, 2, 40
+    lens = [33, 64]
+    c = pc.Cache("mx4", lens, Hk, d, 16, seed=23, device="cuda")
+    c.ks.fill_(96), c.vs.fill_(96)  # 2^-31: the rows' scores are 0, their values nothing
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = torch.randn(2, Hk * G, d, generator=torch.Generator().manual_seed(24)).bfloat16().cuda()
+    kd, vd = depth(2, Hk, L, d, 25)
+    kd, vd = kd * 2, vd.abs()  # sums without cancellation
+    scale = d ** -0.5
+    o, lse = moda.moda_decode_paged(q, *c.args(), n, scale, kd=kd, vd=vd, **c.scales())
+    settled()
+    # the fill rows beyond the sequences hold no NaN here, and are not reached
+    want, _, tol, _ = pc.decode_reference(c, q, lens, kd, vd, scale)
+    # a = sum p |v| = o up to the rows' 2^-31: take HALF_BF16 of it off twice, give 2^-16 twice
+    tight = tol - 2 * (pc.HALF_BF16 - 2.0 ** -16) * want.abs() + 2.0 ** -30
+    assert ((o.double() - want).abs() <= tight).all()
