@@ -61,9 +61,10 @@ def _load_paged(lib):
     ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("paged_py", loader))
     loader.exec_module(ext)
     address = (ctypes.cast(f, ctypes.c_void_p).value
-               for f in (lib.moda_kv_append, lib.moda_kv_gather, lib.moda_decode_paged))
-    ext.setup(torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.uint8,
-              torch.cuda.current_device, torch._C._cuda_getCurrentRawStream, *address)
+               for f in (lib.moda_kv_append, lib.moda_kv_gather, lib.moda_decode_paged,
+                         lib.moda_decode_paged_workspace_bytes))
+    # (for the current device without torch.cuda's start-up: the tensors have seen to it)
+    ext.setup(torch.Tensor, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, *address)
     return ext
 
 
@@ -481,9 +482,9 @@ def moda_decode(q, k_cache, v_cache, kd_tok, vd_tok, scale: float, o=None, lse=N
 
 
 # The paged calls are made once a layer and step, often on small inputs, where
-# this module's own time counts. A call whose tensors are all there and as they
-# should be goes through the extension module; what is below checks again,
-# allocates what is missing (on the call's stream), and says what is wrong.
+# this module's own time counts. A call on the current stream whose tensors are
+# as they should be goes through the extension module; what is below serves the
+# others, and says what is wrong.
 _bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
@@ -600,13 +601,11 @@ def moda_kv_append(q, k, v, k_pages, v_pages, block_table, seq, pos, rope=None, 
     [...,d/2] with k_scales/v_scales[...,d/32] for the 4-bit format.
     Returns (q_out[N,Hq,d], k_out[N,Hk,d]), the turned q and k in bf16 (rows
     of padding are left as they were, in new tensors undefined)."""
-    if stream is None and _paged is not None and (k_out is not None or not want_k_out):
-        st = _paged.append(q, k, v, k_pages, v_pages, block_table, seq, pos, rope, interleaved,
-                           k_scales, v_scales, q_out, k_out)
-        if st is not None:
-            if st:
-                _check(st, "moda_kv_append")
-            return q_out, k_out
+    if stream is None and _paged is not None:
+        out = _paged.append(q, k, v, k_pages, v_pages, block_table, seq, pos, rope, interleaved,
+                            k_scales, v_scales, q_out, k_out, want_k_out)
+        if out is not None:
+            return out if type(out) is tuple else _check(out, "moda_kv_append")
     dev = _current_device()
     cache, Hk, d, _ = _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales)
     N = _tokens(dev, seq, pos)
@@ -647,11 +646,9 @@ def moda_kv_gather(k_pages, v_pages, block_table, seq, pos, k_scales=None, v_sca
     (see moda_kv_append for the cache; rows with seq -1 are left as they
     were, in new tensors undefined)."""
     if stream is None and _paged is not None:
-        st = _paged.gather(k_pages, v_pages, block_table, seq, pos, k_scales, v_scales, k, v)
-        if st is not None:
-            if st:
-                _check(st, "moda_kv_gather")
-            return k, v
+        out = _paged.gather(k_pages, v_pages, block_table, seq, pos, k_scales, v_scales, k, v)
+        if out is not None:
+            return out if type(out) is tuple else _check(out, "moda_kv_gather")
     dev = _current_device()
     cache, Hk, d, _ = _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales)
     N = _tokens(dev, seq, pos)
@@ -683,13 +680,11 @@ def moda_decode_paged(q, k_pages, v_pages, block_table, seq_lens, scale: float, 
     q[B,Hq,d] bf16, block_table[B,max_pages] and seq_lens[B] int32, kd/vd
     [B,Hk,L,d] bf16 views with contiguous rows of d values (None when L == 0).
     Returns (o[B,Hq,d] bf16, lse[B,Hq] fp32 or None)."""
-    if stream is None and _paged is not None and (lse is not None or not want_lse):
-        st = _paged.decode(q, k_pages, v_pages, block_table, seq_lens, scale, kd, vd, k_scales,
-                           v_scales, o, lse, workspace)
-        if st is not None:
-            if st:
-                _check(st, "moda_decode_paged")
-            return o, lse
+    if stream is None and _paged is not None:
+        out = _paged.decode(q, k_pages, v_pages, block_table, seq_lens, scale, kd, vd, k_scales,
+                            v_scales, o, lse, workspace, want_lse)
+        if out is not None:
+            return out if type(out) is tuple else _check(out, "moda_decode_paged")
     dev = _current_device()
     cache, Hk, d, B = _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales)
     if not (_here(q, _bf16, dev) and _here(seq_lens, _i32, dev)):

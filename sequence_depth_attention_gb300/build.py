@@ -5,8 +5,8 @@
 Each .cu under csrc/ is compiled in parallel to an object, then linked into
 ``_build/libmoda.so`` with the CUDA runtime linked statically, so the library
 depends only on the driver. Objects are rebuilt when a source or header is
-newer than them. csrc/paged_py.c becomes the Python extension module
-``_build/paged_py.so`` (gcc, no CUDA).
+newer than them. csrc/paged_py.cpp becomes the Python extension module
+``_build/paged_py.so`` (g++ and PyTorch's headers, no CUDA).
 """
 from __future__ import annotations
 
@@ -43,23 +43,34 @@ def _flags(extra=()):
 
 def build_extension(force: bool = False) -> str:
     """The extension module that marshals the paged calls' arguments."""
-    src = os.path.join(CSRC, "paged_py.c")
+    import torch
+
+    src = os.path.join(CSRC, "paged_py.cpp")
+    stamp = EXT + ".torch"  # it is bound to the torch that it was built for
     newest = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "moda.h")))
-    if not force and os.path.exists(EXT) and os.path.getmtime(EXT) >= newest:
-        return EXT
+    if not force and os.path.exists(EXT) and os.path.exists(stamp) and os.path.getmtime(EXT) >= newest:
+        with open(stamp) as f:
+            if f.read() == torch.__version__:
+                return EXT
     tmp = EXT + f".tmp{os.getpid()}"
-    cmd = [shutil.which("gcc") or "gcc", "-O2", "-shared", "-fPIC", "-Wall", "-I", INCLUDE, "-I",
-           sysconfig.get_paths()["include"], src, "-o", tmp]
+    root = os.path.dirname(torch.__file__)
+    includes = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(root, "include"),
+                os.path.join(root, "include", "torch", "csrc", "api", "include")]
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(x for p in includes for x in ("-isystem", p)), src, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"gcc failed on {os.path.basename(src)}:\n{r.stderr}")
+        raise RuntimeError(f"g++ failed on {os.path.basename(src)}:\n{r.stderr}")
     os.replace(tmp, EXT)
+    with open(stamp, "w") as f:
+        f.write(torch.__version__)
     return EXT
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    build_extension(force)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     headers = (glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
                glob.glob(os.path.join(INCLUDE, "*.h")))
@@ -82,8 +93,10 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        ext = ex.submit(build_extension, force)
         results = list(ex.map(compile_one, srcs))
+        ext.result()
     if verbose:
         for _, log in results:
             if log:

@@ -46,6 +46,8 @@ class Recorder:
         for name in ("moda_kv_append", "moda_kv_gather", "moda_decode_paged"):
             self.c[name] = c_type(lib, name)(self.keep)
             setattr(self, name, self.keep)
+        name = "moda_decode_paged_workspace_bytes"
+        self.c[name] = c_type(lib, name)(lambda *shape: WORKSPACE)
 
     def keep(self, *args):
         self.seen = tuple(plain(a) for a in args)
@@ -70,9 +72,8 @@ def ways(tmp_path, monkeypatch):
     loader = importlib.machinery.ExtensionFileLoader("paged_py", str(path))
     ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("paged_py", loader))
     loader.exec_module(ext)
-    ext.setup(torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.uint8, lambda: -1,
-              lambda dev: STREAM, *(ctypes.cast(rec.c[n], ctypes.c_void_p).value
-                                    for n in ("moda_kv_append", "moda_kv_gather", "moda_decode_paged")))
+    ext.setup(torch.Tensor, lambda: -1, lambda dev: STREAM,
+              *(ctypes.cast(f, ctypes.c_void_p).value for f in rec.c.values()))
     monkeypatch.setattr(binding, "_lib", rec)
     monkeypatch.setattr(binding, "_paged", None)
     monkeypatch.setattr(binding, "_current_device", lambda: -1)
@@ -114,21 +115,22 @@ def arguments(call, mx4):
         fused = bf(N, HQ + 2 * HK, D)
         return dict(q=fused[:, :HQ], k=fused[:, HQ:HQ + HK], v=fused[:, HQ + HK:], **c, seq=i32(N),
                     pos=i32(N), rope=f32(32, 32), interleaved=True, q_out=bf(N, HQ, D),
-                    k_out=bf(N, HK, D))
+                    k_out=bf(N, HK, D), want_k_out=False)
     if call == "gather":
         return dict(**c, seq=i32(N), pos=i32(N), k=bf(N, HK, D), v=bf(N, HK, D))
     return dict(q=bf(B, HQ, D), **c, seq_lens=i32(B), scale=0.3, kd=bf(B, L, HK, D).transpose(1, 2),
-                vd=bf(B, L, HK, D).transpose(1, 2), o=bf(B, HQ, D), lse=f32(B, HQ), workspace=f32(99))
+                vd=bf(B, L, HK, D).transpose(1, 2), o=bf(B, HQ, D), lse=f32(B, HQ), workspace=f32(99),
+                want_lse=False)
 
 
 ORDER = dict(
     append=("q", "k", "v", "k_pages", "v_pages", "block_table", "seq", "pos", "rope", "interleaved",
-            "k_scales", "v_scales", "q_out", "k_out"),
+            "k_scales", "v_scales", "q_out", "k_out", "want_k_out"),
     gather=("k_pages", "v_pages", "block_table", "seq", "pos", "k_scales", "v_scales", "k", "v"),
     decode=("q", "k_pages", "v_pages", "block_table", "seq_lens", "scale", "kd", "vd", "k_scales",
-            "v_scales", "o", "lse", "workspace"))
+            "v_scales", "o", "lse", "workspace", "want_lse"))
 SLOW = dict(append=moda.moda_kv_append, gather=moda.moda_kv_gather, decode=moda.moda_decode_paged)
-EXTRA = dict(append=dict(want_k_out=False), gather={}, decode=dict(want_lse=False))
+OUTS = dict(append=("q_out", "k_out"), gather=("k", "v"), decode=("o", "lse"))
 
 
 def both(rec, ext, call, a):
@@ -136,10 +138,12 @@ def both(rec, ext, call, a):
     exception)."""
     rec.seen = None
     fast = getattr(ext, call)(*(a[n] for n in ORDER[call]))
-    assert (fast is None) == (rec.seen is None) and fast in (None, rec.status)
+    assert (fast is None) == (rec.seen is None)
+    if fast is not None:
+        assert len(fast) == 2 and all(x is a[n] or a[n] is None for x, n in zip(fast, OUTS[call]))
     fast, rec.seen = rec.seen, None
     try:
-        SLOW[call](**a, **EXTRA[call])
+        SLOW[call](**a)
         slow = rec.seen
     except Exception as e:  # noqa: BLE001 (the refusals' types are tested elsewhere)
         slow = e
@@ -200,8 +204,8 @@ def test_what_the_extension_takes_the_checks_take_alike(ways, call, mx4):
     took = 0
     for name, t in base.items():
         for x in (bad(t) if isinstance(t, torch.Tensor) else (None, 0, 1, 2.5, "x", True, bf(1), bf(2))):
-            if call == "decode" and name == "scale" and x is None:
-                continue
+            if x is None and name in OUTS[call] + ("workspace",):
+                continue  # made: see test_missing_outputs_are_made
             fast, slow = both(rec, ext, call, dict(base, **{name: x}))
             if fast is not None:
                 took += 1
@@ -221,14 +225,46 @@ def test_pairs_changed_together(ways, call):
 
 
 @pytest.mark.parametrize("call,mx4", CALLS)
+def test_missing_outputs_are_made(ways, call, mx4):
+    """Outputs and a workspace that are not given: as in the Python path but
+    for where they are."""
+    rec, ext = ways
+    want = dict(append="want_k_out", gather=None, decode="want_lse")[call]
+    full = arguments(call, mx4)
+    gone = OUTS[call] + (("workspace",) if call == "decode" else ())
+    for names in itertools.chain.from_iterable(itertools.combinations(gone, i) for i in range(1, len(gone) + 1)):
+        a = dict(full, **dict.fromkeys(names))
+        for wanted in (True, False) if want else (None,):
+            if want:
+                a[want] = wanted
+            rec.seen = None
+            fast = getattr(ext, call)(*(a[n] for n in ORDER[call]))
+            assert fast is not None and rec.seen is not None
+            seen, rec.seen = rec.seen, None
+            slow = SLOW[call](**a)
+            left_out = want and not wanted and OUTS[call][1] in names
+            for i, (x, y, n) in enumerate(zip(fast, slow, OUTS[call])):
+                if i == 1 and left_out:
+                    assert x is None and y is None
+                else:
+                    assert x.shape == y.shape and x.dtype == y.dtype and x.is_contiguous()
+                    assert (x is a[n]) == (y is a[n]) == (n not in names)
+                    assert x.data_ptr() in seen and y.data_ptr() in rec.seen
+            new = {t.data_ptr() for t in (*fast, *slow) if t is not None}
+            differ = [i for i, (x, y) in enumerate(zip(seen, rec.seen)) if x != y]
+            assert all(seen[i] in new or call == "decode" and i == len(seen) - 3 for i in differ)
+            if call == "decode":  # the workspace's size
+                assert seen[-2] == rec.seen[-2] == (WORKSPACE if "workspace" in names else 99 * 4)
+
+
+@pytest.mark.parametrize("call,mx4", CALLS)
 def test_the_binding_takes_the_extension_and_raises_its_status(ways, monkeypatch, call, mx4):
     rec, ext = ways
     monkeypatch.setattr(binding, "_paged", ext)
     a = arguments(call, mx4)
     monkeypatch.setattr(binding, "_paged_cache", None)  # the checks behind it are not reached
     out = SLOW[call](**a)
-    names = {"append": ("q_out", "k_out"), "gather": ("k", "v"), "decode": ("o", "lse")}[call]
-    assert all(x is a[n] for x, n in zip(out, names)) and rec.seen is not None
+    assert all(x is a[n] for x, n in zip(out, OUTS[call])) and rec.seen is not None
     rec.status = 3
     with pytest.raises(moda.ModaError, match="recorded"):
         SLOW[call](**a)
