@@ -493,8 +493,9 @@ MODA_API moda_status moda_kv_gather(const moda_paged_kv* cache, const int* seq, 
  * head's largest |q| counts for 2^-112 at least.)
  * Supported: G = Hq/Hk from 1 to 16, B*Hq <= 2^24, 0 <= L <= 1024, scale > 0
  * and at most 2e38.
- * The result depends on how the batch is split over the SMs only by the order
- * of fp32 sums; the same call on the same device gives the same bits.
+ * The result depends on how the batch is split over the SMs, for which
+ * max_pages counts, only by the order of fp32 sums; the same call on the same
+ * device gives the same bits.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA; TIMEOUT via
  * moda_get_device_error. B == 0 is a no-op.
  */

@@ -12,7 +12,8 @@
 // of a warp MMA's B tile; G > 8 takes two such tiles. Two CTAs an SM keep up to
 // 192 KB on the way. Measured (d = 128): 48 ragged sequences of up to 16384
 // rows, 803 MB, 121 us (99 % of the copy bandwidth); one context of 65536 rows
-// 27 us, of which its 134 MB take 20, the look-ups before them 3.5, the join 3.
+// 27 us, of which its 134 MB take 20, the look-ups before them 3.5, the join 3;
+// one of 701 rows, in clusters of eight, 4.5 us.
 #include "decode_paged.cuh"
 #include "tensor_map.h"
 
@@ -27,6 +28,7 @@ constexpr int kCols = 64;             // columns of O merged at a time
 template <int D>
 constexpr int kCost = D == 128 ? 1 : 2;  // entering and leaving a segment, in units
 constexpr int kCtasPerSm = 2;
+constexpr int kGroupUnits = 8, kClusterUnits = 3;  // see group_of
 constexpr float kSlack = 8.f;  // weights up to 2^8 lose nothing in bf16
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
@@ -98,7 +100,9 @@ __device__ __forceinline__ void tile_bf16(State<D, NT>& st, const uint32_t (&qb)
   }
 }
 
-template <int D, int NT>
+// GROUP: a short batch, whose segments have p.group CTAs each; else the batch's
+// line in equal shares.
+template <int D, int NT, bool GROUP>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
 decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const __grid_constant__ CUtensorMap tmKd, const __grid_constant__ CUtensorMap tmVd,
@@ -121,13 +125,23 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     sm103::fence_barrier_init();
   }
   wait_for_stream();
-  const Share<kKeys> sh = share_of<kKeys, kWarps, kCost<D>, 1>(p, depth_units, sm.share);
-  if (depth_units == 0) write_empty<D>(p);
-  if (sh.n == 0) {
-    if (tid == 0) wk.opened[blockIdx.x] = make_int2(-1, 0);
-    return;
+  Share<kKeys> sh;
+  if constexpr (GROUP) {
+    __syncthreads();
+    sh = share_of_segment<kKeys>(p, depth_units);
+    if (sh.at.n == 0) return write_empty_segment<D>(p, sh.at.b, sh.at.hk);
+  } else {
+    sh = share_of<kKeys, kWarps, kCost<D>, 1>(p, depth_units, sm.share);
+    if (depth_units == 0) write_empty<D>(p);
+    if (sh.n == 0) {
+      if (tid == 0) wk.opened[blockIdx.x] = make_int2(-1, 0);
+      return;
+    }
   }
   Place<kKeys> at = sh.at;
+  GroupSmem<D, kCW>& last = *reinterpret_cast<GroupSmem<D, kCW>*>(sm.ring);  // when the ring is free
+  static_assert(sizeof(GroupSmem<D, kCW>) <= sizeof(sm.ring));
+  const int64_t first_row = ((int64_t)at.b * p.Hk + at.hk) * p.G;
 
   if (warp == kCW) {
     // ------------------------------------------------------------ producer
@@ -197,6 +211,10 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         }
       atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_TIMEOUT);
     }
+    if constexpr (GROUP) {
+      __syncwarp();
+      if (p.group > 1) join_group<D, kCW>(p, last, first_row);
+    }
     return;
   }
 
@@ -208,7 +226,7 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
   int k = 0, left = sh.n;
   bool opened = false;
   long long seg_end = sh.end;
-  while (left > 0) {
+  while (GROUP || left > 0) {  // (a group's CTA leaves a state even if it has no unit)
     const int cnt = min(left, at.n - at.off);
     const int end = at.off + cnt;
     const bool cut_before = at.off > 0, cut_after = end < at.n;
@@ -249,13 +267,16 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         m1[i * 16 + r0 + 8] = x[3];
       }
     };
+    if constexpr (GROUP) {
+      leave<D, NT>(p, last.merge, st, p.group > 1, &last.o[0][0], &last.ml[0][0], 0, first_row, put);
+      break;
+    }
     const int slot = 2 * blockIdx.x + (cut_before ? 0 : 1);
     const int64_t row0 = ((int64_t)at.b * p.Hk + at.hk) * p.G;
     if (left == cnt)  // the last: the ring is free
-      leave<D, NT>(p, wk, *reinterpret_cast<MergeSmem<kCW, D>*>(sm.ring), st, cut_before || cut_after,
-                   slot, row0, put);
+      leave<D, NT>(p, last.merge, st, cut_before || cut_after, wk.o, wk.ml, slot, row0, put);
     else
-      leave<D, NT>(p, wk, sm.merge, st, cut_before || cut_after, slot, row0, put);
+      leave<D, NT>(p, sm.merge, st, cut_before || cut_after, wk.o, wk.ml, slot, row0, put);
     if (cut_after && !cut_before) {
       opened = true;
       if (tid == 0)
@@ -268,8 +289,11 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
       seg_end += kCost<D> + at.n;
     }
   }
+  if constexpr (GROUP) {
+    if (p.group > 1) join_group<D, kCW>(p, last, first_row);
+  }
   if (tid == 0) {
-    if (!opened) wk.opened[blockIdx.x] = make_int2(-1, 0);
+    if (!GROUP && !opened) wk.opened[blockIdx.x] = make_int2(-1, 0);
     if (sm.abort) atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_TIMEOUT);
   }
 }
@@ -451,13 +475,17 @@ cudaError_t launch(const DecodePagedArgs& a, cudaStream_t stream) {
     tvd = tv;
   }
   const size_t smem = sizeof(Smem<D>) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(decode_paged_split<D, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   int grid = a.num_sms * kCtasPerSm;
   grid = grid < kMaxCtas ? grid : kMaxCtas;
-  e = launch_dependent(decode_paged_split<D, NT>, dim3(grid), kWarps * 32, smem, stream, tk, tv, tkd, tvd,
-                       params_of(a), box);
+  const int max_units = (a.L + kKeys - 1) / kKeys + (c.max_pages * c.page_size + kKeys - 1) / kKeys;
+  const int group = group_of(a, max_units, grid, kGroupUnits, kClusterUnits);
+  const auto kernel = group ? decode_paged_split<D, NT, true> : decode_paged_split<D, NT, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  if (group)
+    return launch_dependent_clusters(kernel, dim3(c.B * c.Hk * group), group, kWarps * 32, smem, stream, tk, tv,
+                                     tkd, tvd, params_of(a, group), box);
+  e = launch_dependent(kernel, dim3(grid), kWarps * 32, smem, stream, tk, tv, tkd, tvd, params_of(a, 0), box);
   return e != cudaSuccess ? e : launch_join(a, grid, stream);
 }
 

@@ -10,6 +10,10 @@
 // head) are a segment. A segment inside one CTA's share is written out there;
 // one that is cut leaves a partial state (m, l, unnormalised o) per CTA, and a
 // dependent kernel joins them.
+//
+// A short batch needs none of that: each segment gets a group of 1 to 8 CTAs, a
+// cluster, which looks up nothing but its own length and joins its partials
+// from shared memory to shared memory, in one launch (group_of).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -53,11 +57,12 @@ struct Params {
   float* lse;
   float* work;
   unsigned int* err;
+  int group;  // CTAs of a segment; 0: shares of the line
 };
-inline Params params_of(const DecodePagedArgs& a) {
+inline Params params_of(const DecodePagedArgs& a, int group) {
   const PagedKv& c = a.c;
   return {(const __nv_bfloat16*)a.q, a.seq_lens, c.table, c.num_pages, __builtin_ctz((unsigned)c.page_size),
-          c.max_pages, c.B, c.Hk, a.G, a.L, a.scale * kLog2e, (__nv_bfloat16*)a.o, a.lse, a.work, c.err};
+          c.max_pages, c.B, c.Hk, a.G, a.L, a.scale * kLog2e, (__nv_bfloat16*)a.o, a.lse, a.work, c.err, group};
 }
 
 // Sequence b's rows, within what its table can name.
@@ -221,6 +226,23 @@ __device__ __forceinline__ Share<KEYS> share_of(const Params& p, int depth_units
   return s;
 }
 
+// Short batches: `group` CTAs, a cluster, for each segment, and this one's part
+// of its units (perhaps none; at.n == 0 when the segment has none).
+template <int KEYS>
+__device__ __forceinline__ Share<KEYS> share_of_segment(const Params& p, int depth_units) {
+  const int segment = blockIdx.x / p.group, rank = blockIdx.x - segment * p.group;
+  Share<KEYS> s;
+  s.at.b = segment / p.Hk;
+  s.at.hk = segment - s.at.b * p.Hk;
+  s.at.enter(p, depth_units);
+  const int raw = p.lens[s.at.b];
+  if (rank == 0 && s.at.hk == 0 && threadIdx.x == 0 && (raw < 0 || raw > p.max_pages << p.page_shift))
+    atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
+  s.at.off = s.at.n * rank / p.group;
+  s.n = s.at.n * (rank + 1) / p.group - s.at.off;
+  return s;
+}
+
 // o = 0 and lse = -infinity for the sequences with nothing to attend to.
 template <int D>
 __device__ __forceinline__ void write_empty(const Params& p) {
@@ -232,6 +254,17 @@ __device__ __forceinline__ void write_empty(const Params& p) {
     if (p.lse)
       for (int i = threadIdx.x; i < Hq; i += blockDim.x) p.lse[(int64_t)b * Hq + i] = -INFINITY;
   }
+}
+
+// The same for one segment, by the first CTA of its group.
+template <int D>
+__device__ __forceinline__ void write_empty_segment(const Params& p, int b, int hk) {
+  if (blockIdx.x % p.group != 0) return;
+  const int64_t row = ((int64_t)b * p.Hk + hk) * p.G;
+  uint32_t* o = reinterpret_cast<uint32_t*>(p.o + row * D);
+  for (int i = threadIdx.x; i < p.G * D / 2; i += blockDim.x) o[i] = 0u;
+  if (p.lse)
+    for (int i = threadIdx.x; i < p.G; i += blockDim.x) p.lse[row + i] = -INFINITY;
 }
 
 // Byte offset of (row, col) in a bf16 tile of ROWS rows: 64-column boxes,
@@ -337,13 +370,14 @@ struct MergeSmem {
 };
 
 // The state of WARPS warps (threads 0 .. 32 * WARPS - 1, which meet at named
-// barrier 1) as the segment's result, or as a partial in `slot` when the
-// segment is cut. put(m0, m1, t, part, sm) stores the warp's columns COLS * part
+// barrier 1) as the segment's result, or where the segment is cut as a partial
+// in part_o [slot][G][D] and part_ml [slot][G][2]. put(m0, m1, t, part, sm) stores the warp's columns COLS * part
 // .. of tile t for its heads 2c and 2c + 1. row0: the segment's first row of
 // o and lse.
 template <int D, int NT, int WARPS, int COLS, class Put>
-__device__ __forceinline__ void leave(const Params& p, const Work& wk, MergeSmem<WARPS, COLS>& sm,
-                                      State<D, NT>& st, bool cut, int slot, int64_t row0, Put put) {
+__device__ __forceinline__ void leave(const Params& p, MergeSmem<WARPS, COLS>& sm, State<D, NT>& st,
+                                      bool cut, float* part_o, float* part_ml, int64_t slot, int64_t row0,
+                                      Put put) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane & 3;
   auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory"); };
 #pragma unroll
@@ -388,10 +422,11 @@ __device__ __forceinline__ void leave(const Params& p, const Work& wk, MergeSmem
         }
         const int g = t * 8 + h, col = part * COLS + d;
         if (cut) {
-          *reinterpret_cast<float4*>(wk.o + ((int64_t)slot * p.G + g) * D + col) = acc;
+          const int64_t r = slot * p.G + g;
+          *reinterpret_cast<float4*>(part_o + r * D + col) = acc;
           if (col == 0) {
-            wk.ml[((int64_t)slot * p.G + g) * 2] = M;
-            wk.ml[((int64_t)slot * p.G + g) * 2 + 1] = L;
+            part_ml[r * 2] = M;
+            part_ml[r * 2 + 1] = L;
           }
         } else {
           const float inv = 1.f / L;
@@ -406,6 +441,67 @@ __device__ __forceinline__ void leave(const Params& p, const Work& wk, MergeSmem
   }
 }
 
+// What the CTAs of a group leave in their shared memory, and the merge of the
+// warps before it.
+template <int D, int WARPS>
+struct GroupSmem {
+  MergeSmem<WARPS, D> merge;
+  float o[16][D];
+  float ml[16][2];
+};
+
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t smem, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem), "r"(rank));
+  return a;
+}
+
+// The segment's result from the partials of its group, each CTA some columns of
+// it. All threads of all the group's CTAs call it.
+template <int D, int WARPS>
+__device__ __forceinline__ void join_group(const Params& p, const GroupSmem<D, WARPS>& sm, int64_t row0) {
+  cluster_meet();
+  const int rank = blockIdx.x % p.group;
+  for (int i = rank * blockDim.x + threadIdx.x; i < p.G * (D / 4); i += p.group * blockDim.x) {
+    const int g = i / (D / 4), col = i % (D / 4) * 4;
+    const uint32_t at_o = sm103::smem_u32(&sm.o[g][col]), at_ml = sm103::smem_u32(&sm.ml[g][0]);
+    float m[8], l[8];
+    float4 o[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+      o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < p.group) {
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                     : "=f"(m[r]), "=f"(l[r]) : "r"(cluster_addr(at_ml, r)) : "memory");
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(o[r].x), "=f"(o[r].y), "=f"(o[r].z), "=f"(o[r].w)
+                     : "r"(cluster_addr(at_o, r)) : "memory");
+      }
+    }
+    float M = m[0], L = 0.f;
+#pragma unroll
+    for (int r = 1; r < 8; ++r) M = fmaxf(M, m[r]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const float a = m[r] == -INFINITY ? 1.f : sm103::ex2_approx(m[r] - M);  // as in leave
+      L = fmaf(a, l[r], L);
+      acc.x = fmaf(a, o[r].x, acc.x); acc.y = fmaf(a, o[r].y, acc.y);
+      acc.z = fmaf(a, o[r].z, acc.z); acc.w = fmaf(a, o[r].w, acc.w);
+    }
+    const float inv = 1.f / L;
+    *reinterpret_cast<uint2*>(p.o + (row0 + g) * D + col) = make_uint2(
+        wmma16::pack_bf16(acc.x * inv, acc.y * inv), wmma16::pack_bf16(acc.z * inv, acc.w * inv));
+    if (col == 0 && p.lse) p.lse[row0 + g] = (M + log2f(L)) * kLn2;
+  }
+  cluster_meet();  // the others' shared memory stays until it has been read
+}
+
 // Every kernel of the paged cache starts as a programmatic dependent: its
 // launch overlaps the end of the kernel before it in the stream, and it waits
 // here, before it touches global memory, until that one has completed. (So
@@ -416,20 +512,55 @@ __device__ __forceinline__ void wait_for_stream() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 template <class... P, class... A>
-cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
-                             cudaStream_t stream, A&&... args) {
+cudaError_t launch_dependent_clusters(void (*kernel)(P...), dim3 grid, int cluster, int threads,
+                                      size_t smem, cudaStream_t stream, A&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                             A&&... args) {
+  return launch_dependent_clusters(kernel, grid, 1, threads, smem, stream, static_cast<A&&>(args)...);
+}
+
+// CTAs for each segment of a short batch: a group, where no segment can have
+// more than `most` units for each; 0 where the batch is better cut into equal
+// shares. What the host knows of the lengths is the table's width. Measured
+// (GPU time; one sequence, then eight, of eight KV heads, and 32 of eight):
+//   bf16, d = 128, most = 8     700 rows  4.6 us a group, 6.1 shares
+//                               2000      6.1             7.2
+//                               4000      7.9             8.0
+//                        8 x 1..1000      6.5             8.3
+//                        8 x 1..4000     13.7            12.6
+//                        32 x 1..256      5.6             9.6
+//   4-bit, d = 128, most = 24   700 rows  5.1             7.4
+//                               4000      7.3             7.9
+//                        8 x 1..2000      9.0            11.5
+//                        8 x 1..4000     13.8            13.5
+//                       32 x 1..1000     13.7            16.6
+// The more CTAs the better, as long as all clusters fit the SMs at once (8 or 4
+// CTAs at 15/16 of the places did not: 6.5 -> 10 us), unless a cluster costs
+// more than it saves: as much as `cluster_units` units of one CTA take.
+inline int group_of(const DecodePagedArgs& a, int max_units, int resident, int most, int cluster_units) {
+  const int64_t segments = (int64_t)a.c.B * a.c.Hk;
+  int group = 8;
+  while (group > 1 && segments * group > resident / 8 * 7) group /= 2;
+  if ((int64_t)max_units * (group - 1) <= cluster_units * group) group = 1;
+  return segments * group <= resident && max_units <= most * group ? group : 0;
 }
 
 cudaError_t launch_join(const DecodePagedArgs& a, int shares, cudaStream_t stream);

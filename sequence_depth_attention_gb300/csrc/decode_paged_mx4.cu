@@ -14,7 +14,8 @@
 //     per block of 32 columns.
 // Measured (d = 128): 64 ragged sequences of up to 32768 rows at G = 8, 584 MB,
 // 123 us, issue 73 % and the ALU 61 % busy in the loop; the same rows in TMA
-// boxes with a producer warp and four codes to a load took 226.
+// boxes with a producer warp and four codes to a load took 226. 16 sequences of
+// up to 999 rows (d = 64, 8 KV heads, G = 8), in clusters of two, 8.0 us.
 // Each warp streams units of its own (32 rows, or 16 depth slots) through its
 // own ring of shared-memory stages by asynchronous copies: no barrier between
 // warps but at the end of a segment.
@@ -37,6 +38,7 @@ constexpr int kCost = D == 128 ? 6 : 10;
 // 168 registers (two head tiles: 255): four at 128 registers were 6 % slower
 template <int NT>
 constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
+constexpr int kGroupUnits = 24, kClusterUnits = 8;  // see group_of
 
 // A stage: codes of K and of V (or kDepthKeys bf16 rows of one of the two),
 // then their scales.
@@ -531,7 +533,9 @@ struct Feed {
   }
 };
 
-template <int D, int NT>
+// GROUP: a short batch, whose segments have p.group CTAs each; else the batch's
+// line in equal shares.
+template <int D, int NT, bool GROUP>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<NT>)
 decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__ Mx4Pages pg) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -541,11 +545,17 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
   const Work wk = work_of(p.work, p.G, D);
 
   wait_for_stream();
-  const Share<kKeys> sh = share_of<kKeys, kWarps, kCost<D>, kWarps>(p, depth_units, sm.share);
-  if (depth_units == 0) write_empty<D>(p);
-  if (sh.n == 0) {
-    if (tid == 0) wk.opened[blockIdx.x] = make_int2(-1, 0);
-    return;
+  Share<kKeys> sh;
+  if constexpr (GROUP) {
+    sh = share_of_segment<kKeys>(p, depth_units);
+    if (sh.at.n == 0) return write_empty_segment<D>(p, sh.at.b, sh.at.hk);
+  } else {
+    sh = share_of<kKeys, kWarps, kCost<D>, kWarps>(p, depth_units, sm.share);
+    if (depth_units == 0) write_empty<D>(p);
+    if (sh.n == 0) {
+      if (tid == 0) wk.opened[blockIdx.x] = make_int2(-1, 0);
+      return;
+    }
   }
   const uint32_t ring = sm103::smem_u32(&sm.ring[warp][0][0]);
   constexpr uint32_t kRing = kNS * Stage<D>::kBytes;
@@ -571,12 +581,15 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
   };
 
   Place<kKeys> at = sh.at;
+  GroupSmem<D, kWarps>& last = *reinterpret_cast<GroupSmem<D, kWarps>*>(sm.ring);  // when the rings are free
+  static_assert(sizeof(GroupSmem<D, kWarps>) <= sizeof(sm.ring));
+  const int64_t first_row = ((int64_t)at.b * p.Hk + at.hk) * p.G;
   State<D, NT> st;
   int left = sh.n;
   int turn = 0;  // the warp that takes the unit at `at`
   bool opened = false;
   long long seg_end = sh.end;
-  while (left > 0) {
+  while (GROUP || left > 0) {  // (a group's CTA leaves a state even if it has no unit)
     const int cnt = min(left, at.n - at.off);
     const int end = at.off + cnt;
     const bool cut_before = at.off > 0, cut_after = end < at.n;
@@ -619,13 +632,17 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
         *reinterpret_cast<float2*>(m1 + d + 16) = make_float2(x[3], y[3]);
       }
     };
+    if constexpr (GROUP) {
+      leave<D, NT>(p, last.merge, st, p.group > 1, &last.o[0][0], &last.ml[0][0], 0, first_row, put);
+      if (p.group > 1) join_group<D, kWarps>(p, last, first_row);
+      return;
+    }
     const int slot = 2 * blockIdx.x + (cut_before ? 0 : 1);
     const int64_t row0 = ((int64_t)at.b * p.Hk + at.hk) * p.G;
     if (left == cnt)  // the last: the rings are free
-      leave<D, NT>(p, wk, *reinterpret_cast<MergeSmem<kWarps, D>*>(sm.ring), st, cut_before || cut_after,
-                   slot, row0, put);
+      leave<D, NT>(p, last.merge, st, cut_before || cut_after, wk.o, wk.ml, slot, row0, put);
     else
-      leave<D, NT>(p, wk, sm.merge, st, cut_before || cut_after, slot, row0, put);
+      leave<D, NT>(p, sm.merge, st, cut_before || cut_after, wk.o, wk.ml, slot, row0, put);
     if (cut_after && !cut_before) {
       opened = true;
       if (tid == 0)
@@ -650,13 +667,19 @@ cudaError_t launch(const DecodePagedArgs& a, cudaStream_t stream) {
                     (const uint8_t*)a.kd,      (const uint8_t*)a.vd,
                     a.depth_b_stride * 2,      a.depth_hk_stride * 2,
                     a.depth_slot_stride * 2};
-  cudaError_t e = cudaFuncSetAttribute(decode_paged_mx4_split<D, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>));
-  if (e != cudaSuccess) return e;
   int grid = a.num_sms * kCtasPerSm<NT>;
   grid = grid < kMaxCtas ? grid : kMaxCtas;
-  e = launch_dependent(decode_paged_mx4_split<D, NT>, dim3(grid), kWarps * 32, sizeof(Smem<D>), stream,
-                       params_of(a), pg);
+  const int max_units =
+      (a.L + kDepthKeys - 1) / kDepthKeys + (c.max_pages * c.page_size + kKeys - 1) / kKeys;
+  const int group = group_of(a, max_units, grid, kGroupUnits, kClusterUnits);
+  const auto kernel = group ? decode_paged_mx4_split<D, NT, true> : decode_paged_mx4_split<D, NT, false>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>));
+  if (e != cudaSuccess) return e;
+  if (group)
+    return launch_dependent_clusters(kernel, dim3(c.B * c.Hk * group), group, kWarps * 32, sizeof(Smem<D>),
+                                     stream, params_of(a, group), pg);
+  e = launch_dependent(kernel, dim3(grid), kWarps * 32, sizeof(Smem<D>), stream, params_of(a, 0), pg);
   return e != cudaSuccess ? e : launch_join(a, grid, stream);
 }
 

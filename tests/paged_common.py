@@ -17,12 +17,15 @@ class Cache:
     lens: rows of each sequence that must have pages. fill: what every row
     that no sequence owns holds ("nan": NaN, and scale bytes of NaN)."""
 
+    least_rows = 0  # columns of the table for as many rows at least
+
     def __init__(self, fmt, lens, Hk, d, page, seed=0, width=None, spare=2, fill="nan", device="cpu"):
         g = torch.Generator().manual_seed(seed)
         self.fmt, self.Hk, self.d, self.page, self.lens = fmt, Hk, d, page, list(lens)
         held = [-(-n // page) for n in lens]
         self.num_pages = sum(held) + spare
-        self.max_pages = max(1, max(held, default=0)) if width is None else width
+        self.max_pages = (max(1, max(held, default=0), -(-self.least_rows // page)) if width is None
+                          else width)
         order = torch.randperm(self.num_pages, generator=g).to(torch.int32)
         # entries past a sequence's end name no page at all
         self.table = torch.full((len(lens), self.max_pages), -7, dtype=torch.int32)

@@ -254,6 +254,15 @@ def check_decode(c, q, lens, kd, vd, scale, o, lse):
     assert (same | ((lse.double() - rl).abs() <= tl)).all()
 
 
+@pytest.fixture(params=[0, 16384], ids=["narrow", "wide"])
+def table_of(request, monkeypatch):
+    """Block tables just wide enough for the longest sequence (short batches then
+    get a group of CTAs for each segment), and wide ones (the batch is cut into
+    equal shares)."""
+    monkeypatch.setattr(pc.Cache, "least_rows", request.param)
+    return request.param
+
+
 RAGGED = [0, 1, 15, 16, 17, 63, 64, 65, 127, 128, 129, 1000]
 DECODES = [
     # d, page, Hk, G, L, lens
@@ -268,12 +277,17 @@ DECODES = [
     (128, 64, 1, 2, 0, [0]),
     (128, 64, 2, 2, 5, [0, 0]),
     (128, 16, 8, 4, 24, [2000, 1, 600] + [77] * 60),
+    # narrow tables: four, two, one and one CTAs a segment
+    (128, 16, 4, 4, 24, RAGGED),
+    (64, 32, 4, 7, 0, RAGGED + RAGGED + [2, 3]),
+    (128, 64, 4, 2, 9, [500, 0, 1, 64, 65] * 10),
+    (64, 16, 4, 4, 0, [33, 0, 64]),
 ]
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "mx4"])
 @pytest.mark.parametrize("case", DECODES, ids=lambda c: "-".join(map(str, c[:5])) + f"-B{len(c[5])}")
-def test_decode(fmt, case):
+def test_decode(fmt, case, table_of):
     d, page, Hk, G, L, lens = case
     B = len(lens)
     c = pc.Cache(fmt, lens, Hk, d, page, seed=11, device="cuda")
@@ -292,7 +306,7 @@ def test_decode(fmt, case):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "mx4"])
-def test_decode_depth_views(fmt):
+def test_decode_depth_views(fmt, table_of):
     """The depth slots in place in layer-major tensors [L, B, Hk, d], and with gaps."""
     d, Hk, L, lens = 128, 2, 7, [40, 0, 100]
     c = pc.Cache(fmt, lens, Hk, d, 16, seed=14, device="cuda")
@@ -309,7 +323,7 @@ def test_decode_depth_views(fmt):
 
 @pytest.mark.parametrize("fmt", ["bf16", "mx4"])
 @pytest.mark.parametrize("mul", [1e-3, 30.0])
-def test_decode_flat_and_peaked(fmt, mul):
+def test_decode_flat_and_peaked(fmt, mul, table_of):
     """Scores from all alike to one key taking all the weight."""
     d, Hk, lens = 128, 2, [900, 64, 3]
     c = pc.Cache(fmt, lens, Hk, d, 32, seed=17, device="cuda")
@@ -321,7 +335,7 @@ def test_decode_flat_and_peaked(fmt, mul):
     check_decode(c, q, lens, kd, vd, d ** -0.5, o, lse)
 
 
-def test_decode_mx4_scales_far_apart():
+def test_decode_mx4_scales_far_apart(table_of):
     """Key and value blocks of very different magnitudes: rows whose values are
     2^40 larger have next to no weight, and queries far from 1. The others'
     part must not be lost beside them."""
@@ -350,7 +364,7 @@ def test_decode_mx4_scales_far_apart():
         check_decode(c, qq, lens, None, None, scale, o, lse)
 
 
-def test_decode_mx4_nan_block():
+def test_decode_mx4_nan_block(table_of):
     """A block stored as NaN makes its head's columns NaN; the other heads are untouched."""
     d, Hk, lens = 64, 2, [50]
     c = pc.Cache("mx4", lens, Hk, d, 16, seed=22, device="cuda")
@@ -429,7 +443,7 @@ def test_offsets_past_32_bits(fmt):
 
 # -------------------------------------------------------- streams and graphs
 @pytest.mark.parametrize("fmt", ["bf16", "mx4"])
-def test_decode_on_streams_and_in_graphs(fmt):
+def test_decode_on_streams_and_in_graphs(fmt, table_of):
     """Two calls at once with a workspace each; a captured step (append and
     decode) replayed on new inputs; two graphs that share a workspace, in turn."""
     d, Hk, lens = 128, 4, [3000, 700, 1, 64]
@@ -498,7 +512,7 @@ def test_decode_on_streams_and_in_graphs(fmt):
 
 # ------------------------------------------------------------- all together
 @pytest.mark.parametrize("fmt", ["bf16", "mx4"])
-def test_prompt_then_steps(fmt):
+def test_prompt_then_steps(fmt, table_of):
     """Two requests: prompts through moda_kv_append and moda_fwd_layer_major,
     the keys' depth slots through what k_out gives, then single tokens through
     append and decode_paged; every row against one fp64 pass over the whole
@@ -708,7 +722,7 @@ def test_what_a_call_allocates_belongs_to_its_stream(fmt, monkeypatch):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "mx4"])
-def test_captured_among_copies_and_other_streams(fmt):
+def test_captured_among_copies_and_other_streams(fmt, table_of):
     """A step captured where what comes before each call is not a kernel (a
     copy, a fill) or is two streams that meet; replayed on new inputs."""
     d, Hk, lens = 64, 2, [130, 17, 1]
@@ -762,7 +776,7 @@ def test_captured_among_copies_and_other_streams(fmt):
 
 
 @pytest.mark.parametrize("G", [1, 8, 16])
-def test_depth_slots_weigh_in_two_parts_over_4_bit_pages(G):
+def test_depth_slots_weigh_in_two_parts_over_4_bit_pages(G, table_of):
     """Where the depth slots hold nearly all of the weight, o is right to its
     own rounding and the sums' (pc.decode_reference without the rounding of a
     probability: two bf16 parts leave 2^-16 of it)."""
@@ -782,3 +796,33 @@ def test_depth_slots_weigh_in_two_parts_over_4_bit_pages(G):
     # a = sum p |v| = o up to the rows' 2^-31: take HALF_BF16 of it off twice, give 2^-16 twice
     tight = tol - 2 * (pc.HALF_BF16 - 2.0 ** -16) * want.abs() + 2.0 ** -30
     assert ((o.double() - want).abs() <= tight).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mx4"])
+def test_bad_lengths_and_pages_of_many(fmt):
+    """test_decode_bad_lengths_and_pages with as many sequences as are cut into
+    shares however narrow the table is, and one at a time."""
+    d, Hk, lens, many = 64, 2, [40, 64, 20], 110
+    c = pc.Cache(fmt, lens, Hk, d, 16, seed=24, fill=None, width=4, device="cuda")
+    c.table[0, 3] = c.table[0, 0]
+    q = torch.randn(3, 4, d, generator=torch.Generator().manual_seed(25)).bfloat16().cuda()
+    n = torch.tensor([40, 1000, -3], dtype=torch.int32, device="cuda")
+    ro, rl, to, tl = pc.decode_reference(c, q, [40, 64, 0], None, None, 0.125)
+    o, lse = moda.moda_decode_paged(q.repeat(many, 1, 1), c.k, c.v, c.table.repeat(many, 1), n.repeat(many),
+                                    0.125, **c.scales())
+    settled(INVALID)
+    assert ((o.double() - ro.repeat(many, 1, 1)).abs() <= to.repeat(many, 1, 1)).all()
+    assert (o.view(many, 3, 4, d)[:, 2] == 0).all() and (lse.view(many, 3, 4)[:, 2] == -math.inf).all()
+    for b, bad in ((0, False), (1, True), (2, True)):
+        o, lse = moda.moda_decode_paged(q[b : b + 1], c.k, c.v, c.table[b : b + 1], n[b : b + 1], 0.125, **c.scales())
+        settled(INVALID if bad else 0)
+        assert ((o.double() - ro[b]).abs() <= to[b]).all()
+        assert b != 2 or (o == 0).all() and (lse == -math.inf).all()
+    table = c.table.repeat(many, 1)
+    table[1::3, 2] = c.num_pages
+    lens = torch.tensor(lens, dtype=torch.int32, device="cuda").repeat(many)
+    o, _ = moda.moda_decode_paged(q.repeat(many, 1, 1), c.k, c.v, table, lens, 0.125, **c.scales())
+    settled(INVALID)
+    ro, _, to, _ = pc.decode_reference(c, q, [40, 64, 20], None, None, 0.125)
+    ok = ((o.double() - ro.repeat(many, 1, 1)).abs() <= to.repeat(many, 1, 1)).view(many, 3, -1).all(-1)
+    assert ok[:, 0].all() and ok[:, 2].all()
