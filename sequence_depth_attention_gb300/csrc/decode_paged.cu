@@ -298,29 +298,6 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
   }
 }
 
-// U partial states (m, l, o) added to the state (M, L, acc). An empty one is
-// (-infinity, 0, 0); one that has met only NaN scores has -infinity too, and
-// its NaN must go on.
-template <int U, int E>
-__device__ __forceinline__ void add_partials(float& M, float& L, float (&acc)[E], const float (&pm)[U],
-                                             const float (&pl)[U], const float (&po)[U][E]) {
-  float Mn = M;
-#pragma unroll
-  for (int u = 0; u < U; ++u) Mn = fmaxf(Mn, pm[u]);
-  const float a = M == -INFINITY ? 1.f : sm103::ex2_approx(M - Mn);
-  M = Mn;
-  L *= a;
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] *= a;
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const float b = pm[u] == -INFINITY ? 1.f : sm103::ex2_approx(pm[u] - M);
-    L = fmaf(b, pl[u], L);
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(b, po[u][e], acc[e]);
-  }
-}
-
 // Joining the partials, where segments have few of them: a warp for each split
 // CTA (the segment that it opened) and head, all of its partials' loads in
 // flight at once, a lane D/32 columns. Few small CTAs, because they have to be
@@ -482,6 +459,10 @@ cudaError_t launch(const DecodePagedArgs& a, cudaStream_t stream) {
   const auto kernel = group ? decode_paged_split<D, NT, true> : decode_paged_split<D, NT, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
+  if (group > 8) {  // beyond the portable size
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   if (group)
     return launch_dependent_clusters(kernel, dim3(c.B * c.Hk * group), group, kWarps * 32, smem, stream, tk, tv,
                                      tkd, tvd, params_of(a, group), box);

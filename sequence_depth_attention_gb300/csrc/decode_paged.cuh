@@ -11,7 +11,7 @@
 // one that is cut leaves a partial state (m, l, unnormalised o) per CTA, and a
 // dependent kernel joins them.
 //
-// A short batch needs none of that: each segment gets a group of 1 to 8 CTAs, a
+// A short batch needs none of that: each segment gets a group of 1 to 16 CTAs, a
 // cluster, which looks up nothing but its own length and joins its partials
 // from shared memory to shared memory, in one launch (group_of).
 #pragma once
@@ -450,6 +450,29 @@ struct GroupSmem {
   float ml[16][2];
 };
 
+// U partial states (m, l, o) added to the state (M, L, acc). An empty one is
+// (-infinity, 0, 0); one that has met only NaN scores has -infinity too, and
+// its NaN must go on.
+template <int U, int E>
+__device__ __forceinline__ void add_partials(float& M, float& L, float (&acc)[E], const float (&pm)[U],
+                                             const float (&pl)[U], const float (&po)[U][E]) {
+  float Mn = M;
+#pragma unroll
+  for (int u = 0; u < U; ++u) Mn = fmaxf(Mn, pm[u]);
+  const float a = M == -INFINITY ? 1.f : sm103::ex2_approx(M - Mn);
+  M = Mn;
+  L *= a;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] *= a;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float b = pm[u] == -INFINITY ? 1.f : sm103::ex2_approx(pm[u] - M);
+    L = fmaf(b, pl[u], L);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(b, po[u][e], acc[e]);
+  }
+}
+
 __device__ __forceinline__ void cluster_meet() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -468,35 +491,28 @@ __device__ __forceinline__ void join_group(const Params& p, const GroupSmem<D, W
   for (int i = rank * blockDim.x + threadIdx.x; i < p.G * (D / 4); i += p.group * blockDim.x) {
     const int g = i / (D / 4), col = i % (D / 4) * 4;
     const uint32_t at_o = sm103::smem_u32(&sm.o[g][col]), at_ml = sm103::smem_u32(&sm.ml[g][0]);
-    float m[8], l[8];
-    float4 o[8];
+    float M = -INFINITY, L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    auto add_eight = [&](int r0) {
+      float m[8], l[8], o[8][4];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      m[r] = -INFINITY;
-      l[r] = 0.f;
-      o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < p.group) {
-        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-                     : "=f"(m[r]), "=f"(l[r]) : "r"(cluster_addr(at_ml, r)) : "memory");
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(o[r].x), "=f"(o[r].y), "=f"(o[r].z), "=f"(o[r].w)
-                     : "r"(cluster_addr(at_o, r)) : "memory");
+      for (int u = 0; u < 8; ++u) {
+        m[u] = -INFINITY;
+        l[u] = o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
+        if (r0 + u < p.group) {
+          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                       : "=f"(m[u]), "=f"(l[u]) : "r"(cluster_addr(at_ml, r0 + u)) : "memory");
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(o[u][0]), "=f"(o[u][1]), "=f"(o[u][2]), "=f"(o[u][3])
+                       : "r"(cluster_addr(at_o, r0 + u)) : "memory");
+        }
       }
-    }
-    float M = m[0], L = 0.f;
-#pragma unroll
-    for (int r = 1; r < 8; ++r) M = fmaxf(M, m[r]);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const float a = m[r] == -INFINITY ? 1.f : sm103::ex2_approx(m[r] - M);  // as in leave
-      L = fmaf(a, l[r], L);
-      acc.x = fmaf(a, o[r].x, acc.x); acc.y = fmaf(a, o[r].y, acc.y);
-      acc.z = fmaf(a, o[r].z, acc.z); acc.w = fmaf(a, o[r].w, acc.w);
-    }
+      add_partials<8, 4>(M, L, acc, m, l, o);
+    };
+    add_eight(0);
+    if (p.group > 8) add_eight(8);
     const float inv = 1.f / L;
     *reinterpret_cast<uint2*>(p.o + (row0 + g) * D + col) = make_uint2(
-        wmma16::pack_bf16(acc.x * inv, acc.y * inv), wmma16::pack_bf16(acc.z * inv, acc.w * inv));
+        wmma16::pack_bf16(acc[0] * inv, acc[1] * inv), wmma16::pack_bf16(acc[2] * inv, acc[3] * inv));
     if (col == 0 && p.lse) p.lse[row0 + g] = (M + log2f(L)) * kLn2;
   }
   cluster_meet();  // the others' shared memory stays until it has been read
@@ -538,25 +554,26 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_
 }
 
 // CTAs for each segment of a short batch: a group, where no segment can have
-// more than `most` units for each; 0 where the batch is better cut into equal
-// shares. What the host knows of the lengths is the table's width. Measured
-// (GPU time; one sequence, then eight, of eight KV heads, and 32 of eight):
-//   bf16, d = 128, most = 8     700 rows  4.6 us a group, 6.1 shares
-//                               2000      6.1             7.2
-//                               4000      7.9             8.0
-//                        8 x 1..1000      6.5             8.3
-//                        8 x 1..4000     13.7            12.6
-//                        32 x 1..256      5.6             9.6
-//   4-bit, d = 128, most = 24   700 rows  5.1             7.4
-//                               4000      7.3             7.9
-//                        8 x 1..2000      9.0            11.5
-//                        8 x 1..4000     13.8            13.5
-//                       32 x 1..1000     13.7            16.6
-// The more CTAs the better, as long as all clusters fit the SMs at once (8 or 4
-// CTAs at 15/16 of the places did not: 6.5 -> 10 us), unless a cluster costs
-// more than it saves: as much as `cluster_units` units of one CTA take.
+// more than `most` units for each (of 16: 3/4 of that); 0 where the batch is
+// better cut into equal shares. What the host knows of the lengths is the
+// table's width. Measured, GPU time in us, d = 128, G = 4:
+//   sequences x KV heads    rows      bf16 (most = 8)        4-bit (most = 21)
+//                                     group      shares      group      shares
+//         1 x 8           700          4.6 (8)     6.1        5.1 (8)     7.4
+//         1 x 8          2000          5.6 (8)     7.3        5.9 (8)     7.5
+//         1 x 4          4000          6.2 (16)    7.2        6.3 (16)    7.5
+//         1 x 4          8000          8.4 (16)    8.2        7.7 (16)    8.4
+//         8 x 8     1 .. 1000          6.5 (4)     8.3        7.3 (4)    10.3
+//         8 x 8     1 .. 4000         13.7 (4)    12.6       13.8 (4)    13.5
+//        32 x 8     1 ..  256          5.6 (1)     9.6        7.9 (1)    12.5
+//        32 x 8     1 .. 1000         12.8 (1)    12.1       13.7 (1)    16.6
+// More CTAs are better as long as all clusters fit the SMs at once (8 or 4 at
+// 15/16 of the places did not: 6.5 -> 10), 16 where 8 would have many units each
+// and there is an SM for each CTA. A cluster costs as much as `cluster_units`
+// units of one CTA take; where it saves less, one CTA has the segment.
 inline int group_of(const DecodePagedArgs& a, int max_units, int resident, int most, int cluster_units) {
   const int64_t segments = (int64_t)a.c.B * a.c.Hk;
+  if (segments * 16 <= a.num_sms && max_units > most * 4) return max_units <= most * 12 ? 16 : 0;
   int group = 8;
   while (group > 1 && segments * group > resident / 8 * 7) group /= 2;
   if ((int64_t)max_units * (group - 1) <= cluster_units * group) group = 1;

@@ -38,7 +38,7 @@ constexpr int kCost = D == 128 ? 6 : 10;
 // 168 registers (two head tiles: 255): four at 128 registers were 6 % slower
 template <int NT>
 constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
-constexpr int kGroupUnits = 24, kClusterUnits = 8;  // see group_of
+constexpr int kGroupUnits = 21, kClusterUnits = 8;  // see group_of
 
 // A stage: codes of K and of V (or kDepthKeys bf16 rows of one of the two),
 // then their scales.
@@ -676,6 +676,10 @@ cudaError_t launch(const DecodePagedArgs& a, cudaStream_t stream) {
   cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>));
   if (e != cudaSuccess) return e;
+  if (group > 8) {  // beyond the portable size
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   if (group)
     return launch_dependent_clusters(kernel, dim3(c.B * c.Hk * group), group, kWarps * 32, sizeof(Smem<D>),
                                      stream, params_of(a, group), pg);

@@ -277,7 +277,9 @@ DECODES = [
     (128, 64, 1, 2, 0, [0]),
     (128, 64, 2, 2, 5, [0, 0]),
     (128, 16, 8, 4, 24, [2000, 1, 600] + [77] * 60),
-    # narrow tables: four, two, one and one CTAs a segment
+    # narrow tables: 16, 16, four, two, one and one CTAs a segment
+    (128, 64, 4, 4, 24, [5000, 40]),
+    (64, 16, 1, 16, 70, [0, 6000, 1, 127, 4097]),
     (128, 16, 4, 4, 24, RAGGED),
     (64, 32, 4, 7, 0, RAGGED + RAGGED + [2, 3]),
     (128, 64, 4, 2, 9, [500, 0, 1, 64, 65] * 10),
