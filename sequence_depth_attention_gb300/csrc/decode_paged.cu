@@ -25,8 +25,8 @@ constexpr int kCW = 4;                // consumer warps
 constexpr int kWarps = kCW + 1;       // and the producer
 constexpr int kKeys = 64;             // cached rows, or depth slots, of a unit
 constexpr int kCols = 64;             // columns of O merged at a time
-template <int D>
-constexpr int kCost = D == 128 ? 1 : 2;  // entering and leaving a segment, in units
+template <int D, int NT>
+constexpr int kCost = D == 128 && NT == 1 ? 1 : 2;  // entering and leaving a segment, in units
 constexpr int kCtasPerSm = 2;
 constexpr int kGroupUnits = 8, kClusterUnits = 3;  // see group_of
 constexpr float kSlack = 8.f;  // weights up to 2^8 lose nothing in bf16
@@ -131,7 +131,7 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     sh = share_of_segment<kKeys>(p, depth_units);
     if (sh.at.n == 0) return write_empty_segment<D>(p, sh.at.b, sh.at.hk);
   } else {
-    sh = share_of<kKeys, kWarps, kCost<D>, 1>(p, depth_units, sm.share);
+    sh = share_of<kKeys, kWarps, kCost<D, NT>, 1>(p, depth_units, sm.share);
     if (depth_units == 0) write_empty<D>(p);
     if (sh.n == 0) {
       if (tid == 0) wk.opened[blockIdx.x] = make_int2(-1, 0);
@@ -286,7 +286,7 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     left -= cnt;
     if (left > 0) {
       at.next_segment(p, depth_units);
-      seg_end += kCost<D> + at.n;
+      seg_end += kCost<D, NT> + at.n;
     }
   }
   if constexpr (GROUP) {

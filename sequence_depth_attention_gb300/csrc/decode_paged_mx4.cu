@@ -31,10 +31,11 @@ constexpr int kWarps = 4;
 constexpr int kKeys = 32;       // cached rows of a unit
 constexpr int kDepthKeys = 16;  // depth slots of a unit; their K and V take a stage each
 constexpr int kNS = 3;          // stages of a warp
-constexpr int kCols = 32;       // columns of O merged at a time
-// entering and leaving a segment, in units (about 2 us of a CTA's time)
-template <int D>
-constexpr int kCost = D == 128 ? 6 : 10;
+// Entering and leaving a segment, in units. (64 ragged sequences of up to 32768
+// rows, G = 8, at 6, 8, 10, 12: 122, 121, 119, 119 us; of up to 8000, G = 16, at
+// 6, 10, 14, 18: 68, 60, 57, 57.)
+template <int D, int NT>
+constexpr int kCost = NT == 1 ? (D == 128 ? 10 : 12) : 14;
 // 168 registers (two head tiles: 255): four at 128 registers were 6 % slower
 template <int NT>
 constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
@@ -52,7 +53,7 @@ struct Stage {
 template <int D>
 struct Smem {
   uint8_t ring[kWarps][kNS][Stage<D>::kBytes];
-  MergeSmem<kWarps, kCols> merge;
+  MergeSmem<kWarps, D> merge;
   ShareSmem<kWarps> share;
 };
 
@@ -550,7 +551,7 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
     sh = share_of_segment<kKeys>(p, depth_units);
     if (sh.at.n == 0) return write_empty_segment<D>(p, sh.at.b, sh.at.hk);
   } else {
-    sh = share_of<kKeys, kWarps, kCost<D>, kWarps>(p, depth_units, sm.share);
+    sh = share_of<kKeys, kWarps, kCost<D, NT>, kWarps>(p, depth_units, sm.share);
     if (depth_units == 0) write_empty<D>(p);
     if (sh.n == 0) {
       if (tid == 0) wk.opened[blockIdx.x] = make_int2(-1, 0);
@@ -633,16 +634,13 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
       }
     };
     if constexpr (GROUP) {
-      leave<D, NT>(p, last.merge, st, p.group > 1, &last.o[0][0], &last.ml[0][0], 0, first_row, put);
+      leave<D, NT>(p, sm.merge, st, p.group > 1, &last.o[0][0], &last.ml[0][0], 0, first_row, put);
       if (p.group > 1) join_group<D, kWarps>(p, last, first_row);
       return;
     }
     const int slot = 2 * blockIdx.x + (cut_before ? 0 : 1);
     const int64_t row0 = ((int64_t)at.b * p.Hk + at.hk) * p.G;
-    if (left == cnt)  // the last: the rings are free
-      leave<D, NT>(p, last.merge, st, cut_before || cut_after, wk.o, wk.ml, slot, row0, put);
-    else
-      leave<D, NT>(p, sm.merge, st, cut_before || cut_after, wk.o, wk.ml, slot, row0, put);
+    leave<D, NT>(p, sm.merge, st, cut_before || cut_after, wk.o, wk.ml, slot, row0, put);
     if (cut_after && !cut_before) {
       opened = true;
       if (tid == 0)
@@ -653,7 +651,7 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
     turn = (turn + cnt) & (kWarps - 1);
     if (left > 0) {
       at.next_segment(p, depth_units);
-      seg_end += kCost<D> + at.n;
+      seg_end += kCost<D, NT> + at.n;
     }
   }
   if (tid == 0 && !opened) wk.opened[blockIdx.x] = make_int2(-1, 0);
