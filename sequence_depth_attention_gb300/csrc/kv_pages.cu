@@ -13,9 +13,11 @@
 //   pairs (or two vectors of 4 interleaved pairs each), so that 16 values of
 //   the table turn 16 elements and no lane needs another's; d/16 lanes a head.
 //   4-bit rows: a lane owns one 16-byte vector, four lanes a block of 32; the
-//   halves of k's pairs come by shuffle.
+//   halves of k's pairs come by shuffle. k is turned in fp32, and again with a
+//   sticky bit only where that could change a code or a scale.
 // Measured: a prompt of 16384 tokens (Hq 16, Hk 4, d 128, 227 MB) 35.4 us, 96 %
-// of the copy bandwidth; two vectors a lane on the way instead of four 41 us.
+// of the copy bandwidth; two vectors a lane on the way instead of four 41 us. Into
+// 4-bit pages (193 MB) 41.4 us, issue-bound.
 // 16001 4-bit rows of 4 heads gathered, 42 MB, 11 us; an elementwise kernel over
 // as many bytes takes 10.4.
 #include <cuda_bf16.h>
@@ -29,8 +31,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarpsPerCta = kThreads / 32;
-// CTAs of an SM, at least: 56 and 64 registers (ragged 4-bit prompts at 8, 9,
-// 10, 11: 54.5, 51.7, 51.8, 61 us, from 10 on with spills)
+// CTAs of an SM, at least: 56 and 64 registers (4-bit, 16384 tokens of 8 KV
+// heads, at 8, 9, 10: 42.5, 41.8, 43.2 us)
 constexpr int kAppendCtasMx4 = 9;
 constexpr int kAppendCtasBf16 = 8;
 
@@ -97,24 +99,32 @@ __device__ __forceinline__ float turn_sticky(float x, float c, float y, float s)
   return __uint_as_float(u);
 }
 
-// A lane's 8 elements of one MX4 row (j: which eighth-of-row vector) into the
-// page: codes by every lane, the block's scale by one lane of its four. All
-// lanes of the warp call it; `on` says whose row exists.
-__device__ __forceinline__ void mx4_store(const float* x, uint8_t* codes, uint8_t* scales,
-                                          int64_t row, int j, int vpr, bool on) {
+// The largest magnitude's bits of a block, from each of its four lanes' own.
+__device__ __forceinline__ uint32_t mx4_amax(uint32_t m) {
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// 2^(127 - e) for scale byte e
+__device__ __forceinline__ float mx4_inv(int e) {
+  return __uint_as_float((uint32_t)(254 - min(e, 253)) << 23);
+}
+
+// A lane's 8 elements of one MX4 row as codes, and the scale byte of its block.
+// All lanes of the warp call it.
+__device__ __forceinline__ uint32_t mx4_row(const float* x, int& e) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const int e = mx4_scale_byte(m);
-  // 2^(127 - e); a block of NaN has codes 0
-  const float inv = __uint_as_float((uint32_t)(254 - min(e, 253)) << 23);
-  const uint32_t w = e == 255 ? 0u : mx4_codes(x, inv);
-  if (on) {
-    reinterpret_cast<uint32_t*>(codes)[row * vpr + j] = w;
-    if ((j & 3) == 0) scales[row * (vpr / 4) + (j >> 2)] = (uint8_t)e;
-  }
+  for (int i = 0; i < 8; ++i) m = max(m, magnitude(x[i]));
+  e = mx4_scale_byte(mx4_amax(m));
+  return e == 255 ? 0u : mx4_codes(x, mx4_inv(e));  // a block of NaN has codes 0
+}
+// They go into the page (j: which eighth-of-row vector): codes by every lane,
+// the block's scale by one lane of its four.
+__device__ __forceinline__ void mx4_store(uint32_t w, int e, void* codes, void* scales, int64_t row, int j,
+                                          int vpr) {
+  reinterpret_cast<uint32_t*>(codes)[row * vpr + j] = w;
+  if ((j & 3) == 0) reinterpret_cast<uint8_t*>(scales)[row * (vpr / 4) + (j >> 2)] = (uint8_t)e;
 }
 
 __device__ __forceinline__ void unpack8(const uint4& v, float* x) {
@@ -140,6 +150,7 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
 struct AppendGrid {
   int q_parts, parts;  // of a token: q's heads, then k's and v's
   uint32_t items;      // warps: no more than rows, which are below 2^31
+  int kv_turns;        // 4-bit pages: heads of k and v that a lane takes, 1 or 2
 };
 
 __device__ __forceinline__ void load4(const float* p, float* x) {
@@ -186,43 +197,39 @@ struct Turn {
 // One head of k and of v as 4-bit rows, and of k_out. The warp's rows are
 // d/8 lanes each; `on`: the lane's head exists.
 template <int D>
-__device__ __forceinline__ void put_mx4(const KvAppendArgs& a, const uint4& kr, const uint4& vr,
+__device__ __forceinline__ void put_mx4(const KvAppendArgs& a, uint4 kr, const uint4& vr,
                                         const float* table, int64_t n, int64_t row, int h, bool on,
                                         int lane) {
   constexpr int VPR = D / 8;
   const int j = lane % VPR, half = a.rot / 16;
-  // cosines and signed sines, and the lane with the pairs' other halves
-  // (itself when they are interleaved)
-  const bool turned = j < 2 * half;
-  float x[8], y[8], z[8];
-  unpack8(kr, x);
-  if (a.interleaved) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
-  } else {
-    const int partner = turned ? lane + (j < half ? half : -half) : lane;
-    uint4 o;
-    o.x = __shfl_sync(0xffffffffu, kr.x, partner);
-    o.y = __shfl_sync(0xffffffffu, kr.y, partner);
-    o.z = __shfl_sync(0xffffffffu, kr.z, partner);
-    o.w = __shfl_sync(0xffffffffu, kr.w, partner);
-    unpack8(o, y);
+  const bool turned = j < 2 * half, low = j < half;
+  // the pairs' other halves: the lane's own when they are interleaved
+  uint4 other = kr;
+  if (!a.interleaved) {
+    const int partner = turned ? lane + (low ? half : -half) : lane;
+    other.x = __shfl_sync(0xffffffffu, kr.x, partner);
+    other.y = __shfl_sync(0xffffffffu, kr.y, partner);
+    other.z = __shfl_sync(0xffffffffu, kr.z, partner);
+    other.w = __shfl_sync(0xffffffffu, kr.w, partner);
   }
-  uint4* dense = a.k_out && on
-                     ? reinterpret_cast<uint4*>(a.k_out) + (n * a.c.Hk + h) * VPR + j : nullptr;
-  if (turned) {
-    float cs[8], sn[8];
-    if (a.interleaved) {
+  float x[8], y[8], z[8], cs[8], sn[8];  // z = x cs + y sn
+  auto inputs = [&] {
+    unpack8(kr, x);
+    unpack8(other, y);
+    if (!turned) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f, y[i] = -0.f;  // z = x, its zero's sign too
+    } else if (a.interleaved) {
       float c[4], s[4];
       load4(table + j * 4, c);
       load4(table + a.rot / 2 + j * 4, s);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
+        y[i] = x[i ^ 1];
         cs[i] = c[i / 2];
         sn[i] = (i & 1) ? s[i / 2] : -s[i / 2];
       }
     } else {
-      const bool low = j < half;
       const float* t = table + (low ? j : j - half) * 8;
       load4(t, cs);
       load4(t + 4, cs + 4);
@@ -231,19 +238,60 @@ __device__ __forceinline__ void put_mx4(const KvAppendArgs& a, const uint4& kr, 
 #pragma unroll
       for (int i = 0; i < 8; ++i) sn[i] = low ? -sn[i] : sn[i];
     }
+  };
+  inputs();
+  // z = x c + y s in fp32 is off by at most 2^-24 (|y s| + |z|). Codes and scale
+  // are the exact value's wherever both ends of an interval of three times that
+  // have the same; at a border, which one warp in hundreds meets, the rotation
+  // is done again with a sticky bit. (16384 tokens of 8 KV heads, d = 128: always
+  // with the sticky bit 51.6 us, so 46.0.)
+  float off = 0.f;
+  uint32_t big = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = fmaf(x[i], cs[i], y[i] * sn[i]);
-    if (dense) *dense = pack8(z);
+  for (int i = 0; i < 8; ++i) {
+    const float p = y[i] * sn[i];
+    z[i] = fmaf(x[i], cs[i], p);
+    off = fmaxf(off, fabsf(p) + fabsf(z[i]));
+    big = max(big, magnitude(z[i]));
+  }
+  if (a.k_out && on)
+    *(reinterpret_cast<uint4*>(a.k_out) + (n * a.c.Hk + h) * VPR + j) = turned ? pack8(z) : kr;
+  const float d = turned ? off * 0x1.8p-23f : 0.f;
+  big = mx4_amax(__float_as_uint(__uint_as_float(big) + d));
+  int e = mx4_scale_byte(big);
+  uint32_t w = 0;
+  if (e != 255) {
+    float lo[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = turn_sticky(x[i], cs[i], y[i], sn[i]);
-  } else {
-    if (dense) *dense = kr;
+    for (int i = 0; i < 8; ++i) lo[i] = z[i] - d;
+    w = mx4_codes(lo, mx4_inv(e));
+  }
+  bool border = e == 255;
+  if (!border) {
+    float hi[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) hi[i] = z[i] + d;
+    // the scale: the exact maximum is within 384 units in the last place below
+    // `big`, as long as no element lost more than 6 bits to cancellation
+    border = w != mx4_codes(hi, mx4_inv(e)) || !(off <= 64.f * __uint_as_float(big)) ||
+             (big & 0x7fffffu) - 0x600001u < 512u;
+  }
+  if (__any_sync(0xffffffffu, turned && border)) {
+    // (from what the registers still hold, and the table)
+    asm volatile("" : "+r"(kr.x), "+r"(kr.y), "+r"(kr.z), "+r"(kr.w) : : "memory");
+    asm volatile("" : "+r"(other.x), "+r"(other.y), "+r"(other.z), "+r"(other.w));
+    inputs();
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] = x[i];
+    if (turned)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = turn_sticky(x[i], cs[i], y[i], sn[i]);
+    w = mx4_row(z, e);
   }
-  mx4_store(z, reinterpret_cast<uint8_t*>(a.c.k), reinterpret_cast<uint8_t*>(a.c.k_scale), row, j, VPR, on);
+  if (on) mx4_store(w, e, a.c.k, a.c.k_scale, row, j, VPR);
   unpack8(vr, z);
-  mx4_store(z, reinterpret_cast<uint8_t*>(a.c.v), reinterpret_cast<uint8_t*>(a.c.v_scale), row, j, VPR, on);
+  w = mx4_row(z, e);
+  if (on) mx4_store(w, e, a.c.v, a.c.v_scale, row, j, VPR);
 }
 
 template <int D, bool MX4>
@@ -261,19 +309,30 @@ kv_append_kernel(const __grid_constant__ KvAppendArgs a, const __grid_constant__
   if (a.rot > 0) limit = min(limit, a.rope_rows);
 
   if (MX4 && part >= g.q_parts) {
+    // one head a lane, or two after one another with all four loads on the way first
     constexpr int HPI = 32 / VPR;
-    const int h = (part - g.q_parts) * HPI + lane / VPR;
-    const bool on = h < a.c.Hk;
-    uint4 kr = make_uint4(0u, 0u, 0u, 0u), vr = kr;
-    if (on) {
-      const int64_t at = (int64_t)h * D + lane % VPR * 8;
-      kr = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.k) + n * a.k_stride + at);
-      vr = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.v) + n * a.v_stride + at);
+    int h = (part - g.q_parts) * (g.kv_turns * HPI) + lane / VPR;
+    const uint16_t* ks = reinterpret_cast<const uint16_t*>(a.k) + n * a.k_stride + h * D + lane % VPR * 8;
+    const uint16_t* vs = reinterpret_cast<const uint16_t*>(a.v) + n * a.v_stride + h * D + lane % VPR * 8;
+    uint4 kr[2], vr[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      kr[i] = vr[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (i < g.kv_turns && h + i * HPI < a.c.Hk) {
+        kr[i] = *reinterpret_cast<const uint4*>(ks + i * HPI * D);
+        vr[i] = *reinterpret_cast<const uint4*>(vs + i * HPI * D);
+      }
     }
     const int row = page_row(a.c, s, p, limit);
     if (row < 0) return;
-    put_mx4<D>(a, kr, vr, a.rope + (int64_t)p * a.rot, n, (int64_t)row + (int64_t)h * a.c.page_size, h,
-               on, lane);
+#pragma unroll 1
+    for (int i = 0; i < g.kv_turns; ++i) {
+      put_mx4<D>(a, kr[0], vr[0], a.rope + (int64_t)p * a.rot, n, (int64_t)row + (int64_t)h * a.c.page_size, h,
+                 h < a.c.Hk, lane);
+      h += HPI;
+      kr[0] = kr[1];
+      vr[0] = vr[1];
+    }
     return;
   }
   // this lane's two vectors of a head; of two heads of q, or of one of k and v
@@ -409,7 +468,12 @@ cudaError_t append_d(const KvAppendArgs& a, cudaStream_t stream) {
   constexpr int VPR = D / 8;
   AppendGrid g;
   g.q_parts = (a.Hq + 128 / VPR - 1) / (128 / VPR);
-  const int kv_heads = (mx4 ? 32 : 64) / VPR;
+  // 4-bit pages: two heads a lane where the warps would not be on the SMs at
+  // once (16384 tokens of 8 KV heads: 46.0 us with one, 41.8), one where each
+  // warp's own time counts (253 tokens: 2.4 us, with two 3.1)
+  const int group = 32 / VPR, one = g.q_parts + (a.c.Hk + group - 1) / group;
+  g.kv_turns = (int64_t)a.N * one <= (int64_t)a.num_sms * kAppendCtasMx4 * kWarpsPerCta ? 1 : 2;
+  const int kv_heads = mx4 ? g.kv_turns * group : 64 / VPR;
   g.parts = g.q_parts + (a.c.Hk + kv_heads - 1) / kv_heads;
   g.items = (uint32_t)a.N * g.parts;
   const unsigned blocks = (g.items + kWarpsPerCta - 1) / kWarpsPerCta;

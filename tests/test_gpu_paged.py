@@ -828,3 +828,31 @@ def test_bad_lengths_and_pages_of_many(fmt):
     ro, _, to, _ = pc.decode_reference(c, q, [40, 64, 20], None, None, 0.125)
     ok = ((o.double() - ro.repeat(many, 1, 1)).abs() <= to.repeat(many, 1, 1)).view(many, 3, -1).all(-1)
     assert ok[:, 0].all() and ok[:, 2].all()
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("d,rot", [(64, 64), (128, 128), (128, 48)])
+def test_turned_keys_on_and_next_to_borders(d, rot, inter):
+    """4-bit rows of K whose turned values lie on the borders between codes and
+    between scales, and off them by 2^-12 to 2^-30 of the other half of the pair:
+    every code is the exact value's (cosines and sines are powers of two, so that
+    fp64 holds it), also where most of a value cancels."""
+    g = torch.Generator().manual_seed(50 + rot + inter)
+    border = torch.tensor([0.0, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 7.0, 6.0, 3.0], dtype=torch.float64)
+    N, Hk, page = 600, 2, 16
+    pick = lambda: border[torch.randint(0, len(border), (N, Hk, d), generator=g)]  # noqa: E731
+    sign = lambda: 1.0 - 2.0 * torch.randint(0, 2, (N, Hk, d), generator=g)  # noqa: E731
+    k = pick() * sign() * torch.exp2(torch.randint(-3, 4, (N, Hk, 1), generator=g).double())
+    k[::3, :, : d // 2] = k[::3, :, d // 2:]  # equal halves, which cancel where cos = -sin
+    cos = torch.tensor([1.0, 0.5, -1.0, 2.0])[torch.randint(0, 4, (N, rot // 2), generator=g)]
+    sin = torch.tensor([0.0, 2.0 ** -12, -2.0 ** -22, 2.0 ** -23, -2.0 ** -24, 2.0 ** -30, 1.0, -0.5])[
+        torch.randint(0, 8, (N, rot // 2), generator=g)]
+    rope = torch.cat((cos, sin), 1).cuda()
+    k = k.bfloat16().cuda()
+    c = pc.Cache("mx4", [N], Hk, d, page, device="cuda")
+    seq, pos = torch.zeros(N, dtype=torch.int32, device="cuda"), torch.arange(N, dtype=torch.int32, device="cuda")
+    moda.moda_kv_append(None, k, k, *c.args(), seq, pos, rope=rope, interleaved=inter, **c.scales())
+    settled()
+    want = pc.mx4_quantised(pc.turned(k, rope, pos, inter)).transpose(0, 1)
+    assert torch.equal(c.rows("k", 0, N), want)
+    assert torch.equal(c.rows("v", 0, N), pc.mx4_quantised(k.double()).transpose(0, 1))
