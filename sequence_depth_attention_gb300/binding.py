@@ -510,7 +510,8 @@ def _allocating(stream, dev):
     if stream is None:
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_raw_stream(stream, dev), device=dev)
+        raw = _raw_stream(stream, dev)  # 0: the default stream, which has no wrapper of its own
+        stream = torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev)
     return torch.cuda.stream(stream)
 
 

@@ -712,12 +712,13 @@ def test_what_a_call_allocates_belongs_to_its_stream(fmt, monkeypatch):
     side.wait_stream(torch.cuda.current_stream())
     on, empty = [], torch.empty
     monkeypatch.setattr(torch, "empty", lambda *a, **kw: (on.append(torch.cuda.current_stream()), empty(*a, **kw))[1])
-    for stream in (side, side.cuda_stream):
+    for stream in (side, side.cuda_stream, torch.cuda.default_stream().cuda_stream):
         on.clear()
         got = (moda.moda_kv_append(q, k, v, *c.args(), seq, pos, stream=stream, **c.scales()),
                moda.moda_kv_gather(*c.args(), seq, pos, stream=stream, **c.scales()),
                moda.moda_decode_paged(qc, *c.args(), n, 0.1, stream=stream, **c.scales()))
-        assert len(on) == 7 and {s.cuda_stream for s in on} == {side.cuda_stream}
+        assert len(on) == 7
+        assert {s.cuda_stream for s in on} == {getattr(stream, "cuda_stream", stream)}
         settled()
         for a, b in zip(want, got):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
