@@ -12,7 +12,7 @@
 // of a warp MMA's B tile; G > 8 takes two such tiles. Two CTAs an SM keep up to
 // 192 KB on the way. Measured (d = 128): 48 ragged sequences of up to 16384
 // rows, 803 MB, 121 us (99 % of the copy bandwidth); one context of 65536 rows
-// 27 us, of which its 134 MB take 20, the look-ups before them 3.5, the join 3;
+// 26.4 us, of which its 134 MB take 20, the look-ups before them 2.7, the join 3;
 // one of 701 rows, in clusters of eight, 4.5 us.
 #include "decode_paged.cuh"
 #include "tensor_map.h"
@@ -100,9 +100,7 @@ __device__ __forceinline__ void tile_bf16(State<D, NT>& st, const uint32_t (&qb)
   }
 }
 
-// GROUP: a short batch, whose segments have p.group CTAs each; else the batch's
-// line in equal shares.
-template <int D, int NT, bool GROUP>
+template <int D, int NT, Split SPLIT>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
 decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const __grid_constant__ CUtensorMap tmKd, const __grid_constant__ CUtensorMap tmVd,
@@ -125,13 +123,17 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     sm103::fence_barrier_init();
   }
   wait_for_stream();
+  constexpr bool GROUP = SPLIT == Split::kGroup;
   Share<kKeys> sh;
+  __syncthreads();
   if constexpr (GROUP) {
-    __syncthreads();
     sh = share_of_segment<kKeys>(p, depth_units);
     if (sh.at.n == 0) return write_empty_segment<D>(p, sh.at.b, sh.at.hk);
   } else {
-    sh = share_of<kKeys, kWarps, kCost<D, NT>, 1>(p, depth_units, sm.share);
+    if constexpr (SPLIT == Split::kOne)
+      sh = share_of_one<kKeys, kCost<D, NT>, 1>(p, depth_units);
+    else
+      sh = share_of<kKeys, kWarps, kCost<D, NT>, 1>(p, depth_units, sm.share);
     if (depth_units == 0) write_empty<D>(p);
     if (sh.n == 0) {
       if (tid == 0) wk.opened[blockIdx.x] = make_int2(-1, 0);
@@ -456,7 +458,9 @@ cudaError_t launch(const DecodePagedArgs& a, cudaStream_t stream) {
   grid = grid < kMaxCtas ? grid : kMaxCtas;
   const int max_units = (a.L + kKeys - 1) / kKeys + (c.max_pages * c.page_size + kKeys - 1) / kKeys;
   const int group = group_of(a, max_units, grid, kGroupUnits, kClusterUnits);
-  const auto kernel = group ? decode_paged_split<D, NT, true> : decode_paged_split<D, NT, false>;
+  const auto kernel = group        ? decode_paged_split<D, NT, Split::kGroup>
+                      : c.B == 1 ? decode_paged_split<D, NT, Split::kOne>
+                                 : decode_paged_split<D, NT, Split::kShares>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   if (group > 8) {  // beyond the portable size

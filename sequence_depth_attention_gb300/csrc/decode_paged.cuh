@@ -47,6 +47,10 @@ __host__ __device__ inline Work work_of(float* w, int G, int D) {
   return k;
 }
 
+// How a batch is divided: into equal shares of the line, that of one sequence,
+// or a group of CTAs for each segment.
+enum class Split { kShares, kOne, kGroup };
+
 struct Params {
   const __nv_bfloat16* q;
   const int* lens;
@@ -108,6 +112,15 @@ struct Share {
   int n;          // units of this CTA
   Place<KEYS> at;
 
+  // `total` points over the grid's CTAs, `least` for each at least
+  __device__ __forceinline__ void divide_line(int least) {
+    shares = (int)min((long long)gridDim.x, divide(total + least - 1, least));
+    base = n = rem = 0;
+    if (shares > 0) {
+      base = divide(total, shares);
+      rem = (int)(total - base * shares);
+    }
+  }
   __device__ __forceinline__ long long first_point(int cta) const {
     return base * cta + min(cta, rem);
   }
@@ -167,12 +180,7 @@ __device__ __forceinline__ Share<KEYS> share_of(const Params& p, int depth_units
   before -= mine;
   Share<KEYS> s;
   s.total = (long long)(all >> 25) * p.Hk;
-  s.shares = (int)min((long long)gridDim.x, divide(s.total + LEAST - 1, LEAST));
-  s.base = s.n = s.rem = 0;
-  if (s.shares > 0) {
-    s.base = divide(s.total, s.shares);
-    s.rem = (int)(s.total - s.base * s.shares);
-  }
+  s.divide_line(LEAST);
   const int cta = blockIdx.x;
   if (cta < s.shares) {
     // where the share begins and ends, by the threads whose sequences these are
@@ -222,6 +230,32 @@ __device__ __forceinline__ Share<KEYS> share_of(const Params& p, int depth_units
     s.at.n = sm.start[3];
     s.at.len = rows_of(p, s.at.b);
     s.end = s.first_point(cta) - sm.start[2] + COST + s.at.n;
+  }
+  return s;
+}
+
+// The same for a single sequence, whose segments are all alike: no scan, no
+// barrier (65536 rows: bf16 26.4 us instead of 27.2, 4-bit 15.6 instead of 16.2;
+// as a branch of share_of it cost the others 0.7 %).
+template <int KEYS, int COST, int LEAST>
+__device__ __forceinline__ Share<KEYS> share_of_one(const Params& p, int depth_units) {
+  const int cta = blockIdx.x, raw = p.lens[0];
+  Share<KEYS> s;
+  s.at.b = 0;
+  s.at.enter(p, depth_units);
+  if (cta == 0 && threadIdx.x == 0 && (raw < 0 || raw > p.max_pages << p.page_shift))
+    atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
+  const int len = s.at.n + COST;
+  s.total = s.at.n > 0 ? (long long)len * p.Hk : 0;
+  s.divide_line(LEAST);
+  if (cta < s.shares) {
+    const long long from = s.first_point(cta), to = s.first_point(cta + 1);
+    s.at.hk = (int)divide(from, len);
+    const int hk_to = (int)divide(to, len);
+    const int off = (int)(from - (long long)s.at.hk * len), off_to = (int)(to - (long long)hk_to * len);
+    s.at.off = max(0, off - COST);
+    s.n = (int)(to - from) - (hk_to - s.at.hk) * COST + min(off, COST) - min(off_to, COST);
+    s.end = from - off + len;
   }
   return s;
 }

@@ -534,9 +534,7 @@ struct Feed {
   }
 };
 
-// GROUP: a short batch, whose segments have p.group CTAs each; else the batch's
-// line in equal shares.
-template <int D, int NT, bool GROUP>
+template <int D, int NT, Split SPLIT>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<NT>)
 decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__ Mx4Pages pg) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -546,12 +544,16 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
   const Work wk = work_of(p.work, p.G, D);
 
   wait_for_stream();
+  constexpr bool GROUP = SPLIT == Split::kGroup;
   Share<kKeys> sh;
   if constexpr (GROUP) {
     sh = share_of_segment<kKeys>(p, depth_units);
     if (sh.at.n == 0) return write_empty_segment<D>(p, sh.at.b, sh.at.hk);
   } else {
-    sh = share_of<kKeys, kWarps, kCost<D, NT>, kWarps>(p, depth_units, sm.share);
+    if constexpr (SPLIT == Split::kOne)
+      sh = share_of_one<kKeys, kCost<D, NT>, kWarps>(p, depth_units);
+    else
+      sh = share_of<kKeys, kWarps, kCost<D, NT>, kWarps>(p, depth_units, sm.share);
     if (depth_units == 0) write_empty<D>(p);
     if (sh.n == 0) {
       if (tid == 0) wk.opened[blockIdx.x] = make_int2(-1, 0);
@@ -670,7 +672,9 @@ cudaError_t launch(const DecodePagedArgs& a, cudaStream_t stream) {
   const int max_units =
       (a.L + kDepthKeys - 1) / kDepthKeys + (c.max_pages * c.page_size + kKeys - 1) / kKeys;
   const int group = group_of(a, max_units, grid, kGroupUnits, kClusterUnits);
-  const auto kernel = group ? decode_paged_mx4_split<D, NT, true> : decode_paged_mx4_split<D, NT, false>;
+  const auto kernel = group        ? decode_paged_mx4_split<D, NT, Split::kGroup>
+                      : c.B == 1 ? decode_paged_mx4_split<D, NT, Split::kOne>
+                                 : decode_paged_mx4_split<D, NT, Split::kShares>;
   cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>));
   if (e != cudaSuccess) return e;

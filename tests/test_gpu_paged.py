@@ -277,6 +277,8 @@ DECODES = [
     (128, 64, 1, 2, 0, [0]),
     (128, 64, 2, 2, 5, [0, 0]),
     (128, 16, 8, 4, 24, [2000, 1, 600] + [77] * 60),
+    (64, 16, 3, 5, 70, [9003]),
+    (128, 32, 7, 2, 0, [14001]),
     # narrow tables: 16, 16, four, two, one and one CTAs a segment
     (128, 64, 4, 4, 24, [5000, 40]),
     (64, 16, 1, 16, 70, [0, 6000, 1, 127, 4097]),
@@ -816,8 +818,10 @@ def test_bad_lengths_and_pages_of_many(fmt):
     settled(INVALID)
     assert ((o.double() - ro.repeat(many, 1, 1)).abs() <= to.repeat(many, 1, 1)).all()
     assert (o.view(many, 3, 4, d)[:, 2] == 0).all() and (lse.view(many, 3, 4)[:, 2] == -math.inf).all()
-    for b, bad in ((0, False), (1, True), (2, True)):
-        o, lse = moda.moda_decode_paged(q[b : b + 1], c.k, c.v, c.table[b : b + 1], n[b : b + 1], 0.125, **c.scales())
+    wide = torch.full((3, 1024), -7, dtype=torch.int32, device="cuda")
+    wide[:, :4] = c.table
+    for b, bad, table in ((0, False, c.table), (1, True, c.table), (2, True, c.table), (2, True, wide)):
+        o, lse = moda.moda_decode_paged(q[b : b + 1], c.k, c.v, table[b : b + 1], n[b : b + 1], 0.125, **c.scales())
         settled(INVALID if bad else 0)
         assert ((o.double() - ro[b]).abs() <= to[b]).all()
         assert b != 2 or (o == 0).all() and (lse == -math.inf).all()
