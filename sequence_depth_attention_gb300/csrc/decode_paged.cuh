@@ -18,6 +18,7 @@
 
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "moda_internal.h"
@@ -588,30 +589,31 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_
 }
 
 // CTAs for each segment of a short batch: a group, where no segment can have
-// more than `most` units for each (of 16: 3/4 of that); 0 where the batch is
+// more than `most` units for each (for each two of 16); 0 where the batch is
 // better cut into equal shares. What the host knows of the lengths is the
-// table's width. Measured, GPU time in us, d = 128, G = 4:
-//   sequences x KV heads    rows      bf16 (most = 8)        4-bit (most = 21)
-//                                     group      shares      group      shares
-//         1 x 8           700          4.6 (8)     6.1        5.1 (8)     7.4
-//         1 x 8          2000          5.6 (8)     7.3        5.9 (8)     7.5
-//         1 x 4          4000          6.2 (16)    7.2        6.3 (16)    7.5
-//         1 x 4          8000          8.4 (16)    8.2        7.7 (16)    8.4
-//         8 x 8     1 .. 1000          6.5 (4)     8.3        7.3 (4)    10.3
-//         8 x 8     1 .. 4000         13.7 (4)    12.6       13.8 (4)    13.5
-//        32 x 8     1 ..  256          5.6 (1)     9.6        7.9 (1)    12.5
-//        32 x 8     1 .. 1000         12.8 (1)    12.1       13.7 (1)    16.6
+// table's width. Measured, GPU time in us, d = 128, G = 4, L = 24, against the
+// same calls with a wide table:
+//   sequences x KV heads     rows      bf16 (most = 8)       4-bit (most = 21)
+//                                      group     shares      group     shares
+//           1 x 8             700     4.6 (8)     5.3       5.0 (8)     6.5
+//           1 x 4            4000     6.0 (16)    6.3       6.4 (16)    6.6
+//           1 x 4            8000     8.4 (16)    7.3       8.0 (16)    7.5
+//           8 x 8       1 .. 1000     6.5 (4)     8.3       7.3 (6)     9.9
+//           8 x 8       1 .. 4000    13.7 (4)    12.5      13.8 (4)    13.0
+//          22 x 4       1 .. 1000     7.1 (3)     9.1       7.7 (4)    10.7
+//          16 x 8       1 ..  700     7.4 (2)     9.3       7.9 (3)    11.0
+//          32 x 8       1 ..  256     5.6 (1)     9.7       7.8 (1)    11.5
+//          32 x 8       1 .. 1000    12.8 (1)    12.2      13.7 (1)    14.6
 // More CTAs are better as long as all clusters fit the SMs at once (8 or 4 at
 // 15/16 of the places did not: 6.5 -> 10), 16 where 8 would have many units each
 // and there is an SM for each CTA. A cluster costs as much as `cluster_units`
 // units of one CTA take; where it saves less, one CTA has the segment.
 inline int group_of(const DecodePagedArgs& a, int max_units, int resident, int most, int cluster_units) {
   const int64_t segments = (int64_t)a.c.B * a.c.Hk;
-  if (segments * 16 <= a.num_sms && max_units > most * 4) return max_units <= most * 12 ? 16 : 0;
-  int group = 8;
-  while (group > 1 && segments * group > resident / 8 * 7) group /= 2;
+  int group = (int)std::max<int64_t>(1, std::min<int64_t>(8, resident / 8 * 7 / segments));
   if ((int64_t)max_units * (group - 1) <= cluster_units * group) group = 1;
-  return segments * group <= resident && max_units <= most * group ? group : 0;
+  if (segments * group > resident || max_units > most * group) return 0;
+  return segments * 16 <= a.num_sms && max_units > most * 5 ? 16 : group;
 }
 
 cudaError_t launch_join(const DecodePagedArgs& a, int shares, cudaStream_t stream);

@@ -15,7 +15,7 @@
 // Measured (d = 128): 64 ragged sequences of up to 32768 rows at G = 8, 584 MB,
 // 123 us, issue 73 % and the ALU 61 % busy in the loop; the same rows in TMA
 // boxes with a producer warp and four codes to a load took 226. 16 sequences of
-// up to 999 rows (d = 64, 8 KV heads, G = 8), in clusters of two, 8.0 us.
+// up to 999 rows (d = 64, 8 KV heads, G = 8), in clusters of three, 7.1 us.
 // Each warp streams units of its own (32 rows, or 16 depth slots) through its
 // own ring of shared-memory stages by asynchronous copies: no barrier between
 // warps but at the end of a segment.

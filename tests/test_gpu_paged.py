@@ -279,9 +279,11 @@ DECODES = [
     (128, 16, 8, 4, 24, [2000, 1, 600] + [77] * 60),
     (64, 16, 3, 5, 70, [9003]),
     (128, 32, 7, 2, 0, [14001]),
-    # narrow tables: 16, 16, four, two, one and one CTAs a segment
-    (128, 64, 4, 4, 24, [5000, 40]),
-    (64, 16, 1, 16, 70, [0, 6000, 1, 127, 4097]),
+    # narrow tables: 16, 16, 6 (4-bit: 8), 5 (7), 5 (8), 2 (3), one and one CTAs a segment
+    (128, 64, 4, 4, 24, [3900, 40]),
+    (64, 16, 1, 16, 70, [0, 3800, 1, 127, 2001]),
+    (64, 32, 4, 3, 0, RAGGED[1:]),
+    (128, 64, 4, 9, 5, [900, 0, 7] + RAGGED[2:]),
     (128, 16, 4, 4, 24, RAGGED),
     (64, 32, 4, 7, 0, RAGGED + RAGGED + [2, 3]),
     (128, 64, 4, 2, 9, [500, 0, 1, 64, 65] * 10),
