@@ -1,6 +1,8 @@
 import os
 import sys
 
+import pytest
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
@@ -12,3 +14,20 @@ if HERE not in sys.path:
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (GB300, sm_103a)")
     config.addinivalue_line("markers", "slow: long-running CPU test")
+
+
+# Host tests that make a call with invented device addresses which validation lets
+# through: without a GPU it ends at the device check, with one it would launch on
+# memory that is not there. They run only where there is no GPU.
+INVENTED_ADDRESSES = {"test_abi_host.py::test_fwd_l0_accepts_null_depth",
+                      "test_abi_paged.py::test_append_without_tokens_or_queries"}
+
+
+def pytest_collection_modifyitems(items):
+    named = [i for i in items if f"{i.path.name}::{i.name}" in INVENTED_ADDRESSES]
+    if not named:
+        return
+    import torch
+    if torch.cuda.is_available():
+        for item in named:
+            item.add_marker(pytest.mark.skip(reason="a GPU is present"))
