@@ -308,7 +308,7 @@ constexpr int kFewWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kFewWarps * 32)
-decode_paged_join_few(float* work, int G, int shares, __nv_bfloat16* o, float* lse) {
+decode_paged_join_few(float* work, int G, int shares, float unit, __nv_bfloat16* o, float* lse) {
   constexpr int E = D / 32;
   constexpr int U = 4;
   const Work wk = work_of(work, G, D);
@@ -342,7 +342,7 @@ decode_paged_join_few(float* work, int G, int shares, __nv_bfloat16* o, float* l
       add_partials<U, E>(M, L, acc, pm, pl, po);
     }
     const int64_t r = (int64_t)seg.x * G + g;
-    const float inv = 1.f / L;
+    const float inv = 1.f / L * unit;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[r * D + lane * E + e] = __float2bfloat16_rn(acc[e] * inv);
     if (lane == 0 && lse) lse[r] = (M + log2f(L)) * kLn2;
@@ -356,7 +356,7 @@ constexpr int kManyWarps = 16;
 
 template <int D>
 __global__ void __launch_bounds__(kManyWarps * 32)
-decode_paged_join_many(float* work, int G, int shares, __nv_bfloat16* o, float* lse) {
+decode_paged_join_many(float* work, int G, int shares, float unit, __nv_bfloat16* o, float* lse) {
   constexpr int E = D / 32;
   constexpr int U = 8;  // partials a warp loads before it adds the first
   __shared__ float sm_o[kManyWarps][D];
@@ -422,7 +422,7 @@ decode_paged_join_many(float* work, int G, int shares, __nv_bfloat16* o, float* 
 #pragma unroll
     for (int w = 0; w < kManyWarps; ++w) ot = fmaf(__shfl_sync(0xffffffffu, a, w), sm_o[w][d], ot);
     const int64_t r = (int64_t)blockIdx.x * G + g;
-    o[r * D + d] = __float2bfloat16_rn(ot / l);
+    o[r * D + d] = __float2bfloat16_rn(ot / l * unit);
     if (d == 0 && lse) lse[r] = (Mt + log2f(l)) * kLn2;
   }
 }
@@ -484,11 +484,11 @@ cudaError_t launch_join(const DecodePagedArgs& a, int shares, cudaStream_t strea
   if (segments * 8 <= shares && segments * a.G <= a.num_sms * 4)
     return launch_dependent(a.c.d == 128 ? decode_paged_join_many<128> : decode_paged_join_many<64>,
                             dim3((unsigned)segments, a.G), kManyWarps * 32, 0, stream, a.work, a.G, shares,
-                            o, a.lse);
+                            unit_of(a), o, a.lse);
   const int ctas = (shares * a.G + kFewWarps - 1) / kFewWarps;
   return launch_dependent(a.c.d == 128 ? decode_paged_join_few<128> : decode_paged_join_few<64>,
                           dim3(ctas < 4 * a.num_sms ? ctas : 4 * a.num_sms), kFewWarps * 32, 0, stream, a.work,
-                          a.G, shares, o, a.lse);
+                          a.G, shares, unit_of(a), o, a.lse);
 }
 
 }  // namespace paged

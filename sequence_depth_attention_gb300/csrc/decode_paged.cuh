@@ -62,12 +62,19 @@ struct Params {
   float* lse;
   float* work;
   unsigned int* err;
-  int group;  // CTAs of a segment; 0: shares of the line
+  int group;   // CTAs of a segment; 0: shares of the line
+  float unit;  // of the sums O that warps merge and CTAs leave, see unit_of
 };
+// O of 4-bit rows leaves a warp in units of 2^32: values are up to 1.5 * 2^127, and
+// sums of up to 2^24 of them, each times a weight of up to 2^8, stay finite; what
+// fp32 drops at the low end is below 2^-117.
+constexpr float kUnit4 = 0x1p32f;
+inline float unit_of(const DecodePagedArgs& a) { return a.c.format == MODA_KV_MX4 ? kUnit4 : 1.f; }
 inline Params params_of(const DecodePagedArgs& a, int group) {
   const PagedKv& c = a.c;
   return {(const __nv_bfloat16*)a.q, a.seq_lens, c.table, c.num_pages, __builtin_ctz((unsigned)c.page_size),
-          c.max_pages, c.B, c.Hk, a.G, a.L, a.scale * kLog2e, (__nv_bfloat16*)a.o, a.lse, a.work, c.err, group};
+          c.max_pages, c.B, c.Hk, a.G, a.L, a.scale * kLog2e, (__nv_bfloat16*)a.o, a.lse, a.work, c.err, group,
+          unit_of(a)};
 }
 
 // Sequence b's rows, within what its table can name.
@@ -326,10 +333,9 @@ struct State {
       for (int i = 0; i < D / 16; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
     }
   }
-  // Raises m of tile t to cover z, N scores (for the 4-bit path plus what
-  // their values carry) of head 2c at even and 2c + 1 at odd places, and brings
-  // l and o to it. Only when one of them is more than `slack` above m, which
-  // most tiles' are not: one vote tells.
+  // Raises m of tile t to cover z, N scores of head 2c at even and 2c + 1 at odd
+  // places, and brings l and o to it. Only when one of them is more than `slack`
+  // above m, which most tiles' are not: one vote tells.
   template <int N>
   __device__ __forceinline__ void raise(int t, const float (&z)[N], float slack) {
     float x0 = z[0], x1 = z[1];
@@ -406,9 +412,10 @@ struct MergeSmem {
 
 // The state of WARPS warps (threads 0 .. 32 * WARPS - 1, which meet at named
 // barrier 1) as the segment's result, or where the segment is cut as a partial
-// in part_o [slot][G][D] and part_ml [slot][G][2]. put(m0, m1, t, part, sm) stores the warp's columns COLS * part
-// .. of tile t for its heads 2c and 2c + 1. row0: the segment's first row of
-// o and lse.
+// in part_o [slot][G][D] and part_ml [slot][G][2]. put(m0, m1, t, part, sm)
+// stores the warp's columns COLS * part .. of tile t for its heads 2c and 2c + 1,
+// sums of 2^(score - m) times values, in p.unit. row0: the segment's first row
+// of o and lse.
 template <int D, int NT, int WARPS, int COLS, class Put>
 __device__ __forceinline__ void leave(const Params& p, MergeSmem<WARPS, COLS>& sm, State<D, NT>& st,
                                       bool cut, float* part_o, float* part_ml, int64_t slot, int64_t row0,
@@ -464,7 +471,7 @@ __device__ __forceinline__ void leave(const Params& p, MergeSmem<WARPS, COLS>& s
             part_ml[r * 2 + 1] = L;
           }
         } else {
-          const float inv = 1.f / L;
+          const float inv = 1.f / L * p.unit;
           const int64_t r = row0 + g;
           *reinterpret_cast<uint2*>(p.o + r * D + col) =
               make_uint2(wmma16::pack_bf16(acc.x * inv, acc.y * inv),
@@ -545,7 +552,7 @@ __device__ __forceinline__ void join_group(const Params& p, const GroupSmem<D, W
     };
     add_eight(0);
     if (p.group > 8) add_eight(8);
-    const float inv = 1.f / L;
+    const float inv = 1.f / L * p.unit;
     *reinterpret_cast<uint2*>(p.o + (row0 + g) * D + col) = make_uint2(
         wmma16::pack_bf16(acc[0] * inv, acc[1] * inv), wmma16::pack_bf16(acc[2] * inv, acc[3] * inv));
     if (col == 0 && p.lse) p.lse[row0 + g] = (M + log2f(L)) * kLn2;

@@ -10,8 +10,8 @@
 //     same order), one conversion gives two fp16 values, two warp MMAs (fp16)
 //     sum a block of 32, and the block's scale is applied to the fp32 sum.
 //   O^T += V^T P^T: a lane pairs the codes of two keys in a byte, one
-//     conversion gives their fp16 pair. V's block scales go into P, one P^T
-//     per block of 32 columns.
+//     conversion gives their fp16 pair. V's block scales go into P (in fp32, then
+//     rounded to fp16, State4), one P^T per block of 32 columns.
 // Measured (d = 128): 64 ragged sequences of up to 32768 rows at G = 8, 584 MB,
 // 123 us, issue 73 % and the ALU 61 % busy in the loop; the same rows in TMA
 // boxes with a producer warp and four codes to a load took 226. 16 sequences of
@@ -20,6 +20,7 @@
 // own ring of shared-memory stages by asynchronous copies: no barrier between
 // warps but at the end of a segment.
 #include <cuda_fp16.h>
+#include <float.h>
 
 #include "decode_paged.cuh"
 
@@ -63,12 +64,105 @@ struct Mx4Pages {
   int64_t depth_b, depth_hk, depth_slot;  // bytes
 };
 
-// m is kept 7 below the largest score (with its values' exponent) when it is
-// raised, and raised again only when a score is 8 above that: weights stay
-// below 2^15.01 in fp16, the largest is 2^7 at least, so that they keep their
-// 11 bits down to 2^-21 of it and lose at most 2^-32 of it below.
-constexpr float kHeadroom = 7.f;
-constexpr float kSlack = 8.f;
+// Weights are held in fp32 as p = 2^(score - m), for the sum l, and as p c, which
+// times a block scale of V goes into the products with fp16's range. m is the
+// scores' alone: what a row weighs in l has nothing to do with its values. (One
+// reference for both, the score's plus the values' exponent, lost rows of zeros
+// from l beside values of 2^60.) c is a factor of the head that puts the
+// largest product so far at 2^kTop when it is set, and is set again when a product
+// passes 2^kMost: products stay in fp16's range, and as the largest is 2^kTop at
+// least, keep their 11 bits down to 2^-21 of it and lose at most 2^-32 of it below
+// (2^-31 beside values of 2^100 and more, where p c has few bits left in fp32).
+// m is raised when a lane's four weights sum to more than kMostWeight.
+constexpr float kTop = 7.f;
+constexpr float kMost = 0x1p15f;
+constexpr float kMostWeight = 0x1p8f;
+
+template <int D, int NT>
+struct State4 : State<D, NT> {
+  using State<D, NT>::m;
+  using State<D, NT>::l;
+  using State<D, NT>::o;  // sums of p c times values
+  float c[NT][2];
+  // m from the least of all scores, for which the first key's weight is infinite.
+  __device__ __forceinline__ void clear() {
+    State<D, NT>::clear();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      m[t][0] = m[t][1] = -FLT_MAX;
+      c[t][0] = c[t][1] = 1.f;
+    }
+  }
+  // x: N scores over `back`, of head 2c at even and 2c + 1 at odd places, two to
+  // a key; v: the largest block scale of each key's values (a power of two).
+  // Adds the keys to l and leaves p c in w.
+  template <int N>
+  __device__ __forceinline__ void weigh(int t, const float (&x)[N], const float (&back)[2],
+                                        const float (&v)[N / 2], float (&w)[N]) {
+    float sum[2], most[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int i = e; i < N; i += 2) w[i] = sm103::ex2_approx(fmaf(x[i], back[e], -m[t][e]));
+      add_up<N>(t, e, v, w, sum[e], most[e]);
+    }
+    if (__any_sync(0xffffffffu, most[0] > kMost || most[1] > kMost || sum[0] > kMostWeight || sum[1] > kMostWeight)) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        rebase<N>(t, e, x, back[e], v);
+#pragma unroll
+        for (int i = e; i < N; i += 2) w[i] = sm103::ex2_approx(fmaf(x[i], back[e], -m[t][e]));
+        add_up<N>(t, e, v, w, sum[e], most[e]);
+      }
+    }
+    l[t][0] += sum[0];
+    l[t][1] += sum[1];
+  }
+  // The sum of head 2c + e's weights, then w = p c and the largest product.
+  template <int N>
+  __device__ __forceinline__ void add_up(int t, int e, const float (&v)[N / 2], float (&w)[N], float& sum,
+                                         float& most) const {
+    sum = w[e] + w[e + 2];
+#pragma unroll
+    for (int i = 4; i < N; i += 4) sum += w[i + e] + w[i + e + 2];
+    most = 0.f;
+#pragma unroll
+    for (int i = e; i < N; i += 2) {
+      w[i] *= c[t][e];
+      most = fmaxf(most, w[i] * v[i >> 1]);
+    }
+  }
+  // m to cover the scores and c the products, where these are more than before;
+  // l and o follow. r = m - log2(c) is what o is relative to. As no row's values
+  // are counted below 2^-80 or above 2^125, c is between 2^-118 and 2^95.
+  template <int N>
+  __device__ __forceinline__ void rebase(int t, int e, const float (&x)[N], float back, const float (&v)[N / 2]) {
+    float s = -INFINITY, z = -INFINITY;
+#pragma unroll
+    for (int i = e; i < N; i += 2) {
+      const float score = x[i] * back;
+      s = fmaxf(s, score);
+      z = fmaxf(z, score + (__uint_as_float(0x4b000000u | (__float_as_uint(v[i >> 1]) >> 23)) -
+                            (8388608.f + 127.f + kTop)));  // v's exponent as a float, by way of 2^23
+    }
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, off));
+      z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, off));
+    }
+    const float m0 = m[t][e], m1 = fmaxf(m0, s);
+    const float r0 = m0 - __log2f(c[t][e]), r1 = fmaxf(r0, z);
+    const float a = sm103::ex2_approx(r0 - r1);
+    l[t][e] *= sm103::ex2_approx(m0 - m1);
+    c[t][e] = sm103::ex2_approx(m1 - r1);
+    m[t][e] = m1;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      o[t][i][e] *= a;
+      o[t][i][e + 2] *= a;
+    }
+  }
+};
 
 // Byte offset of 16-byte vector `v` (block v of 32 codes) of row r, placed so
 // that none of these meet in a bank: whole rows side by side (the copies), 8
@@ -207,7 +301,7 @@ __device__ __forceinline__ void cp_wait() {
 
 // Weights of 16 depth slots, as B tiles of O^T += V^T P^T: bf16 and the rest.
 template <int D, int NT>
-__device__ __forceinline__ void depth_scores(State<D, NT>& st, const uint32_t (&qb)[NT][D / 16][2],
+__device__ __forceinline__ void depth_scores(State4<D, NT>& st, const uint32_t (&qb)[NT][D / 16][2],
                                              uint32_t kb, int there, float scale_log2, int lane,
                                              uint32_t (&pb)[NT][2], uint32_t (&pl)[NT][2]) {
   const int lr = lane & 7, lm = lane >> 3;
@@ -224,19 +318,15 @@ __device__ __forceinline__ void depth_scores(State<D, NT>& st, const uint32_t (&
   }
   const int ka = key_of(lane >> 2);
   const bool k0 = ka < there, k1 = ka + 2 < there;
+  const float back[2] = {scale_log2, scale_log2}, v[2] = {1.f, 1.f};  // their values in bf16 have their own range
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    s[t][0] = k0 ? s[t][0] * scale_log2 : -INFINITY;
-    s[t][1] = k0 ? s[t][1] * scale_log2 : -INFINITY;
-    s[t][2] = k1 ? s[t][2] * scale_log2 : -INFINITY;
-    s[t][3] = k1 ? s[t][3] * scale_log2 : -INFINITY;
-    const float z[4] = {s[t][0] - kHeadroom, s[t][1] - kHeadroom, s[t][2] - kHeadroom,
-                        s[t][3] - kHeadroom};
-    st.template raise<4>(t, z, kSlack);
-    float p[4];
-    st.weigh(t, s[t], p);
-    weights_bf16(p[0], p[1], pb[t][0], pl[t][0]);
-    weights_bf16(p[2], p[3], pb[t][1], pl[t][1]);
+    if (!k0) s[t][0] = s[t][1] = -INFINITY;
+    if (!k1) s[t][2] = s[t][3] = -INFINITY;
+    float w[4];
+    st.template weigh<4>(t, s[t], back, v, w);
+    weights_bf16(w[0], w[1], pb[t][0], pl[t][0]);
+    weights_bf16(w[2], w[3], pb[t][1], pl[t][1]);
   }
 }
 
@@ -244,7 +334,7 @@ __device__ __forceinline__ void depth_scores(State<D, NT>& st, const uint32_t (&
 // d = 32 g + 2 r0 in row r0 and 32 g + 16 + 2 r0 in r0 + 8, tile 2g + 1 the
 // elements after them. Rows past L are zeros.
 template <int D, int NT>
-__device__ __forceinline__ void depth_values(State<D, NT>& st, const uint32_t (&pb)[NT][2],
+__device__ __forceinline__ void depth_values(State4<D, NT>& st, const uint32_t (&pb)[NT][2],
                                              const uint32_t (&pl)[NT][2], uint32_t vb, int lane) {
   const int r0 = lane >> 2, v0 = 4 * (lane & 3);
 #pragma unroll
@@ -297,7 +387,7 @@ struct Lane {
 // The 32 rows of a unit (in the stage at `sb`) into the state, two tiles of 16
 // keys side by side. TAIL: only `there` of them exist.
 template <int D, int NT, bool TAIL>
-__device__ __forceinline__ void unit_mx4(State<D, NT>& st, const uint32_t (&qb)[NT][D / 32][4],
+__device__ __forceinline__ void unit_mx4(State4<D, NT>& st, const uint32_t (&qb)[NT][D / 32][4],
                                          const float (&back)[NT][2], const Lane<D>& at, uint32_t sb, int there,
                                          int lane) {
   using S = Stage<D>;
@@ -328,9 +418,9 @@ __device__ __forceinline__ void unit_mx4(State<D, NT>& st, const uint32_t (&qb)[
       }
     }
   }
-  // V's scales, and the exponent of each row's largest, from -80 so that the
-  // sum of 2^(score - m) stays in range. A block stored as NaN (its codes are
-  // 0, and 0 times infinity is NaN) leaves the other blocks' alone.
+  // V's scales, and each row's largest, 2^-80 at least, so that c stays in range.
+  // A block stored as NaN (its codes are 0, and 0 times infinity is NaN) leaves
+  // the other blocks' alone.
   float f[4][NB], e[4];
   uint32_t dead = 0;  // bit n: this lane's key n does not exist
 #pragma unroll
@@ -354,29 +444,16 @@ __device__ __forceinline__ void unit_mx4(State<D, NT>& st, const uint32_t (&qb)[
         if (f[n][g] < INFINITY) e[n] = fmaxf(e[n], f[n][g]);
     }
   }
-#pragma unroll
-  for (int n = 0; n < 4; ++n)  // as a float, by way of 2^23 + its biased form
-    e[n] = __uint_as_float(0x4b000000u | (__float_as_uint(e[n]) >> 23)) - (8388608.f + 127.f + kHeadroom);
+  float w[NT][8];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    float z[8];
+    float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float& x = s[i >> 2][t][i & 3];
-      if (TAIL && (dead >> (i >> 1) & 1u)) x = -INFINITY;
-      z[i] = fmaf(x, back[t][i & 1], e[i >> 1]);
+      x[i] = s[i >> 2][t][i & 3];
+      if (TAIL && (dead >> (i >> 1) & 1u)) x[i] = -INFINITY;
     }
-    st.template raise<8>(t, z, kSlack);
-    // p = 2^(score - m); a row of no finite score so far keeps m = -infinity
-    const float n0 = st.m[t][0] == -INFINITY ? 0.f : -st.m[t][0];
-    const float n1 = st.m[t][1] == -INFINITY ? 0.f : -st.m[t][1];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float& x = s[i >> 2][t][i & 3];
-      x = sm103::ex2_approx(fmaf(x, back[t][i & 1], i & 1 ? n1 : n0));
-    }
-    st.l[t][0] += (s[0][t][0] + s[0][t][2]) + (s[1][t][0] + s[1][t][2]);
-    st.l[t][1] += (s[0][t][1] + s[0][t][3]) + (s[1][t][1] + s[1][t][3]);
+    st.template weigh<8>(t, x, back[t], e, w[t]);
   }
 #pragma unroll
   for (int j = 0; j < 2; ++j)
@@ -400,7 +477,7 @@ __device__ __forceinline__ void unit_mx4(State<D, NT>& st, const uint32_t (&qb)[
         const float f0 = f[2 * j][g], f1 = f[2 * j + 1][g];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const float(&p)[4] = s[j][t];
+          const float* p = w[t] + 4 * j;
           const uint32_t pb0 = wmma16::movmatrix_t(pack_f16(p[0] * f0, p[1] * f0));
           const uint32_t pb1 = wmma16::movmatrix_t(pack_f16(p[2] * f1, p[3] * f1));
           mma_f16(st.o[t][2 * g], a, pb0, pb1);
@@ -587,7 +664,7 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
   GroupSmem<D, kWarps>& last = *reinterpret_cast<GroupSmem<D, kWarps>*>(sm.ring);  // when the rings are free
   static_assert(sizeof(GroupSmem<D, kWarps>) <= sizeof(sm.ring));
   const int64_t first_row = ((int64_t)at.b * p.Hk + at.hk) * p.G;
-  State<D, NT> st;
+  State4<D, NT> st;
   int left = sh.n;
   int turn = 0;  // the warp that takes the unit at `at`
   bool opened = false;
@@ -624,15 +701,16 @@ decode_paged_mx4_split(const __grid_constant__ Params p, const __grid_constant__
     }
     const auto put = [&](float* m0, float* m1, int t, int part, const auto& buf) {
       constexpr int kBlocks = std::remove_reference_t<decltype(buf)>::kCols / 32;
+      const float u0 = __fdividef(1.f / kUnit4, st.c[t][0]), u1 = __fdividef(1.f / kUnit4, st.c[t][1]);
 #pragma unroll
       for (int g = 0; g < kBlocks; ++g) {
         const float(&x)[4] = st.o[t][2 * (part * kBlocks + g)];
         const float(&y)[4] = st.o[t][2 * (part * kBlocks + g) + 1];
         const int d = g * 32 + (lane >> 2) * 2;
-        *reinterpret_cast<float2*>(m0 + d) = make_float2(x[0], y[0]);
-        *reinterpret_cast<float2*>(m1 + d) = make_float2(x[1], y[1]);
-        *reinterpret_cast<float2*>(m0 + d + 16) = make_float2(x[2], y[2]);
-        *reinterpret_cast<float2*>(m1 + d + 16) = make_float2(x[3], y[3]);
+        *reinterpret_cast<float2*>(m0 + d) = make_float2(x[0] * u0, y[0] * u0);
+        *reinterpret_cast<float2*>(m1 + d) = make_float2(x[1] * u1, y[1] * u1);
+        *reinterpret_cast<float2*>(m0 + d + 16) = make_float2(x[2] * u0, y[2] * u0);
+        *reinterpret_cast<float2*>(m1 + d + 16) = make_float2(x[3] * u1, y[3] * u1);
       }
     };
     if constexpr (GROUP) {
