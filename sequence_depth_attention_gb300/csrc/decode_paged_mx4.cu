@@ -109,9 +109,7 @@ struct State4 : State<D, NT> {
     if (__any_sync(0xffffffffu, most[0] > kMost || most[1] > kMost || sum[0] > kMostWeight || sum[1] > kMostWeight)) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        rebase<N>(t, e, x, back[e], v);
-#pragma unroll
-        for (int i = e; i < N; i += 2) w[i] = sm103::ex2_approx(fmaf(x[i], back[e], -m[t][e]));
+        rebase<N>(t, e, x, back[e], v, w);
         add_up<N>(t, e, v, w, sum[e], most[e]);
       }
     }
@@ -133,28 +131,36 @@ struct State4 : State<D, NT> {
     }
   }
   // m to cover the scores and c the products, where these are more than before;
-  // l and o follow. r = m - log2(c) is what o is relative to. As no row's values
-  // are counted below 2^-80 or above 2^125, c is between 2^-118 and 2^95.
+  // l and o follow. (m - log2(c) is what o is relative to.) As no row's values are
+  // counted below 2^-80 or above 2^125, c is between 2^-118 and 2^95. Leaves p in w.
+  // Works with scores rounded as m is and their differences: the fused product of
+  // weigh keeps what m was rounded by, which is 2^7 at scores of 2^31.
   template <int N>
-  __device__ __forceinline__ void rebase(int t, int e, const float (&x)[N], float back, const float (&v)[N / 2]) {
+  __device__ __forceinline__ void rebase(int t, int e, const float (&x)[N], float back, const float (&v)[N / 2],
+                                         float (&w)[N]) {
+    auto most = [](float a) {
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+      return a;
+    };
     float s = -INFINITY, z = -INFINITY;
 #pragma unroll
     for (int i = e; i < N; i += 2) {
-      const float score = x[i] * back;
-      s = fmaxf(s, score);
-      z = fmaxf(z, score + (__uint_as_float(0x4b000000u | (__float_as_uint(v[i >> 1]) >> 23)) -
-                            (8388608.f + 127.f + kTop)));  // v's exponent as a float, by way of 2^23
+      w[i] = __fmul_rn(x[i], back);
+      s = fmaxf(s, w[i]);
     }
+    const float m1 = fmaxf(m[t][e], most(s)), raised = m[t][e] - m1;
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-      s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, off));
-      z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, off));
+    for (int i = e; i < N; i += 2) {
+      w[i] -= m1;
+      z = fmaxf(z, w[i] + (__uint_as_float(0x4b000000u | (__float_as_uint(v[i >> 1]) >> 23)) -
+                           (8388608.f + 127.f + kTop)));  // v's exponent as a float, by way of 2^23
+      w[i] = sm103::ex2_approx(w[i]);
     }
-    const float m0 = m[t][e], m1 = fmaxf(m0, s);
-    const float r0 = m0 - __log2f(c[t][e]), r1 = fmaxf(r0, z);
+    const float r0 = raised - __log2f(c[t][e]), r1 = fmaxf(r0, most(z));
     const float a = sm103::ex2_approx(r0 - r1);
-    l[t][e] *= sm103::ex2_approx(m0 - m1);
-    c[t][e] = sm103::ex2_approx(m1 - r1);
+    l[t][e] *= sm103::ex2_approx(raised);
+    c[t][e] = sm103::ex2_approx(-r1);
     m[t][e] = m1;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {

@@ -136,3 +136,47 @@ def test_scores_of_zero_values_reach_the_sum(monkeypatch, least_rows):
         empty = n == 0
         assert (lse[empty] == -math.inf).all()
         assert ((lse.double() - want).abs() <= tol)[~empty].all()
+
+
+@pytest.mark.parametrize("least_rows", [0, 16384], ids=["narrow", "wide"])
+@pytest.mark.parametrize("fmt", ["bf16", "mx4"])
+@pytest.mark.parametrize("e,ev", [(20, 0), (30, 0), (45, 100), (90, 0), (90, -60)])
+def test_scores_of_any_size(monkeypatch, fmt, e, ev, least_rows):
+    """Keys of 2^e (and values of 2^ev): the row of the highest score has all of the weight, whatever
+    fp32 rounds a score by, as long as no other is as near as that. o is that row
+    of V, rounded to bf16 once (and by 2^-12 in fp16 over 4-bit pages, with 2^-19
+    for what l and o are rescaled by), lse its score."""
+    monkeypatch.setattr(pc.Cache, "least_rows", least_rows)
+    d, Hk, G, L = 64, 2, 4, 5
+    lens = [1, 40, 700, 3000]
+    c = pc.Cache(fmt, lens, Hk, d, 16, seed=46, device="cuda")
+    if fmt == "mx4":
+        c.ks[c.ks != 255] += e
+        c.vs[c.vs != 255] += ev % 256
+    else:
+        c.k.mul_(2.0 ** e)
+        c.v.mul_(2.0 ** ev)
+    g = torch.Generator().manual_seed(47)
+    q = torch.randn(len(lens), Hk * G, d, generator=g).bfloat16().cuda()
+    kd, vd = (torch.randn(len(lens), Hk, L, d, generator=g).bfloat16().cuda() for _ in range(2))
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = moda.moda_decode_paged(q, *c.args(), n, 0.125, kd=kd, vd=vd, **c.scales())
+    torch.cuda.synchronize()
+    assert moda.moda_get_device_error() == 0
+    clear = 0
+    for b, m in enumerate(lens):
+        k = torch.cat((c.rows("k", b, m), kd[b].double()), 1)
+        v = torch.cat((c.rows("v", b, m), vd[b].double()), 1)
+        qb = q[b].double().view(Hk, G, d)
+        z = qb @ k.transpose(1, 2) * 0.125
+        ds = (d + 4) * pc.HALF_FP32 * 0.125 * (qb.abs() @ k.abs().transpose(1, 2)).amax(-1)
+        top = z.topk(2, -1)
+        alone = (top.values[..., 0] - top.values[..., 1] > 2 * ds + 30).reshape(-1)
+        clear += int(alone.sum())
+        want = torch.gather(v, 1, top.indices[..., :1].expand(-1, -1, d)).reshape(-1, d)
+        assert torch.isfinite(o[b]).all() and torch.isfinite(lse[b]).all()
+        tol = (pc.HALF_BF16 + pc.HALF_FP16 + 2.0 ** -19) * want.abs() + (m + L) * 2.0 ** -31 * v.abs().max()
+        assert ((o[b].double() - want).abs() <= tol)[alone].all()
+        high = top.values[..., 0].reshape(-1)
+        assert ((lse[b].double() - high).abs() <= ds.reshape(-1) + high.abs() * 2.0 ** -22 + 2.0 ** -19)[alone].all()
+    assert clear >= 24  # of 32 heads
