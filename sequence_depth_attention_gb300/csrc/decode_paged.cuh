@@ -421,7 +421,10 @@ __device__ __forceinline__ void leave(const Params& p, MergeSmem<WARPS, COLS>& s
                                       bool cut, float* part_o, float* part_ml, int64_t slot, int64_t row0,
                                       Put put) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane & 3;
-  auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory"); };
+  auto meet = [] {
+    __syncwarp();  // the barrier wants whole warps, whose lanes leave the loops below at different times
+    asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
+  };
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -516,6 +519,7 @@ __device__ __forceinline__ void add_partials(float& M, float& L, float (&acc)[E]
 }
 
 __device__ __forceinline__ void cluster_meet() {
+  __syncwarp();  // .aligned: whole warps, see meet in leave
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t smem, int rank) {

@@ -88,3 +88,19 @@ def test_accuracy_as_documented(fmt, G, d, page, Hk, L, lens, table_of):
     for b, n in enumerate(lens):
         want, tol = pt.one(c, b, n, q, kd, vd, d ** -0.5)
         assert ((o[b].double().view(Hk, G, d) - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mx4"])
+@pytest.mark.parametrize("G", [1, 3, 5, 7, 9, 11, 13, 15])
+def test_odd_head_counts_in_clusters(fmt, G, table_of):
+    """d = 64 and odd G: the columns that a cluster joins do not fill its warps."""
+    lens = [500, 1, 0, 64, 333]
+    c = pc.Cache(fmt, lens, 1, 64, 16, seed=56, device="cuda")
+    q = queries(len(lens), G, 64, 57)
+    o = decode(c, q, None, None, 0.125)
+    for b, n in enumerate(lens):
+        if n == 0:
+            assert (o[b] == 0).all()
+            continue
+        want, tol = pt.one(c, b, n, q, None, None, 0.125)
+        assert ((o[b].double().view(1, G, 64) - want).abs() <= tol).all()
