@@ -15,6 +15,7 @@ import importlib.machinery
 import importlib.util
 import os
 import threading
+import warnings
 
 import torch
 
@@ -54,18 +55,26 @@ _paged = None  # the extension module that marshals the paged calls' arguments
 
 
 def _load_paged(lib):
-    if not os.path.exists(_EXT):
-        raise ModaError(6, "load", f"{_EXT} is missing; build it with "
-                        "`python -m sequence_depth_attention_gb300.build`")
-    loader = importlib.machinery.ExtensionFileLoader("paged_py", _EXT)
-    ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("paged_py", loader))
-    loader.exec_module(ext)
-    address = (ctypes.cast(f, ctypes.c_void_p).value
-               for f in (lib.moda_kv_append, lib.moda_kv_gather, lib.moda_decode_paged,
-                         lib.moda_decode_paged_workspace_bytes))
-    # (for the current device without torch.cuda's start-up: the tensors have seen to it)
-    ext.setup(torch.Tensor, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, *address)
-    return ext
+    """The extension, or None where it is missing, was built for another torch or does
+    not load: the paged calls then go through this module's Python code alone."""
+    try:
+        with open(_EXT + ".torch") as f:
+            built_for = f.read()
+        if built_for != torch.__version__:
+            raise ImportError(f"built for torch {built_for}, this is {torch.__version__}")
+        loader = importlib.machinery.ExtensionFileLoader("paged_py", _EXT)
+        ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("paged_py", loader))
+        loader.exec_module(ext)
+        address = (ctypes.cast(f, ctypes.c_void_p).value
+                   for f in (lib.moda_kv_append, lib.moda_kv_gather, lib.moda_decode_paged,
+                             lib.moda_decode_paged_workspace_bytes))
+        # (for the current device without torch.cuda's start-up: the tensors have seen to it)
+        ext.setup(torch.Tensor, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, *address)
+        return ext
+    except (OSError, ImportError, AttributeError) as e:
+        warnings.warn(f"paged_py is not used ({e}): paged calls take a few us longer; "
+                      "`python -m sequence_depth_attention_gb300.build` makes it", RuntimeWarning, stacklevel=3)
+        return None
 
 
 class ModaError(RuntimeError):

@@ -6,7 +6,8 @@ Each .cu under csrc/ is compiled in parallel to an object, then linked into
 ``_build/libmoda.so`` with the CUDA runtime linked statically, so the library
 depends only on the driver. Objects are rebuilt when a source or header is
 newer than them. csrc/paged_py.cpp becomes the Python extension module
-``_build/paged_py.so`` (g++ and PyTorch's headers, no CUDA).
+``_build/paged_py.so`` (g++, Python's and PyTorch's headers, no CUDA); where that
+fails the library is built all the same, with a warning.
 """
 from __future__ import annotations
 
@@ -17,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -96,7 +98,13 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
         ext = ex.submit(build_extension, force)
         results = list(ex.map(compile_one, srcs))
-        ext.result()
+        try:
+            ext.result()
+        except (ImportError, OSError, RuntimeError) as e:
+            for stale in (EXT, EXT + ".torch"):
+                if os.path.exists(stale):
+                    os.remove(stale)
+            warnings.warn(f"paged_py is not built, paged calls take a few us longer: {e}", RuntimeWarning)
     if verbose:
         for _, log in results:
             if log:
