@@ -18,7 +18,8 @@
  *     nothing is launched. A failure inside a running kernel (a bounded wait
  *     that gave up) is latched in a per-device error word and reported by
  *     moda_get_device_error().
- *   - Batch is 1; callers loop over sequences.
+ *   - Batch is 1 and callers loop over sequences, but for the paged cache's calls
+ *     (moda_kv_append, moda_kv_gather, moda_decode_paged), which take a batch.
  *   - Thread safety: calls may be made from several host threads.
  *   - moda_fwd, moda_fwd_layer_major and moda_fwd_depth_cc hand out their
  *     tiles through a small per-device queue; each call takes the next of 64 queues
@@ -49,7 +50,8 @@ typedef struct CUstream_st* moda_stream_t; /* identical to cudaStream_t */
 typedef enum {
   MODA_OK = 0,
   MODA_ERR_INVALID_ARG = 1, /* NULL pointer, T < 1, L < 0, Hq % Hk != 0, aliasing */
-  MODA_ERR_UNSUPPORTED = 2, /* d not in {64, 128}; G = Hq/Hk not in {1,2,4,8,16}; sizes too large */
+  MODA_ERR_UNSUPPORTED = 2, /* d not in {64, 128}; G = Hq/Hk not in {1,2,4,8,16} (moda_decode_paged: not
+                               1 to 16); sizes too large */
   MODA_ERR_MISALIGNED = 3,  /* a tensor pointer not 16-byte aligned */
   MODA_ERR_CUDA = 4,        /* the CUDA runtime reported an error at launch */
   MODA_ERR_TIMEOUT = 5,     /* a kernel's bounded wait gave up (device-side) */
@@ -444,9 +446,11 @@ MODA_API moda_status moda_kv_append(const void* q, const void* k, const void* v,
  * moda_kv_gather -- rows of the pages as dense bf16: k[n,hk,:] and v[n,hk,:]
  * are the row of (seq[n], pos[n]). For bf16 pages the stored bits, for MX4
  * pages the values that the codes stand for, which bf16 holds exactly (from
- * 2^128 on, which moda_kv_append never stores, infinity). A pass over the next
- * piece of a prompt gathers the rows cached before it. Rows may be named any
- * number of times, in any order.
+ * 2^128 on, which moda_kv_append never stores, infinity). It gives a caller the
+ * rows as later steps will see them: a prompt's own 4-bit rows for its moda_fwd,
+ * or a cached prefix for a pass of the caller's (no call here attends with fewer
+ * queries than keys but moda_decode_paged, which reads the pages itself). Rows may
+ * be named any number of times, in any order.
  *   seq, pos  [N] int32 as in moda_kv_append; a row whose seq is -1 (or whose
  *             index is out of range, which is latched) is left as it was
  *   k, v      [N, Hk, d] bf16 outputs; must not overlap the pages or each other

@@ -151,7 +151,8 @@ __device__ __forceinline__ Share<KEYS> share_of(const Params& p, int depth_units
   constexpr int THREADS = WARPS * 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // The block table is needed as soon as the lengths are known: the grid asks
-  // for it meanwhile, a line a thread (up to 5 MB of it).
+  // for it meanwhile, a line of 128 bytes a thread. (In all up to 6.2 MB in bf16, 7.5 MB
+  // in 4 bits at three CTAs an SM; the table's whole width, whatever the lengths are.)
   {
     const int64_t line = (int64_t)blockIdx.x * THREADS + tid;
     if (line * 32 < (int64_t)p.B * p.max_pages)
@@ -457,8 +458,9 @@ __device__ __forceinline__ void leave(const Params& p, MergeSmem<WARPS, COLS>& s
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
           const float mw = sm.ml[w][h][0];
-          // a state that has met no key is (-infinity, 0, 0); one that has met
-          // only NaN scores has -infinity too, and its NaN must go on
+          // a state that has met no key is (-infinity, 0, 0), or has the least
+          // float for m; one that has met only NaN scores has that too, and its
+          // NaN must go on
           const float a = mw == -INFINITY ? 1.f : sm103::ex2_approx(mw - M);
           const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][h][d]);
           L = fmaf(a, sm.ml[w][h][1], L);
@@ -496,8 +498,8 @@ struct GroupSmem {
 };
 
 // U partial states (m, l, o) added to the state (M, L, acc). An empty one is
-// (-infinity, 0, 0); one that has met only NaN scores has -infinity too, and
-// its NaN must go on.
+// (-infinity, 0, 0), or has the least float for m; one that has met only NaN
+// scores has that too, and its NaN must go on.
 template <int U, int E>
 __device__ __forceinline__ void add_partials(float& M, float& L, float (&acc)[E], const float (&pm)[U],
                                              const float (&pl)[U], const float (&po)[U][E]) {
@@ -602,19 +604,20 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_
 // CTAs for each segment of a short batch: a group, where no segment can have
 // more than `most` units for each (for each two of 16); 0 where the batch is
 // better cut into equal shares. What the host knows of the lengths is the
-// table's width. Measured, GPU time in us, d = 128, G = 4, L = 24, against the
-// same calls with a wide table:
+// table's width: with a table for a model's longest context every batch is cut
+// into shares. Measured, GPU time in us, d = 128, G = 4, L = 24, groups of the
+// given number of CTAs against the same calls with a wide table:
 //   sequences x KV heads     rows      bf16 (most = 8)       4-bit (most = 21)
 //                                      group     shares      group     shares
-//           1 x 8             700     4.6 (8)     5.3       5.0 (8)     6.5
-//           1 x 4            4000     6.0 (16)    6.3       6.4 (16)    6.6
-//           1 x 4            8000     8.4 (16)    7.3       8.0 (16)    7.5
-//           8 x 8       1 .. 1000     6.5 (4)     8.3       7.3 (6)     9.9
-//           8 x 8       1 .. 4000    13.7 (4)    12.5      13.8 (4)    13.0
-//          22 x 4       1 .. 1000     7.1 (3)     9.1       7.7 (4)    10.7
-//          16 x 8       1 ..  700     7.4 (2)     9.3       7.9 (3)    11.0
-//          32 x 8       1 ..  256     5.6 (1)     9.7       7.8 (1)    11.5
-//          32 x 8       1 .. 1000    12.8 (1)    12.2      13.7 (1)    14.6
+//           1 x 8             700     4.6 (8)     5.3       5.2 (8)     6.6
+//           1 x 4            4000     6.1 (16)    6.4       6.4 (16)    7.1
+//           1 x 4            8000     8.4 (16)    7.3       7.9 (16)    7.7
+//           8 x 8       1 .. 1000     6.6 (4)     8.4       7.7 (6)    10.1
+//           8 x 8       1 .. 4000    13.7 (4)    12.5      14.2 (4)    13.4
+//          22 x 4       1 .. 1000     7.1 (3)     9.1       8.1 (4)    10.9
+//          16 x 8       1 ..  700     7.3 (2)     9.3       8.2 (3)    11.3
+//          32 x 8       1 ..  256     5.6 (1)     9.8       8.3 (1)    11.9
+//          32 x 8       1 .. 1000    12.8 (1)    12.2      14.0 (1)    15.1
 // More CTAs are better as long as all clusters fit the SMs at once (8 or 4 at
 // 15/16 of the places did not: 6.5 -> 10), 16 where 8 would have many units each
 // and there is an SM for each CTA. A cluster costs as much as `cluster_units`

@@ -13,9 +13,9 @@
 //     conversion gives their fp16 pair. V's block scales go into P (in fp32, then
 //     rounded to fp16, State4), one P^T per block of 32 columns.
 // Measured (d = 128): 64 ragged sequences of up to 32768 rows at G = 8, 584 MB,
-// 123 us, issue 73 % and the ALU 61 % busy in the loop; the same rows in TMA
-// boxes with a producer warp and four codes to a load took 226. 16 sequences of
-// up to 999 rows (d = 64, 8 KV heads, G = 8), in clusters of three, 7.1 us.
+// 123 us, 675 instructions a unit; the same rows in TMA boxes with a producer
+// warp and four codes to a load took 226. 16 sequences of
+// up to 999 rows (d = 64, 8 KV heads, G = 8), in clusters of three, 7.3 us.
 // Each warp streams units of its own (32 rows, or 16 depth slots) through its
 // own ring of shared-memory stages by asynchronous copies: no barrier between
 // warps but at the end of a segment.
@@ -32,9 +32,9 @@ constexpr int kWarps = 4;
 constexpr int kKeys = 32;       // cached rows of a unit
 constexpr int kDepthKeys = 16;  // depth slots of a unit; their K and V take a stage each
 constexpr int kNS = 3;          // stages of a warp
-// Entering and leaving a segment, in units. (64 ragged sequences of up to 32768
-// rows, G = 8, at 6, 8, 10, 12: 122, 121, 119, 119 us; of up to 8000, G = 16, at
-// 6, 10, 14, 18: 68, 60, 57, 57.)
+// Entering and leaving a segment, in units. (4 KV heads, 64 ragged sequences of up
+// to 32768 rows, G = 8, at 6, 10, 14, 18: 123.6, 123.3, 123.9, 124.6 us; of up to
+// 8000, G = 16, 139 MB: 67, 56.3, 55.1, 56.1.)
 template <int D, int NT>
 constexpr int kCost = NT == 1 ? (D == 128 ? 10 : 12) : 14;
 // 168 registers (two head tiles: 255): four at 128 registers were 6 % slower
@@ -73,6 +73,9 @@ struct Mx4Pages {
 // passes 2^kMost: products stay in fp16's range, and as the largest is 2^kTop at
 // least, keep their 11 bits down to 2^-21 of it and lose at most 2^-32 of it below
 // (2^-31 beside values of 2^100 and more, where p c has few bits left in fp32).
+// One rounding to fp16 is a choice: with what it leaves in a second part and two
+// more products, 64 ragged sequences take 141 us instead of 123, and o, against 64
+// bits, is off by 1.667e-3 of its norm instead of 1.670e-3 (o's own rounding to bf16).
 // m is raised when a lane's four weights sum to more than kMostWeight.
 constexpr float kTop = 7.f;
 constexpr float kMost = 0x1p15f;
