@@ -487,18 +487,18 @@ MODA_API moda_status moda_kv_gather(const moda_paged_kv* cache, const int* seq, 
  * and is latched.
  * Arithmetic: fp32 accumulation, softmax in fp32. bf16 pages and the depth
  * slots: probabilities in two bf16 parts, so that o is right to its own
- * rounding. MX4 pages: the codes'
- * exact values against q in fp16 (scaled per head, so that its 8 bits stay),
- * block scales applied in fp32; probabilities summed in fp32, and times V's block
- * scales rounded to fp16 under a running factor per head: to 11 bits, and to 2^-32
- * of the largest of them where that is more (2^-31 beside V scales of 2^100 and
- * more). (Scale byte 0, which moda_kv_append never writes, is read as 0 here,
- * 2^-80 is the least that V's scales count for in the running factor. K's values
- * below 2^100 cannot overflow a score's fp32 sum, and scale times a head's largest
- * |q| counts for 2^-112 at least.) Both: a probability below 2^-126 of the largest
- * may count as 0; the sums of V are in fp32, of weights up to 2^8 (the depth
- * slots' beside MX4 pages 2^15), and overflow where such sums pass 2^128. (Sums
- * of MX4 values do not, for up to 2^24 rows.)
+ * rounding. MX4 pages: the codes' exact values against q in fp16 (scaled per
+ * head, so that its 8 bits stay down to 2^-24 of the head's largest element),
+ * block scales applied in fp32; probabilities summed in fp32, and times V's
+ * block scales rounded to fp16 under a running factor per head: to 11 bits, and
+ * to 2^-32 of the largest of them where that is more (2^-31 beside V scales of
+ * 2^100 and more). (Scale byte 0, which moda_kv_append never writes, is read as
+ * 0 here, 2^-80 is the least that V's scales count for in the running factor.
+ * K's values below 2^100 cannot overflow a score's fp32 sum, and scale times a
+ * head's largest |q| counts for 2^-112 at least.) Both: a probability below
+ * 2^-126 of the largest may count as 0; the sums of V are in fp32, of weights
+ * up to 2^8 (the depth slots' beside MX4 pages 2^15), and overflow where such
+ * sums pass 2^128. (Sums of MX4 values do not, for up to 2^24 rows.)
  * Supported: G = Hq/Hk from 1 to 16, B*Hq <= 2^24, 0 <= L <= 1024, scale > 0
  * and at most 2e38.
  * The result depends on how the batch is split over the SMs, for which
