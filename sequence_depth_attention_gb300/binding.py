@@ -576,6 +576,13 @@ def _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales):
                     v_pages.data_ptr(), ks, vs, block_table.data_ptr()), Hk, d, table[0]
 
 
+def _tensors(**named):
+    """Raises for the first that is neither None nor a tensor."""
+    for name, t in named.items():
+        if t is not None and not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor")
+
+
 def _rows_stride(dev, t, name, N, H, d):
     """The distance of the tokens of t[N,H,d], bf16 with dense tokens."""
     if not isinstance(t, torch.Tensor) or t.dtype is not _bf16:
@@ -619,6 +626,7 @@ def moda_kv_append(q, k, v, k_pages, v_pages, block_table, seq, pos, rope=None, 
     dev = _current_device()
     cache, Hk, d, _ = _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales)
     N = _tokens(dev, seq, pos)
+    _tensors(q=q, rope=rope)
     Hq = qs = qp = rows = rot = rp = 0
     if q is not None:
         Hq = q.shape[1] if q.dim() == 3 else 0
@@ -707,6 +715,7 @@ def moda_decode_paged(q, k_pages, v_pages, block_table, seq_lens, scale: float, 
     Hq = shape[1]
     L, kp, vp, strides = 0, None, None, (0, 0, 0)
     if kd is not None or vd is not None:
+        _tensors(kd=kd, vd=vd)
         if kd is None or vd is None:
             raise ValueError("kd and vd come together")
         dshape = kd.shape
