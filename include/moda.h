@@ -516,6 +516,56 @@ MODA_API moda_status moda_decode_paged(const void* q, const moda_paged_kv* cache
                                        size_t workspace_bytes, moda_stream_t stream);
 
 /*
+ * moda_prefill_paged -- several new tokens of each sequence over the paged cache: the
+ * next piece of a prompt after a cached prefix, or a draft to verify. The tokens
+ * q_starts[b] .. q_starts[b+1] - 1 are the last rows of sequence b (appended before):
+ * token n is row t = seq_lens[b] - (q_starts[b+1] - n) and attends, under one softmax,
+ * to the rows up to its own and to its L depth slots:
+ *   z = [ scale * q[n,h,:].K[b,j,hk,:]  for j <= t
+ *       | scale * q[n,h,:].kd[l,n,hk,:] for l < L ]
+ *   o[n,h,:] = sum softmax(z) * [ V[b,j,hk,:] | vd[l,n,hk,:] ],  lse = ln(sum exp z)
+ *
+ *   q         [N, Hq, d] bf16, turned by their positions (q_out of moda_kv_append),
+ *             consecutive tokens q_stride elements apart (a multiple of 8, at least
+ *             Hq*d; unused when N == 1)
+ *   q_starts  [B + 1] int32, device memory: 0 <= q_starts[b] <= q_starts[b+1] <= N. A
+ *             sequence may have no token; o and lse of tokens that belong to no
+ *             sequence (a padded batch's, behind the last) are left as they were.
+ *   seq_lens  [B] int32, device memory: rows of each sequence, its tokens' own among
+ *             them: q_starts[b+1] - q_starts[b] <= seq_lens[b] <= max_pages * page_size
+ *             A sequence whose starts or length are outside these ranges is left out,
+ *             which is latched. Entries of block_table past a sequence's last page are
+ *             not read.
+ *   kd, vd    the depth slots of the tokens, as the layers write them: slot l of
+ *             token n for KV head hk is the d bf16 values at l*depth_slot_stride +
+ *             n*depth_tok_stride + hk*depth_hk_stride (elements, multiples of 8, at least
+ *             d; one that steps along an axis of length 1 is unused). NULL when L == 0
+ *   o         [N, Hq, d] bf16; lse [N, Hq] fp32 (natural log) or NULL
+ *   workspace caller-owned device scratch, 16-byte aligned, of at least
+ *             moda_prefill_paged_workspace_bytes(Hq, Hk, d) bytes; holds nothing
+ *             between calls. Calls that may run at the same time need one each.
+ * A page index outside [0, num_pages) makes its sequence's result unspecified and is
+ * latched. What a query does not see (later rows, other tokens' slots, rows past a
+ * sequence's length) has no influence on its result, infinities and NaN included.
+ * Arithmetic: as moda_fwd (fp32 scores and sums, P rounded to bf16 once for the second
+ * product); MX4 rows count with their exact values, which bf16 holds. A weight below
+ * 2^-126 of the largest may count as 0.
+ * Supported: G = Hq/Hk from 1 to 16 (1, 2, 4, 8 and 16 use the tensor core's rows in
+ * full), N <= 2^24, N*Hq <= 2^31 - 1, 0 <= L <= 1024, scale > 0 and at most 2e38.
+ * Result bits depend on the batch as a whole (how it is cut) by the order of fp32 sums;
+ * the same call on the same device gives the same bits.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA; TIMEOUT via
+ * moda_get_device_error. N == 0 or B == 0 is a no-op.
+ */
+MODA_API size_t moda_prefill_paged_workspace_bytes(int Hq, int Hk, int d);
+MODA_API moda_status moda_prefill_paged(const void* q, long long q_stride, const moda_paged_kv* cache,
+                                        const int* q_starts, const int* seq_lens, const void* kd,
+                                        const void* vd, long long depth_slot_stride,
+                                        long long depth_tok_stride, long long depth_hk_stride, int N,
+                                        int Hq, int L, float scale, void* o, float* lse,
+                                        float* workspace, size_t workspace_bytes, moda_stream_t stream);
+
+/*
  * moda_bwd -- gradients of moda_fwd with respect to all of its inputs. The
  * pages time the fused operator forward + backward (Table 2, Table 7) without
  * writing the backward out; this is the chain rule through the joint softmax

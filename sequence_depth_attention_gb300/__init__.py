@@ -11,7 +11,8 @@ from .binding import (MODA_OK, ModaError, library_path, load, moda_bwd, moda_bwd
                       moda_depth_mass, moda_depth_mass_workspace_bytes, moda_depth_write,
                       moda_depth_write_at, moda_fwd, moda_fwd_host_workspace_bytes,
                       moda_fwd_layer_major, moda_fwd_layer_major_host, moda_get_device_error,
-                      moda_kv_append, moda_kv_gather, moda_kv_proj_write, moda_pack_depth, moda_selftest_wait_timeout,
+                      moda_kv_append, moda_kv_gather, moda_kv_proj_write, moda_pack_depth,
+                      moda_prefill_paged, moda_prefill_paged_workspace_bytes, moda_selftest_wait_timeout,
                       moda_status_string)
 
 __all__ = ["MODA_OK", "ModaError", "library_path", "load", "moda_bwd", "moda_bwd_noalloc",
@@ -20,5 +21,6 @@ __all__ = ["MODA_OK", "ModaError", "library_path", "load", "moda_bwd", "moda_bwd
            "moda_depth_mass", "moda_depth_mass_workspace_bytes", "moda_depth_write",
            "moda_depth_write_at", "moda_fwd", "moda_fwd_host_workspace_bytes",
            "moda_fwd_layer_major", "moda_fwd_layer_major_host", "moda_get_device_error",
-           "moda_kv_append", "moda_kv_gather", "moda_kv_proj_write", "moda_pack_depth", "moda_selftest_wait_timeout",
+           "moda_kv_append", "moda_kv_gather", "moda_kv_proj_write", "moda_pack_depth",
+           "moda_prefill_paged", "moda_prefill_paged_workspace_bytes", "moda_selftest_wait_timeout",
            "moda_status_string"]

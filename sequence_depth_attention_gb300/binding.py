@@ -35,7 +35,8 @@ EXPORTS = ("moda_pack_depth", "moda_depth_write", "moda_depth_write_at", "moda_d
            "moda_fwd_host_workspace_bytes", "moda_fwd_depth_cc", "moda_decode",
            "moda_decode_strided",
            "moda_decode_workspace_bytes", "moda_kv_append", "moda_kv_gather", "moda_decode_paged",
-           "moda_decode_paged_workspace_bytes",
+           "moda_decode_paged_workspace_bytes", "moda_prefill_paged",
+           "moda_prefill_paged_workspace_bytes",
            "moda_bwd", "moda_bwd_layer_major", "moda_bwd_noalloc", "moda_get_device_error",
            "moda_selftest_wait_timeout", "moda_status_string", "moda_last_error_detail")
 
@@ -132,6 +133,11 @@ def load():
         lib.moda_decode_paged.argtypes = [vp, cache, vp, vp, vp] + [ll] * 3 + [
             i, i, f, vp, vp, vp, ctypes.c_size_t, vp]
         lib.moda_decode_paged.restype = i
+        lib.moda_prefill_paged_workspace_bytes.argtypes = [i, i, i]
+        lib.moda_prefill_paged_workspace_bytes.restype = ctypes.c_size_t
+        lib.moda_prefill_paged.argtypes = [vp, ll, cache, vp, vp, vp, vp] + [ll] * 3 + [
+            i, i, i, f, vp, vp, vp, ctypes.c_size_t, vp]
+        lib.moda_prefill_paged.restype = i
         lib.moda_fwd.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, vp, vp, vp]
         lib.moda_fwd_depth_cc.restype = i
         lib.moda_fwd_depth_cc.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, vp, vp, vp]
@@ -751,6 +757,77 @@ def moda_decode_paged(q, k_pages, v_pages, block_table, seq_lens, scale: float, 
         _raw_stream(stream, dev))
     if st:
         _check(st, "moda_decode_paged")
+    return o, lse
+
+
+def _depth_views(dev, kd, vd, shape, what):
+    """(L, kd's and vd's addresses, their strides) of depth slots kd, vd whose shape is
+    `shape`, with one None where L stands; `what` names it in errors."""
+    if kd is None and vd is None:
+        return 0, None, None, (0, 0, 0)
+    _tensors(kd=kd, vd=vd)
+    if kd is None or vd is None:
+        raise ValueError("kd and vd come together")
+    have = kd.shape
+    if len(have) != 4 or vd.shape != have or any(w is not None and w != h for w, h in zip(shape, have)):
+        raise ValueError(f"kd and vd must be {what}")
+    L = have[shape.index(None)]
+    if not kd.numel():
+        return 0, None, None, (0, 0, 0)
+    strides = kd.stride()
+    for x, n in ((kd, "kd"), (vd, "vd")):
+        if x.dtype is not _bf16 or x.get_device() != dev or x.stride(3) != 1:
+            raise ValueError(f"{n}: expected a bf16 CUDA view {what} with contiguous rows on the current "
+                             f"device cuda:{dev}")
+    if any(h > 1 and a != b for h, a, b in zip(have, strides, vd.stride())):
+        raise ValueError("kd and vd must have the same strides")
+    return L, kd.data_ptr(), vd.data_ptr(), strides[:3]
+
+
+def moda_prefill_paged_workspace_bytes(Hq: int, Hk: int, d: int) -> int:
+    return int(load().moda_prefill_paged_workspace_bytes(int(Hq), int(Hk), int(d)))
+
+
+def moda_prefill_paged(q, k_pages, v_pages, block_table, q_starts, seq_lens, scale: float, kd=None, vd=None,
+                       k_scales=None, v_scales=None, o=None, lse=None, workspace=None, stream=None,
+                       want_lse: bool = True):
+    """Several new tokens of each sequence over the paged cache (see moda_kv_append):
+    tokens q_starts[b] .. q_starts[b+1]-1 are the last rows of sequence b and attend to
+    its rows up to their own and to their depth slots. q[N,Hq,d] bf16 (a view with dense
+    tokens allowed), q_starts[B+1] and seq_lens[B] int32, kd/vd [L,N,Hk,d] bf16 views with
+    contiguous rows of d values (None when L == 0).
+    Returns (o[N,Hq,d] bf16, lse[N,Hq] fp32 or None); rows of tokens behind the last
+    sequence are left as they were, in new tensors undefined."""
+    dev = _current_device()
+    cache, Hk, d, B = _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales)
+    if not (_here(q_starts, _i32, dev) and _here(seq_lens, _i32, dev)):
+        _refuse(dev, (q_starts, "q_starts", _i32), (seq_lens, "seq_lens", _i32))
+    if q_starts.shape != (B + 1,) or seq_lens.shape != (B,):
+        raise ValueError(f"q_starts must be [B+1] and seq_lens [B] with B={B}")
+    _tensors(q=q)
+    if q is None or q.dim() != 3 or q.shape[2] != d:
+        raise ValueError(f"q must be [N,Hq,d] with d={d}")
+    N, Hq, _ = shape = q.shape
+    qs = _rows_stride(dev, q, "q", N, Hq, d)
+    L, kp, vp, strides = _depth_views(dev, kd, vd, (None, N, Hk, d), f"[L,N,Hk,d] with N={N}, Hk={Hk}, d={d}")
+    with _allocating(stream, dev):
+        if o is None:
+            o = torch.empty(shape, dtype=_bf16, device=q.device)
+        if want_lse and lse is None:
+            lse = torch.empty((N, Hq), dtype=_f32, device=q.device)
+        if workspace is None:
+            need = moda_prefill_paged_workspace_bytes(Hq, Hk, d)
+            workspace = torch.empty(max(4, need // 4), dtype=_f32, device=q.device)
+    if not (_here(o, _bf16, dev) and (lse is None or _here(lse, _f32, dev)) and _here(workspace, _f32, dev)):
+        _refuse(dev, (o, "o", _bf16), (lse, "lse", _f32), (workspace, "workspace", _f32))
+    if o.shape != shape or (lse is not None and lse.shape != (N, Hq)):
+        raise ValueError(f"o must be {(N, Hq, d)} and lse {(N, Hq)}")
+    st = (_lib or load()).moda_prefill_paged(
+        q.data_ptr(), qs, cache, q_starts.data_ptr(), seq_lens.data_ptr(), kp, vp, *strides, N, Hq, L,
+        float(scale), o.data_ptr(), lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
+        workspace.numel() * 4, _raw_stream(stream, dev))
+    if st:
+        _check(st, "moda_prefill_paged")
     return o, lse
 
 

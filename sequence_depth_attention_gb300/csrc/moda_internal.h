@@ -158,6 +158,23 @@ struct DecodePagedArgs {
 size_t decode_paged_workspace_bytes(int Hq, int Hk, int d);
 cudaError_t launch_decode_paged(const DecodePagedArgs& a, cudaStream_t stream);
 
+// Arguments of one paged prefill call after validation on the host.
+struct PrefillPagedArgs {
+  const void *q, *kd, *vd;  // q [N,Hq,d], tokens q_stride apart; depth slots at the strides below
+  int64_t q_stride;
+  PagedKv c;
+  const int *q_starts, *seq_lens;  // [B + 1], [B]
+  int64_t depth_tok_stride, depth_hk_stride, depth_slot_stride;
+  int N, Hq, G, L;
+  float scale;
+  void* o;     // [N,Hq,d] bf16
+  float* lse;  // [N,Hq] or nullptr
+  float* work;
+  int num_sms;
+};
+size_t prefill_paged_workspace_bytes(int d);
+cudaError_t launch_prefill_paged(const PrefillPagedArgs& a, cudaStream_t stream);
+
 cudaError_t launch_selftest_wait(unsigned int* err, int timeout_ms, cudaStream_t stream);
 
 }  // namespace moda

@@ -82,6 +82,37 @@ moda_status check_apart(const Range* outs, int no, const Range* ins, int ni) {
 
 constexpr int kMaxTokens = 1 << 24;
 
+// scale, heads and slots of an attention call; *G = Hq / Hk
+moda_status check_heads(int Hq, int Hk, int L, float scale, int* G) {
+  if (Hq < 1) return report(MODA_ERR_INVALID_ARG, "Hq = %d < 1", Hq);
+  if (Hq % Hk != 0) return report(MODA_ERR_INVALID_ARG, "Hq = %d not a multiple of Hk = %d", Hq, Hk);
+  if (L < 0) return report(MODA_ERR_INVALID_ARG, "L = %d < 0", L);
+  // the kernels work with scale * log2(e)
+  if (!(scale > 0.f) || scale > 2e38f)
+    return report(MODA_ERR_INVALID_ARG, "scale must be positive and at most 2e38");
+  *G = Hq / Hk;
+  if (*G > 16) return report(MODA_ERR_UNSUPPORTED, "G = Hq/Hk = %d (supported: 1 to 16)", *G);
+  if (L > 1024) return report(MODA_ERR_UNSUPPORTED, "L = %d > 1024", L);
+  return MODA_OK;
+}
+
+// The strides of the depth slots of n tokens (or sequences), in elements; what steps
+// along an axis of length 1 is never used, and set to a value that fits. *bytes: what
+// they span.
+moda_status check_depth(int n, int Hk, int L, int d, long long* tok, long long* hk, long long* slot, size_t* bytes) {
+  if (L == 1) *slot = d;
+  if (Hk == 1) *hk = (long long)L * d;
+  if (n == 1) *tok = (long long)Hk * L * d;
+  for (long long x : {*tok, *hk, *slot})
+    if (x < d || x % 8 != 0 || x >= (1LL << 38))
+      return report(MODA_ERR_INVALID_ARG,
+                    "depth strides (token %lld, KV head %lld, slot %lld) must be multiples of 8, at least d "
+                    "and below 2^38",
+                    *tok, *hk, *slot);
+  *bytes = ((size_t)(n - 1) * *tok + (size_t)(Hk - 1) * *hk + (size_t)(L - 1) * *slot + d) * 2;
+  return MODA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -198,15 +229,9 @@ moda_status moda_decode_paged(const void* q, const moda_paged_kv* cache, const i
   moda_status st = check_cache(cache, &a.c, &cr);
   if (st != MODA_OK) return st;
   const int d = a.c.d, Hk = a.c.Hk, B = a.c.B;
-  if (Hq < 1) return report(MODA_ERR_INVALID_ARG, "Hq = %d < 1", Hq);
-  if (Hq % Hk != 0) return report(MODA_ERR_INVALID_ARG, "Hq = %d not a multiple of Hk = %d", Hq, Hk);
-  if (L < 0) return report(MODA_ERR_INVALID_ARG, "L = %d < 0", L);
-  // the kernels work with scale * log2(e)
-  if (!(scale > 0.f) || scale > 2e38f)
-    return report(MODA_ERR_INVALID_ARG, "scale must be positive and at most 2e38");
-  const int G = Hq / Hk;
-  if (G > 16) return report(MODA_ERR_UNSUPPORTED, "G = Hq/Hk = %d (supported: 1 to 16)", G);
-  if (L > 1024) return report(MODA_ERR_UNSUPPORTED, "L = %d > 1024", L);
+  int G = 0;
+  st = check_heads(Hq, Hk, L, scale, &G);
+  if (st != MODA_OK) return st;
   if ((int64_t)B * Hq > (1 << 24))
     return report(MODA_ERR_UNSUPPORTED, "B * Hq = %lld > 2^24", (long long)B * Hq);
   if (B == 0) return ok();
@@ -215,19 +240,8 @@ moda_status moda_decode_paged(const void* q, const moda_paged_kv* cache, const i
   if (L > 0 && (!kd || !vd)) return report(MODA_ERR_INVALID_ARG, "NULL kd or vd with L = %d", L);
   size_t db = 0;
   if (L > 0) {
-    // a stride along an axis of length 1 is never stepped
-    if (L == 1) depth_slot_stride = d;
-    if (Hk == 1) depth_hk_stride = (long long)L * d;
-    if (B == 1) depth_b_stride = (long long)Hk * L * d;
-    const long long s[3] = {depth_b_stride, depth_hk_stride, depth_slot_stride};
-    for (long long x : s)
-      if (x < d || x % 8 != 0 || x >= (1LL << 38))
-        return report(MODA_ERR_INVALID_ARG,
-                      "depth strides (sequence %lld, KV head %lld, slot %lld) must be multiples of "
-                      "8, at least d and below 2^38",
-                      s[0], s[1], s[2]);
-    db = ((size_t)(B - 1) * depth_b_stride + (size_t)(Hk - 1) * depth_hk_stride +
-          (size_t)(L - 1) * depth_slot_stride + d) * 2;
+    st = check_depth(B, Hk, L, d, &depth_b_stride, &depth_hk_stride, &depth_slot_stride, &db);
+    if (st != MODA_OK) return st;
   } else {
     kd = vd = nullptr;
   }
@@ -257,6 +271,73 @@ moda_status moda_decode_paged(const void* q, const moda_paged_kv* cache, const i
   const cudaError_t e = moda::launch_decode_paged(a, (cudaStream_t)stream);
   if (e != cudaSuccess)
     return report(MODA_ERR_CUDA, "decode_paged launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+size_t moda_prefill_paged_workspace_bytes(int Hq, int Hk, int d) {
+  if (Hk < 1 || Hq < Hk || Hq % Hk != 0 || Hq / Hk > 16 || (d != 64 && d != 128)) return 0;
+  return moda::prefill_paged_workspace_bytes(d);
+}
+
+moda_status moda_prefill_paged(const void* q, long long q_stride, const moda_paged_kv* cache,
+                               const int* q_starts, const int* seq_lens, const void* kd, const void* vd,
+                               long long depth_slot_stride, long long depth_tok_stride,
+                               long long depth_hk_stride, int N, int Hq, int L, float scale, void* o,
+                               float* lse, float* workspace, size_t workspace_bytes, moda_stream_t stream) {
+  moda::PrefillPagedArgs a{};
+  CacheRanges cr;
+  moda_status st = check_cache(cache, &a.c, &cr);
+  if (st != MODA_OK) return st;
+  const int d = a.c.d, Hk = a.c.Hk, B = a.c.B;
+  int G = 0;
+  st = check_heads(Hq, Hk, L, scale, &G);
+  if (st != MODA_OK) return st;
+  if (N < 0) return report(MODA_ERR_INVALID_ARG, "N = %d < 0", N);
+  if (N > kMaxTokens || (int64_t)N * Hq > 0x7fffffffLL)
+    return report(MODA_ERR_UNSUPPORTED, "N = %d > 2^24 or N * Hq > 2^31 - 1", N);
+  if (N == 0 || B == 0) return ok();
+  if (!q || !q_starts || !seq_lens || !o || !workspace)
+    return report(MODA_ERR_INVALID_ARG, "NULL q, q_starts, seq_lens, o or workspace");
+  if (L > 0 && (!kd || !vd)) return report(MODA_ERR_INVALID_ARG, "NULL kd or vd with L = %d", L);
+  if (N == 1) q_stride = (long long)Hq * d;
+  if (q_stride < (long long)Hq * d || q_stride % 8 != 0 || q_stride >= (1LL << 38))
+    return report(MODA_ERR_INVALID_ARG, "q_stride = %lld must be a multiple of 8, at least Hq * d and below 2^38",
+                  q_stride);
+  size_t db = 0;
+  if (L > 0) {
+    st = check_depth(N, Hk, L, d, &depth_tok_stride, &depth_hk_stride, &depth_slot_stride, &db);
+    if (st != MODA_OK) return st;
+  } else {
+    kd = vd = nullptr;
+  }
+  const size_t need = moda::prefill_paged_workspace_bytes(d);
+  if (workspace_bytes < need)
+    return report(MODA_ERR_INVALID_ARG, "workspace of %zu bytes < %zu needed", workspace_bytes, need);
+  if (!aligned(q, 16) || !aligned(kd, 16) || !aligned(vd, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
+      !aligned(workspace, 16) || !aligned(q_starts, 4) || !aligned(seq_lens, 4))
+    return report(MODA_ERR_MISALIGNED,
+                  "a tensor pointer is not 16-byte (q_starts, seq_lens, lse: 4-byte) aligned");
+  const Range ins[] = {{q, ((size_t)(N - 1) * q_stride + (size_t)Hq * d) * 2},
+                       cr.r[0], cr.r[1], cr.r[2], cr.r[3], {kd, db}, {vd, db},
+                       {q_starts, (size_t)(B + 1) * 4},
+                       {seq_lens, (size_t)B * 4},
+                       {a.c.table, (size_t)B * a.c.max_pages * 4}};
+  const Range outs[] = {{o, (size_t)N * Hq * d * 2}, {lse, lse ? (size_t)N * Hq * 4 : 0}, {workspace, need}};
+  st = check_apart(outs, 3, ins, 10);
+  if (st != MODA_OK) return st;
+  a.q = q; a.kd = kd; a.vd = vd;
+  a.q_stride = q_stride;
+  a.q_starts = q_starts; a.seq_lens = seq_lens;
+  a.depth_tok_stride = depth_tok_stride; a.depth_hk_stride = depth_hk_stride;
+  a.depth_slot_stride = depth_slot_stride;
+  a.N = N; a.Hq = Hq; a.G = G; a.L = L; a.scale = scale;
+  a.o = o; a.lse = lse; a.work = workspace;
+  int dev;
+  st = moda::device_info(&dev, &a.c.err, &a.num_sms);
+  if (st != MODA_OK) return st;
+  const cudaError_t e = moda::launch_prefill_paged(a, (cudaStream_t)stream);
+  if (e != cudaSuccess)
+    return report(MODA_ERR_CUDA, "prefill_paged launch: %s", cudaGetErrorString(e));
   return ok();
 }
 
