@@ -566,6 +566,77 @@ MODA_API moda_status moda_prefill_paged(const void* q, long long q_stride, const
                                         float* workspace, size_t workspace_bytes, moda_stream_t stream);
 
 /*
+ * moda_page_means -- the summaries of the pages that a step has filled: for every token n
+ * that is the last row of its page, pos[n] % page_size == page_size - 1,
+ *   means[page,hk,:] = bf16( mean over the page's rows of K[row,hk,:] )
+ * with the rows as the cache holds them. Called behind moda_kv_append on the same seq
+ * and pos it keeps the means of all full pages; what the others hold is not touched.
+ *   seq, pos  [N] int32 as in moda_kv_append; padding and rows inside a page are skipped
+ *   means     [num_pages, Hk, d] bf16, 16-byte aligned; must not overlap the pages
+ * Sums are in fp32, of rows times 1 / page_size. The same page may be named twice.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. N == 0 is a no-op.
+ */
+MODA_API moda_status moda_page_means(const moda_paged_kv* cache, const int* seq, const int* pos, int N,
+                                     void* means, moda_stream_t stream);
+
+/*
+ * moda_select_pages -- which pages each token attends to where it does not attend to all.
+ * Token n, row pos[n] of sequence seq[n], sees the m = pos[n] / page_size + 1 pages up to
+ * its own. For each KV head hk the first `sink` and the last `recent` of them are always
+ * taken, and of the others those with the highest scores
+ *   s(i) = max over the group's queries of q[n,h,:] . means[block_table[seq[n]][i],hk,:]
+ * up to S pages in all; where m <= S, all. Equal scores: the lower i first. The choice is
+ * that of the scores in fp64, whatever the order of the kernel's own sums. A NaN counts as
+ * -infinity. `recent` covers the token's own page, which may not be full: the
+ * means of pages that are always taken are not read.
+ *   q      [N, Hq, d] bf16, dense (q_out of moda_kv_append)
+ *   means  [num_pages, Hk, d] bf16 (moda_page_means)
+ *   cache  its geometry and block_table; its pages are not read
+ *   seq, pos  [N] int32 as in moda_kv_append; a token whose seq is -1 (or whose index is out
+ *          of range, which is latched) gets no pages and 0 rows
+ *   pages  [N, Hk, S] int32: the chosen pages in the sequence's order, as row blocks of the
+ *          pool: page * Hk + hk, index of the [page_size, d] rows of a (page, KV head); -1
+ *          behind the last
+ *   rows   [N, Hk] int32: the rows in them that the token sees (all but the last page's are
+ *          full)
+ * A page index outside [0, num_pages) is latched; it is chosen last and given as -1.
+ * Supported: G = Hq/Hk from 1 to 16, 1 <= recent, 0 <= sink, sink + recent <= S, max_pages <=
+ * 32768, N <= 2^24, N*Hq <= 2^28, N*Hk*S <= 2^31 - 1.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. N == 0 is a no-op.
+ */
+MODA_API moda_status moda_select_pages(const void* q, const void* means, const moda_paged_kv* cache,
+                                       const int* seq, const int* pos, int N, int Hq, int S, int sink,
+                                       int recent, int* pages, int* rows, moda_stream_t stream);
+
+/*
+ * moda_decode_selected -- moda_decode_paged where each (token, KV head) has pages of its
+ * own: token n's G queries of KV head hk attend, under one softmax, to the first
+ * rows[n,hk] rows of the row blocks pages[n,hk,:], one behind the other, and to the L depth
+ * slots of (n, hk). With the output of moda_select_pages that is attention to the
+ * selected pages; tokens may be one of each sequence or several of some (the rows
+ * that select counts are those up to the token's own).
+ *   q, o, lse, workspace  as in moda_decode_paged with B = N (workspace of
+ *             moda_decode_paged_workspace_bytes(Hq, Hk, d) bytes)
+ *   cache     its pages; B, max_pages and block_table are not used
+ *   pages     [N, Hk, S] int32, page * Hk + hk; entries past the last of rows[n,hk] rows
+ *             are not read. One outside [0, num_pages * Hk) makes the result of (n, hk)
+ *             unspecified and is latched.
+ *   rows      [N, Hk] int32, 0 <= rows <= S * page_size; one outside is taken as the nearer
+ *             end, and latched. Where it is 0 and L == 0: o = 0, lse = -infinity.
+ *   kd, vd    slot l of KV head hk of token n at n*depth_tok_stride + hk*depth_hk_stride +
+ *             l*depth_slot_stride, as in moda_decode_paged
+ * Arithmetic, support and errors as moda_decode_paged: N*Hq <= 2^24, S * page_size <= 2^30,
+ * N * Hk * S * page_size <= 2^40. N == 0 is a no-op.
+ */
+MODA_API moda_status moda_decode_selected(const void* q, const moda_paged_kv* cache, const int* pages,
+                                          const int* rows, int N, int S, const void* kd,
+                                          const void* vd, long long depth_tok_stride,
+                                          long long depth_hk_stride, long long depth_slot_stride,
+                                          int Hq, int L, float scale, void* o, float* lse,
+                                          float* workspace, size_t workspace_bytes,
+                                          moda_stream_t stream);
+
+/*
  * moda_bwd -- gradients of moda_fwd with respect to all of its inputs. The
  * pages time the fused operator forward + backward (Table 2, Table 7) without
  * writing the backward out; this is the chain rule through the joint softmax

@@ -36,7 +36,8 @@ EXPORTS = ("moda_pack_depth", "moda_depth_write", "moda_depth_write_at", "moda_d
            "moda_decode_strided",
            "moda_decode_workspace_bytes", "moda_kv_append", "moda_kv_gather", "moda_decode_paged",
            "moda_decode_paged_workspace_bytes", "moda_prefill_paged",
-           "moda_prefill_paged_workspace_bytes",
+           "moda_prefill_paged_workspace_bytes", "moda_page_means", "moda_select_pages",
+           "moda_decode_selected",
            "moda_bwd", "moda_bwd_layer_major", "moda_bwd_noalloc", "moda_get_device_error",
            "moda_selftest_wait_timeout", "moda_status_string", "moda_last_error_detail")
 
@@ -138,6 +139,13 @@ def load():
         lib.moda_prefill_paged.argtypes = [vp, ll, cache, vp, vp, vp, vp] + [ll] * 3 + [
             i, i, i, f, vp, vp, vp, ctypes.c_size_t, vp]
         lib.moda_prefill_paged.restype = i
+        lib.moda_page_means.argtypes = [cache, vp, vp, i, vp, vp]
+        lib.moda_page_means.restype = i
+        lib.moda_select_pages.argtypes = [vp, vp, cache, vp, vp] + [i] * 5 + [vp, vp, vp]
+        lib.moda_select_pages.restype = i
+        lib.moda_decode_selected.argtypes = [vp, cache, vp, vp, i, i, vp, vp] + [ll] * 3 + [
+            i, i, f, vp, vp, vp, ctypes.c_size_t, vp]
+        lib.moda_decode_selected.restype = i
         lib.moda_fwd.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, vp, vp, vp]
         lib.moda_fwd_depth_cc.restype = i
         lib.moda_fwd_depth_cc.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, vp, vp, vp]
@@ -828,6 +836,103 @@ def moda_prefill_paged(q, k_pages, v_pages, block_table, q_starts, seq_lens, sca
         workspace.numel() * 4, _raw_stream(stream, dev))
     if st:
         _check(st, "moda_prefill_paged")
+    return o, lse
+
+
+def moda_page_means(k_pages, v_pages, block_table, seq, pos, means, k_scales=None, v_scales=None, stream=None):
+    """The mean keys of the pages that the tokens (seq[n], pos[n]) are the last rows of, into
+    means[num_pages,Hk,d] bf16 (see moda_kv_append for the cache). Returns means."""
+    dev = _current_device()
+    cache, Hk, d, _ = _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales)
+    N = _tokens(dev, seq, pos)
+    if not _here(means, _bf16, dev):
+        _refuse(dev, (means, "means", _bf16))
+    _tensors(means=means)
+    if means is None or means.shape != (k_pages.shape[0], Hk, d):
+        raise ValueError(f"means must be [num_pages,Hk,d] = {(k_pages.shape[0], Hk, d)}")
+    st = (_lib or load()).moda_page_means(cache, seq.data_ptr(), pos.data_ptr(), N, means.data_ptr(),
+                                          _raw_stream(stream, dev))
+    if st:
+        _check(st, "moda_page_means")
+    return means
+
+
+def moda_select_pages(q, means, k_pages, v_pages, block_table, seq, pos, S: int, sink: int = 1, recent: int = 1,
+                      k_scales=None, v_scales=None, pages=None, rows=None, stream=None):
+    """The pages that each token attends to, S of them at most: for each KV head the first
+    `sink` and the last `recent` that the token (seq[n], pos[n]) sees and those whose means
+    (moda_page_means) score highest against the group's queries. q[N,Hq,d] bf16.
+    Returns (pages[N,Hk,S] int32: page * Hk + hk in the sequence's order, -1 behind the last;
+    rows[N,Hk] int32: the rows in them that the token sees), for moda_decode_selected."""
+    dev = _current_device()
+    cache, Hk, d, _ = _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales)
+    N = _tokens(dev, seq, pos)
+    if not (_here(q, _bf16, dev) and _here(means, _bf16, dev)):
+        _refuse(dev, (q, "q", _bf16), (means, "means", _bf16))
+    _tensors(q=q, means=means)
+    if q is None or len(q.shape) != 3 or q.shape[0] != N or q.shape[2] != d:
+        raise ValueError(f"q must be [N,Hq,d] with N={N}, d={d}")
+    if means is None or means.shape != (k_pages.shape[0], Hk, d):
+        raise ValueError(f"means must be [num_pages,Hk,d] = {(k_pages.shape[0], Hk, d)}")
+    S = int(S)
+    with _allocating(stream, dev):
+        if pages is None:
+            pages = torch.empty((N, Hk, max(S, 0)), dtype=_i32, device=q.device)
+        if rows is None:
+            rows = torch.empty((N, Hk), dtype=_i32, device=q.device)
+    if not (_here(pages, _i32, dev) and _here(rows, _i32, dev)):
+        _refuse(dev, (pages, "pages", _i32), (rows, "rows", _i32))
+    if pages.shape != (N, Hk, S) or rows.shape != (N, Hk):
+        raise ValueError(f"pages must be {(N, Hk, S)} and rows {(N, Hk)}")
+    st = (_lib or load()).moda_select_pages(q.data_ptr(), means.data_ptr(), cache, seq.data_ptr(), pos.data_ptr(), N,
+                                            q.shape[1], S, int(sink), int(recent), pages.data_ptr(),
+                                            rows.data_ptr(), _raw_stream(stream, dev))
+    if st:
+        _check(st, "moda_select_pages")
+    return pages, rows
+
+
+def moda_decode_selected(q, k_pages, v_pages, pages, rows, scale: float, kd=None, vd=None, k_scales=None,
+                         v_scales=None, o=None, lse=None, workspace=None, stream=None, want_lse: bool = True):
+    """One token each over the pages that were selected for it: the queries of KV head hk of
+    token n attend to the first rows[n,hk] rows of the row blocks pages[n,hk,:] (page * Hk +
+    hk, see moda_select_pages) and to the token's depth slots. q[N,Hq,d] bf16, pages[N,Hk,S]
+    and rows[N,Hk] int32, kd/vd [N,Hk,L,d] bf16 views with contiguous rows of d values (None
+    when L == 0). Returns (o[N,Hq,d] bf16, lse[N,Hq] fp32 or None)."""
+    dev = _current_device()
+    if not _here(pages, _i32, dev):
+        _refuse(dev, (pages, "pages", _i32))
+    if pages is None or len(pages.shape) != 3:
+        raise ValueError("pages must be [N,Hk,S]")
+    cache, Hk, d, _ = _paged_cache(dev, k_pages, v_pages, pages.view(pages.shape[0], -1) if pages.numel() else
+                                   pages.new_empty((0, 1)), k_scales, v_scales)
+    if not (_here(q, _bf16, dev) and _here(rows, _i32, dev)):
+        _refuse(dev, (q, "q", _bf16), (rows, "rows", _i32))
+    _tensors(q=q, rows=rows)
+    if q is None or len(q.shape) != 3 or q.shape[2] != d:
+        raise ValueError(f"q must be [N,Hq,d] with d={d}")
+    N, Hq, _ = shape = q.shape
+    if pages.shape[:2] != (N, Hk) or rows is None or rows.shape != (N, Hk):
+        raise ValueError(f"pages must be [N,Hk,S] and rows [N,Hk] with N={N}, Hk={Hk}")
+    L, kp, vp, strides = _depth_views(dev, kd, vd, (N, Hk, None, d), f"[N,Hk,L,d] with N={N}, Hk={Hk}, d={d}")
+    with _allocating(stream, dev):
+        if o is None:
+            o = torch.empty(shape, dtype=_bf16, device=q.device)
+        if want_lse and lse is None:
+            lse = torch.empty((N, Hq), dtype=_f32, device=q.device)
+        if workspace is None:
+            need = moda_decode_paged_workspace_bytes(Hq, Hk, d)
+            workspace = torch.empty(max(4, need // 4), dtype=_f32, device=q.device)
+    if not (_here(o, _bf16, dev) and (lse is None or _here(lse, _f32, dev)) and _here(workspace, _f32, dev)):
+        _refuse(dev, (o, "o", _bf16), (lse, "lse", _f32), (workspace, "workspace", _f32))
+    if o.shape != shape or (lse is not None and lse.shape != (N, Hq)):
+        raise ValueError(f"o must be {(N, Hq, d)} and lse {(N, Hq)}")
+    st = (_lib or load()).moda_decode_selected(
+        q.data_ptr(), cache, pages.data_ptr(), rows.data_ptr(), N, pages.shape[2], kp, vp, *strides, Hq, L,
+        float(scale), o.data_ptr(), lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
+        workspace.numel() * 4, _raw_stream(stream, dev))
+    if st:
+        _check(st, "moda_decode_selected")
     return o, lse
 
 

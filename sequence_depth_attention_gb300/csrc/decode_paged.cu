@@ -176,10 +176,11 @@ decode_paged_split(const __grid_constant__ CUtensorMap tmK, const __grid_constan
           constexpr uint32_t kBox = kKeys * 128;  // 64 columns
           sm103::mbar_arrive_expect_tx(bar, 2 * (D / 64) * kBox);
           const int l = cur.off * kKeys;
+          const int2 of = depth_of(p, cur.b, cur.hk);
 #pragma unroll
           for (int x = 0; x < D / 64; ++x) {
-            sm103::tma_load_4d(kt + x * kBox, &tmKd, bar, x * 64, l, cur.hk, cur.b);
-            sm103::tma_load_4d(vt + x * kBox, &tmVd, bar, x * 64, l, cur.hk, cur.b);
+            sm103::tma_load_4d(kt + x * kBox, &tmKd, bar, x * 64, l, of.y, of.x);
+            sm103::tma_load_4d(vt + x * kBox, &tmVd, bar, x * 64, l, of.y, of.x);
           }
         }
       } else {
@@ -442,7 +443,7 @@ cudaError_t launch(const DecodePagedArgs& a, cudaStream_t stream) {
       return cudaErrorInvalidValue;
   }
   if (a.L > 0) {
-    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)a.L, (uint64_t)c.Hk, (uint64_t)c.B};
+    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)a.L, (uint64_t)c.Hk * a.fold, (uint64_t)c.B / a.fold};
     const uint64_t str[3] = {(uint64_t)a.depth_slot_stride * 2, (uint64_t)a.depth_hk_stride * 2,
                              (uint64_t)a.depth_b_stride * 2};
     const uint32_t bx[4] = {64, (uint32_t)kKeys, 1, 1};

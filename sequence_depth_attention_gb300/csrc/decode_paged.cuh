@@ -64,6 +64,7 @@ struct Params {
   unsigned int* err;
   int group;   // CTAs of a segment; 0: shares of the line
   float unit;  // of the sums O that warps merge and CTAs leave, see unit_of
+  int fold;    // sequences that share a token's depth slots, see DecodePagedArgs
 };
 // O of 4-bit rows leaves a warp in units of 2^32: values are up to 1.5 * 2^127, and
 // sums of up to 2^24 of them, each times a weight of up to 2^8, stay finite; what
@@ -74,7 +75,14 @@ inline Params params_of(const DecodePagedArgs& a, int group) {
   const PagedKv& c = a.c;
   return {(const __nv_bfloat16*)a.q, a.seq_lens, c.table, c.num_pages, __builtin_ctz((unsigned)c.page_size),
           c.max_pages, c.B, c.Hk, a.G, a.L, a.scale * kLog2e, (__nv_bfloat16*)a.o, a.lse, a.work, c.err, group,
-          unit_of(a)};
+          unit_of(a), a.fold};
+}
+
+// The token and KV head whose depth slots (b, hk) reads.
+__device__ __forceinline__ int2 depth_of(const Params& p, int b, int hk) {
+  if (p.fold == 1) return make_int2(b, hk);
+  const int token = b / p.fold;
+  return make_int2(token, b - token * p.fold);
 }
 
 // Sequence b's rows, within what its table can name.

@@ -596,7 +596,8 @@ struct Feed {
     } else if (left > 0) {
       if (at.off < depth_units) {
         const int l0 = at.off * kDepthKeys;
-        const uint8_t* src = (part ? pg.vd : pg.kd) + at.b * pg.depth_b + at.hk * pg.depth_hk +
+        const int2 of = depth_of(p, at.b, at.hk);
+        const uint8_t* src = (part ? pg.vd : pg.kd) + of.x * pg.depth_b + of.y * pg.depth_hk +
                              l0 * pg.depth_slot;
         constexpr int VPR = D / 8;  // 16-byte vectors of a row
 #pragma unroll

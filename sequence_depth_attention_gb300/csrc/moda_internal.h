@@ -149,6 +149,9 @@ struct DecodePagedArgs {
   const int* seq_lens;  // [B]
   int64_t depth_b_stride, depth_hk_stride, depth_slot_stride;
   int Hq, G, L;
+  // Where each (token, KV head) has pages of its own, it is a sequence with one KV head
+  // here, and `fold` of them share a token's depth slots; else 1.
+  int fold;
   float scale;
   void* o;     // [B,Hq,d] bf16
   float* lse;  // [B,Hq] or nullptr
@@ -172,6 +175,18 @@ struct PrefillPagedArgs {
   float* work;
   int num_sms;
 };
+cudaError_t launch_page_means(const PagedKv& c, const int* seq, const int* pos, int N, void* means,
+                              cudaStream_t stream);
+// Arguments of one choice of pages after validation on the host.
+struct SelectPagesArgs {
+  const void *q, *means;  // [N,Hq,d], [num_pages,Hk,d] bf16
+  PagedKv c;
+  const int *seq, *pos;  // [N]
+  int N, G, S, sink, recent;
+  int *pages, *rows;  // [N,Hk,S], [N,Hk]
+  int num_sms;
+};
+cudaError_t launch_select_pages(const SelectPagesArgs& a, cudaStream_t stream);
 size_t prefill_paged_workspace_bytes(int d);
 cudaError_t launch_prefill_paged(const PrefillPagedArgs& a, cudaStream_t stream);
 

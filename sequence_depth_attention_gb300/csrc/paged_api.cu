@@ -81,6 +81,7 @@ moda_status check_apart(const Range* outs, int no, const Range* ins, int ni) {
 }
 
 constexpr int kMaxTokens = 1 << 24;
+constexpr int kMaxSelectPages = 1 << 15;  // their scores lie in shared memory
 
 // scale, heads and slots of an attention call; *G = Hq / Hk
 moda_status check_heads(int Hq, int Hk, int L, float scale, int* G) {
@@ -264,6 +265,7 @@ moda_status moda_decode_paged(const void* q, const moda_paged_kv* cache, const i
   a.depth_b_stride = depth_b_stride; a.depth_hk_stride = depth_hk_stride;
   a.depth_slot_stride = depth_slot_stride;
   a.Hq = Hq; a.G = G; a.L = L; a.scale = scale;
+  a.fold = 1;
   a.o = o; a.lse = lse; a.work = workspace;
   int dev;
   st = moda::device_info(&dev, &a.c.err, &a.num_sms);
@@ -271,6 +273,150 @@ moda_status moda_decode_paged(const void* q, const moda_paged_kv* cache, const i
   const cudaError_t e = moda::launch_decode_paged(a, (cudaStream_t)stream);
   if (e != cudaSuccess)
     return report(MODA_ERR_CUDA, "decode_paged launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+moda_status moda_page_means(const moda_paged_kv* cache, const int* seq, const int* pos, int N, void* means,
+                            moda_stream_t stream) {
+  moda::PagedKv c;
+  CacheRanges cr;
+  moda_status st = check_cache(cache, &c, &cr);
+  if (st != MODA_OK) return st;
+  if (N < 0) return report(MODA_ERR_INVALID_ARG, "N = %d < 0", N);
+  if (N > kMaxTokens) return report(MODA_ERR_UNSUPPORTED, "N = %d > 2^24", N);
+  if (N == 0) return ok();
+  if (!seq || !pos || !means) return report(MODA_ERR_INVALID_ARG, "NULL input or output");
+  if (!aligned(means, 16) || !aligned(seq, 4) || !aligned(pos, 4))
+    return report(MODA_ERR_MISALIGNED, "a tensor pointer is not 16-byte (seq, pos: 4-byte) aligned");
+  const Range ins[] = {cr.r[0], cr.r[1], cr.r[2], cr.r[3],
+                       {seq, (size_t)N * 4},
+                       {pos, (size_t)N * 4},
+                       {c.table, (size_t)c.B * c.max_pages * 4}};
+  const Range outs[] = {{means, (size_t)c.num_pages * c.Hk * c.d * 2}};
+  st = check_apart(outs, 1, ins, 7);
+  if (st != MODA_OK) return st;
+  int dev, sms;
+  st = moda::device_info(&dev, &c.err, &sms);
+  if (st != MODA_OK) return st;
+  const cudaError_t e = moda::launch_page_means(c, seq, pos, N, means, (cudaStream_t)stream);
+  if (e != cudaSuccess) return report(MODA_ERR_CUDA, "page_means launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+moda_status moda_select_pages(const void* q, const void* means, const moda_paged_kv* cache, const int* seq,
+                              const int* pos, int N, int Hq, int S, int sink, int recent, int* pages,
+                              int* rows, moda_stream_t stream) {
+  moda::SelectPagesArgs a{};
+  CacheRanges cr;
+  moda_status st = check_cache(cache, &a.c, &cr);
+  if (st != MODA_OK) return st;
+  const int d = a.c.d, Hk = a.c.Hk;
+  int G = 0;
+  st = check_heads(Hq, Hk, 0, 1.f, &G);
+  if (st != MODA_OK) return st;
+  if (N < 0) return report(MODA_ERR_INVALID_ARG, "N = %d < 0", N);
+  if (sink < 0 || recent < 1 || S < 1 || (int64_t)sink + recent > S)
+    return report(MODA_ERR_INVALID_ARG, "sink = %d, recent = %d (at least 1) of S = %d pages", sink, recent, S);
+  if (a.c.max_pages > kMaxSelectPages)
+    return report(MODA_ERR_UNSUPPORTED, "max_pages = %d > %d", a.c.max_pages, kMaxSelectPages);
+  if (N > kMaxTokens || (int64_t)N * Hq > (1LL << 28))
+    return report(MODA_ERR_UNSUPPORTED, "N = %d > 2^24 or N * Hq > 2^28", N);
+  // (a quotient: the product may pass 64 bits)
+  if (N > 0 && S > 0x7fffffffLL / ((int64_t)N * Hk))
+    return report(MODA_ERR_UNSUPPORTED, "N * Hk * S exceeds 2^31 - 1");
+  if (N == 0) return ok();
+  if (!q || !means || !seq || !pos || !pages || !rows)
+    return report(MODA_ERR_INVALID_ARG, "NULL input or output");
+  if (!aligned(q, 16) || !aligned(means, 16) || !aligned(seq, 4) || !aligned(pos, 4) || !aligned(pages, 4) ||
+      !aligned(rows, 4))
+    return report(MODA_ERR_MISALIGNED,
+                  "a tensor pointer is not 16-byte (seq, pos, pages, rows: 4-byte) aligned");
+  const Range ins[] = {{q, (size_t)N * Hq * d * 2},
+                       {means, (size_t)a.c.num_pages * Hk * d * 2},
+                       {seq, (size_t)N * 4},
+                       {pos, (size_t)N * 4},
+                       {a.c.table, (size_t)a.c.B * a.c.max_pages * 4}};
+  const Range outs[] = {{pages, (size_t)N * Hk * S * 4}, {rows, (size_t)N * Hk * 4}};
+  st = check_apart(outs, 2, ins, 5);
+  if (st != MODA_OK) return st;
+  a.q = q; a.means = means; a.seq = seq; a.pos = pos;
+  a.N = N; a.G = G; a.S = S; a.sink = sink; a.recent = recent;
+  a.pages = pages; a.rows = rows;
+  int dev;
+  st = moda::device_info(&dev, &a.c.err, &a.num_sms);
+  if (st != MODA_OK) return st;
+  const cudaError_t e = moda::launch_select_pages(a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return report(MODA_ERR_CUDA, "select_pages launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+moda_status moda_decode_selected(const void* q, const moda_paged_kv* cache, const int* pages, const int* rows,
+                                 int N, int S, const void* kd, const void* vd, long long depth_tok_stride,
+                                 long long depth_hk_stride, long long depth_slot_stride, int Hq, int L,
+                                 float scale, void* o, float* lse, float* workspace, size_t workspace_bytes,
+                                 moda_stream_t stream) {
+  moda::DecodePagedArgs a{};
+  CacheRanges cr;
+  if (!cache) return report(MODA_ERR_INVALID_ARG, "NULL cache");
+  moda_paged_kv pool = *cache;  // its sequences have no part in this call
+  pool.B = 0;
+  pool.max_pages = 1;
+  pool.block_table = nullptr;
+  moda_status st = check_cache(&pool, &a.c, &cr);
+  if (st != MODA_OK) return st;
+  const int d = a.c.d, Hk = a.c.Hk, P = a.c.page_size;
+  int G = 0;
+  st = check_heads(Hq, Hk, L, scale, &G);
+  if (st != MODA_OK) return st;
+  if (N < 0 || S < 1) return report(MODA_ERR_INVALID_ARG, "N = %d < 0 or S = %d < 1", N, S);
+  if ((int64_t)N * Hq > (1 << 24))
+    return report(MODA_ERR_UNSUPPORTED, "N * Hq = %lld > 2^24", (long long)N * Hq);
+  if ((int64_t)S * P > (1 << 30))
+    return report(MODA_ERR_UNSUPPORTED, "S * page_size = %lld > 2^30", (long long)S * P);
+  if (N > 0 && (int64_t)S * P > (1LL << 40) / ((int64_t)N * Hk))
+    return report(MODA_ERR_UNSUPPORTED, "N * Hk * S * page_size exceeds 2^40 rows");
+  if (N == 0) return ok();
+  if (!q || !pages || !rows || !o || !workspace)
+    return report(MODA_ERR_INVALID_ARG, "NULL q, pages, rows, o or workspace");
+  if (L > 0 && (!kd || !vd)) return report(MODA_ERR_INVALID_ARG, "NULL kd or vd with L = %d", L);
+  size_t db = 0;
+  if (L > 0) {
+    st = check_depth(N, Hk, L, d, &depth_tok_stride, &depth_hk_stride, &depth_slot_stride, &db);
+    if (st != MODA_OK) return st;
+  } else {
+    kd = vd = nullptr;
+  }
+  const size_t need = moda::decode_paged_workspace_bytes(Hq, Hk, d);
+  if (workspace_bytes < need)
+    return report(MODA_ERR_INVALID_ARG, "workspace of %zu bytes < %zu needed", workspace_bytes, need);
+  if (!aligned(q, 16) || !aligned(kd, 16) || !aligned(vd, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
+      !aligned(workspace, 16) || !aligned(pages, 4) || !aligned(rows, 4))
+    return report(MODA_ERR_MISALIGNED, "a tensor pointer is not 16-byte (pages, rows, lse: 4-byte) aligned");
+  const size_t qb = (size_t)N * Hq * d * 2;
+  const Range ins[] = {{q, qb}, cr.r[0], cr.r[1], cr.r[2], cr.r[3], {kd, db}, {vd, db},
+                       {pages, (size_t)N * Hk * S * 4},
+                       {rows, (size_t)N * Hk * 4}};
+  const Range outs[] = {{o, qb}, {lse, lse ? (size_t)N * Hq * 4 : 0}, {workspace, need}};
+  st = check_apart(outs, 3, ins, 9);
+  if (st != MODA_OK) return st;
+  // each (token, KV head) is a sequence with one KV head over the pool's row blocks
+  a.c.num_pages *= Hk;
+  a.c.Hk = 1;
+  a.c.B = N * Hk;
+  a.c.max_pages = S;
+  a.c.table = pages;
+  a.q = q; a.kd = kd; a.vd = vd;
+  a.seq_lens = rows;
+  a.depth_b_stride = depth_tok_stride; a.depth_hk_stride = depth_hk_stride;
+  a.depth_slot_stride = depth_slot_stride;
+  a.Hq = G; a.G = G; a.L = L; a.fold = Hk; a.scale = scale;
+  a.o = o; a.lse = lse; a.work = workspace;
+  int dev;
+  st = moda::device_info(&dev, &a.c.err, &a.num_sms);
+  if (st != MODA_OK) return st;
+  const cudaError_t e = moda::launch_decode_paged(a, (cudaStream_t)stream);
+  if (e != cudaSuccess)
+    return report(MODA_ERR_CUDA, "decode_selected launch: %s", cudaGetErrorString(e));
   return ok();
 }
 

@@ -78,3 +78,65 @@ def prefill_reference(cache, q, q_starts, lens, kd, vd, scale):
                 for to, x in zip((o, lse, tol_o, tol_lse), got):
                     to[here, heads] = x.view(c, G, *x.shape[1:])
     return o, lse, tol_o, tol_lse
+
+
+def page_means(cache):
+    """[num_pages,Hk,d] fp64: every page's mean key."""
+    k = cache.k.double() if cache.fmt == "bf16" else pc.mx4_values(cache.k, cache.ks)
+    return k.mean(2)
+
+
+def selection(cache, q, means, seq, pos, S, sink, recent):
+    """(pages[N,Hk,S], rows[N,Hk]) of moda_select_pages, scores in fp64 by a sum from the
+    first element to the last."""
+    N, Hk = q.shape[0], cache.Hk
+    G, d = q.shape[1] // Hk, q.shape[2]
+    q, means, table = q.double().cpu(), means.double().cpu(), cache.table.cpu()
+    pages = torch.full((N, Hk, S), -1, dtype=torch.int32)
+    rows = torch.zeros((N, Hk), dtype=torch.int32)
+    for n in range(N):
+        b, t = int(seq[n]), int(pos[n])
+        if b < 0:
+            continue
+        m = t // cache.page + 1
+        ids = table[b, :m].long()
+        for h in range(Hk):
+            score = torch.full((m,), -math.inf, dtype=torch.float64)
+            for g in range(G):
+                s = (q[n, h * G + g] * means[ids, h]).sum(-1)
+                score = torch.where(torch.isnan(s), score, torch.maximum(score, s))
+            always = [i for i in range(m) if i < sink or i >= m - recent] if m > S else list(range(m))
+            rest = sorted(set(range(m)) - set(always), key=lambda i: (-score[i].item(), i))
+            keep = sorted(always + rest[: max(0, S - len(always))])
+            pages[n, h, : len(keep)] = (ids[keep] * Hk + h).int()
+            rows[n, h] = (len(keep) - 1) * cache.page + t % cache.page + 1
+    return pages, rows
+
+
+def selected_reference(cache, q, pages, rows, kd, vd, scale):
+    """attention() for every (token, KV head) over the first rows[n,hk] rows of its row
+    blocks; kd, vd [N,Hk,L,d] or None."""
+    N, Hq, d = q.shape
+    Hk = cache.Hk
+    G = Hq // Hk
+    outs = [], [], [], []
+    for n in range(N):
+        for h in range(Hk):
+            r = int(rows[n, h])
+            ids = pages[n, h, : -(-r // cache.page)].long()
+            kv = []
+            for x, s in ((cache.k, cache.ks), (cache.v, cache.vs)):
+                x = x.flatten(0, 1)[ids]
+                x = x.double() if s is None else pc.mx4_values(x, s.flatten(0, 1)[ids])
+                kv.append(x.reshape(-1, d)[:r] if r else torch.zeros(0, d, dtype=torch.float64, device=q.device))
+            scales = None
+            if cache.fmt == "mx4" and r:
+                scales = torch.exp2(cache.vs.flatten(0, 1)[ids].double() - 127).amax(-1).reshape(-1)[:r]
+                scales = torch.cat((scales, scales.new_zeros(0 if kd is None else kd.shape[2])))[None]
+            if kd is not None:
+                kv = [torch.cat((x, y[n, h].double())) for x, y in zip(kv, (kd, vd))]
+            seen = torch.ones(G, kv[0].shape[0], dtype=torch.bool, device=q.device)
+            got = attention(q[n, h * G : (h + 1) * G].double(), *kv, seen, scale, mx4_products=scales)
+            for to, x in zip(outs, got):
+                to.append(x)
+    return tuple(torch.cat(x).view(N, Hq, *x[0].shape[1:]) for x in outs)
