@@ -72,6 +72,9 @@ def _load_paged(lib):
                              lib.moda_decode_paged_workspace_bytes))
         # (for the current device without torch.cuda's start-up: the tensors have seen to it)
         ext.setup(torch.Tensor, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, *address)
+        ext.more(*(ctypes.cast(f, ctypes.c_void_p).value
+                   for f in (lib.moda_prefill_paged, lib.moda_prefill_paged_workspace_bytes, lib.moda_page_means,
+                             lib.moda_select_pages, lib.moda_decode_selected)))
         return ext
     except (OSError, ImportError, AttributeError) as e:
         warnings.warn(f"paged_py is not used ({e}): paged calls take a few us longer; "
@@ -555,10 +558,11 @@ def _refuse(dev, *tensors):
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
-def _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales):
-    """moda_paged_kv for the tensors of a cache."""
+def _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales, sequences=True):
+    """moda_paged_kv for the tensors of a cache; without sequences, of the pages alone."""
+    listed = not sequences or _here(block_table, _i32, dev)
     if k_scales is None and v_scales is None:
-        if not (_here(k_pages, _bf16, dev) and _here(v_pages, _bf16, dev) and _here(block_table, _i32, dev)):
+        if not (_here(k_pages, _bf16, dev) and _here(v_pages, _bf16, dev) and listed):
             _refuse(dev, (k_pages, "k_pages", _bf16), (v_pages, "v_pages", _bf16),
                     (block_table, "block_table", _i32))
         shape = k_pages.shape
@@ -569,7 +573,7 @@ def _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales):
     else:
         if k_scales is None or v_scales is None:
             raise ValueError("k_scales and v_scales come together")
-        if not (_here(k_pages, _u8, dev) and _here(v_pages, _u8, dev) and _here(block_table, _i32, dev)
+        if not (_here(k_pages, _u8, dev) and _here(v_pages, _u8, dev) and listed
                 and _here(k_scales, _u8, dev) and _here(v_scales, _u8, dev)):
             _refuse(dev, (k_pages, "k_pages", _u8), (v_pages, "v_pages", _u8),
                     (block_table, "block_table", _i32), (k_scales, "k_scales", _u8),
@@ -583,11 +587,11 @@ def _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales):
         if k_scales.shape != want or v_scales.shape != want:
             raise ValueError(f"k_scales and v_scales must be [num_pages,Hk,page_size,d/32] = {want}")
         fmt, ks, vs = MODA_KV_MX4, k_scales.data_ptr(), v_scales.data_ptr()
-    table = block_table.shape
+    table = block_table.shape if sequences else (0, 1)
     if len(table) != 2:
         raise ValueError("block_table must be [B,max_pages]")
     return _PagedKv(fmt, num_pages, page_size, Hk, d, table[0], table[1], k_pages.data_ptr(),
-                    v_pages.data_ptr(), ks, vs, block_table.data_ptr()), Hk, d, table[0]
+                    v_pages.data_ptr(), ks, vs, block_table.data_ptr() if sequences else None), Hk, d, table[0]
 
 
 def _tensors(**named):
@@ -806,6 +810,11 @@ def moda_prefill_paged(q, k_pages, v_pages, block_table, q_starts, seq_lens, sca
     contiguous rows of d values (None when L == 0).
     Returns (o[N,Hq,d] bf16, lse[N,Hq] fp32 or None); rows of tokens behind the last
     sequence are left as they were, in new tensors undefined."""
+    if stream is None and _paged is not None:
+        out = _paged.prefill(q, k_pages, v_pages, block_table, q_starts, seq_lens, scale, kd, vd, k_scales,
+                             v_scales, o, lse, workspace, want_lse)
+        if out is not None:
+            return out if type(out) is tuple else _check(out, "moda_prefill_paged")
     dev = _current_device()
     cache, Hk, d, B = _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales)
     if not (_here(q_starts, _i32, dev) and _here(seq_lens, _i32, dev)):
@@ -842,6 +851,10 @@ def moda_prefill_paged(q, k_pages, v_pages, block_table, q_starts, seq_lens, sca
 def moda_page_means(k_pages, v_pages, block_table, seq, pos, means, k_scales=None, v_scales=None, stream=None):
     """The mean keys of the pages that the tokens (seq[n], pos[n]) are the last rows of, into
     means[num_pages,Hk,d] bf16 (see moda_kv_append for the cache). Returns means."""
+    if stream is None and _paged is not None:
+        out = _paged.means(k_pages, v_pages, block_table, seq, pos, means, k_scales, v_scales)
+        if out is not None:
+            return out[0] if type(out) is tuple else _check(out, "moda_page_means")
     dev = _current_device()
     cache, Hk, d, _ = _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales)
     N = _tokens(dev, seq, pos)
@@ -864,6 +877,11 @@ def moda_select_pages(q, means, k_pages, v_pages, block_table, seq, pos, S: int,
     (moda_page_means) score highest against the group's queries. q[N,Hq,d] bf16.
     Returns (pages[N,Hk,S] int32: page * Hk + hk in the sequence's order, -1 behind the last;
     rows[N,Hk] int32: the rows in them that the token sees), for moda_decode_selected."""
+    if stream is None and _paged is not None:
+        out = _paged.select(q, means, k_pages, v_pages, block_table, seq, pos, S, sink, recent, k_scales, v_scales,
+                            pages, rows)
+        if out is not None:
+            return out if type(out) is tuple else _check(out, "moda_select_pages")
     dev = _current_device()
     cache, Hk, d, _ = _paged_cache(dev, k_pages, v_pages, block_table, k_scales, v_scales)
     N = _tokens(dev, seq, pos)
@@ -899,13 +917,17 @@ def moda_decode_selected(q, k_pages, v_pages, pages, rows, scale: float, kd=None
     hk, see moda_select_pages) and to the token's depth slots. q[N,Hq,d] bf16, pages[N,Hk,S]
     and rows[N,Hk] int32, kd/vd [N,Hk,L,d] bf16 views with contiguous rows of d values (None
     when L == 0). Returns (o[N,Hq,d] bf16, lse[N,Hq] fp32 or None)."""
+    if stream is None and _paged is not None:
+        out = _paged.selected(q, k_pages, v_pages, pages, rows, scale, kd, vd, k_scales, v_scales, o, lse,
+                              workspace, want_lse)
+        if out is not None:
+            return out if type(out) is tuple else _check(out, "moda_decode_selected")
     dev = _current_device()
     if not _here(pages, _i32, dev):
         _refuse(dev, (pages, "pages", _i32))
     if pages is None or len(pages.shape) != 3:
         raise ValueError("pages must be [N,Hk,S]")
-    cache, Hk, d, _ = _paged_cache(dev, k_pages, v_pages, pages.view(pages.shape[0], -1) if pages.numel() else
-                                   pages.new_empty((0, 1)), k_scales, v_scales)
+    cache, Hk, d, _ = _paged_cache(dev, k_pages, v_pages, None, k_scales, v_scales, sequences=False)
     if not (_here(q, _bf16, dev) and _here(rows, _i32, dev)):
         _refuse(dev, (q, "q", _bf16), (rows, "rows", _i32))
     _tensors(q=q, rows=rows)
