@@ -2,7 +2,10 @@
 // pairs, exactly.
 #pragma once
 
+#include <cuda_fp16.h>
 #include <stdint.h>
+
+#include "sm103.cuh"
 
 namespace moda {
 namespace mx4 {
@@ -10,42 +13,32 @@ namespace mx4 {
 // bf16 pairs: bit 15 or 31 set where a half is an infinity or a NaN.
 __device__ __forceinline__ uint32_t not_finite(uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
-// 8 codes of a word times 2^(byte - 127), as bf16 pairs. A code's three magnitude
-// bits in bits 6 to 8 of a bf16 are its value times 2^-126 (a subnormal for 0.5),
-// so one exact product by 2^(byte - 1) gives the value; above 2^127 the product is
-// made in two steps.
+// 8 codes of a word times a power of two given as a bf16 pair (scale_of), as bf16 pairs in
+// their order. Exact but at the ends of bf16's range, where it rounds to subnormals and
+// infinities. (Conversions to fp16 and fp32 and back take half of the ALU's slots of what
+// placing the code's bits takes: a 4-bit prefill's blocks 3700 cycles with that.)
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ void unpack8(uint32_t w, uint32_t mul, uint32_t mul2, uint32_t (&out)[4]) {
-  // halves hold codes j and j + 4
-  uint32_t x[4];
-  x[0] = ((w << 6) & 0x01c001c0u) | ((w << 12) & 0x80008000u);
-  x[1] = ((w << 2) & 0x01c001c0u) | ((w << 8) & 0x80008000u);
-  x[2] = ((w >> 2) & 0x01c001c0u) | ((w << 4) & 0x80008000u);
-  x[3] = ((w >> 6) & 0x01c001c0u) | (w & 0x80008000u);
+__device__ __forceinline__ void unpack8(uint32_t w, uint32_t scale, uint32_t (&out)[4]) {
+  uint32_t h[4];
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
 #pragma unroll
-  for (int j = 0; j < 4; ++j) x[j] = mul_bf16x2(x[j], mul);
-  if (mul2 != 0x3f803f80u) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = mul_bf16x2(x[j], mul2);
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    out[i] = mul_bf16x2(sm103::pack_bf16x2(f.x, f.y), scale);
   }
-  out[0] = __byte_perm(x[0], x[1], 0x5410);
-  out[1] = __byte_perm(x[2], x[3], 0x5410);
-  out[2] = __byte_perm(x[0], x[1], 0x7632);
-  out[3] = __byte_perm(x[2], x[3], 0x7632);
 }
-// The two factors for a scale byte, each in both halves: 2^(b - 1) up to b = 128,
-// then 2^127 and 2^(b - 128); 255 is NaN.
-__device__ __forceinline__ void factors(uint32_t b, uint32_t& mul, uint32_t& mul2) {
-  const uint32_t e = min(b + 126u, 254u);  // biased exponent of the first; b = 0: 2^-1
-  uint32_t m = e << 7, n = 0x3f80u;
-  if (b > 128u) n = (b - 1u) << 7;         // 2^(b - 128)
-  if (b == 255u) m = 0x7fc0u;
-  mul = m | m << 16;
-  mul2 = n | n << 16;
+// A block's scale byte b as a bf16 pair of 2^(b - 127); 255 is NaN.
+__device__ __forceinline__ uint32_t scale_of(uint32_t b) {
+  const uint32_t x = b == 255u ? 0x7fc0u : b == 0u ? 0x0040u : b << 7;
+  return x | x << 16;
 }
 
 }  // namespace mx4

@@ -96,11 +96,11 @@ page_means_kernel(const __grid_constant__ PagedKv c, const int* seq, const int* 
           acc[at + 1] = fmaf(__uint_as_float(pair & 0xffff0000u), inv, acc[at + 1]);
         };
         if constexpr (MX4) {
-          uint32_t mul, mul2, y[4];
-          mx4::factors(b[u], mul, mul2);
+          uint32_t y[4];
+          const uint32_t scale = mx4::scale_of(b[u]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            mx4::unpack8(w[q], mul, mul2, y);
+            mx4::unpack8(w[q], scale, y);
 #pragma unroll
             for (int i = 0; i < 4; ++i) add(q * 8 + 2 * i, y[i]);
           }

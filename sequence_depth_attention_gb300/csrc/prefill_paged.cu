@@ -3,31 +3,34 @@
 // softmax, to the rows of their sequence's pages up to their own and to the L depth
 // slots of their own position.
 //
-// The forward's organisation (fwd_tc.cu) over pages and ragged sequences: a tile
-// is the G heads of one KV head x P positions of one sequence, 128 rows;
-// S = Q K^T and O += P V on tcgen05 with S, P, Q and O in tensor memory, K and V
-// through shared memory by TMA, one softmax thread per row, the depth slots
-// gathered as blocks with a block-diagonal mask. What differs:
-//   * the work is cut into equal shares of a line of blocks (prefill_paged.cuh):
-//     a draft of five tokens over a long context is spread over the SMs like a
-//     long prompt, and the lengths stay on the device;
-//   * a block of 128 keys is up to 8 pages, each looked up and copied by a lane;
-//   * 4-bit pages come as codes and scales; four warps unpack them into the bf16
-//     tiles that the tensor core reads (exactly: a code times a power of two);
-//   * those warps also see to it that a row that a query must not see has no
-//     influence whatever it holds. Its weight is 0, but 0 times an infinity or a
-//     NaN in V is NaN: in the blocks that some row of a tile sees in part (the
-//     causal border, the depth blocks), rows that no query of the tile sees
-//     become 0, and an infinity or NaN among the others becomes 0 too and is added
-//     at the end to the rows that do see it.
+// A tile is the G heads of one KV head x 2 P positions of one sequence, in two halves
+// of 128 rows. Both halves see (nearly) the same keys, so a block of 128 keys is
+// brought into shared memory once for both: S = Q K^T and O += P V on tcgen05, the halves
+// in turn, so that the softmax of one half runs beside the products of the other. A
+// softmax thread has one row. The work is cut into equal shares of a line of blocks
+// (prefill_paged.cuh), so a draft of five tokens over a long context is spread over
+// the SMs like a long prompt, and the lengths stay on the device.
+//   * A block of 128 keys is up to 8 pages, each looked up and copied by a lane.
+//   * Depth slots are gathered by TMA, a block of each half's own positions, under a
+//     block-diagonal mask (a softmax warp has a 32-row word of it), and spread evenly
+//     among the sequence blocks.
+//   * 4-bit pages come as codes and scales, and warps unpack them into the bf16 tiles
+//     that the tensor core reads (exactly: a code times a power of two), once for both
+//     halves.
+//   * A row that a query must not see has no influence whatever it holds. Its weight is
+//     0, but 0 times an infinity or a NaN in V is NaN: in the blocks that some row of a
+//     tile sees in part (the causal border, the depth blocks), rows that no query of the
+//     tile sees become 0, and an infinity or NaN among the others becomes 0 too and is
+//     added at the end to the rows that do see it.
 //
-// Roles (12 warps):
-//   warp 0  TMA producer of Q and K     warp 1  issuer of S = Q K^T, TMEM
-//   warp 2  TMA producer of V           warp 3  issuer of O += P V
-//   warps 4-7   softmax, Q into TMEM, epilogue: one thread per row (TMEM lane)
-//   warps 8-11  4-bit pages unpacked, partly seen V blocks made harmless
-// TMEM (512 columns): S double buffer [0,128) [128,256), O [256, 256+d), P (bf16
-// pairs) [384,448), Q (bf16 pairs) [448, 448+d/2).
+// Roles (16 warps):
+//   warp 0        TMA producer of Q and K     warp 1  issuer of all MMAs, TMEM
+//   warp 2        TMA producer of V           warp 3  4-bit pages: depth blocks' producer
+//   warps 4-7     softmax and epilogue of the first half, one thread per row (TMEM lane)
+//   warps 8-11    of the second half
+//   warps 12-15   partly seen V blocks made harmless, 4-bit pages unpacked
+// TMEM (512 columns): S of the halves [0,128) [128,256), each half's P (bf16 pairs) in the
+// first 64 columns of its S, O of the halves at 256 and 256 + d.
 // P is rounded to bf16 once, as in the forward: the sum l keeps fp32 weights, and
 // what o is off by that is about as much as its own rounding to bf16.
 //
@@ -47,64 +50,70 @@ using namespace sm103;
 using paged::kLn2;
 using paged::kLog2e;
 
-constexpr int BM = kRows, BN = 128;
-constexpr int kWarps = 12, kThreads = kWarps * 32;
+constexpr int BM = 128, BN = 128;  // rows of a half tile, keys of a block
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr float kSumBound = 256.0f;        // 2^kRescaleThreshold
+constexpr float kSumBound = 256.0f;  // of a row's weights in a block, see the softmax warps
 constexpr int kLeast = 2;                  // points that are worth a CTA
-// Registers: 384 threads x 168 at launch; the softmax warps take 240 and the first
-// four give theirs (128 x (96 + 240 + 168) <= 384 x 168).
-constexpr int kRegsIssue = 96, kRegsSoftmax = 240;
-static_assert(128 * (kRegsIssue + kRegsSoftmax + 168) <= kThreads * 168, "within the launch's registers");
 
 template <int D, bool MX4>
 struct Cfg {
+  static constexpr int kWarps = 16, kThreads = kWarps * 32;
+  // Registers of the four groups of four warps; they add up to what the block is launched
+  // with (512 threads x 128).
+  static constexpr int kRegsIssue = 72, kRegsSoftmax = 192, kRegsTame = 56;
+  static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsTame <= 4 * 128);
   static constexpr int kBoxes = D / 64;  // 64-column (128-byte) swizzle boxes per row
   static constexpr int kBoxBytes = BN * 128;
-  static constexpr int kQBytes = BM * D * 2;
+  static constexpr int kQBytes = BM * D * 2;  // of a half
   static constexpr int kTileBytes = BN * D * 2;
-  static constexpr int kNS = MX4 ? (D == 128 ? 2 : 4) : (D == 128 ? 3 : 6);  // stages of K, and of V
-  // 4-bit rows on their way: codes, then scales
-  static constexpr int kRawCodes = BN * D / 2, kRawScales = BN * D / 32;
+  static constexpr int kNK = D == 128 ? 2 : 4;                     // stages of K
+  static constexpr int kNV = D == 128 ? (MX4 ? 2 : 3) : (MX4 ? 4 : 5);  // of V
+  // 4-bit rows on their way, half a block of them: codes, then scales
+  static constexpr int kRawRows = 64;
+  static constexpr int kRawCodes = kRawRows * D / 2, kRawScales = kRawRows * D / 32;
   static constexpr int kRawBytes = kRawCodes + kRawScales;
-  // (at most kNS: a producer that finds an entry free then knows that the tile before the
-  // last in its stage is done with, so it cannot take that one's phase for the last one's)
-  static constexpr int kNR = MX4 ? (D == 128 ? 2 : 3) : 0;
-  static_assert(kNR <= kNS);
-  static constexpr int kOffK = kQBytes;
-  static constexpr int kOffV = kOffK + kNS * kTileBytes;
-  static constexpr int kOffRawK = kOffV + kNS * kTileBytes;
+  static constexpr int kNR = MX4 ? (D == 128 ? 3 : 4) : 0;
+  static constexpr int kOffK = 2 * kQBytes;
+  static constexpr int kOffV = kOffK + kNK * kTileBytes;
+  static constexpr int kOffRawK = kOffV + kNV * kTileBytes;
   static constexpr int kOffRawV = kOffRawK + kNR * kRawBytes;
   static constexpr int kOffBar = kOffRawV + kNR * kRawBytes;
-  static constexpr int kSmemBytes = kOffBar + 1536 + 1024;  // barriers, alignment
-  static constexpr uint32_t kColS = 0, kColO = 256, kColP = 384, kColQ = 448;
+  static constexpr int kSmemBytes = kOffBar + 2048 + 1024;  // barriers, alignment
+  static constexpr uint32_t kColS = 0, kColO = 256;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
   static_assert(kOffBar % 16 == 0 && kRawBytes % 16 == 0);
 };
 
+constexpr int kMaxStages = 5, kMaxRaw = 4;
+
 struct alignas(16) Barriers {
-  uint64_t q_full, q_tmem;  // Q of the current tile landed / copied into TMEM
-  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+  uint64_t q_full, q_free;  // Q of the current tile landed / its last S = Q K^T completed
+  uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
   // bf16 pages: a partly seen V block lands at v_check and not at v_full, and is v_ready
   // once it has been made harmless. (A barrier of its own, whose phases the warps that
-  // do it wait for one by one: they skip the other blocks.)
-  uint64_t v_check[6], v_ready[6];
-  uint64_t raw_k_full[4], raw_k_empty[4], raw_v_full[4], raw_v_empty[4];
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
-  uint64_t mma_done, mma_done_pv;
+  // do it wait for one by one: they skip the other blocks.) 4-bit pages: a depth block
+  // lands at k_check and v_check, and is full once the unpacking warps have seen it.
+  uint64_t k_check[kMaxStages], v_check[kMaxStages], v_ready[kMaxStages];
+  uint64_t raw_k_full[kMaxRaw], raw_k_empty[kMaxRaw], raw_v_full[kMaxRaw], raw_v_empty[kMaxRaw];
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
-  int poison[8];  // [k % 8] = k + 1: tile k had infinities or NaN taken out (at most kNS tiles are under way)
-  ShareSmem<kWarps> find;
+  int poison[8];  // [k % 8] = k + 1: tile k had infinities or NaN taken out (fewer tiles are under way)
+  ShareSmem find;
   Share share;
-  Walk walk[4];  // of the softmax warps, whose registers are full
+  Walk walk[8];  // of the softmax warps, whose registers are full
 };
-static_assert(sizeof(Barriers) <= 1536, "barrier block");
+static_assert(sizeof(Barriers) <= 2048, "barrier block");
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   const bool ok = mbar_wait_bounded(bar, parity, abort, kTimeoutNs);
   return __all_sync(0xffffffffu, ok);
+}
+// One arrival for the warp, behind what its lanes have done.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(bar));
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -113,6 +122,20 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
+
+// Waits for tcgen05.ld and ties the 32 registers to it: nothing that reads them moves up.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+#define MODA_RW8(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), \
+                    "+r"(r[i + 6]), "+r"(r[i + 7])
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : MODA_RW8(0), MODA_RW8(8), MODA_RW8(16), MODA_RW8(24)::"memory");
+}
+__device__ __forceinline__ void tmem_ld_wait128(uint32_t (&r)[128]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : MODA_RW8(0), MODA_RW8(8), MODA_RW8(16)::"memory");
+#pragma unroll
+  for (int i = 24; i < 120; i += 24) asm volatile("" : MODA_RW8(i), MODA_RW8(i + 8), MODA_RW8(i + 16)::"memory");
+  asm volatile("" : MODA_RW8(120)::"memory");
+}
+#undef MODA_RW8
 
 // Is block (depth, index) of the walk's tile one that some row sees in part?
 __device__ __forceinline__ bool partly_seen(const Walk& w, const Sched& sch) {
@@ -148,67 +171,78 @@ __device__ __forceinline__ bool tame_row(uint8_t* tile, int r, bool counts) {
   return true;
 }
 
-// A 4-bit tile (codes, then scales) into a bf16 tile, by four warps: lane group
-// of D / 32 lanes a row, a block of 32 elements a lane. TAME: as tame_row, with
+// Half a block of 4-bit rows (codes, then scales) into rows row0 .. of a bf16 tile, by
+// four warps: D / 32 lanes a row, a block of 32 elements a lane. TAME: as tame_row, with
 // counts(r) for the rows.
 template <int D, bool TAME, class Counts>
-__device__ __forceinline__ bool unpack_tile(const uint8_t* raw, uint8_t* tile, int warp, int lane, Counts counts) {
-  constexpr int BPR = D / 32;          // blocks, and lanes, of a row
-  constexpr int RPI = 32 / BPR;        // rows a warp takes at once
-  constexpr int kBoxBytes = BN * 128;
+__device__ __forceinline__ bool unpack_rows(const uint8_t* raw, uint8_t* tile, int row0, int warp, int lane,
+                                            Counts counts) {
+  constexpr int BPR = D / 32;    // blocks, and lanes, of a row
+  constexpr int RPI = 32 / BPR;  // rows a warp takes at once
+  constexpr int kBoxBytes = BN * 128, kRows64 = 64;
   const int qtr = lane % BPR;
   bool found = false;
 #pragma unroll
-  for (int it = 0; it < BN / (4 * RPI); ++it) {
-    const int r = (it * 4 + warp) * RPI + lane / BPR;
-    const uint4 codes = *reinterpret_cast<const uint4*>(raw + r * (D / 2) + qtr * 16);
-    const uint32_t b = raw[BN * D / 2 + r * BPR + qtr];
-    uint32_t mul, mul2;
-    factors(b, mul, mul2);
-    const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
-    // the block's four 16-byte chunks; in the order that the lanes of eight
-    // (two rows) meet different banks
-    uint8_t* row = tile + (qtr >> 1) * kBoxBytes + r * 128;
-    uint32_t y[4][4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) unpack8(cw[j], mul, mul2, y[j]);
-    if constexpr (TAME) {
-      const bool c = counts(r);
-      if (!c || b >= 253u) {
-        uint32_t bad = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t f = not_finite(y[j][i]);
-            bad |= f;
-            y[j][i] &= c ? ~(((f & 0x8000u) ? 0xffffu : 0u) | ((f & 0x80000000u) ? 0xffff0000u : 0u)) : 0u;
-          }
-        found |= c && bad;
-      }
-    }
-    const int turn = (qtr >> 1) << 1;
+  for (int it = 0; it < kRows64 / (4 * RPI); ++it) {
+    const int rr = (it * 4 + warp) * RPI + lane / BPR, r = row0 + rr;
+    const uint4 codes = *reinterpret_cast<const uint4*>(raw + rr * (D / 2) + qtr * 16);
+    const uint32_t b = raw[kRows64 * D / 2 + rr * BPR + qtr];
+    const uint32_t scale = scale_of(b);
+    // the block's four 16-byte chunks 4 (qtr & 1) + j of the 64-column box; lanes of the
+    // upper box take them in another order, so that eight lanes (two rows) meet different
+    // banks
+    const bool upper = qtr >> 1;
+    uint8_t* row = tile + (upper ? kBoxBytes : 0) + r * 128;
+    const uint32_t cw[4] = {upper ? codes.z : codes.x, upper ? codes.w : codes.y, upper ? codes.x : codes.z,
+                            upper ? codes.y : codes.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int jj = j;  // chunk 4 (qtr & 1) + j of the 64-column box
-      const int chunk = 4 * (qtr & 1) + (jj ^ turn);
-      // y is indexed by the chunk that is stored: a select between two, both static
-      const uint32_t* lo = y[jj];
-      const uint32_t* hi = y[jj ^ 2];
-      const uint4 v = turn ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      *reinterpret_cast<uint4*>(row + ((chunk ^ (r & 7)) << 4)) = v;
+      uint32_t y[4];
+      unpack8(cw[j], scale, y);
+      if constexpr (TAME) {
+        const bool c = counts(r);
+        if (!c || b >= 253u) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t f = not_finite(y[i]);
+            found |= c && f;
+            y[i] &= c ? ~(((f & 0x8000u) ? 0xffffu : 0u) | ((f & 0x80000000u) ? 0xffff0000u : 0u)) : 0u;
+          }
+        }
+      }
+      const int chunk = 4 * (qtr & 1) + (upper ? j ^ 2 : j);
+      *reinterpret_cast<uint4*>(row + ((chunk ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
     }
   }
   return found;
 }
 
+// p = 2^(s sl - m) of N scores as bf16 pairs, added up in acc.
+template <int N>
+__device__ __forceinline__ void weigh(const uint32_t* x, uint32_t* pk, float sl, float m, uint64_t (&acc)[4]) {
+  const uint64_t sl2 = f2(sl, sl), nb2 = f2(-m, -m);
+#pragma unroll
+  for (int c = 0; c < N / 2; ++c) {
+    float u, w;
+    f2_split(ffma2(f2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sl2, nb2), u, w);
+    const float e0 = ex2_approx(u), e1 = ex2_approx(w);
+    pk[c] = pack_bf16x2(e0, e1);
+    acc[c & 3] = fadd2(acc[c & 3], f2(e0, e1));
+  }
+}
+__device__ __forceinline__ float total_of(uint64_t (&acc)[4]) {
+  float u, w;
+  f2_split(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), u, w);
+  return u + w;
+}
+
 template <int D, bool MX4>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, MX4>::kThreads, 1)
 prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKd,
                      const __grid_constant__ CUtensorMap tmVd, const __grid_constant__ Params p) {
   using C = Cfg<D, MX4>;
-  constexpr int NS = C::kNS, NR = MX4 ? C::kNR : 1;
+  constexpr int NK = C::kNK, NV = C::kNV, NR = MX4 ? C::kNR : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -216,36 +250,36 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   const uint32_t sQ = smem_u32(smem), sK = smem_u32(smem + C::kOffK), sV = smem_u32(smem + C::kOffV);
   volatile int* abort = &bars->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G2 = 1 << p.lgG, P = BM >> p.lgG;
+  const int P = BM >> p.lgG;           // positions of a half
   const int PW = P >> 2, SP = 32 / PW;  // positions and slots of a softmax warp's word of a depth block
 
   if (tid == 0) {
     bars->abort = 0;
     for (int& x : bars->poison) x = 0;
     mbar_init(smem_u32(&bars->q_full), 1);
-    mbar_init(smem_u32(&bars->q_tmem), 128);
-    for (int s = 0; s < 6; ++s) {
-      mbar_init(smem_u32(&bars->k_full[s]), MX4 ? 128 : 1);
+    mbar_init(smem_u32(&bars->q_free), 1);
+    for (int s = 0; s < kMaxStages; ++s) {
+      // 4-bit pages: the unpacking warps, and warp 3, which sees every stage free
+      mbar_init(smem_u32(&bars->k_full[s]), MX4 ? 5 : 1);
       mbar_init(smem_u32(&bars->k_empty[s]), 1);
-      mbar_init(smem_u32(&bars->v_full[s]), MX4 ? 128 : 1);
+      mbar_init(smem_u32(&bars->v_full[s]), MX4 ? 5 : 1);
       mbar_init(smem_u32(&bars->v_empty[s]), 1);
+      mbar_init(smem_u32(&bars->k_check[s]), 1);
       mbar_init(smem_u32(&bars->v_check[s]), 1);
-      mbar_init(smem_u32(&bars->v_ready[s]), 128);
+      mbar_init(smem_u32(&bars->v_ready[s]), 4);
     }
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < kMaxRaw; ++s) {
       mbar_init(smem_u32(&bars->raw_k_full[s]), 1);
-      mbar_init(smem_u32(&bars->raw_k_empty[s]), 128);
+      mbar_init(smem_u32(&bars->raw_k_empty[s]), 4);
       mbar_init(smem_u32(&bars->raw_v_full[s]), 1);
-      mbar_init(smem_u32(&bars->raw_v_empty[s]), 128);
+      mbar_init(smem_u32(&bars->raw_v_empty[s]), 4);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_u32(&bars->s_full[b]), 1);
-      mbar_init(smem_u32(&bars->s_free[b]), 128);
-      mbar_init(smem_u32(&bars->p_full[b]), 128);
-      mbar_init(smem_u32(&bars->pv_done[b]), 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(smem_u32(&bars->s_full[x]), 1);
+      mbar_init(smem_u32(&bars->p_full[x]), 4);
+      mbar_init(smem_u32(&bars->o_done[x]), 1);
     }
     mbar_init(smem_u32(&bars->mma_done), 1);
-    mbar_init(smem_u32(&bars->mma_done_pv), 1);
     fence_barrier_init();
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmKd);
@@ -257,7 +291,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   }
   paged::wait_for_stream();
   {
-    const Share mine = share_of<kWarps, kLeast>(p, bars->find);
+    const Share mine = share_of<C::kWarps, kLeast>(p, bars->find);
     if (mine.from >= mine.to) {
       if (tid == 0) work_of(p.work, D).opened[blockIdx.x] = {0, 0, 0, 0};
       return;
@@ -275,250 +309,314 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   const Share& sh = bars->share;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsIssue));
     if (warp == 0 || warp == 2) {
       // ---------------------------------------------------- TMA producers
       const bool is_k = warp == 0;
       const bool leader = elect_one();
       const uint64_t pol_once = l2_policy_evict_first();
-      const CUtensorMap* seq_map = is_k ? &tmK : &tmV;
-      const CUtensorMap* dep_map = is_k ? &tmKd : &tmVd;
+      const int ns = is_k ? NK : NV;  // stages
       uint64_t* full = MX4 ? (is_k ? bars->raw_k_full : bars->raw_v_full) : (is_k ? bars->k_full : bars->v_full);
       uint64_t* empty = MX4 ? (is_k ? bars->raw_k_empty : bars->raw_v_empty) : (is_k ? bars->k_empty : bars->v_empty);
-      uint64_t* tile_empty = is_k ? bars->k_empty : bars->v_empty;
-      constexpr int NF = MX4 ? NR : NS;  // entries of `full`
-      const uint32_t tiles = is_k ? sK : sV;
-      const uint32_t raws = smem_u32(smem + (is_k ? C::kOffRawK : C::kOffRawV));
       const int page_rows = 1 << p.page_shift;  // at most 128
-      // a lane copies one page's rows (bf16: 64 columns of them)
+      // a lane copies one page's rows (bf16: 64 columns of them; 4-bit: at most 64 rows)
       constexpr int kParts = MX4 ? 1 : C::kBoxes;
       const int my_box = lane / kParts, my_part = lane % kParts;
-      int g = 0, nq = 0;
+      const int box_rows = MX4 ? min(page_rows, C::kRawRows) : page_rows;
+      int e = 0, f = 0, fph = 0, nq = 0;  // entries; the next one's stage (raw entry) and phase; Q loads
       uint32_t checks = 0, wholes = 0;  // of V's stages: parities of what went to v_check, to v_full
       uint32_t any_check = 0, any_whole = 0;
       Walk w;
       w.begin(p, sh);
       bool ok = true;
       for (int k = 0; ok && w.next(p, sh); ++k) {
+        const int halves = w.npos > P ? 2 : 1;
         if (is_k) {
-          // Q, once the softmax warps have copied the previous one into TMEM
-          if (k > 0 && !warp_wait(smem_u32(&bars->q_tmem), (k - 1) & 1, abort)) break;
+          // Q, once the last S product of the tile before has completed
+          if (k > 0 && !warp_wait(smem_u32(&bars->q_free), (k - 1) & 1, abort)) break;
           if (leader) {
             const uint32_t qb = smem_u32(&bars->q_full);
-            mbar_arrive_expect_tx(qb, C::kQBytes);
-            for (int c = 0; c < C::kBoxes; ++c)
-              tma_load_3d_hint(sQ + c * C::kBoxBytes, &tmQ, qb, c * 64, w.hk * p.G, w.token, pol_once);
+            mbar_arrive_expect_tx(qb, halves * C::kQBytes);
+            for (int x = 0; x < halves; ++x)
+              for (int c = 0; c < C::kBoxes; ++c)
+                tma_load_3d_hint(sQ + x * C::kQBytes + c * C::kBoxBytes, &tmQ, qb, c * 64, w.hk * p.G,
+                                 w.token + x * P, pol_once);
           }
           ++nq;
         }
         Sched sch(p.n_depth, w.nb, w.j0);
         const int* table = p.table + (int64_t)w.b * p.max_pages;
-        // the lane's page of the sequence block after this one, looked up ahead
+        // the lane's page of a sequence block, looked up one block ahead
         auto page_of = [&](int index) -> int {
-          const int key = index * BN + (my_box << p.page_shift);
-          return my_box << p.page_shift < BN && key <= w.t_last ? table[key >> p.page_shift] : -1;
+          const int key = index * BN + my_box * box_rows;
+          return my_box * box_rows < BN && key <= w.t_last ? table[key >> p.page_shift] : -1;
         };
         int page = page_of(sch.sbk);
-        for (int j = w.j0; j < w.j1; ++j, ++g) {
+        for (int j = w.j0; ok && j < w.j1; ++j) {
           sch.next(p.n_depth, w.nb);
-          const int f = g % NF, s = g % NS;
           int pg = page;
           if (!sch.depth) page = page_of(sch.index + 1);
-          if (!warp_wait(smem_u32(&empty[f]), ((g / NF) & 1) ^ 1, abort)) {
-            ok = false;
-            break;
-          }
-          uint32_t fb = smem_u32(&full[f]);
-          if (!MX4 && !is_k) {
-            if (partly_seen(w, sch)) {
-              fb = smem_u32(&bars->v_check[s]);
-              checks ^= 1u << s;
-              any_check |= 1u << s;
-            } else {
-              wholes ^= 1u << s;
-              any_whole |= 1u << s;
-            }
-          }
-          if (sch.depth) {
-            // the words of the softmax warps that have positions: slots [SP index, + SP)
-            // of warp w's PW positions, row slot * PW + position (4-bit pages: straight
-            // into the tile, whose consumers are done then)
-            if (MX4 && !warp_wait(smem_u32(&tile_empty[s]), ((g / NS) & 1) ^ 1, abort)) {
+          // a depth block of each half, or a sequence block for both
+          const int entries = sch.depth ? (MX4 ? 0 : halves) : (MX4 ? 2 : 1);
+          for (int x = 0; x < entries; ++x) {
+            if (!warp_wait(smem_u32(&empty[f]), fph ^ 1, abort)) {
               ok = false;
               break;
             }
-            if (leader) {
-              const int words = (w.npos + PW - 1) / PW;
-              mbar_arrive_expect_tx(fb, words * 32 * D * 2);
-              const uint32_t dst = tiles + s * C::kTileBytes;
-              for (int x = 0; x < words; ++x)
-                for (int c = 0; c < C::kBoxes; ++c)
-                  tma_load_4d_hint(dst + c * C::kBoxBytes + x * 32 * 128, dep_map, fb, c * 64, w.hk,
-                                   w.token + x * PW, sch.index * SP, pol_once);
-            }
-          } else {
-            const int rows = min(BN, w.t_last + 1 - sch.index * BN);
-            const int boxes = (rows + page_rows - 1) >> p.page_shift;
-            if (leader) mbar_arrive_expect_tx(fb, boxes * page_rows * (MX4 ? D / 2 + D / 32 : D * 2));
-            __syncwarp();
-            if (my_box < boxes) {
-              if (pg < 0 || pg >= p.num_pages) {
-                atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
-                pg = 0;
+            uint32_t fb = smem_u32(&full[f]);
+            if constexpr (!MX4) {
+              if (!is_k) {
+                if (partly_seen(w, sch)) {
+                  fb = smem_u32(&bars->v_check[f]);
+                  checks ^= 1u << f;
+                  any_check |= 1u << f;
+                } else {
+                  wholes ^= 1u << f;
+                  any_whole |= 1u << f;
+                }
               }
-              const int head = pg * p.Hk + w.hk;
-              if constexpr (MX4) {
-                const uint32_t dst = raws + f * C::kRawBytes;
-                const int64_t row = (int64_t)head << p.page_shift;
-                bulk_load(dst + my_box * page_rows * (D / 2), (is_k ? p.k : p.v) + row * (D / 2),
-                          page_rows * (D / 2), fb);
-                bulk_load(dst + C::kRawCodes + my_box * page_rows * (D / 32),
-                          (is_k ? p.k_scale : p.v_scale) + row * (D / 32), page_rows * (D / 32), fb);
+              const uint32_t dst = (is_k ? sK : sV) + f * C::kTileBytes;
+              if (sch.depth) {
+                // the words of the softmax warps that have positions: slots [SP index, + SP)
+                // of a warp's PW positions, row slot * PW + position
+                if (leader) {
+                  const int words = (min(w.npos - x * P, P) + PW - 1) / PW;
+                  mbar_arrive_expect_tx(fb, words * 32 * D * 2);
+                  for (int y = 0; y < words; ++y)
+                    for (int c = 0; c < C::kBoxes; ++c)
+                      tma_load_4d_hint(dst + c * C::kBoxBytes + y * 32 * 128, is_k ? &tmKd : &tmVd, fb, c * 64, w.hk,
+                                       w.token + x * P + y * PW, sch.index * SP, pol_once);
+                }
               } else {
-                tma_load_3d(tiles + s * C::kTileBytes + my_part * C::kBoxBytes + my_box * page_rows * 128, seq_map,
-                            fb, my_part * 64, 0, head);
+                const int rows = min(BN, w.t_last + 1 - sch.index * BN);
+                const int boxes = (rows + page_rows - 1) >> p.page_shift;
+                if (leader) mbar_arrive_expect_tx(fb, boxes * page_rows * D * 2);
+                __syncwarp();
+                if (my_box < boxes) {
+                  if (pg < 0 || pg >= p.num_pages) {
+                    atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
+                    pg = 0;
+                  }
+                  tma_load_3d(dst + my_part * C::kBoxBytes + my_box * page_rows * 128, is_k ? &tmK : &tmV, fb,
+                              my_part * 64, 0, pg * p.Hk + w.hk);
+                }
               }
+            } else {
+              // half of the block's rows; lane y has page rows [y box_rows, ..) of the block
+              const int rows = min(C::kRawRows, w.t_last + 1 - sch.index * BN - x * C::kRawRows);
+              const int boxes = rows > 0 ? (rows + box_rows - 1) / box_rows : 0;
+              if (leader) mbar_arrive_expect_tx(fb, boxes * box_rows * (D / 2 + D / 32));
+              __syncwarp();
+              const int mine = my_box - x * (C::kRawRows / box_rows);
+              if (mine >= 0 && mine < boxes) {
+                if (pg < 0 || pg >= p.num_pages) {
+                  atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
+                  pg = 0;
+                }
+                const uint32_t dst = smem_u32(smem + (is_k ? C::kOffRawK : C::kOffRawV)) + f * C::kRawBytes;
+                const int64_t row = ((int64_t)(pg * p.Hk + w.hk) << p.page_shift) +
+                                    (my_box * box_rows & (page_rows - 1));
+                bulk_load(dst + mine * box_rows * (D / 2), (is_k ? p.k : p.v) + row * (D / 2), box_rows * (D / 2),
+                          fb);
+                bulk_load(dst + C::kRawCodes + mine * box_rows * (D / 32),
+                          (is_k ? p.k_scale : p.v_scale) + row * (D / 32), box_rows * (D / 32), fb);
+              }
+            }
+            __syncwarp();
+            ++e;
+            if (++f == (MX4 ? NR : ns)) {
+              f = 0;
+              fph ^= 1;
             }
           }
-          __syncwarp();
         }
       }
       // every copy of this warp has landed before its shared memory is released
       if (leader) {
         int never = 0;
         if (!MX4 && !is_k) {
-          for (int s = 0; s < NS; ++s) {
+          for (int s = 0; s < NV; ++s) {
             if (any_whole >> s & 1)
               mbar_wait_bounded(smem_u32(&bars->v_full[s]), (wholes >> s & 1) ^ 1, &never, kTimeoutNs);
             if (any_check >> s & 1)
               mbar_wait_bounded(smem_u32(&bars->v_check[s]), (checks >> s & 1) ^ 1, &never, kTimeoutNs);
           }
         } else {
-          for (int j = max(0, g - NF); j < g; ++j)
-            mbar_wait_bounded(smem_u32(&full[j % NF]), (j / NF) & 1, &never, kTimeoutNs);
+          const int n = MX4 ? NR : ns;
+          for (int j = max(0, e - n); j < e; ++j)
+            mbar_wait_bounded(smem_u32(&full[j % n]), (j / n) & 1, &never, kTimeoutNs);
         }
         if (is_k && nq > 0) mbar_wait_bounded(smem_u32(&bars->q_full), (nq - 1) & 1, &never, kTimeoutNs);
       }
       __syncwarp();
+    } else if (warp == 3) {
+      if constexpr (MX4) {
+        // ------------------------- depth blocks beside 4-bit pages, and every stage seen free
+        // (a stage's next user waits for this warp too, so that it misses no phase)
+        if (elect_one()) {
+          const uint64_t pol_once = l2_policy_evict_first();
+          uint32_t landed[2] = {0, 0}, any[2] = {0, 0};  // of K, of V: parities and use of k_check, v_check
+          int e = 0;
+          bool ok = true;
+          Walk w;
+          w.begin(p, sh);
+          while (ok && w.next(p, sh)) {
+            const int halves = w.npos > P ? 2 : 1;
+            Sched sch(p.n_depth, w.nb, w.j0);
+            for (int j = w.j0; ok && j < w.j1; ++j) {
+              sch.next(p.n_depth, w.nb);
+              for (int x = 0; ok && x < (sch.depth ? halves : 1); ++x, ++e) {
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                  const int ns = v ? NV : NK, s = e % ns;
+                  if (!mbar_wait_bounded(smem_u32(v ? &bars->v_empty[s] : &bars->k_empty[s]), ((e / ns) & 1) ^ 1, abort,
+                                         kTimeoutNs)) {
+                    ok = false;
+                    break;
+                  }
+                  if (sch.depth) {
+                    const uint32_t fb = smem_u32(v ? &bars->v_check[s] : &bars->k_check[s]);
+                    const int words = (min(w.npos - x * P, P) + PW - 1) / PW;
+                    landed[v] ^= 1u << s;
+                    any[v] |= 1u << s;
+                    mbar_arrive_expect_tx(fb, words * 32 * D * 2);
+                    const uint32_t dst = (v ? sV : sK) + s * C::kTileBytes;
+                    for (int y = 0; y < words; ++y)
+                      for (int c = 0; c < C::kBoxes; ++c)
+                        tma_load_4d_hint(dst + c * C::kBoxBytes + y * 32 * 128, v ? &tmVd : &tmKd, fb, c * 64, w.hk,
+                                         w.token + x * P + y * PW, sch.index * SP, pol_once);
+                  }
+                  mbar_arrive(smem_u32(v ? &bars->v_full[s] : &bars->k_full[s]));
+                }
+              }
+            }
+          }
+          int never = 0;
+          for (int v = 0; v < 2; ++v)
+            for (int s = 0; s < (v ? NV : NK); ++s)
+              if (any[v] >> s & 1)
+                mbar_wait_bounded(smem_u32(v ? &bars->v_check[s] : &bars->k_check[s]), (landed[v] >> s & 1) ^ 1, &never,
+                                  kTimeoutNs);
+        }
+        __syncwarp();
+      }
     } else if (elect_one()) {
-      // ------------------------------------------------------- MMA issuers
+      // -------------------------------------------------------- MMA issuer
+      // One thread issues everything, in the order S of the halves, then for each block
+      // and half P V of the block before and S of this one: MMAs complete in order, so a
+      // half's S may overwrite the P that the P V before it reads.
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         return mbar_wait_bounded(smem_u32(bar), parity, abort, kTimeoutNs);
       };
-      const uint64_t dk = sdesc_sw128(sK, 16, 1024);
-      const uint32_t hi = (uint32_t)(dk >> 32);
-      int g = 0;
+      constexpr uint32_t idS = idesc_bf16_f32(BM, BN, false), idPV = idesc_bf16_f32(BM, D, true);
+      const uint64_t dq = sdesc_sw128(sQ, 16, 1024);
+      const uint32_t hi = (uint32_t)(dq >> 32), q_lo = (uint32_t)dq;
+      const uint32_t k_lo = (uint32_t)sdesc_sw128(sK, 16, 1024), v_lo = (uint32_t)sdesc_sw128(sV, C::kBoxBytes, 1024);
+      // entries of K: stage and phase of the next; of V (one block later): the next, and
+      // bf16 pages' parities of v_ready and v_full, a bit for each stage
+      int ks = 0, kph = 0, vs = 0, vph = 0;
+      uint32_t ready = 0, whole = 0, pph = 0;  // pph: parities of p_full
+      auto wait_v = [&](bool part) -> bool {
+        if (MX4) return wait(&bars->v_full[vs], vph);
+        if (part) {
+          if (!wait(&bars->v_ready[vs], ready >> vs & 1)) return false;
+          ready ^= 1u << vs;
+        } else {
+          if (!wait(&bars->v_full[vs], whole >> vs & 1)) return false;
+          whole ^= 1u << vs;
+        }
+        return true;
+      };
+      auto next_v = [&] {
+        tc_commit(smem_u32(&bars->v_empty[vs]));
+        if (++vs == NV) {
+          vs = 0;
+          vph ^= 1;
+        }
+      };
+      // P V of half x with the V in stage vs
+      auto pv = [&](int x, uint32_t accumulate) {
+        const uint32_t vb = v_lo + ((uint32_t)(vs * C::kTileBytes) >> 4);
+        const uint32_t pcol = tbase + C::kColS + x * 128, ocol = tbase + C::kColO + x * D;
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          mma_ts(ocol, pcol + kk * 8, desc_join(vb + ((uint32_t)(kk * 2048) >> 4), hi), idPV, kk > 0 ? 1u : accumulate);
+      };
       bool ok = true;
       Walk w;
       w.begin(p, sh);
-      if (warp == 1) {
-        constexpr uint32_t idS = idesc_bf16_f32(BM, BN, false);
-        const uint32_t k_lo = (uint32_t)dk;
-        for (int k = 0; ok && w.next(p, sh); ++k) {
-          if (!wait(&bars->q_tmem, k & 1)) break;
-          for (int j = w.j0; j < w.j1; ++j, ++g) {
-            const int ks = g % NS;
-            if ((g >= 2 && !wait(&bars->s_free[g & 1], ((g - 2) >> 1) & 1)) ||
-                !wait(&bars->k_full[ks], (g / NS) & 1)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t kb = k_lo + ((uint32_t)(ks * C::kTileBytes) >> 4);
-            const uint32_t dcol = tbase + C::kColS + (g & 1) * 128;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = ((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4;
-              mma_ts(dcol, tbase + C::kColQ + kk * 8, desc_join(kb + off, hi), idS, kk > 0);
-            }
-            tc_commit(smem_u32(&bars->k_empty[ks]));
-            tc_commit(smem_u32(&bars->s_full[g & 1]));
-          }
-        }
-      } else {
-        constexpr uint32_t idPV = idesc_bf16_f32(BM, D, true);
-        const uint32_t v_lo = (uint32_t)sdesc_sw128(sV, C::kBoxBytes, 1024);
-        const uint32_t pcol = tbase + C::kColP;
-        uint32_t ready = 0, whole = 0;  // bf16: parities of v_ready and v_full, a bit for each stage
-        for (int k = 0; ok && w.next(p, sh); ++k) {
-          Sched sch(p.n_depth, w.nb, w.j0);
-          for (int j = w.j0; j < w.j1; ++j, ++g) {
+      for (int k = 0; ok && w.next(p, sh); ++k) {
+        const int halves = w.npos > P ? 2 : 1;
+        if (!wait(&bars->q_full, k & 1)) break;
+        Sched sch(p.n_depth, w.nb, w.j0);
+        bool depth = false, part = false;  // of the block before
+        for (int j = w.j0; ok && j <= w.j1; ++j) {
+          const bool was_depth = depth, was_part = part, last = j == w.j1;
+          if (!last) {
             sch.next(p.n_depth, w.nb);
-            const int sb = g & 1, vs = g % NS;
-            bool there;
-            if (MX4) {
-              there = wait(&bars->v_full[vs], (g / NS) & 1);
-            } else if (partly_seen(w, sch)) {
-              there = wait(&bars->v_ready[vs], (ready >> vs) & 1);
-              ready ^= 1u << vs;
-            } else {
-              there = wait(&bars->v_full[vs], (whole >> vs) & 1);
-              whole ^= 1u << vs;
+            depth = sch.depth;
+            part = partly_seen(w, sch);
+          }
+          for (int x = 0; x < halves; ++x) {
+            if (j > w.j0) {
+              if (((x == 0 || was_depth) && !wait_v(was_part)) || !wait(&bars->p_full[x], pph >> x & 1)) {
+                ok = false;
+                break;
+              }
+              pph ^= 1u << x;
+              tc_fence_after();
+              // a tile's first P V overwrites O (the softmax warps have read the tile
+              // before's O before they stored this P)
+              pv(x, j - 1 > w.j0 ? 1u : 0u);
+              if (last) tc_commit(smem_u32(&bars->o_done[x]));
+              if (x == halves - 1 || was_depth) next_v();
             }
-            if (!there || !wait(&bars->p_full[sb], (g >> 1) & 1)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t vb = v_lo + ((uint32_t)(vs * C::kTileBytes) >> 4);
-            // a tile's first P V overwrites O (the softmax warps have read the previous
-            // tile's O before they stored this P)
-            const uint32_t acc0 = j > w.j0 ? 1u : 0u;
+            if (!last) {
+              if ((x == 0 || depth) && !wait(&bars->k_full[ks], kph)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t kb = k_lo + ((uint32_t)(ks * C::kTileBytes) >> 4);
+              const uint32_t qb = q_lo + ((uint32_t)(x * C::kQBytes) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk)
-              mma_ts(tbase + C::kColO, pcol + kk * 8, desc_join(vb + ((uint32_t)(kk * 2048) >> 4), hi), idPV,
-                     kk > 0 ? 1u : acc0);
-            tc_commit(smem_u32(&bars->v_empty[vs]));
-            tc_commit(smem_u32(&bars->pv_done[sb]));
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4;
+                mma_ss(tbase + C::kColS + x * 128, desc_join(qb + off, hi), desc_join(kb + off, hi), idS, kk > 0);
+              }
+              tc_commit(smem_u32(&bars->s_full[x]));
+              if (x == halves - 1 || depth) {
+                tc_commit(smem_u32(&bars->k_empty[ks]));
+                if (++ks == NK) {
+                  ks = 0;
+                  kph ^= 1;
+                }
+              }
+              if (j == w.j1 - 1 && x == halves - 1) tc_commit(smem_u32(&bars->q_free));
+            }
           }
         }
       }
-      // every MMA issued by this thread has completed before TMEM is freed
-      uint64_t* done = warp == 1 ? &bars->mma_done : &bars->mma_done_pv;
+      // every MMA has completed before TMEM is freed
       int never = 0;
-      tc_commit(smem_u32(done));
-      mbar_wait_bounded(smem_u32(done), 0, &never, kTimeoutNs);
+      tc_commit(smem_u32(&bars->mma_done));
+      mbar_wait_bounded(smem_u32(&bars->mma_done), 0, &never, kTimeoutNs);
     }
     __syncwarp();
-  } else if (warp < 8) {
+  } else if (warp < 12) {
     // ----------------------------------------------------- softmax, epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int row = tid - 128;  // tile row == TMEM lane
-    const uint32_t lane_base = (uint32_t)(warp & 3) * 32;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
+    const int half = warp >= 8;
+    const int row = tid & 127;  // row of the half == TMEM lane
+    const uint32_t scol = tmem_addr(tbase, (uint32_t)(warp & 3) * 32, C::kColS + half * 128);
+    const uint32_t ocol = tmem_addr(tbase, (uint32_t)(warp & 3) * 32, C::kColO + half * D);
     const int wq = warp & 3;  // this warp's word of a depth block
-    const int lp = row >> p.lgG, h_off = row & (G2 - 1);
+    const int lp = half * P + (row >> p.lgG), h_off = row & ((1 << p.lgG) - 1);
     const int lpw = (row & 31) >> p.lgG;  // the row's position among its warp's
     const uint32_t own_cols = PW >= 32 ? 1u << lpw : (0xffffffffu / ((1u << PW) - 1u)) << lpw;
     const float sl = p.scale_log2;
-    const uint32_t zeros[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-    bool p_zero = false;  // this warp's P columns outside its depth word hold zeros
-    int g = 0;
-    // Q of tile k -> TMEM as bf16 pairs, the A operand of S = Q K^T; rows that no
-    // query has become 0. Called once every S product of the tile before has completed.
-    auto copy_q = [&](int k, const Walk& t) -> bool {
-      if (!warp_wait(smem_u32(&bars->q_full), k & 1, abort)) return false;
-      const bool there = lp < t.npos && h_off < p.G;
-      const uint8_t* qrow = smem + row * 128;
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t x[32];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 v = *reinterpret_cast<const uint4*>(qrow + c * C::kBoxBytes + ((i ^ (row & 7)) << 4));
-          x[4 * i] = there ? v.x : 0u;
-          x[4 * i + 1] = there ? v.y : 0u;
-          x[4 * i + 2] = there ? v.z : 0u;
-          x[4 * i + 3] = there ? v.w : 0u;
-        }
-        tmem_st32(tmem_addr(tbase, lane_base, C::kColQ + c * 32), x);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      fence_async();  // the Q region takes the next tile's Q (a TMA write): order these reads first
-      mbar_arrive(smem_u32(&bars->q_tmem));
-      return true;
-    };
-    Walk& w = bars->walk[wq];
+    uint32_t sph = 0, oph = 0;  // parities of s_full, o_done
+    Walk& w = bars->walk[warp - 4];
     // to the next tile; the warp has read what it wants of the one before
     auto advance = [&](bool first) -> bool {
       bool any = false;
@@ -531,293 +629,299 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       __syncwarp();  // what lane 0 has written is seen
       return any;
     };
-    bool more = advance(true), ok = !more || copy_q(0, w);
-    bool opened = false;
-    for (int k = 0; ok && more; ++k) {
+    bool opened = false, ok = true, more = advance(true);
+    for (int k = 0; ok && more; ++k, more = advance(false)) {
+      if (half && w.npos <= P) continue;
+      // rows without a query go along: their scores are the next tokens' (or zeros), and
+      // what they hold is not looked at
+      const bool there = lp < w.npos && h_off < p.G;
       float m_ref = -INFINITY, l = 0.f;
-      // Rescale O and l to a new reference when a block's raw max mx (log2 units) rose
-      // more than the threshold above it; false on a timeout. O holds blocks j0 .. j - 1.
-      auto rescale = [&](float mx, int j) -> bool {
-        const bool need = mx > m_ref + kRescaleThreshold;
-        if (__any_sync(0xffffffffu, need)) {
+      // Rescale O and l to a new reference where a block's raw max mx (log2 units) is
+      // above it. O holds blocks j0 .. j - 1: their P V has
+      // completed, since S of block j, issued behind it, has.
+      auto rescale = [&](float mx, int j) {
+        const bool need = mx > m_ref;
+        if (__any_sync(0xffffffffu, need && there)) {
           const float m_new = need ? mx : m_ref;
           const float alpha = need ? ex2_approx(m_ref - m_new) : 1.f;
           if (j > w.j0) {
-            if (!warp_wait(smem_u32(&bars->pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, abort)) return false;
-            tc_fence_after();
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               uint32_t r[32];
-              const uint32_t ta = tmem_addr(tbase, lane_base, C::kColO + c * 32);
-              tmem_ld32(ta, r);
-              tmem_ld_wait();
+              tmem_ld32(ocol + c * 32, r);
+              tmem_ld_wait(r);
 #pragma unroll
               for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-              tmem_st32(ta, r);
+              tmem_st32(ocol + c * 32, r);
             }
             tmem_st_wait();
           }
           l *= alpha;
           m_ref = m_new;
         }
-        return true;
       };
       // Every block: exponentiate against the running reference right away. Every p is
-      // at most the block's sum, so a sum within 2^threshold proves that no score rose
-      // more than that above it, and the block needs no maximum at all.
-      Sched sch(p.n_depth, w.nb, w.j0);
-      for (int j = w.j0; j < w.j1; ++j, ++g) {
-        sch.next(p.n_depth, w.nb);
-        const int sb = g & 1;
-        if (!warp_wait(smem_u32(&bars->s_full[sb]), (g >> 1) & 1, abort)) {
+      // at most the block's sum, so a sum within kSumBound proves that no score rose more
+      // than 8 (log2 units) above it, and the block needs no maximum at all. Else the
+      // reference becomes the row's maximum, and the block is weighed again.
+      const int nb = w.nb, j1 = w.j1, border0 = (w.t0 + 1) / BN;  // the first sequence block at the causal border
+      bool unset = true;  // some row has no reference yet
+      Sched sch(p.n_depth, nb, w.j0);
+      for (int j = w.j0; j < j1; ++j) {
+        sch.next(p.n_depth, nb);
+        if (!warp_wait(smem_u32(&bars->s_full[half]), sph, abort)) {
           ok = false;
           break;
         }
+        sph ^= 1;
         tc_fence_after();
-        const uint32_t pcol = tmem_addr(tbase, lane_base, C::kColP);
+        if (unset) unset = __any_sync(0xffffffffu, there && m_ref == -INFINITY);
+        bool slow = unset;
         float sum = 0.f;
         if (sch.depth) {
           // only this warp's word of 32 columns can hold its rows' slots: column c is
           // slot index * SP + c / PW of the warp's position c % PW
-          uint32_t xs[32];
-          tmem_ld32(tmem_addr(tbase, lane_base, C::kColS + sb * 128 + wq * 32), xs);
-          tmem_ld_wait();
-          tc_fence_before();
-          mbar_arrive(smem_u32(&bars->s_free[sb]));
           const int nbits = min(SP, p.L - sch.index * SP) * PW;
-          const uint32_t word =
-              lp < w.npos ? own_cols & (nbits >= 32 ? 0xffffffffu : (1u << nbits) - 1u) : 0u;
+          const uint32_t word = lp < w.npos ? own_cols & (nbits >= 32 ? 0xffffffffu : (1u << nbits) - 1u) : 0u;
+          uint32_t x[32], pk[16];
+          tmem_ld32(scol + wq * 32, x);
+          tmem_ld_wait(x);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) xs[i] = (word & (1u << i)) ? xs[i] : 0xff800000u;  // -inf
-          uint32_t pk[16];
-          bool slow = __any_sync(0xffffffffu, m_ref == -INFINITY);
-          if (!slow) {
-            sum = exp_block<32>(xs, pk, sl, m_ref);
-            slow = __any_sync(0xffffffffu, !(sum <= kSumBound));
+          for (int i = 0; i < 32; ++i) x[i] = (word & (1u << i)) ? x[i] : 0xff800000u;  // -inf
+          for (int pass = 0; pass < 2; ++pass) {
+            if (slow) rescale(raw_max32(x) * sl, j);
+            uint64_t acc[4] = {0, 0, 0, 0};
+            weigh<32>(x, pk, sl, m_ref == -INFINITY ? 0.f : m_ref, acc);
+            sum = total_of(acc);
+            if (slow) break;
+            slow = __any_sync(0xffffffffu, there && !(sum <= kSumBound));
+            if (!slow) break;
           }
-          if (slow) {
-            if (!rescale(raw_max32(xs) * sl, j)) {
-              ok = false;
-              break;
-            }
-            sum = exp_block<32>(xs, pk, sl, m_ref);
-          }
-          l += sum;
-          // P_g overwrites P_{g-1}: the tensor core must have consumed it
-          if (g >= 1) {
-            if (!warp_wait(smem_u32(&bars->pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, abort)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-          }
-          tmem_st16(pcol + wq * 16, pk);
-          if (!p_zero) {
-            for (int kk = 1; kk < 4; ++kk) tmem_st16(pcol + ((wq + kk) & 3) * 16, zeros);
-          }
-          p_zero = true;
+          const uint32_t zeros[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+          tmem_st16(scol + wq * 16, pk);
+          for (int kk = 1; kk < 4; ++kk) tmem_st16(scol + ((wq + kk) & 3) * 16, zeros);
         } else {
-          uint32_t x[BN];
+          // columns that the row sees: all, but at the causal border
+          const bool border = sch.index >= border0;
+          const int end = border ? min(w.t0 + lp, w.t_last) - sch.index * BN + 1 : BN;
+          uint32_t x[BN], pk[BN / 2];
+          for (int pass = 0; pass < 2; ++pass) {
+            if (slow) {
+              float mx = -INFINITY;
+#pragma unroll 1
+              for (int c = 0; c < BN / 32; ++c) {
+                uint32_t y[32];
+                tmem_ld32(scol + c * 32, y);
+                tmem_ld_wait(y);
 #pragma unroll
-          for (int c = 0; c < BN / 32; ++c)
-            tmem_ld32(tmem_addr(tbase, lane_base, C::kColS + sb * 128 + c * 32), x + c * 32);
-          tmem_ld_wait();
-          tc_fence_before();
-          mbar_arrive(smem_u32(&bars->s_free[sb]));
-          const int k0 = sch.index * BN;
-          if (k0 + BN - 1 > w.t0) {
-            const int end = min(w.t0 + lp, w.t_last) - k0 + 1;
-#pragma unroll
-            for (int c = 0; c < BN; ++c) x[c] = c < end ? x[c] : 0xff800000u;  // -inf
-          }
-          uint32_t pk[BN / 2];
-          bool slow = __any_sync(0xffffffffu, m_ref == -INFINITY);
-          if (!slow) {
-            sum = exp_block<BN>(x, pk, sl, m_ref);
-            slow = __any_sync(0xffffffffu, !(sum <= kSumBound));
-          }
-          if (slow) {
-            if (!rescale(raw_max128(x) * sl, j)) {
-              ok = false;
-              break;
+                for (int i = 0; i < 32; ++i) y[i] = c * 32 + i < end ? y[i] : 0xff800000u;  // -inf
+                mx = fmaxf(mx, raw_max32(y));
+              }
+              rescale(mx * sl, j);
             }
-            sum = exp_block<BN>(x, pk, sl, m_ref);
-          }
-          l += sum;
-          if (g >= 1) {
-            if (!warp_wait(smem_u32(&bars->pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, abort)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-          }
 #pragma unroll
-          for (int c = 0; c < BN / 64; ++c) tmem_st32(pcol + c * 32, pk + c * 32);
-          p_zero = false;
+            for (int c = 0; c < BN / 32; ++c) tmem_ld32(scol + c * 32, x + c * 32);
+            tmem_ld_wait128(x);
+            if (border) {
+#pragma unroll
+              for (int c = 0; c < BN; ++c) x[c] = c < end ? x[c] : 0xff800000u;  // -inf
+            }
+            uint64_t acc[4] = {0, 0, 0, 0};
+            weigh<BN>(x, pk, sl, m_ref == -INFINITY ? 0.f : m_ref, acc);
+            sum = total_of(acc);
+            if (slow) break;
+            slow = __any_sync(0xffffffffu, there && !(sum <= kSumBound));
+            if (!slow) break;
+          }
+          tmem_st32(scol, pk);
+          tmem_st32(scol + 32, pk + 32);
         }
+        l += sum;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(smem_u32(&bars->p_full[sb]));
+        warp_arrive(&bars->p_full[half], lane);
       }
       if (!ok) break;
-      const bool there = lp < w.npos && h_off < p.G;
-      const int token = w.token + lp, head = w.hk * p.G + h_off;
-      const int j0 = w.j0, j1 = w.j1, nb = w.nb;
       const bool cut = w.cut();
-      if (cut && j0 == 0 && tid == 128)  // the tile's first block is here: the join begins at this CTA
-        work_of(p.work, D).opened[blockIdx.x] = {w.token, w.hk, w.npos, sh.owner_of(w.next_at - 1) - (int)blockIdx.x + 1};
-      opened |= cut && j0 == 0;
-      const int64_t out = (int64_t)token * p.Hq + head;  // the row of o and lse
-      const int b = w.b, hk = w.hk, t0 = w.t0;
-      // The next tile's Q goes into TMEM now that every S product that used this one has
-      // completed, so that its first products run during this tile's epilogue.
-      more = advance(false);
-      if (more && !copy_q(k + 1, w)) {
+      if (cut && w.j0 == 0 && tid == 128)  // the tile's first block is here: the join begins at this CTA
+        work_of(p.work, D).opened[blockIdx.x] = {w.token, w.hk, w.npos,
+                                                 sh.owner_of(w.next_at - 1) - (int)blockIdx.x + 1};
+      opened |= cut && w.j0 == 0;
+      if (!warp_wait(smem_u32(&bars->o_done[half]), oph, abort)) {
         ok = false;
         break;
       }
-      if (!warp_wait(smem_u32(&bars->pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, abort)) {
-        ok = false;
-        break;
-      }
+      oph ^= 1;
       tc_fence_after();
-      float r[D];
+      const bool poisoned = *(volatile int*)&bars->poison[k & 7] == k + 1;
+      const int64_t out = (int64_t)(w.token + lp) * p.Hq + w.hk * p.G + h_off;  // the row of o and lse
+      const Work wk = work_of(p.work, D);
+      const int64_t part_row = (2 * (int64_t)blockIdx.x + (w.j0 > 0 ? 0 : 1)) * kRows + half * BM + row;
+      const float inv = 1.f / l;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[32];
+        __syncwarp();
+        tmem_ld32(ocol + c * 32, x);
+        tmem_ld_wait(x);
+        float r[32];
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c)
-        tmem_ld32(tmem_addr(tbase, lane_base, C::kColO + c * 32), reinterpret_cast<uint32_t*>(r) + c * 32);
-      tmem_ld_wait();
-      // (the next tile's first P V, which overwrites O, follows this warp's next p_full)
-      tc_fence_before();
-      if (*(volatile int*)&bars->poison[k & 7] == k + 1 && there) {
-        // infinities or NaN were taken out of V rows that not all queries see: this
-        // row's own are added, found again in global memory
-        Sched again(p.n_depth, nb, j0);
-        auto add = [&](int c0, uint4 y) {  // 8 elements of a row of V
-          const uint32_t e[4] = {y.x, y.y, y.z, y.w};
+        for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(x[i]);
+        if (poisoned && there) {
+          // infinities or NaN were taken out of V rows that not all queries see: this
+          // row's own are added, found again in global memory
+          auto add = [&](int i0, const uint4& y) {  // elements i0 .. i0 + 7 of the 32
+            const uint32_t q[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int cc = 0; cc < D; cc += 8)
-            if (cc == c0) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t f = not_finite(e[i]);
-                if (f & 0x8000u) r[cc + 2 * i] += __uint_as_float(e[i] << 16);
-                if (f & 0x80000000u) r[cc + 2 * i + 1] += __uint_as_float(e[i] & 0xffff0000u);
+            for (int i = 0; i < 32; i += 2)
+              if (i >> 3 == i0 >> 3) {
+                const uint32_t v = q[(i & 7) >> 1], f = not_finite(v);
+                if (f & 0x8000u) r[i] += __uint_as_float(v << 16);
+                if (f & 0x80000000u) r[i + 1] += __uint_as_float(v & 0xffff0000u);
               }
-            }
-        };
+          };
+          Sched again(p.n_depth, w.nb, w.j0);
 #pragma unroll 1
-        for (int j = j0; j < j1; ++j) {
-          again.next(p.n_depth, nb);
-          if (again.depth) {
-            const int l_end = min(p.L, (again.index + 1) * SP);
+          for (int j = w.j0; j < w.j1; ++j) {
+            again.next(p.n_depth, w.nb);
+            if (again.depth) {
+              const int l_end = min(p.L, (again.index + 1) * SP);
 #pragma unroll 1
-            for (int slot = again.index * SP; slot < l_end; ++slot) {
-              const uint4* v = reinterpret_cast<const uint4*>(p.vd + (int64_t)token * p.depth_tok +
-                                                              (int64_t)hk * p.depth_hk + (int64_t)slot * p.depth_slot);
+              for (int slot = again.index * SP; slot < l_end; ++slot) {
+                const uint4* v = reinterpret_cast<const uint4*>(p.vd + (int64_t)(w.token + lp) * p.depth_tok +
+                                                                (int64_t)w.hk * p.depth_hk +
+                                                                (int64_t)slot * p.depth_slot + c * 32);
 #pragma unroll 1
-              for (int c = 0; c < D / 8; ++c) add(c * 8, v[c]);
-            }
-          } else if (again.index * BN + BN - 1 > t0) {
-            const int k_end = min(t0 + lp + 1, (again.index + 1) * BN);
+                for (int i = 0; i < 4; ++i) add(i * 8, v[i]);
+              }
+            } else if (again.index * BN + BN - 1 > w.t0) {
+              const int k_end = min(w.t0 + lp + 1, (again.index + 1) * BN);
 #pragma unroll 1
-            for (int key = again.index * BN; key < k_end; ++key) {
-              int pg = p.table[(int64_t)b * p.max_pages + (key >> p.page_shift)];
-              if (pg < 0 || pg >= p.num_pages) pg = 0;
-              const int64_t vr = ((int64_t)(pg * p.Hk + hk) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
+              for (int key = again.index * BN; key < k_end; ++key) {
+                int pg = p.table[(int64_t)w.b * p.max_pages + (key >> p.page_shift)];
+                if (pg < 0 || pg >= p.num_pages) pg = 0;
+                const int64_t vr = ((int64_t)(pg * p.Hk + w.hk) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
 #pragma unroll 1
-              for (int c = 0; c < D / 8; ++c) {
-                uint4 y;
-                if constexpr (MX4) {
-                  uint32_t mul, mul2, z[4];
-                  factors(p.v_scale[vr * (D / 32) + (c >> 2)], mul, mul2);
-                  unpack8(*reinterpret_cast<const uint32_t*>(p.v + vr * (D / 2) + c * 4), mul, mul2, z);
-                  y = make_uint4(z[0], z[1], z[2], z[3]);
-                } else {
-                  y = *reinterpret_cast<const uint4*>(p.v + (vr * D + c * 8) * 2);
+                for (int i = 0; i < 4; ++i) {
+                  uint4 y;
+                  if constexpr (MX4) {
+                    uint32_t z[4];
+                    unpack8(*reinterpret_cast<const uint32_t*>(p.v + vr * (D / 2) + c * 16 + i * 4),
+                            scale_of(p.v_scale[vr * (D / 32) + c]), z);
+                    y = make_uint4(z[0], z[1], z[2], z[3]);
+                  } else {
+                    y = *reinterpret_cast<const uint4*>(p.v + (vr * D + c * 32 + i * 8) * 2);
+                  }
+                  add(i * 8, y);
                 }
-                add(c * 8, y);
               }
             }
           }
         }
-      }
-      if (cut) {
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (j0 > 0 ? 0 : 1);
-        const Work wk = work_of(p.work, D);
-        if (there) {
-          float4* po = reinterpret_cast<float4*>(wk.o + (slot * kRows + row) * D);
+        if (!there) continue;
+        if (cut) {
+          float4* po = reinterpret_cast<float4*>(wk.o + part_row * D + c * 32);
 #pragma unroll
-          for (int i = 0; i < D / 4; ++i) po[i] = make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-          *reinterpret_cast<float2*>(wk.ml + (slot * kRows + row) * 2) = make_float2(m_ref, l);
+          for (int i = 0; i < 8; ++i) po[i] = make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+        } else {
+          uint4* po = reinterpret_cast<uint4*>(p.o + out * D + c * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            po[i] = make_uint4(pack_bf16x2(r[8 * i] * inv, r[8 * i + 1] * inv),
+                               pack_bf16x2(r[8 * i + 2] * inv, r[8 * i + 3] * inv),
+                               pack_bf16x2(r[8 * i + 4] * inv, r[8 * i + 5] * inv),
+                               pack_bf16x2(r[8 * i + 6] * inv, r[8 * i + 7] * inv));
         }
-      } else if (there) {
-        const float inv = 1.f / l;
-        uint4* po = reinterpret_cast<uint4*>(p.o + out * D);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          po[i] = make_uint4(pack_bf16x2(r[8 * i] * inv, r[8 * i + 1] * inv),
-                             pack_bf16x2(r[8 * i + 2] * inv, r[8 * i + 3] * inv),
-                             pack_bf16x2(r[8 * i + 4] * inv, r[8 * i + 5] * inv),
-                             pack_bf16x2(r[8 * i + 6] * inv, r[8 * i + 7] * inv));
-        if (p.lse) p.lse[out] = (m_ref + log2f(l)) * kLn2;
       }
+      if (there && cut)
+        *reinterpret_cast<float2*>(wk.ml + part_row * 2) = make_float2(m_ref, l);
+      else if (there && p.lse)
+        p.lse[out] = (m_ref + log2f(l)) * kLn2;
+      // (the next tile's first P V, which overwrites O, follows this warp's next p_full)
+      tc_fence_before();
     }
     if (tid == 128 && !opened) work_of(p.work, D).opened[blockIdx.x] = {0, 0, 0, 0};
   } else {
     // ----------------------------- 4-bit pages unpacked, V blocks made harmless
-    const int hw = warp - 8, r = tid - 256;  // a row of the tile each
-    int g = 0;
-    uint32_t checks = 0;  // bf16: parities of v_check
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsTame));
+    const int hw = warp & 3, r = tid & 127;  // a row of a tile each
+    int e = 0;
+    int f = 0, fph = 0;  // raw entry and its phase
+    uint32_t checks_k = 0, checks_v = 0;  // parities of k_check, v_check
     bool ok = true;
     Walk w;
     w.begin(p, sh);
     for (int k = 0; ok && w.next(p, sh); ++k) {
+      const int halves = w.npos > P ? 2 : 1;
       Sched sch(p.n_depth, w.nb, w.j0);
-      for (int j = w.j0; j < w.j1; ++j, ++g) {
+      for (int j = w.j0; ok && j < w.j1; ++j) {
         sch.next(p.n_depth, w.nb);
         const bool part = partly_seen(w, sch);
-        if (!MX4 && !part) continue;
-        const int s = g % NS, f = g % NR;
-        uint8_t* vt = smem + C::kOffV + s * C::kTileBytes;
-        // rows that some query of the tile sees
-        auto counts = [&](int x) -> bool {
-          if (!sch.depth) return sch.index * BN + x <= w.t_last;
-          return (x >> 5) * PW + (x & (PW - 1)) < w.npos && sch.index * SP + (x & 31) / PW < p.L;
-        };
-        bool found = false;
-        if constexpr (MX4) {
-          const uint8_t* rk = smem + C::kOffRawK + f * C::kRawBytes;
-          const uint8_t* rv = smem + C::kOffRawV + f * C::kRawBytes;
-          if (!warp_wait(smem_u32(&bars->raw_k_full[f]), (g / NR) & 1, abort)) { ok = false; break; }
-          if (!sch.depth) {
-            if (!warp_wait(smem_u32(&bars->k_empty[s]), ((g / NS) & 1) ^ 1, abort)) { ok = false; break; }
-            unpack_tile<D, false>(rk, smem + C::kOffK + s * C::kTileBytes, hw, lane, counts);
+        for (int x = 0; x < (sch.depth ? halves : 1); ++x, ++e) {
+          if (!MX4 && !part) continue;
+          // rows that some query of the tile sees
+          auto counts = [&](int y) -> bool {
+            if (!sch.depth) return sch.index * BN + y <= w.t_last;
+            return x * P + (y >> 5) * PW + (y & (PW - 1)) < w.npos && sch.index * SP + (y & 31) / PW < p.L;
+          };
+          const int vs = e % NV;
+          uint8_t* vt = smem + C::kOffV + vs * C::kTileBytes;
+          bool found = false;
+          if constexpr (MX4) {
+            const int ks = e % NK;
+            // (each stage's phases one by one; a depth block's are seen by warp 3 too)
+            auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(smem_u32(bar), parity, abort); };
+            if (!(ok = wait(&bars->k_empty[ks], ((e / NK) & 1) ^ 1))) break;
+            if (sch.depth) {
+              if (!(ok = wait(&bars->k_check[ks], checks_k >> ks & 1))) break;
+              checks_k ^= 1u << ks;
+            } else {
+              uint8_t* kt = smem + C::kOffK + ks * C::kTileBytes;
+#pragma unroll 1
+              for (int y = 0; y < 2; ++y) {
+                const int at = f + y < NR ? f + y : f + y - NR;
+                if (!(ok = wait(&bars->raw_k_full[at], f + y < NR ? fph : fph ^ 1))) break;
+                unpack_rows<D, false>(smem + C::kOffRawK + at * C::kRawBytes, kt, y * 64, hw, lane, counts);
+                warp_arrive(&bars->raw_k_empty[at], lane);
+              }
+              if (!ok) break;
+            }
+            fence_async();
+            warp_arrive(&bars->k_full[ks], lane);
+            if (!(ok = wait(&bars->v_empty[vs], ((e / NV) & 1) ^ 1))) break;
+            if (sch.depth) {
+              if (!(ok = wait(&bars->v_check[vs], checks_v >> vs & 1))) break;
+              checks_v ^= 1u << vs;
+              found = tame_row<D>(vt, r, counts(r));
+            } else {
+#pragma unroll 1
+              for (int y = 0; y < 2; ++y) {
+                if (!(ok = wait(&bars->raw_v_full[f], fph))) break;
+                const uint8_t* raw = smem + C::kOffRawV + f * C::kRawBytes;
+                if (part)
+                  found |= unpack_rows<D, true>(raw, vt, y * 64, hw, lane, counts);
+                else
+                  unpack_rows<D, false>(raw, vt, y * 64, hw, lane, counts);
+                warp_arrive(&bars->raw_v_empty[f], lane);
+                if (++f == NR) {
+                  f = 0;
+                  fph ^= 1;
+                }
+              }
+              if (!ok) break;
+            }
+          } else {
+            if (!(ok = warp_wait(smem_u32(&bars->v_check[vs]), checks_v >> vs & 1, abort))) break;
+            checks_v ^= 1u << vs;
+            found = tame_row<D>(vt, r, counts(r));
+          }
+          if (found) {
+            *(volatile int*)&bars->poison[k & 7] = k + 1;
+            __threadfence_block();
           }
           fence_async();
-          mbar_arrive(smem_u32(&bars->k_full[s]));
-          mbar_arrive(smem_u32(&bars->raw_k_empty[f]));
-          if (!warp_wait(smem_u32(&bars->raw_v_full[f]), (g / NR) & 1, abort)) { ok = false; break; }
-          if (sch.depth) {
-            found = tame_row<D>(vt, r, counts(r));
-          } else {
-            if (!warp_wait(smem_u32(&bars->v_empty[s]), ((g / NS) & 1) ^ 1, abort)) { ok = false; break; }
-            if (part)
-              found = unpack_tile<D, true>(rv, vt, hw, lane, counts);
-            else
-              unpack_tile<D, false>(rv, vt, hw, lane, counts);
-          }
-        } else {
-          if (!warp_wait(smem_u32(&bars->v_check[s]), (checks >> s) & 1, abort)) { ok = false; break; }
-          checks ^= 1u << s;
-          found = tame_row<D>(vt, r, counts(r));
+          warp_arrive(MX4 ? &bars->v_full[vs] : &bars->v_ready[vs], lane);
         }
-        if (found) {
-          *(volatile int*)&bars->poison[k & 7] = k + 1;
-          __threadfence_block();
-        }
-        fence_async();
-        mbar_arrive(smem_u32(MX4 ? &bars->v_full[s] : &bars->v_ready[s]));
-        if (MX4) mbar_arrive(smem_u32(&bars->raw_v_empty[f]));
       }
     }
   }
@@ -934,7 +1038,7 @@ cudaError_t launch(const PrefillPagedArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(prefill_paged_kernel<D, MX4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  e = paged::launch_dependent(prefill_paged_kernel<D, MX4>, dim3(grid), kThreads, C::kSmemBytes, stream, tq, tk, tv,
+  e = paged::launch_dependent(prefill_paged_kernel<D, MX4>, dim3(grid), C::kThreads, C::kSmemBytes, stream, tq, tk, tv,
                               tkd, tvd, p);
   if (e != cudaSuccess) return e;
   return paged::launch_dependent(prefill_join_kernel<D>, dim3(grid, kJoinParts), kJoinWarps * 32, 0, stream, p);

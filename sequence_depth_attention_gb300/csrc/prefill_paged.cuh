@@ -1,7 +1,8 @@
 // The division of a chunked prefill's work over the CTAs, see prefill_paged.cu.
 //
-// A tile is P positions of one sequence (P a power of two) and one KV head, and
-// has as many blocks of 128 keys as its last position sees, and its depth blocks.
+// A tile is 2 P positions of one sequence (P a power of two) and one KV head, two halves
+// of 128 rows that share its keys, and has as many blocks of 128 keys as its last
+// position sees, and its depth blocks.
 // All tiles lie in one line, by sequence, KV head and position, each with
 // kTileCost points in front of its blocks (what entering and leaving a tile
 // costs), and CTA i of n takes the i-th n-th of the line, whatever tiles it
@@ -18,7 +19,7 @@ namespace moda {
 namespace prefill {
 
 constexpr int kMaxCtas = 160;  // one per SM of 152; sizes the workspace
-constexpr int kRows = 128;     // rows of a tile: positions times heads
+constexpr int kRows = 256;     // rows of a tile: positions times heads
 constexpr int kTileCost = 3;   // points in front of a tile's blocks
 
 // The workspace: for each CTA the cut tile whose first block is its own (parts 0:
@@ -74,8 +75,8 @@ __device__ __forceinline__ bool read_seq(const Params& p, int b, Seq& s) {
 struct SeqLine {
   int nt, q, u, base, lgP, lgR, last;
   __device__ __forceinline__ SeqLine(const Params& p, const Seq& s) {
-    lgR = p.lgG;  // tiles of 128 rows: 128 / P = 2^lgG
-    lgP = 7 - lgR;
+    lgP = 8 - p.lgG;     // positions of a tile
+    lgR = p.lgG - 1;     // tiles of 128 positions, 2^lgR; -1: a tile has 256
     nt = (s.n + (1 << lgP) - 1) >> lgP;
     const int first_end = s.len - s.n + (1 << lgP) - 1;  // last position of tile 0, were it whole
     q = first_end >> 7;
@@ -86,6 +87,7 @@ struct SeqLine {
   // points of the first m tiles, m < nt: tile i's last position is first_end + i P,
   // and the sum of floor((u + i) / R) over i below m, u below R, is one over y below u + m
   __device__ __forceinline__ long long before(int m) const {
+    if (lgR < 0) return (long long)m * (base + q) + (long long)m * (m - 1);
     const int x = u + m, a = x >> lgR, r = x & ((1 << lgR) - 1);
     return (long long)m * (base + q) + (((long long)a * (a - 1)) >> 1 << lgR) + (long long)a * r;
   }
@@ -103,16 +105,16 @@ struct Share {
     return point < wide ? (int)paged::divide(point, base + 1) : rem + (int)paged::divide(point - wide, base);
   }
 };
-template <int WARPS>
 struct ShareSmem {
-  unsigned long long warp_sum[WARPS];
+  unsigned long long warp_sum[20];
   long long tile_at;
   int b, hk, tile;
 };
 
 // All threads of the CTA call it. LEAST: points that are worth a CTA.
 template <int WARPS, int LEAST>
-__device__ __forceinline__ Share share_of(const Params& p, ShareSmem<WARPS>& sm) {
+__device__ __forceinline__ Share share_of(const Params& p, ShareSmem& sm) {
+  static_assert(WARPS <= 20);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (p.B + WARPS * 32 - 1) / (WARPS * 32);
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
@@ -204,7 +206,7 @@ struct Walk {
     read_seq(p, b, seq);
   }
   __device__ __forceinline__ bool next(const Params& p, const Share& s) {
-    const int lgP = 7 - p.lgG, P = 1 << lgP;
+    const int lgP = 8 - p.lgG, P = 1 << lgP;
     while (true) {
       if (next_at >= s.to) return false;
       at = next_at;
