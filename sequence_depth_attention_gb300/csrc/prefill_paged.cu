@@ -14,21 +14,21 @@
 //   * Depth slots are gathered by TMA, a block of each half's own positions, under a
 //     block-diagonal mask (a softmax warp has a 32-row word of it), and spread evenly
 //     among the sequence blocks.
-//   * 4-bit pages come as codes and scales, and warps unpack them into the bf16 tiles
-//     that the tensor core reads (exactly: a code times a power of two), once for both
-//     halves.
+//   * 4-bit pages are unpacked into the bf16 tiles that the tensor core reads (exactly: a
+//     code times a power of two), once for both halves.
 //   * A row that a query must not see has no influence whatever it holds. Its weight is
 //     0, but 0 times an infinity or a NaN in V is NaN: in the blocks that some row of a
 //     tile sees in part (the causal border, the depth blocks), rows that no query of the
 //     tile sees become 0, and an infinity or NaN among the others becomes 0 too and is
 //     added at the end to the rows that do see it.
 //
-// Roles (16 warps):
+// Roles (16 warps; 20 for 4-bit pages):
 //   warp 0        TMA producer of Q and K     warp 1  issuer of all MMAs, TMEM
-//   warp 2        TMA producer of V           warp 3  4-bit pages: depth blocks' producer
+//   warp 2        TMA producer of V           warp 3  4-bit pages: of the depth blocks
 //   warps 4-7     softmax and epilogue of the first half, one thread per row (TMEM lane)
 //   warps 8-11    of the second half
-//   warps 12-15   partly seen V blocks made harmless, 4-bit pages unpacked
+//   warps 12-15   partly seen V blocks made harmless
+//         (12-19) and 4-bit pages unpacked, by way of registers
 // TMEM (512 columns): S of the halves [0,128) [128,256), each half's P (bf16 pairs) in the
 // first 64 columns of its S, O of the halves at 256 and 256 + d.
 // P is rounded to bf16 once, as in the forward: the sum l keeps fp32 weights, and
@@ -53,38 +53,31 @@ using paged::kLog2e;
 constexpr int BM = 128, BN = 128;  // rows of a half tile, keys of a block
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr float kSumBound = 256.0f;  // of a row's weights in a block, see the softmax warps
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kLeast = 2;                  // points that are worth a CTA
 
 template <int D, bool MX4>
 struct Cfg {
-  static constexpr int kWarps = 16, kThreads = kWarps * 32;
-  // Registers of the four groups of four warps; they add up to what the block is launched
-  // with (512 threads x 128).
-  static constexpr int kRegsIssue = 72, kRegsSoftmax = 192, kRegsTame = 56;
-  static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsTame <= 4 * 128);
+  static constexpr int kTameWarps = MX4 ? 8 : 4;
+  static constexpr int kWarps = 12 + kTameWarps, kThreads = kWarps * 32;
+  // Registers of a thread of each group of four warps; they add up to what the block is
+  // launched with (at 128 and, 4-bit pages, 96 a thread).
+  static constexpr int kRegsIssue = 64, kRegsSoftmax = MX4 ? 120 : 184, kRegsTame = MX4 ? 88 : 80;
+  static_assert(kRegsIssue + 2 * kRegsSoftmax + kTameWarps / 4 * kRegsTame <= kWarps / 4 * (MX4 ? 96 : 128));
   static constexpr int kBoxes = D / 64;  // 64-column (128-byte) swizzle boxes per row
   static constexpr int kBoxBytes = BN * 128;
   static constexpr int kQBytes = BM * D * 2;  // of a half
   static constexpr int kTileBytes = BN * D * 2;
-  static constexpr int kNK = D == 128 ? 2 : 4;                     // stages of K
-  static constexpr int kNV = D == 128 ? (MX4 ? 2 : 3) : (MX4 ? 4 : 5);  // of V
-  // 4-bit rows on their way, half a block of them: codes, then scales
-  static constexpr int kRawRows = 64;
-  static constexpr int kRawCodes = kRawRows * D / 2, kRawScales = kRawRows * D / 32;
-  static constexpr int kRawBytes = kRawCodes + kRawScales;
-  static constexpr int kNR = MX4 ? (D == 128 ? 3 : 4) : 0;
+  static constexpr int kNK = D == 128 ? 2 : 4, kNV = D == 128 ? 3 : 5;  // stages of K and of V
   static constexpr int kOffK = 2 * kQBytes;
   static constexpr int kOffV = kOffK + kNK * kTileBytes;
-  static constexpr int kOffRawK = kOffV + kNV * kTileBytes;
-  static constexpr int kOffRawV = kOffRawK + kNR * kRawBytes;
-  static constexpr int kOffBar = kOffRawV + kNR * kRawBytes;
+  static constexpr int kOffBar = kOffV + kNV * kTileBytes;
   static constexpr int kSmemBytes = kOffBar + 2048 + 1024;  // barriers, alignment
   static constexpr uint32_t kColS = 0, kColO = 256;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
-  static_assert(kOffBar % 16 == 0 && kRawBytes % 16 == 0);
 };
 
-constexpr int kMaxStages = 5, kMaxRaw = 4;
+constexpr int kMaxStages = 5;
 
 struct alignas(16) Barriers {
   uint64_t q_full, q_free;  // Q of the current tile landed / its last S = Q K^T completed
@@ -94,7 +87,6 @@ struct alignas(16) Barriers {
   // do it wait for one by one: they skip the other blocks.) 4-bit pages: a depth block
   // lands at k_check and v_check, and is full once the unpacking warps have seen it.
   uint64_t k_check[kMaxStages], v_check[kMaxStages], v_ready[kMaxStages];
-  uint64_t raw_k_full[kMaxRaw], raw_k_empty[kMaxRaw], raw_v_full[kMaxRaw], raw_v_empty[kMaxRaw];
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t mma_done;
   uint32_t tmem_base;
@@ -102,7 +94,7 @@ struct alignas(16) Barriers {
   int poison[8];  // [k % 8] = k + 1: tile k had infinities or NaN taken out (fewer tiles are under way)
   ShareSmem find;
   Share share;
-  Walk walk[8];  // of the softmax warps, whose registers are full
+  Walk walk[16];  // of warps 4 on, whose registers are full
 };
 static_assert(sizeof(Barriers) <= 2048, "barrier block");
 
@@ -116,12 +108,6 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   if (lane == 0) mbar_arrive(smem_u32(bar));
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
 
 // Waits for tcgen05.ld and ties the 32 registers to it: nothing that reads them moves up.
 __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
@@ -137,6 +123,20 @@ __device__ __forceinline__ void tmem_ld_wait128(uint32_t (&r)[128]) {
 }
 #undef MODA_RW8
 
+// A warp's walk in shared memory on to its next tile; the warp has read what it wants of
+// the one before.
+__device__ __forceinline__ bool warp_next(Walk& w, const Params& p, const Share& sh, int lane, bool first) {
+  bool any = false;
+  __syncwarp();
+  if (lane == 0) {
+    if (first) w.begin(p, sh);
+    any = w.next(p, sh);
+  }
+  any = __shfl_sync(0xffffffffu, any, 0);
+  __syncwarp();  // what lane 0 has written is seen
+  return any;
+}
+
 // Is block (depth, index) of the walk's tile one that some row sees in part?
 __device__ __forceinline__ bool partly_seen(const Walk& w, const Sched& sch) {
   return sch.depth || sch.index * BN + BN - 1 > w.t0;
@@ -148,7 +148,7 @@ template <int D>
 __device__ __forceinline__ bool tame_row(uint8_t* tile, int r, bool counts) {
   constexpr int kBoxBytes = BN * 128;
   uint32_t bad = 0;
-#pragma unroll
+#pragma unroll 1
   for (int c = 0; c < D / 64; ++c)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -171,51 +171,60 @@ __device__ __forceinline__ bool tame_row(uint8_t* tile, int r, bool counts) {
   return true;
 }
 
-// Half a block of 4-bit rows (codes, then scales) into rows row0 .. of a bf16 tile, by
-// four warps: D / 32 lanes a row, a block of 32 elements a lane. TAME: as tame_row, with
-// counts(r) for the rows.
-template <int D, bool TAME, class Counts>
-__device__ __forceinline__ bool unpack_rows(const uint8_t* raw, uint8_t* tile, int row0, int warp, int lane,
-                                            Counts counts) {
-  constexpr int BPR = D / 32;    // blocks, and lanes, of a row
-  constexpr int RPI = 32 / BPR;  // rows a warp takes at once
-  constexpr int kBoxBytes = BN * 128, kRows64 = 64;
-  const int qtr = lane % BPR;
-  bool found = false;
-#pragma unroll
-  for (int it = 0; it < kRows64 / (4 * RPI); ++it) {
-    const int rr = (it * 4 + warp) * RPI + lane / BPR, r = row0 + rr;
-    const uint4 codes = *reinterpret_cast<const uint4*>(raw + rr * (D / 2) + qtr * 16);
-    const uint32_t b = raw[kRows64 * D / 2 + rr * BPR + qtr];
-    const uint32_t scale = scale_of(b);
-    // the block's four 16-byte chunks 4 (qtr & 1) + j of the 64-column box; lanes of the
+// A lane's 4-bit blocks of a tile, from global memory by way of registers to bf16: D / 32
+// lanes a row, a block of 32 elements a lane, four warps. The next tile's are on their way
+// while this one's are unpacked. One loop for K and V and all turns: beside the softmax's
+// code, unrolled ones waited for their instructions (1.7 of 5 warps, FIXME).
+template <int D>
+struct Codes {
+  static constexpr int BPR = D / 32;        // blocks, and lanes, of a row
+  static constexpr int RPT = 4 * 32 / BPR;  // rows the warps take at once
+  static constexpr int kTurns = BN / RPT;
+  uint4 codes[kTurns];
+  uint32_t scale[kTurns];  // bytes
+  static __device__ __forceinline__ int row(int turn, int hw, int lane) {
+    return turn * RPT + hw * (32 / BPR) + lane / BPR;
+  }
+  // Into a bf16 tile; `tame`: with zeros for infinities and NaN. True if there were any.
+  __device__ __forceinline__ bool unpack(uint8_t* tile, int hw, int lane, bool tame) {
+    const int qtr = lane % BPR;
+    // A block is four 16-byte chunks of a 64-column box from 4 (qtr & 1) on; lanes of the
     // upper box take them in another order, so that eight lanes (two rows) meet different
-    // banks
+    // banks.
     const bool upper = qtr >> 1;
-    uint8_t* row = tile + (upper ? kBoxBytes : 0) + r * 128;
-    const uint32_t cw[4] = {upper ? codes.z : codes.x, upper ? codes.w : codes.y, upper ? codes.x : codes.z,
-                            upper ? codes.y : codes.w};
+    uint32_t found = 0;
+#pragma unroll 1
+    for (int t = 0; t < kTurns; ++t) {
+      const int r = row(t, hw, lane);
+      uint8_t* to = tile + (upper ? BN * 128 : 0) + r * 128;
+      const uint32_t cw[4] = {upper ? codes[0].z : codes[0].x, upper ? codes[0].w : codes[0].y,
+                              upper ? codes[0].x : codes[0].z, upper ? codes[0].y : codes[0].w};
+      const uint32_t s = scale_of(scale[0]);
+      uint32_t y[4][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t y[4];
-      unpack8(cw[j], scale, y);
-      if constexpr (TAME) {
-        const bool c = counts(r);
-        if (!c || b >= 253u) {
+      for (int j = 0; j < 4; ++j) unpack8(cw[j], s, y[j]);
+      if (tame && scale[0] >= 253u) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t f = not_finite(y[i]);
-            found |= c && f;
-            y[i] &= c ? ~(((f & 0x8000u) ? 0xffffu : 0u) | ((f & 0x80000000u) ? 0xffff0000u : 0u)) : 0u;
-          }
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t f = not_finite(y[i >> 2][i & 3]);
+          found |= f;
+          y[i >> 2][i & 3] &= ~(((f & 0x8000u) ? 0xffffu : 0u) | ((f & 0x80000000u) ? 0xffff0000u : 0u));
         }
       }
-      const int chunk = 4 * (qtr & 1) + (upper ? j ^ 2 : j);
-      *reinterpret_cast<uint4*>(row + ((chunk ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int chunk = 4 * (qtr & 1) + (upper ? j ^ 2 : j);
+        *reinterpret_cast<uint4*>(to + ((chunk ^ (r & 7)) << 4)) = make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]);
+      }
+#pragma unroll
+      for (int i = 0; i + 1 < kTurns; ++i) {
+        codes[i] = codes[i + 1];
+        scale[i] = scale[i + 1];
+      }
     }
+    return found != 0;
   }
-  return found;
-}
+};
 
 // p = 2^(s sl - m) of N scores as bf16 pairs, added up in acc.
 template <int N>
@@ -242,7 +251,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKd,
                      const __grid_constant__ CUtensorMap tmVd, const __grid_constant__ Params p) {
   using C = Cfg<D, MX4>;
-  constexpr int NK = C::kNK, NV = C::kNV, NR = MX4 ? C::kNR : 1;
+  constexpr int NK = C::kNK, NV = C::kNV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -267,12 +276,6 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       mbar_init(smem_u32(&bars->k_check[s]), 1);
       mbar_init(smem_u32(&bars->v_check[s]), 1);
       mbar_init(smem_u32(&bars->v_ready[s]), 4);
-    }
-    for (int s = 0; s < kMaxRaw; ++s) {
-      mbar_init(smem_u32(&bars->raw_k_full[s]), 1);
-      mbar_init(smem_u32(&bars->raw_k_empty[s]), 4);
-      mbar_init(smem_u32(&bars->raw_v_full[s]), 1);
-      mbar_init(smem_u32(&bars->raw_v_empty[s]), 4);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(smem_u32(&bars->s_full[x]), 1);
@@ -311,19 +314,17 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsIssue));
     if (warp == 0 || warp == 2) {
-      // ---------------------------------------------------- TMA producers
+      // ------------------- TMA producers (4-bit pages: of Q alone)
       const bool is_k = warp == 0;
       const bool leader = elect_one();
       const uint64_t pol_once = l2_policy_evict_first();
       const int ns = is_k ? NK : NV;  // stages
-      uint64_t* full = MX4 ? (is_k ? bars->raw_k_full : bars->raw_v_full) : (is_k ? bars->k_full : bars->v_full);
-      uint64_t* empty = MX4 ? (is_k ? bars->raw_k_empty : bars->raw_v_empty) : (is_k ? bars->k_empty : bars->v_empty);
+      uint64_t* full = is_k ? bars->k_full : bars->v_full;
+      uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
       const int page_rows = 1 << p.page_shift;  // at most 128
-      // a lane copies one page's rows (bf16: 64 columns of them; 4-bit: at most 64 rows)
-      constexpr int kParts = MX4 ? 1 : C::kBoxes;
-      const int my_box = lane / kParts, my_part = lane % kParts;
-      const int box_rows = MX4 ? min(page_rows, C::kRawRows) : page_rows;
-      int e = 0, f = 0, fph = 0, nq = 0;  // entries; the next one's stage (raw entry) and phase; Q loads
+      // a lane copies 64 columns of one page's rows
+      const int my_box = lane / C::kBoxes, my_part = lane % C::kBoxes;
+      int e = 0, f = 0, fph = 0, nq = 0;  // entries; the next one's stage and phase; Q loads
       uint32_t checks = 0, wholes = 0;  // of V's stages: parities of what went to v_check, to v_full
       uint32_t any_check = 0, any_whole = 0;
       Walk w;
@@ -344,27 +345,26 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           }
           ++nq;
         }
-        Sched sch(p.n_depth, w.nb, w.j0);
-        const int* table = p.table + (int64_t)w.b * p.max_pages;
-        // the lane's page of a sequence block, looked up one block ahead
-        auto page_of = [&](int index) -> int {
-          const int key = index * BN + my_box * box_rows;
-          return my_box * box_rows < BN && key <= w.t_last ? table[key >> p.page_shift] : -1;
-        };
-        int page = page_of(sch.sbk);
-        for (int j = w.j0; ok && j < w.j1; ++j) {
-          sch.next(p.n_depth, w.nb);
-          int pg = page;
-          if (!sch.depth) page = page_of(sch.index + 1);
-          // a depth block of each half, or a sequence block for both
-          const int entries = sch.depth ? (MX4 ? 0 : halves) : (MX4 ? 2 : 1);
-          for (int x = 0; x < entries; ++x) {
-            if (!warp_wait(smem_u32(&empty[f]), fph ^ 1, abort)) {
-              ok = false;
-              break;
-            }
-            uint32_t fb = smem_u32(&full[f]);
-            if constexpr (!MX4) {
+        if constexpr (!MX4) {
+          Sched sch(p.n_depth, w.nb, w.j0);
+          const int* table = p.table + (int64_t)w.b * p.max_pages;
+          // the lane's page of a sequence block, looked up one block ahead
+          auto page_of = [&](int index) -> int {
+            const int key = index * BN + (my_box << p.page_shift);
+            return my_box << p.page_shift < BN && key <= w.t_last ? table[key >> p.page_shift] : -1;
+          };
+          int page = page_of(sch.sbk);
+          for (int j = w.j0; ok && j < w.j1; ++j) {
+            sch.next(p.n_depth, w.nb);
+            int pg = page;
+            if (!sch.depth) page = page_of(sch.index + 1);
+            // a depth block of each half, or a sequence block for both
+            for (int x = 0; x < (sch.depth ? halves : 1); ++x) {
+              if (!warp_wait(smem_u32(&empty[f]), fph ^ 1, abort)) {
+                ok = false;
+                break;
+              }
+              uint32_t fb = smem_u32(&full[f]);
               if (!is_k) {
                 if (partly_seen(w, sch)) {
                   fb = smem_u32(&bars->v_check[f]);
@@ -401,40 +401,22 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                               my_part * 64, 0, pg * p.Hk + w.hk);
                 }
               }
-            } else {
-              // half of the block's rows; lane y has page rows [y box_rows, ..) of the block
-              const int rows = min(C::kRawRows, w.t_last + 1 - sch.index * BN - x * C::kRawRows);
-              const int boxes = rows > 0 ? (rows + box_rows - 1) / box_rows : 0;
-              if (leader) mbar_arrive_expect_tx(fb, boxes * box_rows * (D / 2 + D / 32));
               __syncwarp();
-              const int mine = my_box - x * (C::kRawRows / box_rows);
-              if (mine >= 0 && mine < boxes) {
-                if (pg < 0 || pg >= p.num_pages) {
-                  atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
-                  pg = 0;
-                }
-                const uint32_t dst = smem_u32(smem + (is_k ? C::kOffRawK : C::kOffRawV)) + f * C::kRawBytes;
-                const int64_t row = ((int64_t)(pg * p.Hk + w.hk) << p.page_shift) +
-                                    (my_box * box_rows & (page_rows - 1));
-                bulk_load(dst + mine * box_rows * (D / 2), (is_k ? p.k : p.v) + row * (D / 2), box_rows * (D / 2),
-                          fb);
-                bulk_load(dst + C::kRawCodes + mine * box_rows * (D / 32),
-                          (is_k ? p.k_scale : p.v_scale) + row * (D / 32), box_rows * (D / 32), fb);
+              ++e;
+              if (++f == ns) {
+                f = 0;
+                fph ^= 1;
               }
             }
-            __syncwarp();
-            ++e;
-            if (++f == (MX4 ? NR : ns)) {
-              f = 0;
-              fph ^= 1;
-            }
           }
+        } else if (!is_k) {
+          break;
         }
       }
       // every copy of this warp has landed before its shared memory is released
       if (leader) {
         int never = 0;
-        if (!MX4 && !is_k) {
+        if (!is_k) {
           for (int s = 0; s < NV; ++s) {
             if (any_whole >> s & 1)
               mbar_wait_bounded(smem_u32(&bars->v_full[s]), (wholes >> s & 1) ^ 1, &never, kTimeoutNs);
@@ -442,9 +424,8 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
               mbar_wait_bounded(smem_u32(&bars->v_check[s]), (checks >> s & 1) ^ 1, &never, kTimeoutNs);
           }
         } else {
-          const int n = MX4 ? NR : ns;
-          for (int j = max(0, e - n); j < e; ++j)
-            mbar_wait_bounded(smem_u32(&full[j % n]), (j / n) & 1, &never, kTimeoutNs);
+          for (int j = max(0, e - ns); j < e; ++j)
+            mbar_wait_bounded(smem_u32(&full[j % ns]), (j / ns) & 1, &never, kTimeoutNs);
         }
         if (is_k && nq > 0) mbar_wait_bounded(smem_u32(&bars->q_full), (nq - 1) & 1, &never, kTimeoutNs);
       }
@@ -617,18 +598,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     const float sl = p.scale_log2;
     uint32_t sph = 0, oph = 0;  // parities of s_full, o_done
     Walk& w = bars->walk[warp - 4];
-    // to the next tile; the warp has read what it wants of the one before
-    auto advance = [&](bool first) -> bool {
-      bool any = false;
-      __syncwarp();
-      if (lane == 0) {
-        if (first) w.begin(p, sh);
-        any = w.next(p, sh);
-      }
-      any = __shfl_sync(0xffffffffu, any, 0);
-      __syncwarp();  // what lane 0 has written is seen
-      return any;
-    };
+    auto advance = [&](bool first) -> bool { return warp_next(w, p, sh, lane, first); };
     bool opened = false, ok = true, more = advance(true);
     for (int k = 0; ok && more; ++k, more = advance(false)) {
       if (half && w.npos <= P) continue;
@@ -704,37 +674,69 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           // columns that the row sees: all, but at the causal border
           const bool border = sch.index >= border0;
           const int end = border ? min(w.t0 + lp, w.t_last) - sch.index * BN + 1 : BN;
-          uint32_t x[BN], pk[BN / 2];
-          for (int pass = 0; pass < 2; ++pass) {
-            if (slow) {
-              float mx = -INFINITY;
-#pragma unroll 1
-              for (int c = 0; c < BN / 32; ++c) {
-                uint32_t y[32];
-                tmem_ld32(scol + c * 32, y);
-                tmem_ld_wait(y);
+          if constexpr (MX4) {
+            // The maximum first, then the weights, 32 scores at a time, in place: loops of
+            // few instructions and registers, which the unpacking warps want too.
+            float mx = -INFINITY;
+            auto load = [&](int c, uint32_t (&x)[32]) {
+              tmem_ld32(scol + c * 32, x);
+              tmem_ld_wait(x);
+              if (border) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) y[i] = c * 32 + i < end ? y[i] : 0xff800000u;  // -inf
-                mx = fmaxf(mx, raw_max32(y));
+                for (int i = 0; i < 32; ++i) x[i] = c * 32 + i < end ? x[i] : 0xff800000u;  // -inf
               }
-              rescale(mx * sl, j);
+            };
+#pragma unroll 1
+            for (int c = 0; c < BN / 32; ++c) {
+              uint32_t x[32];
+              load(c, x);
+              mx = fmaxf(mx, raw_max32(x));
             }
-#pragma unroll
-            for (int c = 0; c < BN / 32; ++c) tmem_ld32(scol + c * 32, x + c * 32);
-            tmem_ld_wait128(x);
-            if (border) {
-#pragma unroll
-              for (int c = 0; c < BN; ++c) x[c] = c < end ? x[c] : 0xff800000u;  // -inf
-            }
+            if (__any_sync(0xffffffffu, there && mx * sl > m_ref + kRescaleThreshold)) rescale(mx * sl, j);
+            const float m = m_ref == -INFINITY ? 0.f : m_ref;
             uint64_t acc[4] = {0, 0, 0, 0};
-            weigh<BN>(x, pk, sl, m_ref == -INFINITY ? 0.f : m_ref, acc);
+#pragma unroll 1
+            for (int c = 0; c < BN / 32; ++c) {
+              uint32_t x[32], pk[16];
+              load(c, x);
+              weigh<32>(x, pk, sl, m, acc);
+              tmem_st16(scol + c * 16, pk);
+            }
             sum = total_of(acc);
-            if (slow) break;
-            slow = __any_sync(0xffffffffu, there && !(sum <= kSumBound));
-            if (!slow) break;
+          } else {
+            uint32_t pk[BN / 2];
+            for (int pass = 0; pass < 2; ++pass) {
+              if (slow) {
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < BN / 32; ++c) {
+                  uint32_t y[32];
+                  tmem_ld32(scol + c * 32, y);
+                  tmem_ld_wait(y);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) y[i] = c * 32 + i < end ? y[i] : 0xff800000u;  // -inf
+                  mx = fmaxf(mx, raw_max32(y));
+                }
+                rescale(mx * sl, j);
+              }
+              uint64_t acc[4] = {0, 0, 0, 0};
+              uint32_t x[BN];
+#pragma unroll
+              for (int c = 0; c < BN / 32; ++c) tmem_ld32(scol + c * 32, x + c * 32);
+              tmem_ld_wait128(x);
+              if (border) {
+#pragma unroll
+                for (int c = 0; c < BN; ++c) x[c] = c < end ? x[c] : 0xff800000u;  // -inf
+              }
+              weigh<BN>(x, pk, sl, m_ref == -INFINITY ? 0.f : m_ref, acc);
+              sum = total_of(acc);
+              if (slow) break;
+              slow = __any_sync(0xffffffffu, there && !(sum <= kSumBound));
+              if (!slow) break;
+            }
+            tmem_st32(scol, pk);
+            tmem_st32(scol + 32, pk + 32);
           }
-          tmem_st32(scol, pk);
-          tmem_st32(scol + 32, pk + 32);
         }
         l += sum;
         tmem_st_wait();
@@ -844,83 +846,88 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   } else {
     // ----------------------------- 4-bit pages unpacked, V blocks made harmless
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsTame));
+    const bool is_v = warp < 16;
     const int hw = warp & 3, r = tid & 127;  // a row of a tile each
-    int e = 0;
-    int f = 0, fph = 0;  // raw entry and its phase
-    uint32_t checks_k = 0, checks_v = 0;  // parities of k_check, v_check
+    const int ns = is_v ? NV : NK;
+    uint64_t* full = is_v ? (MX4 ? bars->v_full : bars->v_ready) : bars->k_full;
+    uint64_t* check = is_v ? bars->v_check : bars->k_check;
+    int s = 0, ph = 0;    // the next entry's stage and phase
+    uint32_t checks = 0;  // parities of `check`
     bool ok = true;
-    Walk w;
-    w.begin(p, sh);
-    for (int k = 0; ok && w.next(p, sh); ++k) {
+    Walk& w = bars->walk[warp - 4];
+    for (int k = 0; ok && warp_next(w, p, sh, lane, k == 0); ++k) {
       const int halves = w.npos > P ? 2 : 1;
       Sched sch(p.n_depth, w.nb, w.j0);
+      using Cd = Codes<D>;
+      Cd c;                  // of the next sequence block
+      int page[Cd::kTurns];  // of the rows of the one after
+      // pages of the lane's rows of a sequence block, -1: none that a query sees
+      auto look_up = [&](int index) {
+#pragma unroll
+        for (int t = 0; t < Cd::kTurns; ++t) {
+          const int key = index * BN + Cd::row(t, hw, lane);
+          page[t] = key <= w.t_last ? p.table[(int64_t)w.b * p.max_pages + (key >> p.page_shift)] : -1;
+        }
+      };
+      // (rows that no query sees unpack to zeros)
+      auto fetch = [&](int index) {
+        const uint8_t *codes = is_v ? p.v : p.k, *scales = is_v ? p.v_scale : p.k_scale;
+#pragma unroll
+        for (int t = 0; t < Cd::kTurns; ++t) {
+          const int row = Cd::row(t, hw, lane);
+          c.codes[t] = make_uint4(0u, 0u, 0u, 0u);
+          c.scale[t] = 127;
+          if (index * BN + row <= w.t_last) {
+            int pg = page[t];
+            if (pg < 0 || pg >= p.num_pages) {
+              atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
+              pg = 0;
+            }
+            const int64_t at = ((int64_t)(pg * p.Hk + w.hk) << p.page_shift) + (row & ((1 << p.page_shift) - 1));
+            c.codes[t] = *reinterpret_cast<const uint4*>(codes + at * (D / 2) + lane % Cd::BPR * 16);
+            c.scale[t] = scales[at * Cd::BPR + lane % Cd::BPR];
+          }
+        }
+      };
+      if constexpr (MX4) {
+        look_up(sch.sbk);
+        fetch(sch.sbk);
+        look_up(sch.sbk + 1);
+      }
       for (int j = w.j0; ok && j < w.j1; ++j) {
         sch.next(p.n_depth, w.nb);
         const bool part = partly_seen(w, sch);
-        for (int x = 0; x < (sch.depth ? halves : 1); ++x, ++e) {
-          if (!MX4 && !part) continue;
-          // rows that some query of the tile sees
-          auto counts = [&](int y) -> bool {
-            if (!sch.depth) return sch.index * BN + y <= w.t_last;
-            return x * P + (y >> 5) * PW + (y & (PW - 1)) < w.npos && sch.index * SP + (y & 31) / PW < p.L;
-          };
-          const int vs = e % NV;
-          uint8_t* vt = smem + C::kOffV + vs * C::kTileBytes;
-          bool found = false;
-          if constexpr (MX4) {
-            const int ks = e % NK;
-            // (each stage's phases one by one; a depth block's are seen by warp 3 too)
-            auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return warp_wait(smem_u32(bar), parity, abort); };
-            if (!(ok = wait(&bars->k_empty[ks], ((e / NK) & 1) ^ 1))) break;
-            if (sch.depth) {
-              if (!(ok = wait(&bars->k_check[ks], checks_k >> ks & 1))) break;
-              checks_k ^= 1u << ks;
+        for (int x = 0; ok && x < (sch.depth ? halves : 1); ++x) {
+          uint8_t* tile = smem + (is_v ? C::kOffV : C::kOffK) + s * C::kTileBytes;
+          if (MX4 || part) {
+            // rows that some query of the tile sees
+            auto counts = [&](int y) -> bool {
+              if (!sch.depth) return sch.index * BN + y <= w.t_last;
+              return x * P + (y >> 5) * PW + (y & (PW - 1)) < w.npos && sch.index * SP + (y & 31) / PW < p.L;
+            };
+            bool found = false;
+            // (4-bit pages: each stage's phases one by one; a depth block's are seen by warp 3 too)
+            if (MX4 && !(ok = warp_wait(smem_u32(is_v ? &bars->v_empty[s] : &bars->k_empty[s]), ph ^ 1, abort))) break;
+            if (!MX4 || sch.depth) {
+              if (!(ok = warp_wait(smem_u32(&check[s]), checks >> s & 1, abort))) break;
+              checks ^= 1u << s;
+              if (is_v) found = tame_row<D>(tile, r, counts(r));
             } else {
-              uint8_t* kt = smem + C::kOffK + ks * C::kTileBytes;
-#pragma unroll 1
-              for (int y = 0; y < 2; ++y) {
-                const int at = f + y < NR ? f + y : f + y - NR;
-                if (!(ok = wait(&bars->raw_k_full[at], f + y < NR ? fph : fph ^ 1))) break;
-                unpack_rows<D, false>(smem + C::kOffRawK + at * C::kRawBytes, kt, y * 64, hw, lane, counts);
-                warp_arrive(&bars->raw_k_empty[at], lane);
-              }
-              if (!ok) break;
+              found = c.unpack(tile, hw, lane, is_v && part);
+              fetch(sch.index + 1);
+              look_up(sch.index + 2);
+            }
+            if (found) {
+              *(volatile int*)&bars->poison[k & 7] = k + 1;
+              __threadfence_block();
             }
             fence_async();
-            warp_arrive(&bars->k_full[ks], lane);
-            if (!(ok = wait(&bars->v_empty[vs], ((e / NV) & 1) ^ 1))) break;
-            if (sch.depth) {
-              if (!(ok = wait(&bars->v_check[vs], checks_v >> vs & 1))) break;
-              checks_v ^= 1u << vs;
-              found = tame_row<D>(vt, r, counts(r));
-            } else {
-#pragma unroll 1
-              for (int y = 0; y < 2; ++y) {
-                if (!(ok = wait(&bars->raw_v_full[f], fph))) break;
-                const uint8_t* raw = smem + C::kOffRawV + f * C::kRawBytes;
-                if (part)
-                  found |= unpack_rows<D, true>(raw, vt, y * 64, hw, lane, counts);
-                else
-                  unpack_rows<D, false>(raw, vt, y * 64, hw, lane, counts);
-                warp_arrive(&bars->raw_v_empty[f], lane);
-                if (++f == NR) {
-                  f = 0;
-                  fph ^= 1;
-                }
-              }
-              if (!ok) break;
-            }
-          } else {
-            if (!(ok = warp_wait(smem_u32(&bars->v_check[vs]), checks_v >> vs & 1, abort))) break;
-            checks_v ^= 1u << vs;
-            found = tame_row<D>(vt, r, counts(r));
+            warp_arrive(&full[s], lane);
           }
-          if (found) {
-            *(volatile int*)&bars->poison[k & 7] = k + 1;
-            __threadfence_block();
+          if (++s == ns) {
+            s = 0;
+            ph ^= 1;
           }
-          fence_async();
-          warp_arrive(MX4 ? &bars->v_full[vs] : &bars->v_ready[vs], lane);
         }
       }
     }
