@@ -53,7 +53,6 @@ using paged::kLog2e;
 constexpr int BM = 128, BN = 128;  // rows of a half tile, keys of a block
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr float kSumBound = 256.0f;  // of a row's weights in a block, see the softmax warps
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kLeast = 2;                  // points that are worth a CTA
 
 template <int D, bool MX4>
@@ -115,7 +114,7 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
                     "+r"(r[i + 6]), "+r"(r[i + 7])
   asm volatile("tcgen05.wait::ld.sync.aligned;" : MODA_RW8(0), MODA_RW8(8), MODA_RW8(16), MODA_RW8(24)::"memory");
 }
-__device__ __forceinline__ void tmem_ld_wait128(uint32_t (&r)[128]) {
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[128]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : MODA_RW8(0), MODA_RW8(8), MODA_RW8(16)::"memory");
 #pragma unroll
   for (int i = 24; i < 120; i += 24) asm volatile("" : MODA_RW8(i), MODA_RW8(i + 8), MODA_RW8(i + 16)::"memory");
@@ -185,8 +184,9 @@ struct Codes {
   static __device__ __forceinline__ int row(int turn, int hw, int lane) {
     return turn * RPT + hw * (32 / BPR) + lane / BPR;
   }
-  // Into a bf16 tile; `tame`: with zeros for infinities and NaN. True if there were any.
-  __device__ __forceinline__ bool unpack(uint8_t* tile, int hw, int lane, bool tame) {
+  // Into a bf16 tile, zeros from row `rows` on; `tame`: and in place of infinities and NaN.
+  // True if there were any.
+  __device__ __forceinline__ bool unpack(uint32_t tile, int hw, int lane, int rows, bool tame) {
     const int qtr = lane % BPR;
     // A block is four 16-byte chunks of a 64-column box from 4 (qtr & 1) on; lanes of the
     // upper box take them in another order, so that eight lanes (two rows) meet different
@@ -196,25 +196,28 @@ struct Codes {
 #pragma unroll 1
     for (int t = 0; t < kTurns; ++t) {
       const int r = row(t, hw, lane);
-      uint8_t* to = tile + (upper ? BN * 128 : 0) + r * 128;
-      const uint32_t cw[4] = {upper ? codes[0].z : codes[0].x, upper ? codes[0].w : codes[0].y,
-                              upper ? codes[0].x : codes[0].z, upper ? codes[0].y : codes[0].w};
-      const uint32_t s = scale_of(scale[0]);
-      uint32_t y[4][4];
+      const uint32_t to = tile + (upper ? BN * 128 : 0) + r * 128;
+      const uint32_t s = r < rows ? scale_of(scale[0]) : 0u;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) unpack8(cw[j], s, y[j]);
-      if (tame && scale[0] >= 253u) {
+      for (int j = 0; j < 4; j += 2) {
+        uint32_t y[2][4];
+        unpack8(upper == (j == 0) ? codes[0].z : codes[0].x, s, y[0]);
+        unpack8(upper == (j == 0) ? codes[0].w : codes[0].y, s, y[1]);
+        if (tame && scale[0] >= 253u) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t f = not_finite(y[i >> 2][i & 3]);
-          found |= f;
-          y[i >> 2][i & 3] &= ~(((f & 0x8000u) ? 0xffffu : 0u) | ((f & 0x80000000u) ? 0xffff0000u : 0u));
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t f = not_finite(y[i >> 2][i & 3]);
+            found |= f;
+            y[i >> 2][i & 3] &= ~(((f & 0x8000u) ? 0xffffu : 0u) | ((f & 0x80000000u) ? 0xffff0000u : 0u));
+          }
         }
-      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int chunk = 4 * (qtr & 1) + (upper ? j ^ 2 : j);
-        *reinterpret_cast<uint4*>(to + ((chunk ^ (r & 7)) << 4)) = make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]);
+        for (int i = 0; i < 2; ++i) {
+          const int chunk = 4 * (qtr & 1) + (upper ? (j ^ 2) + i : j + i);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((chunk ^ (r & 7)) << 4)), "r"(y[i][0]),
+                       "r"(y[i][1]), "r"(y[i][2]), "r"(y[i][3])
+                       : "memory");
+        }
       }
 #pragma unroll
       for (int i = 0; i + 1 < kTurns; ++i) {
@@ -674,36 +677,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           // columns that the row sees: all, but at the causal border
           const bool border = sch.index >= border0;
           const int end = border ? min(w.t0 + lp, w.t_last) - sch.index * BN + 1 : BN;
-          if constexpr (MX4) {
-            // The maximum first, then the weights, 32 scores at a time, in place: loops of
-            // few instructions and registers, which the unpacking warps want too.
-            float mx = -INFINITY;
-            auto load = [&](int c, uint32_t (&x)[32]) {
-              tmem_ld32(scol + c * 32, x);
-              tmem_ld_wait(x);
-              if (border) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = c * 32 + i < end ? x[i] : 0xff800000u;  // -inf
-              }
-            };
-#pragma unroll 1
-            for (int c = 0; c < BN / 32; ++c) {
-              uint32_t x[32];
-              load(c, x);
-              mx = fmaxf(mx, raw_max32(x));
-            }
-            if (__any_sync(0xffffffffu, there && mx * sl > m_ref + kRescaleThreshold)) rescale(mx * sl, j);
-            const float m = m_ref == -INFINITY ? 0.f : m_ref;
-            uint64_t acc[4] = {0, 0, 0, 0};
-#pragma unroll 1
-            for (int c = 0; c < BN / 32; ++c) {
-              uint32_t x[32], pk[16];
-              load(c, x);
-              weigh<32>(x, pk, sl, m, acc);
-              tmem_st16(scol + c * 16, pk);
-            }
-            sum = total_of(acc);
-          } else {
+          {
             uint32_t pk[BN / 2];
             for (int pass = 0; pass < 2; ++pass) {
               if (slow) {
@@ -719,16 +693,21 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                 }
                 rescale(mx * sl, j);
               }
+              const float m = m_ref == -INFINITY ? 0.f : m_ref;
               uint64_t acc[4] = {0, 0, 0, 0};
-              uint32_t x[BN];
+              constexpr int NL = MX4 ? 32 : BN;  // at a time: the unpacking warps have the other registers
 #pragma unroll
-              for (int c = 0; c < BN / 32; ++c) tmem_ld32(scol + c * 32, x + c * 32);
-              tmem_ld_wait128(x);
-              if (border) {
+              for (int c0 = 0; c0 < BN; c0 += NL) {
+                uint32_t x[NL];
 #pragma unroll
-                for (int c = 0; c < BN; ++c) x[c] = c < end ? x[c] : 0xff800000u;  // -inf
+                for (int c = 0; c < NL; c += 32) tmem_ld32(scol + c0 + c, x + c);
+                tmem_ld_wait(x);
+                if (border) {
+#pragma unroll
+                  for (int c = 0; c < NL; ++c) x[c] = c0 + c < end ? x[c] : 0xff800000u;  // -inf
+                }
+                weigh<NL>(x, pk + c0 / 2, sl, m, acc);
               }
-              weigh<BN>(x, pk, sl, m_ref == -INFINITY ? 0.f : m_ref, acc);
               sum = total_of(acc);
               if (slow) break;
               slow = __any_sync(0xffffffffu, there && !(sum <= kSumBound));
@@ -849,8 +828,8 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     const bool is_v = warp < 16;
     const int hw = warp & 3, r = tid & 127;  // a row of a tile each
     const int ns = is_v ? NV : NK;
-    uint64_t* full = is_v ? (MX4 ? bars->v_full : bars->v_ready) : bars->k_full;
-    uint64_t* check = is_v ? bars->v_check : bars->k_check;
+    const uint32_t full = smem_u32(is_v ? (MX4 ? bars->v_full : bars->v_ready) : bars->k_full);
+    const uint32_t check = smem_u32(is_v ? bars->v_check : bars->k_check);
     int s = 0, ph = 0;    // the next entry's stage and phase
     uint32_t checks = 0;  // parities of `check`
     bool ok = true;
@@ -859,41 +838,36 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       const int halves = w.npos > P ? 2 : 1;
       Sched sch(p.n_depth, w.nb, w.j0);
       using Cd = Codes<D>;
-      Cd c;                  // of the next sequence block
-      int page[Cd::kTurns];  // of the rows of the one after
-      // pages of the lane's rows of a sequence block, -1: none that a query sees
-      auto look_up = [&](int index) {
+      Cd c;  // of the next sequence block
+      const int* table = p.table + (int64_t)w.b * p.max_pages;
+      // A sequence block's codes on their way (for rows that no query sees those of the last
+      // that one does), and the pages of the one after into L1. Nothing here may wait for
+      // what it loads: registers spilled or chosen between cost 2400 cycles a block.
+      auto fetch = [&](int index) {
+        uint32_t at[Cd::kTurns];
 #pragma unroll
         for (int t = 0; t < Cd::kTurns; ++t) {
-          const int key = index * BN + Cd::row(t, hw, lane);
-          page[t] = key <= w.t_last ? p.table[(int64_t)w.b * p.max_pages + (key >> p.page_shift)] : -1;
+          const int key = min(index * BN + Cd::row(t, hw, lane), w.t_last);
+          at[t] = (uint32_t)table[key >> p.page_shift];
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(table + (min(key + BN, w.t_last) >> p.page_shift)));
         }
-      };
-      // (rows that no query sees unpack to zeros)
-      auto fetch = [&](int index) {
+        bool bad = false;
+#pragma unroll
+        for (int t = 0; t < Cd::kTurns; ++t) {
+          const int key = min(index * BN + Cd::row(t, hw, lane), w.t_last);
+          bad |= at[t] >= (uint32_t)p.num_pages;
+          at[t] = ((min(at[t], (uint32_t)p.num_pages - 1) * p.Hk + w.hk) << p.page_shift) +
+                  (key & ((1 << p.page_shift) - 1));
+        }
+        if (bad) atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
         const uint8_t *codes = is_v ? p.v : p.k, *scales = is_v ? p.v_scale : p.k_scale;
 #pragma unroll
         for (int t = 0; t < Cd::kTurns; ++t) {
-          const int row = Cd::row(t, hw, lane);
-          c.codes[t] = make_uint4(0u, 0u, 0u, 0u);
-          c.scale[t] = 127;
-          if (index * BN + row <= w.t_last) {
-            int pg = page[t];
-            if (pg < 0 || pg >= p.num_pages) {
-              atomicCAS(p.err, 0u, (unsigned int)MODA_ERR_INVALID_ARG);
-              pg = 0;
-            }
-            const int64_t at = ((int64_t)(pg * p.Hk + w.hk) << p.page_shift) + (row & ((1 << p.page_shift) - 1));
-            c.codes[t] = *reinterpret_cast<const uint4*>(codes + at * (D / 2) + lane % Cd::BPR * 16);
-            c.scale[t] = scales[at * Cd::BPR + lane % Cd::BPR];
-          }
+          c.codes[t] = *reinterpret_cast<const uint4*>(codes + (uint64_t)at[t] * (D / 2) + lane % Cd::BPR * 16);
+          c.scale[t] = scales[(uint64_t)at[t] * Cd::BPR + lane % Cd::BPR];
         }
       };
-      if constexpr (MX4) {
-        look_up(sch.sbk);
-        fetch(sch.sbk);
-        look_up(sch.sbk + 1);
-      }
+      if constexpr (MX4) fetch(sch.sbk);
       for (int j = w.j0; ok && j < w.j1; ++j) {
         sch.next(p.n_depth, w.nb);
         const bool part = partly_seen(w, sch);
@@ -909,20 +883,20 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             // (4-bit pages: each stage's phases one by one; a depth block's are seen by warp 3 too)
             if (MX4 && !(ok = warp_wait(smem_u32(is_v ? &bars->v_empty[s] : &bars->k_empty[s]), ph ^ 1, abort))) break;
             if (!MX4 || sch.depth) {
-              if (!(ok = warp_wait(smem_u32(&check[s]), checks >> s & 1, abort))) break;
+              if (!(ok = warp_wait(check + s * 8, checks >> s & 1, abort))) break;
               checks ^= 1u << s;
               if (is_v) found = tame_row<D>(tile, r, counts(r));
             } else {
-              found = c.unpack(tile, hw, lane, is_v && part);
+              found = c.unpack(smem_u32(tile), hw, lane, w.t_last + 1 - sch.index * BN, is_v && part);
               fetch(sch.index + 1);
-              look_up(sch.index + 2);
             }
             if (found) {
               *(volatile int*)&bars->poison[k & 7] = k + 1;
               __threadfence_block();
             }
             fence_async();
-            warp_arrive(&full[s], lane);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full + s * 8);
           }
           if (++s == ns) {
             s = 0;
