@@ -142,7 +142,9 @@ struct SelectParams {
 
 struct SelectSmem {
   uint32_t hist[256];
-  uint32_t reach[kMaxCluster][kSelWarps];  // largest sums of magnitudes, as bits
+  // of each warp of the group: the largest sum of magnitudes, as bits, and the largest and
+  // the smallest key
+  uint32_t reach[kMaxCluster][kSelWarps], top[kMaxCluster][kSelWarps], bottom[kMaxCluster][kSelWarps];
   double key[kFew];
   int index[kFew];
   int count[kSelWarps][2];
@@ -188,24 +190,32 @@ __device__ __forceinline__ void choose_bin(SelectSmem& sm, int lane, uint32_t* b
   __syncwarp();
 }
 
-// The exact score of a page: max over the group's queries of q . mean in fp64. All
-// lanes call it and get it. NaN counts as -infinity.
+// The exact score of a page: max over the group's queries of q . mean in fp64, of which an
+// SM does two a cycle: all lanes have a head (the lanes of a head a part of it). All lanes
+// call it and get it. NaN counts as -infinity.
 template <int D>
 __device__ __forceinline__ double exact_score(const __nv_bfloat16* q, const __nv_bfloat16* mean, int G, int lane) {
-  constexpr int E = D / 32;
-  double best = -INFINITY;
-  float m[E];
+  int lgL = D == 128 ? 5 : 4;  // log2 of the lanes of a head, each two pairs of elements at least
+  while (32 >> lgL < G) --lgL;
+  const int head = lane >> lgL, part = lane & ((1 << lgL) - 1);
+  // pairs of elements, those of a head's lanes side by side
+  const uint32_t* qr = reinterpret_cast<const uint32_t*>(q + min(head, G - 1) * D) + part;
+  const uint32_t* mr = reinterpret_cast<const uint32_t*>(mean) + part;
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  const int steps = D / 2 >> lgL;  // 2 to D / 4
+#pragma unroll 2
+  for (int i = 0; i < steps; i += 2)
 #pragma unroll
-  for (int e = 0; e < E; ++e) m[e] = __bfloat162float(mean[lane * E + e]);
-  for (int g = 0; g < G; ++g) {
-    double s = 0.0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fma((double)__bfloat162float(q[g * D + lane * E + e]), (double)m[e], s);
-#pragma unroll
-    for (int sh = 1; sh < 32; sh <<= 1) s += __shfl_xor_sync(0xffffffffu, s, sh);
-    if (s > best) best = s;
-  }
-  return best;
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t a = qr[(i + e) << lgL], b = mr[(i + e) << lgL];
+      s[2 * e] = fma((double)__uint_as_float(a << 16), (double)__uint_as_float(b << 16), s[2 * e]);
+      s[2 * e + 1] = fma((double)__uint_as_float(a & 0xffff0000u), (double)__uint_as_float(b & 0xffff0000u), s[2 * e + 1]);
+    }
+  double x = (s[0] + s[1]) + (s[2] + s[3]);
+  for (int sh = 1; sh < 1 << lgL; sh <<= 1) x += __shfl_xor_sync(0xffffffffu, x, sh);
+  if (!(x == x)) x = -INFINITY;
+  for (int sh = 1 << lgL; sh < 32; sh <<= 1) x = fmax(x, __shfl_xor_sync(0xffffffffu, x, sh));
+  return x;
 }
 
 template <int D, int NT>
@@ -289,6 +299,7 @@ select_pages_kernel(const __grid_constant__ SelectParams p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) some_q |= qb[t][i][e];
     auto id_of = [&](int i) -> int { return i < i1 ? block_of(p.sink + i) : -1; };
+    uint32_t top = 0, bottom = 0xffffffffu;
     int a_next = id_of(i0 + warp * 16 + r0), b_next = id_of(i0 + warp * 16 + r0 + 8);
     for (int i = i0 + warp * 16; i < i1; i += kSelWarps * 16) {
       const int ia = a_next, ib = b_next;
@@ -341,19 +352,30 @@ select_pages_kernel(const __grid_constant__ SelectParams p) {
         if (at < i1) {
           const uint32_t key = key_of((cl ? ib : ia) < 0 ? -INFINITY : best[cl]);
           asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + at * 4), "r"(key) : "memory");
+          top = max(top, key);
+          bottom = min(bottom, key);
         }
       }
     }
 #pragma unroll
-    for (int sh = 1; sh < 32; sh <<= 1) reach = max(reach, __shfl_xor_sync(0xffffffffu, reach, sh));
+    for (int sh = 1; sh < 32; sh <<= 1) {
+      reach = max(reach, __shfl_xor_sync(0xffffffffu, reach, sh));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, sh));
+      bottom = min(bottom, __shfl_xor_sync(0xffffffffu, bottom, sh));
+    }
     // products next to or below the smallest floats: fp32 decides nothing
     const bool any_q = __any_sync(0xffffffffu, (some_q & 0x7fff7fffu) != 0);
     const bool any_mean = __any_sync(0xffffffffu, (some_mean & 0x7fff7fffu) != 0);
     if (any_q && any_mean && reach < __float_as_uint(0x1p-100f)) reach = 0x7f800000u;
     if (lane == 0) {
-      uint32_t at = sm103::smem_u32(&sm.reach[rank][warp]);
-      if (clustered) at = paged::cluster_addr(at, 0);
-      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(reach) : "memory");
+      uint32_t at[3] = {sm103::smem_u32(&sm.reach[rank][warp]), sm103::smem_u32(&sm.top[rank][warp]),
+                        sm103::smem_u32(&sm.bottom[rank][warp])};
+      const uint32_t x[3] = {reach, top, bottom};
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        if (clustered) at[i] = paged::cluster_addr(at[i], 0);
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at[i]), "r"(x[i]) : "memory");
+      }
     }
   }
   if (clustered) {
@@ -365,38 +387,51 @@ select_pages_kernel(const __grid_constant__ SelectParams p) {
 
   // ------------------------------------------------------------------- choice
   uint32_t* keys = reinterpret_cast<uint32_t*>(scores);
-  uint32_t reach = 0;
-  for (int i = 0; i < p.group * kSelWarps; ++i) reach = max(reach, (&sm.reach[0][0])[i]);
+  uint32_t reach = 0, top = 0, bottom = 0xffffffffu;
+  for (int i = lane; i < p.group * kSelWarps; i += 32) {
+    reach = max(reach, (&sm.reach[0][0])[i]);
+    top = max(top, (&sm.top[0][0])[i]);
+    bottom = min(bottom, (&sm.bottom[0][0])[i]);
+  }
+  reach = __reduce_max_sync(0xffffffffu, reach);
+  top = __reduce_max_sync(0xffffffffu, top);
+  bottom = __reduce_min_sync(0xffffffffu, bottom);
   const float eps = __uint_as_float(reach) * kEps;  // infinite or NaN: nothing is decided by fp32
-  // tau, the want-th largest key
+  // The want-th largest key is in [low, high]: a radix choice of 8 bits at a time from the
+  // first that differs at all, until what is between them is no more than eps.
   if (tid == 0) {
     sm.want = want;
-    sm.prefix32 = 0;
     sm.listed = 0;
   }
-  for (int byte = 3; byte >= 0; --byte) {
+  int bits = 32 - __clz(top ^ bottom);  // of the keys that are not known yet
+  uint32_t low = bits < 32 ? top >> bits << bits : 0u, high = low | (bits < 32 ? (1u << bits) - 1u : 0xffffffffu);
+  while (bits > 0 && !(eps > FLT_MAX) && eps == eps && !(score_of(high) - score_of(low) <= eps)) {
+    const int step = min(bits, 8);
+    const uint32_t mask = bits < 32 ? 0xffffffffu << bits : 0u;
+    bits -= step;
     sm.hist[tid] = 0;
     __syncthreads();
-    const uint32_t prefix = sm.prefix32, mask = byte == 3 ? 0u : 0xffffffffu << (8 * byte + 8);
     for (int i = tid; i < nc; i += kSelThreads)
-      if ((keys[i] & mask) == prefix) atomicAdd(&sm.hist[keys[i] >> (8 * byte) & 255u], 1u);
+      if ((keys[i] & mask) == low) atomicAdd(&sm.hist[keys[i] >> bits & ((1u << step) - 1u)], 1u);
     __syncthreads();
     if (warp == 0) {
       uint32_t bin = 256;
       choose_bin(sm, lane, &bin);
-      if (bin < 256) sm.prefix32 = prefix | bin << (8 * byte);
+      if (bin < 256) sm.prefix32 = low | bin << bits;
     }
     __syncthreads();
+    low = sm.prefix32;
+    high = low | ((1u << bits) - 1u);
   }
-  const uint32_t tau = sm.prefix32;
   // The keys that are undecided: [least, most]; above, a page is chosen.
-  uint32_t least = tau, most = tau;
-  if (eps > 0.f || !(eps == eps)) {
-    const float t = score_of(tau);
-    // (rounding outwards; a tau of -infinity stays alone)
-    least = eps <= FLT_MAX ? key_of(__fadd_rd(t, -2.f * eps)) : 0u;
-    most = eps <= FLT_MAX ? key_of(__fadd_ru(t, 2.f * eps)) : 0xffffffffu;
+  uint32_t least = low, most = high;
+  if (!(eps == 0.f) || bits > 0) {
+    // (rounding outwards; an infinity stays alone)
+    const bool any = eps <= FLT_MAX;
+    least = any ? key_of(__fadd_rd(score_of(low), -2.f * eps)) : 0u;
+    most = any ? key_of(__fadd_ru(score_of(high), 2.f * eps)) : 0xffffffffu;
   }
+  __syncthreads();  // sm.listed is 0
   // a warp's part of the candidates, in order
   const int part = ((nc + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
   const int w0 = min(nc, warp * part), w1 = min(nc, w0 + part);
@@ -423,8 +458,8 @@ select_pages_kernel(const __grid_constant__ SelectParams p) {
   int ties = 0;
   __syncthreads();  // sm.count is used again
   if (need < all_open && least == most) {  // equal scores, exact ones: by the page's number
-    from = tau + 1;
-    tie = tau;
+    from = least + 1;
+    tie = least;
     ties = need;
   } else if (need < all_open) {
     // Exact scores of the open ones; what is chosen gets the largest key, what is not
@@ -511,22 +546,25 @@ select_pages_kernel(const __grid_constant__ SelectParams p) {
     }
     __syncthreads();
   }
-  // In order of their numbers.
-  int mine = 0, tied = 0;
-  for (int i = w0 + lane; i < w0 + part; i += 32) {
-    const uint32_t k = i < w1 ? keys[i] : 0u;
-    mine += __popc(__ballot_sync(0xffffffffu, i < w1 && k >= from));
-    tied += __popc(__ballot_sync(0xffffffffu, i < w1 && ties > 0 && k == tie));
+  // In order of their numbers. (What is chosen without more ado has been counted above.)
+  int mine = above + open, tied = 0;
+  if (need < all_open) {
+    mine = 0;
+    for (int i = w0 + lane; i < w0 + part; i += 32) {
+      const uint32_t k = i < w1 ? keys[i] : 0u;
+      mine += __popc(__ballot_sync(0xffffffffu, i < w1 && k >= from));
+      tied += __popc(__ballot_sync(0xffffffffu, i < w1 && ties > 0 && k == tie));
+    }
+    if (lane == 0) {
+      sm.count[warp][0] = mine;
+      sm.count[warp][1] = tied;
+    }
+    __syncthreads();
   }
-  if (lane == 0) {
-    sm.count[warp][0] = mine;
-    sm.count[warp][1] = tied;
-  }
-  __syncthreads();
   int at = 0, tied_before = 0;
   for (int w = 0; w < warp; ++w) {
-    at += sm.count[w][0];
-    tied_before += sm.count[w][1];
+    at += sm.count[w][0] + (need < all_open ? 0 : sm.count[w][1]);
+    if (need < all_open) tied_before += sm.count[w][1];
   }
   at += min(tied_before, ties);
   for (int i = w0; i < w1; i += 32) {
@@ -536,14 +574,16 @@ select_pages_kernel(const __grid_constant__ SelectParams p) {
     const uint32_t below = (1u << lane) - 1u;
     const bool yes = (i + lane < w1 && k >= from) || (is_tie && tied_before + __popc(tie_set & below) < ties);
     const uint32_t set = __ballot_sync(0xffffffffu, yes);
-    if (yes) out[p.sink + at + __popc(set & below)] = block_of(p.sink + i + lane);
+    if (yes) out[p.sink + at + __popc(set & below)] = i + lane;
     at += __popc(set);
     tied_before += __popc(tie_set);
   }
-  for (int i = tid; i < p.sink + p.recent; i += kSelThreads) {
-    const bool front = i < p.sink;
-    out[front ? i : p.S - p.recent + i - p.sink] = block_of(front ? i : held - p.recent + i - p.sink);
-  }
+  __syncthreads();
+  // their row blocks, looked up at once
+  for (int i = tid; i < p.S; i += kSelThreads)
+    out[i] = block_of(i < p.sink                 ? i
+                      : i < p.S - p.recent ? p.sink + out[i]
+                                           : held - p.S + i);
   if (tid == 0) p.rows[item] = ((p.S - 1) << shift) + (pos & (c.page_size - 1)) + 1;
 }
 
@@ -557,10 +597,11 @@ cudaError_t select_d(const SelectPagesArgs& a, cudaStream_t stream) {
   p.seq = a.seq; p.pos = a.pos;
   p.G = a.G; p.S = a.S; p.sink = a.sink; p.recent = a.recent;
   p.pages = a.pages; p.rows = a.rows;
-  // CTAs of a (token, KV head): as many as there are SMs for, while each has 128 pages
+  // CTAs of a (token, KV head): a warp takes 16 pages at a time, and waits for them, so a
+  // CTA has 256 pages or so where there are enough SMs for that. FIXME
   const int64_t items = (int64_t)a.N * c.Hk;
   int group = 1;
-  while (group < kMaxCluster && items * group * 2 <= a.num_sms * 2 && c.max_pages >= 256 * group) group *= 2;
+  while (group < kMaxCluster && items * group * 2 <= a.num_sms * 8 && c.max_pages >= 256 * group) group *= 2;
   p.group = group;
   const size_t smem = ((size_t)c.max_pages * 4 + 15) / 16 * 16;
   const auto kernel = a.G <= 8 ? select_pages_kernel<D, 1> : select_pages_kernel<D, 2>;

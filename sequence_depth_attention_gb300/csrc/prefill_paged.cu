@@ -918,7 +918,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 
 // The cut tiles' rows from their partials: a warp for each row of the tile that
 // CTA blockIdx.x begins (if any), its partials' loads in flight at once.
-constexpr int kJoinWarps = 8, kJoinParts = 4;  // warps of a CTA, CTAs of a tile
+constexpr int kJoinWarps = 8, kJoinParts = 16;  // warps of a CTA, CTAs of a tile
 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32)
