@@ -152,6 +152,7 @@ struct DecodePagedArgs {
   // Where each (token, KV head) has pages of its own, it is a sequence with one KV head
   // here, and `fold` of them share a token's depth slots; else 1.
   int fold;
+  int even;  // lengths are about as long as the table is wide (selected pages)
   float scale;
   void* o;     // [B,Hq,d] bf16
   float* lse;  // [B,Hq] or nullptr

@@ -190,10 +190,19 @@ __device__ __forceinline__ void choose_bin(SelectSmem& sm, int lane, uint32_t* b
   __syncwarp();
 }
 
-// The exact score of a page: max over the group's queries of q . mean in fp64, of which an
-// SM does two a cycle: all lanes have a head (the lanes of a head a part of it). All lanes
-// call it and get it. NaN counts as -infinity.
-template <int D>
+// a + b and what its rounding leaves, exactly (Knuth).
+__device__ __forceinline__ float two_sum(float a, float b, float& rest) {
+  const float s = __fadd_rn(a, b), x = __fsub_rn(s, a);
+  rest = __fadd_rn(__fsub_rn(a, __fsub_rn(s, x)), __fsub_rn(b, x));
+  return s;
+}
+
+// The exact score of a page: max over the group's queries of q . mean, to fp64's precision.
+// All lanes have a head (the lanes of a head a part of it); all call it and get it. NaN
+// counts as -infinity. SINGLE: products are exact in fp32 (none overflows, and those that
+// underflow do not count) and are summed there in three parts, which fp64 adds up: of fp64
+// operations an SM does two a cycle, conversions among them (a page took 6000 cycles).
+template <int D, bool SINGLE>
 __device__ __forceinline__ double exact_score(const __nv_bfloat16* q, const __nv_bfloat16* mean, int G, int lane) {
   int lgL = D == 128 ? 5 : 4;  // log2 of the lanes of a head, each two pairs of elements at least
   while (32 >> lgL < G) --lgL;
@@ -201,20 +210,36 @@ __device__ __forceinline__ double exact_score(const __nv_bfloat16* q, const __nv
   // pairs of elements, those of a head's lanes side by side
   const uint32_t* qr = reinterpret_cast<const uint32_t*>(q + min(head, G - 1) * D) + part;
   const uint32_t* mr = reinterpret_cast<const uint32_t*>(mean) + part;
-  double s[4] = {0.0, 0.0, 0.0, 0.0};
   const int steps = D / 2 >> lgL;  // 2 to D / 4
-#pragma unroll 2
-  for (int i = 0; i < steps; i += 2)
+  double x = 0.0;
+  float s[2] = {0.f, 0.f}, r[2] = {0.f, 0.f}, rr[2] = {0.f, 0.f};
+#pragma unroll 4
+  for (int i = 0; i < steps; ++i) {
+    const uint32_t a = qr[i << lgL], b = mr[i << lgL];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const uint32_t a = qr[(i + e) << lgL], b = mr[(i + e) << lgL];
-      s[2 * e] = fma((double)__uint_as_float(a << 16), (double)__uint_as_float(b << 16), s[2 * e]);
-      s[2 * e + 1] = fma((double)__uint_as_float(a & 0xffff0000u), (double)__uint_as_float(b & 0xffff0000u), s[2 * e + 1]);
+      const float u = __uint_as_float(e ? a & 0xffff0000u : a << 16), v = __uint_as_float(e ? b & 0xffff0000u : b << 16);
+      if constexpr (SINGLE) {
+        float t, t2;
+        s[e] = two_sum(s[e], __fmul_rn(u, v), t);
+        r[e] = two_sum(r[e], t, t2);
+        rr[e] = __fadd_rn(rr[e], t2);
+      } else {
+        x = fma((double)u, (double)v, x);
+      }
     }
-  double x = (s[0] + s[1]) + (s[2] + s[3]);
+  }
+  if constexpr (SINGLE) {
+    float t, t2, t3;
+    const float s0 = two_sum(s[0], s[1], t), r0 = two_sum(r[0], r[1], t2), r1 = two_sum(r0, t, t3);
+    x = (double)s0 + ((double)r1 + (double)(t2 + t3 + rr[0] + rr[1]));
+  }
   for (int sh = 1; sh < 1 << lgL; sh <<= 1) x += __shfl_xor_sync(0xffffffffu, x, sh);
   if (!(x == x)) x = -INFINITY;
-  for (int sh = 1 << lgL; sh < 32; sh <<= 1) x = fmax(x, __shfl_xor_sync(0xffffffffu, x, sh));
+  for (int sh = 1 << lgL; sh < 32; sh <<= 1) {
+    const double y = __shfl_xor_sync(0xffffffffu, x, sh);
+    if (y > x) x = y;
+  }
   return x;
 }
 
@@ -465,26 +490,33 @@ select_pages_kernel(const __grid_constant__ SelectParams p) {
     // Exact scores of the open ones; what is chosen gets the largest key, what is not
     // the least. (A key of 0 or of all ones would be a NaN's, which no score is.)
     from = 0xffffffffu;
-    auto each_open = [&](auto&& f) {  // this warp's, one after another in order, by all lanes
+    const float most_sum = __uint_as_float(reach);
+    const bool single = most_sum >= 0x1p-60f && most_sum <= 0x1p120f;
+    auto exact = [&](int at) -> double {  // of a candidate, by all lanes
+      const int page = block_of(p.sink + at);
+      const __nv_bfloat16* mean = p.means + (int64_t)max(page, 0) * D;
+      const double x = single ? exact_score<D, true>(q, mean, p.G, lane) : exact_score<D, false>(q, mean, p.G, lane);
+      return page < 0 ? (double)-INFINITY : x;
+    };
+    auto each_open = [&](auto&& f) {  // this warp's, one after another in order
       for (int i = w0; i < w1; i += 32) {
         const uint32_t k = i + lane < w1 ? keys[i + lane] : 0u;
         uint32_t set = __ballot_sync(0xffffffffu, i + lane < w1 && k >= least && k <= most);
         while (set) {
-          const int at = i + __ffs(set) - 1;
+          f(i + __ffs(set) - 1);
           set &= set - 1;
-          const int page = block_of(p.sink + at);
-          f(at, page < 0 ? (double)-INFINITY : exact_score<D>(q, p.means + (int64_t)page * D, p.G, lane));
         }
       }
     };
     if (all_open <= kFew) {
-      each_open([&](int at, double x) {
-        if (lane == 0) {
-          const int l = atomicAdd(&sm.listed, 1);
-          sm.key[l] = x + 0.0;
-          sm.index[l] = at;
-        }
+      each_open([&](int at) {
+        if (lane == 0) sm.index[atomicAdd(&sm.listed, 1)] = at;
       });
+      __syncthreads();
+      for (int l = warp; l < all_open; l += kSelWarps) {
+        const double x = exact(sm.index[l]);
+        if (lane == 0) sm.key[l] = x + 0.0;
+      }
       __syncthreads();
       if (warp == 0 && lane < all_open) {
         const double x = sm.key[lane];
@@ -510,8 +542,8 @@ select_pages_kernel(const __grid_constant__ SelectParams p) {
         __syncthreads();
         const unsigned long long prefix = sm.prefix;
         const unsigned long long mask = byte == 7 ? 0ull : ~0ull << (8 * byte + 8);
-        each_open([&](int, double x) {
-          const unsigned long long k = key_of(x);
+        each_open([&](int at) {
+          const unsigned long long k = key_of(exact(at));
           if (lane == 0 && (k & mask) == prefix) atomicAdd(&sm.hist[k >> (8 * byte) & 255u], 1u);
         });
         __syncthreads();
@@ -526,15 +558,15 @@ select_pages_kernel(const __grid_constant__ SelectParams p) {
       // sm.want of the pages that equal t64, the first ones: this warp's after the
       // earlier warps'
       int equal = 0;
-      each_open([&](int, double x) { equal += key_of(x) == t64; });
+      each_open([&](int at) { equal += key_of(exact(at)) == t64; });
       if (lane == 0) sm.count[warp][0] = equal;
       __syncthreads();
       int seen = 0;
       for (int w = 0; w < warp; ++w) seen += sm.count[w][0];
       const int first = sm.want;
       // (a warp changes keys of its own part alone, of one that it is past)
-      each_open([&](int at, double x) {
-        const unsigned long long k = key_of(x);
+      each_open([&](int at) {
+        const unsigned long long k = key_of(exact(at));
         const bool yes = k > t64 || (k == t64 && seen < first);
         seen += k == t64;
         __syncwarp();
@@ -601,7 +633,7 @@ cudaError_t select_d(const SelectPagesArgs& a, cudaStream_t stream) {
   // CTA has 256 pages or so where there are enough SMs for that. FIXME
   const int64_t items = (int64_t)a.N * c.Hk;
   int group = 1;
-  while (group < kMaxCluster && items * group * 2 <= a.num_sms * 8 && c.max_pages >= 256 * group) group *= 2;
+  while (group < kMaxCluster && items * group * 2 <= a.num_sms * 4 && c.max_pages >= 256 * group) group *= 2;
   p.group = group;
   const size_t smem = ((size_t)c.max_pages * 4 + 15) / 16 * 16;
   const auto kernel = a.G <= 8 ? select_pages_kernel<D, 1> : select_pages_kernel<D, 2>;

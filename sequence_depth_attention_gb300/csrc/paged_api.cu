@@ -409,7 +409,7 @@ moda_status moda_decode_selected(const void* q, const moda_paged_kv* cache, cons
   a.seq_lens = rows;
   a.depth_b_stride = depth_tok_stride; a.depth_hk_stride = depth_hk_stride;
   a.depth_slot_stride = depth_slot_stride;
-  a.Hq = G; a.G = G; a.L = L; a.fold = Hk; a.scale = scale;
+  a.Hq = G; a.G = G; a.L = L; a.fold = Hk; a.even = 1; a.scale = scale;
   a.o = o; a.lse = lse; a.work = workspace;
   int dev;
   st = moda::device_info(&dev, &a.c.err, &a.num_sms);
