@@ -235,3 +235,89 @@ def test_attention_over_selected_pages(case, layer_major):
     empty = wl == -math.inf
     assert torch.equal(lse == -math.inf, empty)
     assert ((lse.double() - wl).abs()[~empty] <= tl[~empty]).all()
+
+
+def test_bad_indexes_are_latched():
+    Hk, d, page = 2, 64, 16
+    c = bare([100, 300], Hk, d, page)
+    q, means = normal(4, 8, d, seed=20), normal(c.num_pages, Hk, d, seed=21)
+    good = choose(c, q[:2], means, i32([0, 1]), i32([99, 299]), 5, 1, 1)
+    # sequences and rows that are not there: no pages; the others as they were
+    for seq, pos in (([0, 1, 2, 0], [99, 299, 5, -1]), ([0, 1, -2, 1], [99, 299, 5, c.max_pages * page])):
+        got = choose(c, q, means, i32(seq), i32(pos), 5, 1, 1, want=INVALID)
+        assert torch.equal(got[0][:2], good[0]) and torch.equal(got[1][:2], good[1])
+        assert (got[0][2:] == -1).all() and (got[1][2:] == 0).all()
+    # pages that are not in the pool: chosen last, and given as -1
+    was = c.table.clone()
+    for bad in (c.num_pages, -1, 2**31 - 1):
+        c.table[1, 3:15] = bad
+        pages, rows = choose(c, q[:2], means, i32([0, 1]), i32([99, 299]), 5, 1, 1, want=INVALID)
+        assert torch.equal(pages[0], good[0][0]) and (pages[1] >= 0).all() and (rows == good[1]).all()
+        pages, _ = choose(c, q[:2], means, i32([0, 1]), i32([99, 299]), 18, 1, 1, want=INVALID)
+        assert ((pages[1] == -1).sum(-1) == 11).all()  # 19 pages, of which 12 are not there: one is left out
+        c.table.copy_(was)
+    fresh = torch.full((c.num_pages, Hk, d), 3.5, dtype=torch.bfloat16, device="cuda")
+    c.table[0, 0] = c.num_pages
+    moda.moda_page_means(*c.args(), i32([0, 1, 5, 1]), i32([15, 31, 15, 1 << 20]), fresh)
+    settled(INVALID)
+    touched = (fresh != 3.5).flatten(1).any(1).nonzero().flatten().tolist()
+    assert touched == [int(was[1, 1])]
+    x = normal(1, 4, 64, seed=22)
+    k = v = normal(3, 2, 16, 64, seed=23)
+    for pages, rows in (([[[6, 1], [1, 2]]], [[20, 30]]), ([[[0, 1], [1, -1]]], [[20, 30]]), ([[[0, 1], [1, 2]]], [[33, -1]])):
+        moda.moda_decode_selected(x, k, v, i32(pages), i32(rows), 0.1)
+        settled(INVALID)
+
+
+def test_captured_selection_and_attention():
+    """Captured together, replayed with other tokens and rows; a batch padded to its
+    captured size."""
+    Hq, Hk, d, page, S = 8, 2, 128, 16, 7
+    lens = [900, 20, 333, 1]
+    c = pc.Cache("bf16", lens, Hk, d, page, seed=24, device="cuda")
+    means = cc.page_means(c).bfloat16()
+    means[torch.isnan(means)] = 0
+    q = normal(6, Hq, d, seed=25)
+    seq, pos = i32([0, 1, 2, 3, -1, -1]), i32([n - 1 for n in lens] + [0, 0])
+    need = moda.moda_decode_paged_workspace_bytes(Hq, Hk, d) // 4
+    pages, rows = torch.zeros(6, Hk, S, dtype=torch.int32, device="cuda"), torch.zeros(6, Hk, dtype=torch.int32, device="cuda")
+    o, lse, ws = torch.zeros_like(q), torch.zeros(6, Hq, device="cuda"), torch.empty(need, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        moda.moda_select_pages(q, means, *c.args(), seq, pos, S, sink=1, recent=2, pages=pages, rows=rows)
+        moda.moda_decode_selected(q, c.k, c.v, pages, rows, 0.1, o=o, lse=lse, workspace=ws)
+    for s, t in (([0, 1, 2, 3, -1, -1], [899, 19, 332, 0, 0, 0]), ([2, -1, 0, 0, 0, 1], [100, 7, 500, 300, 15, 16])):
+        seq.copy_(i32(s))
+        pos.copy_(i32(t))
+        q.copy_(torch.randn_like(q))
+        torch.cuda.synchronize()
+        for _ in range(2):
+            g.replay()
+        settled()
+        want = cc.selection(c, q, means, seq.cpu(), pos.cpu(), S, 1, 2)
+        assert torch.equal(pages.cpu(), want[0]) and torch.equal(rows.cpu(), want[1])
+        wo, wl, to, tl = cc.selected_reference(c, q, pages, rows, None, None, 0.1)
+        assert ((o.double() - wo).abs() <= to).all()
+        some = wl > -math.inf
+        assert torch.equal(lse == -math.inf, ~some) and ((lse.double() - wl).abs()[some] <= tl[some]).all()
+
+
+def test_streams_of_their_own():
+    Hk, d, page = 2, 64, 16
+    c = pc.Cache("bf16", [500], Hk, d, page, seed=26, device="cuda")
+    q, means = normal(1, 8, d, seed=27), normal(c.num_pages, Hk, d, seed=28)
+    pages, rows = choose(c, q, means, i32([0]), i32([499]), 6, 1, 1)
+    want, wl = moda.moda_decode_selected(q, c.k, c.v, pages.cuda(), rows.cuda(), 0.1)
+    filled = moda.moda_page_means(*c.args(), i32([0]), i32([15]), torch.zeros_like(means))
+    settled()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream, 0):
+        got = moda.moda_select_pages(q, means, *c.args(), i32([0]), i32([499]), 6, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0].cpu(), pages) and torch.equal(got[1].cpu(), rows)
+        o, lse = moda.moda_decode_selected(q, c.k, c.v, *got, 0.1, stream=stream)
+        m = moda.moda_page_means(*c.args(), i32([0]), i32([15]), torch.zeros_like(means), stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and torch.equal(lse, wl) and torch.equal(m, filled)
+    assert moda.moda_decode_selected(q, c.k, c.v, pages.cuda(), rows.cuda(), 0.1, want_lse=False)[1] is None
