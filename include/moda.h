@@ -19,7 +19,8 @@
  *     that gave up) is latched in a per-device error word and reported by
  *     moda_get_device_error().
  *   - Batch is 1 and callers loop over sequences, but for the paged cache's calls
- *     (moda_kv_append, moda_kv_gather, moda_decode_paged), which take a batch.
+ *     (moda_kv_append, moda_kv_gather, moda_decode_paged, moda_prefill_paged,
+ *     moda_page_means, moda_select_pages, moda_decode_selected), which take a batch.
  *   - Thread safety: calls may be made from several host threads.
  *   - moda_fwd, moda_fwd_layer_major and moda_fwd_depth_cc hand out their
  *     tiles through a small per-device queue; each call takes the next of 64 queues
@@ -448,9 +449,10 @@ MODA_API moda_status moda_kv_append(const void* q, const void* k, const void* v,
  * pages the values that the codes stand for, which bf16 holds exactly (from
  * 2^128 on, which moda_kv_append never stores, infinity). It gives a caller the
  * rows as later steps will see them: a prompt's own 4-bit rows for its moda_fwd,
- * or a cached prefix for a pass of the caller's (no call here attends with fewer
- * queries than keys but moda_decode_paged, which reads the pages itself). Rows may
- * be named any number of times, in any order.
+ * or a cached prefix for a pass of the caller's. (The calls that attend with fewer
+ * queries than keys, moda_prefill_paged, moda_decode_paged and
+ * moda_decode_selected, read the pages themselves.) Rows may be named any number of
+ * times, in any order.
  *   seq, pos  [N] int32 as in moda_kv_append; a row whose seq is -1 (or whose
  *             index is out of range, which is latched) is left as it was
  *   k, v      [N, Hk, d] bf16 outputs; must not overlap the pages or each other

@@ -34,6 +34,18 @@
 // P is rounded to bf16 once, as in the forward: the sum l keeps fp32 weights, and
 // what o is off by that is about as much as its own rounding to bf16.
 //
+// What bounds it, measured (us; the floor is that of the products or of the rows):
+//   d = 128, 2048 tokens at 65536 rows, G = 4    790 (561)   tensor pipe 72 % busy, power;
+//            703 on a cool GPU. What it is not busy is the halves' hand-over of S and P.
+//   d = 64, 7 prompts' pieces, G = 8            1411 (577)   a block's exponentials take as
+//            long as at 128, its products half: tensor pipe 40 %. Two threads a row with an O
+//            of their own took 1467, S ahead in columns of its own 1418 to 1530.
+//   4-bit, 1024 tokens at 32768, G = 4           307 (140)   the unpacking warps and the softmax
+//            share the issue slots (55 %) and the registers.
+//   32 drafts of up to 8 tokens, to 16000 rows    99 (80)    HBM: 81 % of the copy rate.
+//   5 tokens at 701 rows                          15 (0.3)   latencies one behind another: share
+//            2, first rows 3, blocks 4, the join behind the last CTA 3.
+//
 // Every wait is bounded (2 s); on expiry the CTA stops issuing work, waits for its
 // copies and MMAs in flight, frees TMEM and latches MODA_ERR_TIMEOUT.
 #include "mx4.cuh"
@@ -53,7 +65,10 @@ using paged::kLog2e;
 constexpr int BM = 128, BN = 128;  // rows of a half tile, keys of a block
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr float kSumBound = 256.0f;  // of a row's weights in a block, see the softmax warps
-constexpr int kLeast = 2;                  // points that are worth a CTA
+// Points that are worth a CTA. Measured (us) with 1, 2, 3, 4, 6: 5 tokens at 701 rows 15.5,
+// 15.8, 15.5, 16.9, 19.0; 128 tokens at 2000 32.7, 29.0, 28.8, 29.3, 33.1; where there is more
+// work than that, no difference.
+constexpr int kLeast = 2;
 
 template <int D, bool MX4>
 struct Cfg {
@@ -173,7 +188,7 @@ __device__ __forceinline__ bool tame_row(uint8_t* tile, int r, bool counts) {
 // A lane's 4-bit blocks of a tile, from global memory by way of registers to bf16: D / 32
 // lanes a row, a block of 32 elements a lane, four warps. The next tile's are on their way
 // while this one's are unpacked. One loop for K and V and all turns: beside the softmax's
-// code, unrolled ones waited for their instructions (1.7 of 5 warps, FIXME).
+// code, unrolled ones waited for their instructions (1.7 of a scheduler's 5 warps did).
 template <int D>
 struct Codes {
   static constexpr int BPR = D / 32;        // blocks, and lanes, of a row
