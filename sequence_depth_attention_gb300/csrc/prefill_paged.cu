@@ -7,7 +7,9 @@
 // of 128 rows. Both halves see (nearly) the same keys, so a block of 128 keys is
 // brought into shared memory once for both: S = Q K^T and O += P V on tcgen05, the halves
 // in turn, so that the softmax of one half runs beside the products of the other. A
-// softmax thread has one row. The work is cut into equal shares of a line of blocks
+// softmax thread has one row, or (bf16 pages, d = 64) the keys of half a block for one row,
+// with an O of its own: the two threads of a row go their own ways (reference, sum, O) until
+// the end of a tile, where their states are merged. The work is cut into equal shares of a line of blocks
 // (prefill_paged.cuh), so a draft of five tokens over a long context is spread over
 // the SMs like a long prompt, and the lengths stay on the device.
 //   * A block of 128 keys is up to 8 pages, each looked up and copied by a lane.
@@ -22,29 +24,34 @@
 //     tile sees become 0, and an infinity or NaN among the others becomes 0 too and is
 //     added at the end to the rows that do see it.
 //
-// Roles (16 warps; 20 for 4-bit pages):
+// Roles (16 warps; 20 for 4-bit pages; 24 with two softmax threads a row):
 //   warp 0        TMA producer of Q and K     warp 1  issuer of all MMAs, TMEM
 //   warp 2        TMA producer of V           warp 3  4-bit pages: of the depth blocks
 //   warps 4-7     softmax and epilogue of the first half, one thread per row (TMEM lane)
-//   warps 8-11    of the second half
-//   warps 12-15   partly seen V blocks made harmless
-//         (12-19) and 4-bit pages unpacked, by way of registers
+//   warps 8-11    of the second half (two threads a row: 4-11 of the first, 12-19)
+//   the last 4    partly seen V blocks made harmless
+//         (8)     and 4-bit pages unpacked, by way of registers
 // TMEM (512 columns): S of the halves [0,128) [128,256), each half's P (bf16 pairs) in the
-// first 64 columns of its S, O of the halves at 256 and 256 + d.
+// first 64 columns of its S, O of the halves at 256 and 256 + d. (Two threads a row: each P in
+// the first 32 of its thread's 64 columns of S, O of the threads 64 columns each from 256 on.)
 // P is rounded to bf16 once, as in the forward: the sum l keeps fp32 weights, and
 // what o is off by that is about as much as its own rounding to bf16.
 //
 // What bounds it, measured (us; the floor is that of the products or of the rows):
 //   d = 128, 2048 tokens at 65536 rows, G = 4    790 (561)   tensor pipe 72 % busy, power;
-//            703 on a cool GPU. What it is not busy is the halves' hand-over of S and P.
-//   d = 64, 7 prompts' pieces, G = 8            1411 (577)   a block's exponentials take as
-//            long as at 128, its products half: tensor pipe 40 %. Two threads a row with an O
-//            of their own took 1467, S ahead in columns of its own 1418 to 1530.
-//   4-bit, 1024 tokens at 32768, G = 4           307 (140)   the unpacking warps and the softmax
+//            700 on a cool GPU. What it is not busy is the halves' hand-over of S and P.
+//   d = 64, 7 prompts' pieces, G = 8            1330 (577)   a block's exponentials take as
+//            long as at 128, its products half. One thread a row: 1410; S ahead in columns of
+//            its own: 1418 to 1530.
+//   4-bit, 1024 tokens at 32768, G = 4           305 (140)   the unpacking warps and the softmax
 //            share the issue slots (55 %) and the registers.
-//   32 drafts of up to 8 tokens, to 16000 rows    99 (80)    HBM: 81 % of the copy rate.
+//   32 drafts of up to 8 tokens, to 16000 rows    98 (80)    HBM: 81 % of the copy rate.
 //   5 tokens at 701 rows                          15 (0.3)   latencies one behind another: share
 //            2, first rows 3, blocks 4, the join behind the last CTA 3.
+// The softmax loop bears neither waits among its exponentials nor spilled registers. At d = 64
+// with two threads a row: 32 scores at a time 1330, 16 with the next on their way 1467, 64 (80
+// spilled bytes) 1563, 32 with 160 spilled bytes 1632; with one, 128 scores 1410, 32 with the
+// next on their way 1600.
 //
 // Every wait is bounded (2 s); on expiry the CTA stops issuing work, waits for its
 // copies and MMAs in flight, frees TMEM and latches MODA_ERR_TIMEOUT.
@@ -73,11 +80,15 @@ constexpr int kLeast = 2;
 template <int D, bool MX4>
 struct Cfg {
   static constexpr int kTameWarps = MX4 ? 8 : 4;
-  static constexpr int kWarps = 12 + kTameWarps, kThreads = kWarps * 32;
+  // Threads of a row. (Two take more registers than 4-bit pages leave, and at d = 128 more TMEM
+  // than there is.)
+  static constexpr int kCh = D == 64 && !MX4 ? 2 : 1;
+  static constexpr int kTame0 = 4 + 8 * kCh, kWarps = kTame0 + kTameWarps, kThreads = kWarps * 32;
   // Registers of a thread of each group of four warps; they add up to what the block is
-  // launched with (at 128 and, 4-bit pages, 96 a thread).
-  static constexpr int kRegsIssue = 64, kRegsSoftmax = MX4 ? 120 : 184, kRegsTame = MX4 ? 88 : 80;
-  static_assert(kRegsIssue + 2 * kRegsSoftmax + kTameWarps / 4 * kRegsTame <= kWarps / 4 * (MX4 ? 96 : 128));
+  // launched with (kRegsLaunch a thread).
+  static constexpr int kRegsIssue = 64, kRegsSoftmax = kCh == 2 ? 88 : MX4 ? 120 : 184;
+  static constexpr int kRegsTame = kCh == 2 ? 64 : MX4 ? 88 : 80, kRegsLaunch = kCh == 2 ? 80 : MX4 ? 96 : 128;
+  static_assert(kRegsIssue + 2 * kCh * kRegsSoftmax + kTameWarps / 4 * kRegsTame <= kWarps / 4 * kRegsLaunch);
   static constexpr int kBoxes = D / 64;  // 64-column (128-byte) swizzle boxes per row
   static constexpr int kBoxBytes = BN * 128;
   static constexpr int kQBytes = BM * D * 2;  // of a half
@@ -86,13 +97,15 @@ struct Cfg {
   static constexpr int kOffK = 2 * kQBytes;
   static constexpr int kOffV = kOffK + kNK * kTileBytes;
   static constexpr int kOffBar = kOffV + kNV * kTileBytes;
-  static constexpr int kSmemBytes = kOffBar + 2048 + 1024;  // barriers, alignment
+  static constexpr int kOffMl = kOffBar + (kCh == 2 ? 3072 : 2048);  // m and l of a row's threads
+  static constexpr int kSmemBytes = kOffMl + (kCh == 2 ? 4 * BM * 8 : 0) + 1024;  // alignment
   static constexpr uint32_t kColS = 0, kColO = 256;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
 constexpr int kMaxStages = 5;
 
+template <int WALKS>
 struct alignas(16) Barriers {
   uint64_t q_full, q_free;  // Q of the current tile landed / its last S = Q K^T completed
   uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
@@ -102,15 +115,15 @@ struct alignas(16) Barriers {
   // lands at k_check and v_check, and is full once the unpacking warps have seen it.
   uint64_t k_check[kMaxStages], v_check[kMaxStages], v_ready[kMaxStages];
   uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t ml_full[8];  // two threads a row: a pair of warps have left their m and l
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
   int poison[8];  // [k % 8] = k + 1: tile k had infinities or NaN taken out (fewer tiles are under way)
   ShareSmem find;
   Share share;
-  Walk walk[16];  // of warps 4 on, whose registers are full
+  Walk walk[WALKS];  // of warps 4 on, whose registers are full
 };
-static_assert(sizeof(Barriers) <= 2048, "barrier block");
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   const bool ok = mbar_wait_bounded(bar, parity, abort, kTimeoutNs);
@@ -123,11 +136,26 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Waits for tcgen05.ld and ties the 32 registers to it: nothing that reads them moves up.
+// 16 or 32 columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) { tmem_st16(taddr, r); }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) { tmem_st32(taddr, r); }
+
+// Waits for tcgen05.ld and ties the registers to it: nothing that reads them moves up.
 __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
 #define MODA_RW8(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), \
                     "+r"(r[i + 6]), "+r"(r[i + 7])
   asm volatile("tcgen05.wait::ld.sync.aligned;" : MODA_RW8(0), MODA_RW8(8), MODA_RW8(16), MODA_RW8(24)::"memory");
+}
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : MODA_RW8(0), MODA_RW8(8)::"memory");
 }
 __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[128]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : MODA_RW8(0), MODA_RW8(8), MODA_RW8(16)::"memory");
@@ -273,7 +301,9 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  Barriers* bars = reinterpret_cast<Barriers*>(smem + C::kOffBar);
+  using Bars = Barriers<C::kWarps - 4>;
+  static_assert(sizeof(Bars) <= C::kOffMl - C::kOffBar, "barrier block");
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::kOffBar);
   const uint32_t sQ = smem_u32(smem), sK = smem_u32(smem + C::kOffK), sV = smem_u32(smem + C::kOffV);
   volatile int* abort = &bars->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -297,9 +327,10 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(smem_u32(&bars->s_full[x]), 1);
-      mbar_init(smem_u32(&bars->p_full[x]), 4);
+      mbar_init(smem_u32(&bars->p_full[x]), 4 * C::kCh);
       mbar_init(smem_u32(&bars->o_done[x]), 1);
     }
+    for (uint64_t& x : bars->ml_full) mbar_init(smem_u32(&x), 2);
     mbar_init(smem_u32(&bars->mma_done), 1);
     fence_barrier_init();
     tma_prefetch_desc(&tmQ);
@@ -536,10 +567,12 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       // P V of half x with the V in stage vs
       auto pv = [&](int x, uint32_t accumulate) {
         const uint32_t vb = v_lo + ((uint32_t)(vs * C::kTileBytes) >> 4);
-        const uint32_t pcol = tbase + C::kColS + x * 128, ocol = tbase + C::kColO + x * D;
+        constexpr int KC = BN / 16 / C::kCh;  // steps of a chain
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
-          mma_ts(ocol, pcol + kk * 8, desc_join(vb + ((uint32_t)(kk * 2048) >> 4), hi), idPV, kk > 0 ? 1u : accumulate);
+          mma_ts(tbase + C::kColO + (x * C::kCh + kk / KC) * D,
+                 tbase + C::kColS + x * 128 + kk / KC * (BN / C::kCh) + kk % KC * 8,
+                 desc_join(vb + ((uint32_t)(kk * 2048) >> 4), hi), idPV, kk % KC > 0 ? 1u : accumulate);
       };
       bool ok = true;
       Walk w;
@@ -602,19 +635,23 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       mbar_wait_bounded(smem_u32(&bars->mma_done), 0, &never, kTimeoutNs);
     }
     __syncwarp();
-  } else if (warp < 12) {
+  } else if (warp < C::kTame0) {
     // ----------------------------------------------------- softmax, epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
-    const int half = warp >= 8;
+    constexpr int CH = C::kCh, W = BN / CH;  // columns of a thread
+    constexpr int NE = CH == 2 ? 16 : 32;    // of O at a time
+    const int half = (warp - 4) / (4 * CH), ch = (warp - 4) / 4 % CH;  // ch: which of a row's threads
     const int row = tid & 127;  // row of the half == TMEM lane
-    const uint32_t scol = tmem_addr(tbase, (uint32_t)(warp & 3) * 32, C::kColS + half * 128);
-    const uint32_t ocol = tmem_addr(tbase, (uint32_t)(warp & 3) * 32, C::kColO + half * D);
+    const uint32_t scol = tmem_addr(tbase, (uint32_t)(warp & 3) * 32, C::kColS + half * 128 + ch * W);
+    const uint32_t ocol = tmem_addr(tbase, (uint32_t)(warp & 3) * 32, C::kColO + half * CH * D);
     const int wq = warp & 3;  // this warp's word of a depth block
+    const int wl = wq % (4 / CH);  // and where it is among the thread's columns, if it is
+    const bool word_here = wq / (4 / CH) == ch;
     const int lp = half * P + (row >> p.lgG), h_off = row & ((1 << p.lgG) - 1);
     const int lpw = (row & 31) >> p.lgG;  // the row's position among its warp's
     const uint32_t own_cols = PW >= 32 ? 1u << lpw : (0xffffffffu / ((1u << PW) - 1u)) << lpw;
     const float sl = p.scale_log2;
-    uint32_t sph = 0, oph = 0;  // parities of s_full, o_done
+    uint32_t sph = 0, oph = 0, mph = 0;  // parities of s_full, o_done, ml_full
     Walk& w = bars->walk[warp - 4];
     auto advance = [&](bool first) -> bool { return warp_next(w, p, sh, lane, first); };
     bool opened = false, ok = true, more = advance(true);
@@ -634,13 +671,13 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           const float alpha = need ? ex2_approx(m_ref - m_new) : 1.f;
           if (j > w.j0) {
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t r[32];
-              tmem_ld32(ocol + c * 32, r);
+            for (int c = 0; c < D / NE; ++c) {
+              uint32_t r[NE];
+              tmem_ld(ocol + ch * D + c * NE, r);
               tmem_ld_wait(r);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-              tmem_st32(ocol + c * 32, r);
+              for (int i = 0; i < NE; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+              tmem_st(ocol + ch * D + c * NE, r);
             }
             tmem_st_wait();
           }
@@ -671,34 +708,38 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           // slot index * SP + c / PW of the warp's position c % PW
           const int nbits = min(SP, p.L - sch.index * SP) * PW;
           const uint32_t word = lp < w.npos ? own_cols & (nbits >= 32 ? 0xffffffffu : (1u << nbits) - 1u) : 0u;
-          uint32_t x[32], pk[16];
-          tmem_ld32(scol + wq * 32, x);
-          tmem_ld_wait(x);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = (word & (1u << i)) ? x[i] : 0xff800000u;  // -inf
-          for (int pass = 0; pass < 2; ++pass) {
-            if (slow) rescale(raw_max32(x) * sl, j);
-            uint64_t acc[4] = {0, 0, 0, 0};
-            weigh<32>(x, pk, sl, m_ref == -INFINITY ? 0.f : m_ref, acc);
-            sum = total_of(acc);
-            if (slow) break;
-            slow = __any_sync(0xffffffffu, there && !(sum <= kSumBound));
-            if (!slow) break;
-          }
           const uint32_t zeros[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-          tmem_st16(scol + wq * 16, pk);
-          for (int kk = 1; kk < 4; ++kk) tmem_st16(scol + ((wq + kk) & 3) * 16, zeros);
+          if (word_here) {
+            uint32_t x[32], pk[16];
+            tmem_ld32(scol + wl * 32, x);
+            tmem_ld_wait(x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = (word & (1u << i)) ? x[i] : 0xff800000u;  // -inf
+            for (int pass = 0; pass < 2; ++pass) {
+              if (slow) rescale(raw_max32(x) * sl, j);
+              uint64_t acc[4] = {0, 0, 0, 0};
+              weigh<32>(x, pk, sl, m_ref == -INFINITY ? 0.f : m_ref, acc);
+              sum = total_of(acc);
+              if (slow) break;
+              slow = __any_sync(0xffffffffu, there && !(sum <= kSumBound));
+              if (!slow) break;
+            }
+            tmem_st16(scol + wl * 16, pk);
+          } else {
+            tmem_st16(scol + wl * 16, zeros);
+          }
+          for (int kk = 1; kk < 4 / CH; ++kk) tmem_st16(scol + (wl + kk) % (4 / CH) * 16, zeros);
         } else {
           // columns that the row sees: all, but at the causal border
           const bool border = sch.index >= border0;
-          const int end = border ? min(w.t0 + lp, w.t_last) - sch.index * BN + 1 : BN;
+          const int end = border ? min(w.t0 + lp, w.t_last) - sch.index * BN + 1 - ch * W : W;
           {
-            uint32_t pk[BN / 2];
+            uint32_t pk[W / 2];
             for (int pass = 0; pass < 2; ++pass) {
               if (slow) {
                 float mx = -INFINITY;
 #pragma unroll 1
-                for (int c = 0; c < BN / 32; ++c) {
+                for (int c = 0; c < W / 32; ++c) {
                   uint32_t y[32];
                   tmem_ld32(scol + c * 32, y);
                   tmem_ld_wait(y);
@@ -710,9 +751,9 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
               }
               const float m = m_ref == -INFINITY ? 0.f : m_ref;
               uint64_t acc[4] = {0, 0, 0, 0};
-              constexpr int NL = MX4 ? 32 : BN;  // at a time: the unpacking warps have the other registers
+              constexpr int NL = CH == 2 || MX4 ? 32 : BN;  // at a time: the other warps have the other registers
 #pragma unroll
-              for (int c0 = 0; c0 < BN; c0 += NL) {
+              for (int c0 = 0; c0 < W; c0 += NL) {
                 uint32_t x[NL];
 #pragma unroll
                 for (int c = 0; c < NL; c += 32) tmem_ld32(scol + c0 + c, x + c);
@@ -729,7 +770,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
               if (!slow) break;
             }
             tmem_st32(scol, pk);
-            tmem_st32(scol + 32, pk + 32);
+            if constexpr (CH == 1) tmem_st32(scol + 32, pk + 32);
           }
         }
         l += sum;
@@ -749,27 +790,48 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       }
       oph ^= 1;
       tc_fence_after();
+      float own = 1.f, other = 0.f;  // what the O of each of a row's threads counts
+      if constexpr (CH == 2) {
+        // the state of the row's other thread, whose O is in the same TMEM lane
+        float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl) + half * 2 * BM + row;
+        ml[ch * BM] = make_float2(m_ref, l);
+        warp_arrive(&bars->ml_full[half * 4 + wq], lane);
+        if (!(ok = warp_wait(smem_u32(&bars->ml_full[half * 4 + wq]), mph, abort))) break;
+        mph ^= 1;
+        const float2 o = ml[(ch ^ 1) * BM];
+        const float m = fmaxf(m_ref, o.x);
+        own = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m);
+        other = o.x == -INFINITY ? 0.f : ex2_approx(o.x - m);
+        l = l * own + o.y * other;
+        m_ref = m;
+      }
       const bool poisoned = *(volatile int*)&bars->poison[k & 7] == k + 1;
       const int64_t out = (int64_t)(w.token + lp) * p.Hq + w.hk * p.G + h_off;  // the row of o and lse
       const Work wk = work_of(p.work, D);
       const int64_t part_row = (2 * (int64_t)blockIdx.x + (w.j0 > 0 ? 0 : 1)) * kRows + half * BM + row;
       const float inv = 1.f / l;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t x[32];
+      for (int c = ch; c < D / NE; c += CH) {
+        uint32_t x[NE];
         __syncwarp();
-        tmem_ld32(ocol + c * 32, x);
+        tmem_ld(ocol + ch * D + c * NE, x);
         tmem_ld_wait(x);
-        float r[32];
+        float r[NE];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(x[i]);
+        for (int i = 0; i < NE; ++i) r[i] = __uint_as_float(x[i]);
+        if constexpr (CH == 2) {
+          tmem_ld(ocol + (ch ^ 1) * D + c * NE, x);
+          tmem_ld_wait(x);
+#pragma unroll
+          for (int i = 0; i < NE; ++i) r[i] = r[i] * own + __uint_as_float(x[i]) * other;
+        }
         if (poisoned && there) {
           // infinities or NaN were taken out of V rows that not all queries see: this
           // row's own are added, found again in global memory
-          auto add = [&](int i0, const uint4& y) {  // elements i0 .. i0 + 7 of the 32
+          auto add = [&](int i0, const uint4& y) {  // elements i0 .. i0 + 7 of the NE
             const uint32_t q[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int i = 0; i < 32; i += 2)
+            for (int i = 0; i < NE; i += 2)
               if (i >> 3 == i0 >> 3) {
                 const uint32_t v = q[(i & 7) >> 1], f = not_finite(v);
                 if (f & 0x8000u) r[i] += __uint_as_float(v << 16);
@@ -786,9 +848,9 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
               for (int slot = again.index * SP; slot < l_end; ++slot) {
                 const uint4* v = reinterpret_cast<const uint4*>(p.vd + (int64_t)(w.token + lp) * p.depth_tok +
                                                                 (int64_t)w.hk * p.depth_hk +
-                                                                (int64_t)slot * p.depth_slot + c * 32);
+                                                                (int64_t)slot * p.depth_slot + c * NE);
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) add(i * 8, v[i]);
+                for (int i = 0; i < NE / 8; ++i) add(i * 8, v[i]);
               }
             } else if (again.index * BN + BN - 1 > w.t0) {
               const int k_end = min(w.t0 + lp + 1, (again.index + 1) * BN);
@@ -798,15 +860,15 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                 if (pg < 0 || pg >= p.num_pages) pg = 0;
                 const int64_t vr = ((int64_t)(pg * p.Hk + w.hk) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < NE / 8; ++i) {
                   uint4 y;
                   if constexpr (MX4) {
                     uint32_t z[4];
-                    unpack8(*reinterpret_cast<const uint32_t*>(p.v + vr * (D / 2) + c * 16 + i * 4),
-                            scale_of(p.v_scale[vr * (D / 32) + c]), z);
+                    unpack8(*reinterpret_cast<const uint32_t*>(p.v + vr * (D / 2) + c * (NE / 2) + i * 4),
+                            scale_of(p.v_scale[vr * (D / 32) + c * NE / 32]), z);
                     y = make_uint4(z[0], z[1], z[2], z[3]);
                   } else {
-                    y = *reinterpret_cast<const uint4*>(p.v + (vr * D + c * 32 + i * 8) * 2);
+                    y = *reinterpret_cast<const uint4*>(p.v + (vr * D + c * NE + i * 8) * 2);
                   }
                   add(i * 8, y);
                 }
@@ -816,22 +878,22 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         }
         if (!there) continue;
         if (cut) {
-          float4* po = reinterpret_cast<float4*>(wk.o + part_row * D + c * 32);
+          float4* po = reinterpret_cast<float4*>(wk.o + part_row * D + c * NE);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) po[i] = make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+          for (int i = 0; i < NE / 4; ++i) po[i] = make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
         } else {
-          uint4* po = reinterpret_cast<uint4*>(p.o + out * D + c * 32);
+          uint4* po = reinterpret_cast<uint4*>(p.o + out * D + c * NE);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < NE / 8; ++i)
             po[i] = make_uint4(pack_bf16x2(r[8 * i] * inv, r[8 * i + 1] * inv),
                                pack_bf16x2(r[8 * i + 2] * inv, r[8 * i + 3] * inv),
                                pack_bf16x2(r[8 * i + 4] * inv, r[8 * i + 5] * inv),
                                pack_bf16x2(r[8 * i + 6] * inv, r[8 * i + 7] * inv));
         }
       }
-      if (there && cut)
+      if (there && ch == 0 && cut)
         *reinterpret_cast<float2*>(wk.ml + part_row * 2) = make_float2(m_ref, l);
-      else if (there && p.lse)
+      else if (there && ch == 0 && p.lse)
         p.lse[out] = (m_ref + log2f(l)) * kLn2;
       // (the next tile's first P V, which overwrites O, follows this warp's next p_full)
       tc_fence_before();
@@ -840,7 +902,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   } else {
     // ----------------------------- 4-bit pages unpacked, V blocks made harmless
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsTame));
-    const bool is_v = warp < 16;
+    const bool is_v = warp < C::kTame0 + 4;
     const int hw = warp & 3, r = tid & 127;  // a row of a tile each
     const int ns = is_v ? NV : NK;
     const uint32_t full = smem_u32(is_v ? (MX4 ? bars->v_full : bars->v_ready) : bars->k_full);

@@ -109,7 +109,7 @@ struct Share {
   }
 };
 struct ShareSmem {
-  unsigned long long warp_sum[20];
+  unsigned long long warp_sum[24];
   long long tile_at;
   int b, hk, tile;
 };
@@ -117,7 +117,7 @@ struct ShareSmem {
 // All threads of the CTA call it. LEAST: points that are worth a CTA.
 template <int WARPS, int LEAST>
 __device__ __forceinline__ Share share_of(const Params& p, ShareSmem& sm) {
-  static_assert(WARPS <= 20);
+  static_assert(WARPS <= 24);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (p.B + WARPS * 32 - 1) / (WARPS * 32);
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
