@@ -45,13 +45,13 @@
 //            its own: 1418 to 1530.
 //   4-bit, 1024 tokens at 32768, G = 4           305 (140)   the unpacking warps and the softmax
 //            share the issue slots (55 %) and the registers.
-//   32 drafts of up to 8 tokens, to 16000 rows    98 (80)    HBM: 81 % of the copy rate.
+//   32 drafts of up to 8 tokens, to 16000 rows    97 (80)    HBM: 82 % of the copy rate.
 //   5 tokens at 701 rows                          15 (0.3)   latencies one behind another: share
 //            2, first rows 3, blocks 4, the join behind the last CTA 3.
-// The softmax loop bears neither waits among its exponentials nor spilled registers. At d = 64
-// with two threads a row: 32 scores at a time 1330, 16 with the next on their way 1467, 64 (80
-// spilled bytes) 1563, 32 with 160 spilled bytes 1632; with one, 128 scores 1410, 32 with the
-// next on their way 1600.
+// The softmax takes 32 scores at a time. At d = 64 with two threads a row: 1330; 16 at a time 1478, 16
+// with the next on their way 1467, 64 1563, 32 with 160 spilled bytes 1632. At d = 128: 1024 tokens
+// without a past 40.9, 128 tokens at 2000 27.9, 2048 at 65536 720 to 770; 128 at a time 42.4, 28.8
+// and 705 to 764. Over 4-bit pages: 305; 16 at a time 313, 64 320.
 //
 // Every wait is bounded (2 s); on expiry the CTA stops issuing work, waits for its
 // copies and MMAs in flight, frees TMEM and latches MODA_ERR_TIMEOUT.
@@ -84,10 +84,10 @@ struct Cfg {
   // than there is.)
   static constexpr int kCh = D == 64 && !MX4 ? 2 : 1;
   static constexpr int kTame0 = 4 + 8 * kCh, kWarps = kTame0 + kTameWarps, kThreads = kWarps * 32;
-  // Registers of a thread of each group of four warps; they add up to what the block is
-  // launched with (kRegsLaunch a thread).
-  static constexpr int kRegsIssue = 64, kRegsSoftmax = kCh == 2 ? 88 : MX4 ? 120 : 184;
-  static constexpr int kRegsTame = kCh == 2 ? 64 : MX4 ? 88 : 80, kRegsLaunch = kCh == 2 ? 80 : MX4 ? 96 : 128;
+  // Registers of a thread of each group of four warps; they add up to no more than the block
+  // is launched with (kRegsLaunch a thread).
+  static constexpr int kRegsIssue = kCh == 2 || MX4 ? 64 : 96, kRegsSoftmax = kCh == 2 ? 88 : MX4 ? 120 : 152;
+  static constexpr int kRegsTame = kCh == 2 ? 64 : MX4 ? 88 : 104, kRegsLaunch = kCh == 2 ? 80 : MX4 ? 96 : 128;
   static_assert(kRegsIssue + 2 * kCh * kRegsSoftmax + kTameWarps / 4 * kRegsTame <= kWarps / 4 * kRegsLaunch);
   static constexpr int kBoxes = D / 64;  // 64-column (128-byte) swizzle boxes per row
   static constexpr int kBoxBytes = BN * 128;
@@ -156,12 +156,6 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
 }
 __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : MODA_RW8(0), MODA_RW8(8)::"memory");
-}
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[128]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : MODA_RW8(0), MODA_RW8(8), MODA_RW8(16)::"memory");
-#pragma unroll
-  for (int i = 24; i < 120; i += 24) asm volatile("" : MODA_RW8(i), MODA_RW8(i + 8), MODA_RW8(i + 16)::"memory");
-  asm volatile("" : MODA_RW8(120)::"memory");
 }
 #undef MODA_RW8
 
@@ -272,12 +266,11 @@ struct Codes {
   }
 };
 
-// p = 2^(s sl - m) of N scores as bf16 pairs, added up in acc.
-template <int N>
+// p = 2^(s sl - m) of 32 scores as bf16 pairs, added up in acc.
 __device__ __forceinline__ void weigh(const uint32_t* x, uint32_t* pk, float sl, float m, uint64_t (&acc)[4]) {
   const uint64_t sl2 = f2(sl, sl), nb2 = f2(-m, -m);
 #pragma unroll
-  for (int c = 0; c < N / 2; ++c) {
+  for (int c = 0; c < 16; ++c) {
     float u, w;
     f2_split(ffma2(f2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sl2, nb2), u, w);
     const float e0 = ex2_approx(u), e1 = ex2_approx(w);
@@ -718,7 +711,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             for (int pass = 0; pass < 2; ++pass) {
               if (slow) rescale(raw_max32(x) * sl, j);
               uint64_t acc[4] = {0, 0, 0, 0};
-              weigh<32>(x, pk, sl, m_ref == -INFINITY ? 0.f : m_ref, acc);
+              weigh(x, pk, sl, m_ref == -INFINITY ? 0.f : m_ref, acc);
               sum = total_of(acc);
               if (slow) break;
               slow = __any_sync(0xffffffffu, there && !(sum <= kSumBound));
@@ -751,18 +744,16 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
               }
               const float m = m_ref == -INFINITY ? 0.f : m_ref;
               uint64_t acc[4] = {0, 0, 0, 0};
-              constexpr int NL = CH == 2 || MX4 ? 32 : BN;  // at a time: the other warps have the other registers
 #pragma unroll
-              for (int c0 = 0; c0 < W; c0 += NL) {
-                uint32_t x[NL];
-#pragma unroll
-                for (int c = 0; c < NL; c += 32) tmem_ld32(scol + c0 + c, x + c);
+              for (int c0 = 0; c0 < W; c0 += 32) {
+                uint32_t x[32];
+                tmem_ld32(scol + c0, x);
                 tmem_ld_wait(x);
                 if (border) {
 #pragma unroll
-                  for (int c = 0; c < NL; ++c) x[c] = c0 + c < end ? x[c] : 0xff800000u;  // -inf
+                  for (int c = 0; c < 32; ++c) x[c] = c0 + c < end ? x[c] : 0xff800000u;  // -inf
                 }
-                weigh<NL>(x, pk + c0 / 2, sl, m, acc);
+                weigh(x, pk + c0 / 2, sl, m, acc);
               }
               sum = total_of(acc);
               if (slow) break;
