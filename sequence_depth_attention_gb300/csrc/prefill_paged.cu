@@ -43,15 +43,15 @@
 //   d = 64, 7 prompts' pieces, G = 8            1330 (577)   a block's exponentials take as
 //            long as at 128, its products half. One thread a row: 1410; S ahead in columns of
 //            its own: 1418 to 1530.
-//   4-bit, 1024 tokens at 32768, G = 4           305 (140)   the unpacking warps and the softmax
-//            share the issue slots (55 %) and the registers.
+//   4-bit, 1024 tokens at 32768, G = 4           285 (140)   the unpacking warps and the softmax
+//            share the issue slots and the registers.
 //   32 drafts of up to 8 tokens, to 16000 rows    97 (80)    HBM: 82 % of the copy rate.
 //   5 tokens at 701 rows                          15 (0.3)   latencies one behind another: share
 //            2, first rows 3, blocks 4, the join behind the last CTA 3.
 // The softmax takes 32 scores at a time. At d = 64 with two threads a row: 1330; 16 at a time 1478, 16
 // with the next on their way 1467, 64 1563, 32 with 160 spilled bytes 1632. At d = 128: 1024 tokens
 // without a past 40.9, 128 tokens at 2000 27.9, 2048 at 65536 720 to 770; 128 at a time 42.4, 28.8
-// and 705 to 764. Over 4-bit pages: 305; 16 at a time 313, 64 320.
+// and 705 to 764. Over 4-bit pages 16 at a time 3 % slower, 64 5 %.
 //
 // Every wait is bounded (2 s); on expiry the CTA stops issuing work, waits for its
 // copies and MMAs in flight, frees TMEM and latches MODA_ERR_TIMEOUT.
@@ -209,8 +209,10 @@ __device__ __forceinline__ bool tame_row(uint8_t* tile, int r, bool counts) {
 
 // A lane's 4-bit blocks of a tile, from global memory by way of registers to bf16: D / 32
 // lanes a row, a block of 32 elements a lane, four warps. The next tile's are on their way
-// while this one's are unpacked. One loop for K and V and all turns: beside the softmax's
-// code, unrolled ones waited for their instructions (1.7 of a scheduler's 5 warps did).
+// while this one's are unpacked. One loop for K and V, all turns and both halves of a block:
+// beside the softmax's code, unrolled ones waited for their instructions (1.7 of a scheduler's
+// 5 warps did). 1024 tokens at 32768 285 us; the halves unrolled 294, two turns as well 301,
+// a chunk at a time 341.
 template <int D>
 struct Codes {
   static constexpr int BPR = D / 32;        // blocks, and lanes, of a row
@@ -235,7 +237,7 @@ struct Codes {
       const int r = row(t, hw, lane);
       const uint32_t to = tile + (upper ? BN * 128 : 0) + r * 128;
       const uint32_t s = r < rows ? scale_of(scale[0]) : 0u;
-#pragma unroll
+#pragma unroll 1
       for (int j = 0; j < 4; j += 2) {
         uint32_t y[2][4];
         unpack8(upper == (j == 0) ? codes[0].z : codes[0].x, s, y[0]);
@@ -632,7 +634,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     // ----------------------------------------------------- softmax, epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
     constexpr int CH = C::kCh, W = BN / CH;  // columns of a thread
-    constexpr int NE = CH == 2 ? 16 : 32;    // of O at a time
+    constexpr int NE = CH == 2 || MX4 ? 16 : 32;  // of O at a time: spilled registers cost more
     const int half = (warp - 4) / (4 * CH), ch = (warp - 4) / 4 % CH;  // ch: which of a row's threads
     const int row = tid & 127;  // row of the half == TMEM lane
     const uint32_t scol = tmem_addr(tbase, (uint32_t)(warp & 3) * 32, C::kColS + half * 128 + ch * W);
