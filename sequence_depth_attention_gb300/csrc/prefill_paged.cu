@@ -97,7 +97,7 @@ struct Cfg {
   static constexpr int kOffK = 2 * kQBytes;
   static constexpr int kOffV = kOffK + kNK * kTileBytes;
   static constexpr int kOffBar = kOffV + kNV * kTileBytes;
-  static constexpr int kOffMl = kOffBar + (kCh == 2 ? 3072 : 2048);  // m and l of a row's threads
+  static constexpr int kOffMl = kOffBar + (kCh == 2 ? 4096 : 2048);  // m and l of a row's threads
   static constexpr int kSmemBytes = kOffMl + (kCh == 2 ? 4 * BM * 8 : 0) + 1024;  // alignment
   static constexpr uint32_t kColS = 0, kColO = 256;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
