@@ -402,3 +402,68 @@ def test_a_prompt_in_pieces_then_selected_decoding(fmt):
         settled()
         wo, wl, to, tl = cc.selected_reference(c, q, pages, rows, kd, vd, d ** -0.5)
         assert ((o.double() - wo).abs() <= to).all() and ((lse.double() - wl).abs() <= tl).all()
+
+
+# ------------------------------ small heads: each half of a block's keys by itself
+def test_halves_of_a_block_that_hold_nothing():
+    """One to 70 rows and no depth slots: the second 64 keys are none or few."""
+    new, past = [5, 64, 65, 1, 6], [0, 0, 0, 63, 64]
+    x = chunk("bf16", new, past, 16, 2, 64, 0, 16)
+    o, lse = run(*x, 64 ** -0.5)
+    check(*x, 64 ** -0.5, o, lse)
+
+
+@pytest.mark.parametrize("loud", [0, 1])
+@pytest.mark.parametrize("new,past", [([40], [500]), ([3, 20], [30000, 9000])])
+def test_halves_of_a_block_far_apart(loud, new, past):
+    """Scores of one half of every 128 keys are some 20 times the other's."""
+    c, q, starts, lens, kd, vd = chunk("bf16", new, past, 8, 1, 64, 3, 64)
+    for b, n in enumerate(lens):
+        for i in range(-(-n // 64)):
+            if i % 2 == loud:
+                c.k[c.table[b, i].long()] *= 20
+    o, lse = run(c, q, starts, lens, kd, vd, 64 ** -0.5)
+    check(c, q, starts, lens, kd, vd, 64 ** -0.5, o, lse)
+
+
+def test_infinite_values_of_seen_rows_in_small_heads():
+    x = chunk("bf16", [64], [300], 4, 1, 64, 2, 16)
+    c, q, starts, lens, kd, vd = x
+    plant(c, 0, 10, "v", math.inf, col=3)
+    plant(c, 0, 320, "v", -math.inf, col=3)
+    plant(c, 0, 340, "v", -math.inf, col=61)
+    o, _ = run(*x, 64 ** -0.5)
+    assert (o[:20, :, 3] == math.inf).all() and torch.isnan(o[20:, :, 3]).all()
+    assert torch.isfinite(o[:40, :, 61]).all() and (o[40:, :, 61] == -math.inf).all()
+    rest = torch.ones(64, dtype=torch.bool, device="cuda")
+    rest[[3, 61]] = False
+    assert torch.isfinite(o[..., rest]).all()
+
+
+def test_small_heads_captured_and_replayed():
+    """Other lengths behind the captured addresses: other tiles, shares and joins."""
+    new, past = [30, 2, 9], [200, 900, 0]
+    c, q, starts, lens, kd, vd = chunk("bf16", new, past, 8, 2, 64, 4, 32)
+    s, n = i32(starts), i32(lens)
+    o = torch.zeros(q.shape, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(q.shape[:2], dtype=torch.float32, device="cuda")
+    work = torch.zeros(moda.moda_prefill_paged_workspace_bytes(8, 2, 64) // 4, dtype=torch.float32, device="cuda")
+
+    def call():
+        moda.moda_prefill_paged(q, *c.args(), s, n, 64 ** -0.5, kd=kd, vd=vd, o=o, lse=lse, workspace=work)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for m, rows in (([30, 2, 9], lens), ([41, 0, 0], [60, 0, 0]), ([20, 20, 1], [100, 620, 6])):
+        starts = [0, m[0], m[0] + m[1], sum(m)]
+        s.copy_(i32(starts))
+        n.copy_(i32(rows))
+        torch.cuda.synchronize()
+        graph.replay()
+        settled()
+        check(c, q, starts, rows, kd, vd, 64 ** -0.5, o, lse)
