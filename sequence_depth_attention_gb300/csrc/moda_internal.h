@@ -178,6 +178,7 @@ struct PrefillPagedArgs {
 };
 cudaError_t launch_page_means(const PagedKv& c, const int* seq, const int* pos, int N, void* means,
                               cudaStream_t stream);
+constexpr int kMaxSelectPages = 1 << 15;  // columns of a table: their scores lie in shared memory
 // Arguments of one choice of pages after validation on the host.
 struct SelectPagesArgs {
   const void *q, *means;  // [N,Hq,d], [num_pages,Hk,d] bf16

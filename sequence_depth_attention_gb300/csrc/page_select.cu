@@ -651,7 +651,10 @@ cudaError_t select_d(const SelectPagesArgs& a, cudaStream_t stream) {
   const size_t smem = ((size_t)c.max_pages * 4 + 15) / 16 * 16;
   const auto kernel = a.G <= 8 ? select_pages_kernel<D, 1> : select_pages_kernel<D, 2>;
   if (smem > 32768) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the limit is the function's, not the call's: one value for all, so that calls from several
+    // host threads do not lower it for each other)
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kMaxSelectPages * 4);
     if (e != cudaSuccess) return e;
   }
   return paged::launch_dependent_clusters(kernel, dim3((unsigned)(items * group)), group, kSelThreads, smem, stream, p);

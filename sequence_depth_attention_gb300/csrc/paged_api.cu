@@ -81,7 +81,6 @@ moda_status check_apart(const Range* outs, int no, const Range* ins, int ni) {
 }
 
 constexpr int kMaxTokens = 1 << 24;
-constexpr int kMaxSelectPages = 1 << 15;  // their scores lie in shared memory
 
 // scale, heads and slots of an attention call; *G = Hq / Hk
 moda_status check_heads(int Hq, int Hk, int L, float scale, int* G) {
@@ -317,8 +316,8 @@ moda_status moda_select_pages(const void* q, const void* means, const moda_paged
   if (N < 0) return report(MODA_ERR_INVALID_ARG, "N = %d < 0", N);
   if (sink < 0 || recent < 1 || S < 1 || (int64_t)sink + recent > S)
     return report(MODA_ERR_INVALID_ARG, "sink = %d, recent = %d (at least 1) of S = %d pages", sink, recent, S);
-  if (a.c.max_pages > kMaxSelectPages)
-    return report(MODA_ERR_UNSUPPORTED, "max_pages = %d > %d", a.c.max_pages, kMaxSelectPages);
+  if (a.c.max_pages > moda::kMaxSelectPages)
+    return report(MODA_ERR_UNSUPPORTED, "max_pages = %d > %d", a.c.max_pages, moda::kMaxSelectPages);
   if (N > kMaxTokens || (int64_t)N * Hq > (1LL << 28))
     return report(MODA_ERR_UNSUPPORTED, "N = %d > 2^24 or N * Hq > 2^28", N);
   // (a quotient: the product may pass 64 bits)
