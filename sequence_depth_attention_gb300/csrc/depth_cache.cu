@@ -24,8 +24,9 @@
 namespace moda {
 namespace {
 
-constexpr int kMassWarps = 4;     // warps per CTA of the mass kernel
-constexpr int kMassMaxCtas = 2048;  // CTAs over all KV heads (per-CTA partials)
+constexpr int kMassWarps = 4;       // warps per CTA of the mass kernel
+constexpr int kMaxMassSlots = 1024;  // L, as the entry point checks
+constexpr int kMassMaxCtas = 2048;   // CTAs over all KV heads (per-CTA partials)
 constexpr float kLog2e = 1.4426950408889634f;
 
 // CTAs per KV head of the mass kernel; each takes a contiguous run of
@@ -247,8 +248,12 @@ cudaError_t launch_mass_dg(const DepthMassArgs& a, cudaStream_t st) {
   const int nblk = mass_blocks(a.T, a.Hk);
   const int run = (a.T + nblk - 1) / nblk;
   const size_t smem = sizeof(MassWarpSmem<D, G>) * kMassWarps + (size_t)kMassWarps * a.L * 4;
+  // the limit is the function's, not the call's: that of the most slots for all, so that calls
+  // from several host threads do not lower it for each other
+  constexpr size_t kMost = sizeof(MassWarpSmem<D, G>) * kMassWarps + (size_t)kMassWarps * kMaxMassSlots * 4;
+  static_assert(kMost <= 232448, "shared memory budget");
   cudaError_t e = cudaFuncSetAttribute(depth_mass_kernel<D, G>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
   if (e != cudaSuccess) return e;
   depth_mass_kernel<D, G><<<dim3(nblk, a.Hk), kMassWarps * 32, smem, st>>>(
       (const __nv_bfloat16*)a.q, (const __nv_bfloat16*)a.kd, a.lse, a.T, a.Hq, a.L, run,

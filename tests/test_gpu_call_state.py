@@ -1,5 +1,6 @@
 """Calls of one kernel that need different amounts of shared memory, from two host threads
 at once and in one captured graph: a call must not take away what another one needs."""
+import ctypes
 import sys
 import threading
 
@@ -46,8 +47,39 @@ def select(max_pages, seed):
     return fresh, bind
 
 
+def mass(L, seed):
+    """The same for the depth slots' mass, by the library's function itself: what Python does
+    around it keeps two calls apart."""
+    T, Hk, G, d = 64, 1, 16, 128
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn(T, Hk * G, d, generator=g).bfloat16().cuda()
+    kd = torch.randn(Hk, T, L, d, generator=g).bfloat16().cuda()
+    lse = torch.full((T, Hk * G), 8.0, device="cuda")
+    work = torch.empty(moda.moda_depth_mass_workspace_bytes(T, Hk, L) // 4, device="cuda")
+
+    def fresh():
+        return (torch.full((Hk, L), 99.0, device="cuda"),)
+
+    def bind(out):
+        f = moda.load().moda_depth_mass
+        vp = ctypes.c_void_p
+        tensors = q, kd, lse, out[0], work
+        ptr = [vp(x.data_ptr()) for x in tensors]
+        args = (*ptr[:3], T, Hk * G, Hk, d, L, ctypes.c_float(d ** -0.5), *ptr[3:], work.numel() * 4,
+                vp(torch.cuda.current_stream().cuda_stream))
+
+        def call():
+            st = f(*args)
+            assert st == 0, moda.moda_status_string(st)
+
+        call.keeps = tensors
+        return call
+
+    return fresh, bind
+
+
 # the kernel, and what makes one call need more shared memory than the other
-KERNELS = [(select, (32768, 9000))]
+KERNELS = [(select, (32768, 9000)), (mass, (1024, 8))]
 
 
 def of_each_size(make, sizes):
