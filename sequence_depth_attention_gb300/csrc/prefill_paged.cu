@@ -1078,6 +1078,8 @@ cudaError_t launch(const PrefillPagedArgs& a, cudaStream_t stream) {
   p.N = a.N; p.num_pages = c.num_pages; p.page_shift = __builtin_ctz((unsigned)c.page_size);
   p.max_pages = c.max_pages; p.B = c.B; p.Hq = a.Hq; p.Hk = c.Hk; p.G = a.G; p.L = a.L;
   p.lgG = lgG;
+  p.lg_per = 0;
+  while ((int64_t)C::kThreads << p.lg_per < c.B) ++p.lg_per;
   p.n_depth = (PW * a.L + 31) / 32;
   p.scale_log2 = a.scale * kLog2e;
   p.o = (__nv_bfloat16*)a.o; p.lse = a.lse; p.work = a.work; p.err = c.err;

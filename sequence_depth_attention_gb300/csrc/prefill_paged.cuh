@@ -47,6 +47,7 @@ __host__ __device__ inline Work work_of(float* w, int D) {
 struct Params {
   const int *q_starts, *lens, *table;
   int N, num_pages, page_shift, max_pages, B, Hq, Hk, G, L;
+  int lg_per;   // log2 of a thread's sequences in share_of
   int lgG;      // log2 of G rounded up to a power of two: rows of a position in a tile
   int n_depth;  // depth blocks of a tile
   float scale_log2;
@@ -103,12 +104,26 @@ struct Share {
   int shares, rem;
   int b, hk, tile;
   long long tile_at;  // the tile's first point
+  const uint32_t* some;  // see ShareSmem
+  // The next sequence that may have tokens, where the line goes on behind sequence b: of the
+  // same thread's in share_of, or the first of the next thread that found any. (One by one a
+  // sequence without tokens costs 94 ns; a table of 65536 with two in use took 6.2 ms.)
+  __device__ __forceinline__ int behind(const Params& p, int b) const {
+    ++b;
+    if (b & ((1 << p.lg_per) - 1)) return b;
+    const int thread = b >> p.lg_per;
+    int w = thread >> 5;
+    uint32_t set = some[w] >> (thread & 31) << (thread & 31);
+    while (set == 0) set = some[++w];
+    return (w * 32 + __ffs(set) - 1) << p.lg_per;
+  }
   __device__ __forceinline__ int owner_of(long long point) const {
     const long long wide = (base + 1) * rem;  // points of the CTAs with base + 1
     return point < wide ? (int)paged::divide(point, base + 1) : rem + (int)paged::divide(point - wide, base);
   }
 };
 struct ShareSmem {
+  uint32_t some[24];  // of each warp: a bit for each thread some of whose sequences have tokens
   unsigned long long warp_sum[24];
   long long tile_at;
   int b, hk, tile;
@@ -119,8 +134,9 @@ template <int WARPS, int LEAST>
 __device__ __forceinline__ Share share_of(const Params& p, ShareSmem& sm) {
   static_assert(WARPS <= 24);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int per = (p.B + WARPS * 32 - 1) / (WARPS * 32);
-  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  // (at most 2^32 - 1: half as many a thread would be fewer than B, below 2^31)
+  const int b0 = (int)min((unsigned)p.B, (unsigned)tid << p.lg_per);
+  const int b1 = (int)min((unsigned)p.B, (unsigned)(tid + 1) << p.lg_per);
   unsigned long long mine = 0;
   for (int b = b0; b < b1; ++b) {
     Seq s;
@@ -133,7 +149,11 @@ __device__ __forceinline__ Share share_of(const Params& p, ShareSmem& sm) {
     const unsigned long long x = __shfl_up_sync(0xffffffffu, before, off);
     if (lane >= off) before += x;
   }
-  if (lane == 31) sm.warp_sum[warp] = before;
+  const uint32_t some = __ballot_sync(0xffffffffu, mine > 0);
+  if (lane == 31) {
+    sm.warp_sum[warp] = before;
+    sm.some[warp] = some;
+  }
   __syncthreads();
   unsigned long long total = 0;
 #pragma unroll
@@ -145,6 +165,7 @@ __device__ __forceinline__ Share share_of(const Params& p, ShareSmem& sm) {
   Share s;
   const long long all = (long long)total;
   s.shares = (int)min((long long)gridDim.x, paged::divide(all + LEAST - 1, LEAST));
+  s.some = sm.some;
   s.base = s.rem = 0;
   s.from = s.to = 0;
   const int cta = blockIdx.x;
@@ -218,7 +239,7 @@ struct Walk {
         if (++hk == p.Hk) {
           hk = 0;
           do {
-            ++b;
+            b = s.behind(p, b);
             read_seq(p, b, seq);
           } while (seq.n == 0);  // there is another: the line goes on
         }
