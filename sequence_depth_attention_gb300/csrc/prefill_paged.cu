@@ -119,10 +119,17 @@ struct alignas(16) Barriers {
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
-  int poison[8];  // [k % 8] = k + 1: tile k had infinities or NaN taken out (fewer tiles are under way)
-  ShareSmem find;
+  // Had a tile infinities or NaN taken out? [half][n % 8] = n for the n-th of the tiles that the
+  // half has rows of. (Its next tile's V stages are freed behind its P alone, so that the warps which
+  // say so are never more than the stages ahead of it. Counted over all tiles, a run of tiles of one
+  // half could pass the second half by, and take the place of an answer that it had not read.)
+  int poison[2][8];
+  uint32_t some[24];  // see Share
   Share share;
-  Walk walk[WALKS];  // of warps 4 on, whose registers are full
+  union {
+    ShareSmem find;    // before the roles begin
+    Walk walk[WALKS];  // of warps 4 on, whose registers are full
+  };
 };
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
@@ -307,7 +314,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 
   if (tid == 0) {
     bars->abort = 0;
-    for (int& x : bars->poison) x = 0;
+    for (int i = 0; i < 16; ++i) bars->poison[i >> 3][i & 7] = 0;
     mbar_init(smem_u32(&bars->q_full), 1);
     mbar_init(smem_u32(&bars->q_free), 1);
     for (int s = 0; s < kMaxStages; ++s) {
@@ -338,7 +345,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   }
   paged::wait_for_stream();
   {
-    const Share mine = share_of<C::kWarps, kLeast>(p, bars->find);
+    const Share mine = share_of<C::kWarps, kLeast>(p, bars->find, bars->some);
     if (mine.from >= mine.to) {
       if (tid == 0) work_of(p.work, D).opened[blockIdx.x] = {0, 0, 0, 0};
       return;
@@ -650,7 +657,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     Walk& w = bars->walk[warp - 4];
     auto advance = [&](bool first) -> bool { return warp_next(w, p, sh, lane, first); };
     bool opened = false, ok = true, more = advance(true);
-    for (int k = 0; ok && more; ++k, more = advance(false)) {
+    for (; ok && more; more = advance(false)) {
       if (half && w.npos <= P) continue;
       // rows without a query go along: their scores are the next tokens' (or zeros), and
       // what they hold is not looked at
@@ -798,7 +805,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         l = l * own + o.y * other;
         m_ref = m;
       }
-      const bool poisoned = *(volatile int*)&bars->poison[k & 7] == k + 1;
+      const bool poisoned = *(volatile int*)&bars->poison[half][w.nth[half] & 7] == w.nth[half];
       const int64_t out = (int64_t)(w.token + lp) * p.Hq + w.hk * p.G + h_off;  // the row of o and lse
       const Work wk = work_of(p.work, D);
       const int64_t part_row = (2 * (int64_t)blockIdx.x + (w.j0 > 0 ? 0 : 1)) * kRows + half * BM + row;
@@ -904,7 +911,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     uint32_t checks = 0;  // parities of `check`
     bool ok = true;
     Walk& w = bars->walk[warp - 4];
-    for (int k = 0; ok && warp_next(w, p, sh, lane, k == 0); ++k) {
+    for (bool first = true; ok && warp_next(w, p, sh, lane, first); first = false) {
       const int halves = w.npos > P ? 2 : 1;
       Sched sch(p.n_depth, w.nb, w.j0);
       using Cd = Codes<D>;
@@ -961,7 +968,9 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
               fetch(sch.index + 1);
             }
             if (found) {
-              *(volatile int*)&bars->poison[k & 7] = k + 1;
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (h < halves) *(volatile int*)&bars->poison[h][w.nth[h] & 7] = w.nth[h];
               __threadfence_block();
             }
             fence_async();

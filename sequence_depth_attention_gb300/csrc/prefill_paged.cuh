@@ -104,7 +104,7 @@ struct Share {
   int shares, rem;
   int b, hk, tile;
   long long tile_at;  // the tile's first point
-  const uint32_t* some;  // see ShareSmem
+  const uint32_t* some;  // of each warp: a bit for each thread some of whose sequences have tokens
   // The next sequence that may have tokens, where the line goes on behind sequence b: of the
   // same thread's in share_of, or the first of the next thread that found any. (One by one a
   // sequence without tokens costs 94 ns; a table of 65536 with two in use took 6.2 ms.)
@@ -123,7 +123,6 @@ struct Share {
   }
 };
 struct ShareSmem {
-  uint32_t some[24];  // of each warp: a bit for each thread some of whose sequences have tokens
   unsigned long long warp_sum[24];
   long long tile_at;
   int b, hk, tile;
@@ -131,7 +130,7 @@ struct ShareSmem {
 
 // All threads of the CTA call it. LEAST: points that are worth a CTA.
 template <int WARPS, int LEAST>
-__device__ __forceinline__ Share share_of(const Params& p, ShareSmem& sm) {
+__device__ __forceinline__ Share share_of(const Params& p, ShareSmem& sm, uint32_t (&some)[24]) {
   static_assert(WARPS <= 24);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // (at most 2^32 - 1: half as many a thread would be fewer than B, below 2^31)
@@ -149,10 +148,10 @@ __device__ __forceinline__ Share share_of(const Params& p, ShareSmem& sm) {
     const unsigned long long x = __shfl_up_sync(0xffffffffu, before, off);
     if (lane >= off) before += x;
   }
-  const uint32_t some = __ballot_sync(0xffffffffu, mine > 0);
+  const uint32_t have = __ballot_sync(0xffffffffu, mine > 0);
   if (lane == 31) {
     sm.warp_sum[warp] = before;
-    sm.some[warp] = some;
+    some[warp] = have;
   }
   __syncthreads();
   unsigned long long total = 0;
@@ -165,7 +164,7 @@ __device__ __forceinline__ Share share_of(const Params& p, ShareSmem& sm) {
   Share s;
   const long long all = (long long)total;
   s.shares = (int)min((long long)gridDim.x, paged::divide(all + LEAST - 1, LEAST));
-  s.some = sm.some;
+  s.some = some;
   s.base = s.rem = 0;
   s.from = s.to = 0;
   const int cta = blockIdx.x;
@@ -222,11 +221,13 @@ struct Walk {
   // of the current tile
   int token, npos, t0, t_last;  // first token, positions, first and last position
   int nb, j0, j1;               // blocks, and those of this share: j0 .. j1 - 1
+  uint16_t nth[2];              // the how-manieth of this share it is, of all and of those of two halves
   __device__ __forceinline__ void begin(const Params& p, const Share& s) {
     b = s.b;
     hk = s.hk;
     tile = s.tile - 1;
     next_at = s.tile_at;
+    nth[0] = nth[1] = 0;
     read_seq(p, b, seq);
   }
   __device__ __forceinline__ bool next(const Params& p, const Share& s) {
@@ -254,7 +255,11 @@ struct Walk {
       const long long begin = at + kTileCost;
       j0 = s.from > begin ? (int)(s.from - begin) : 0;
       j1 = s.to < next_at ? (int)max(s.to - begin, 0LL) : nb;
-      if (j1 > j0) return true;
+      if (j1 > j0) {
+        ++nth[0];
+        nth[1] += npos > P >> 1;
+        return true;
+      }
     }
   }
   __device__ __forceinline__ bool cut() const { return j1 - j0 < nb; }

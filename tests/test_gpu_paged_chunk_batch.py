@@ -72,3 +72,44 @@ def test_a_batch_of_empty_sequences_takes_no_time():
     c.table = held
     check(c, q, starts, lens, kd, vd, 0.1, o, lse)
     assert best < 2.0, f"{best:.2f} ms"
+
+
+@pytest.mark.parametrize("fmt,d", [("bf16", 128), ("bf16", 64), ("mx4", 128), ("mx4", 64)])
+def test_infinite_values_before_many_short_tiles(fmt, d):
+    """Tiles of two halves whose border holds infinities and NaN, each with a run of tiles of
+    one half behind it in the same CTA's share: what a tile had taken out is told apart from
+    what the tiles behind it had, or had not, for both halves."""
+    G, L = 4, 2
+    P = 128 // G
+    run_of = [2 * P] + [1] * 300
+    new = run_of * 10
+    past = [3] * len(new)
+    x = chunk(fmt, new, past, G, 1, d, L, 16)
+    c, q, starts, lens, kd, vd = x
+    clean, clean_lse = run(*x, d ** -0.5)
+    tables = c.table[torch.arange(0, len(new), len(run_of), device="cuda")].long()
+    row = 3 + P // 2  # seen by the tokens from P / 2 on: some of the first half, all of the second
+    page, off = tables[:, row // 16], row % 16
+    if fmt == "bf16":
+        for col, value in ((5, math.nan), (6, math.inf), (7, -math.inf)):
+            c.v[page, 0, off, col] = value
+        cols = slice(5, 8)
+    else:
+        c.vs[page, 0, off, 0] = 255
+        cols = slice(0, 32)
+    last = torch.tensor(starts[0 : len(new) : len(run_of)], device="cuda") + 2 * P - 1
+    vd[1, last, 0, d - 1] = math.inf  # and of one token of the second half in a slot of its own
+    hit = torch.zeros(q.shape, dtype=torch.bool, device="cuda")
+    for first in starts[0 : len(new) : len(run_of)]:
+        hit[first + P // 2 : first + 2 * P, :, cols] = True
+        hit[first + 2 * P - 1, :, d - 1] = True
+    for _ in range(20):
+        o, lse = run(*x, d ** -0.5)
+        assert torch.equal(lse, clean_lse) and torch.equal(o[~hit], clean[~hit])
+        assert not torch.isfinite(o[hit]).any()
+        if fmt == "bf16":
+            for first in starts[0 : len(new) : len(run_of)]:
+                seen = o[first + P // 2 : first + 2 * P]
+                assert torch.isnan(seen[..., 5]).all() and (seen[..., 6] == math.inf).all()
+                assert (seen[..., 7] == -math.inf).all()
+        assert (o[last, :, d - 1] == math.inf).all()
