@@ -549,9 +549,15 @@ MODA_API moda_status moda_decode_paged(const void* q, const moda_paged_kv* cache
  * A page index outside [0, num_pages) makes its sequence's result unspecified and is
  * latched. What a query does not see (later rows, other tokens' slots, rows past a
  * sequence's length) has no influence on its result, infinities and NaN included.
- * Arithmetic: as moda_fwd (fp32 scores and sums, P rounded to bf16 once for the second
- * product); MX4 rows count with their exact values, which bf16 holds. A weight below
- * 2^-126 of the largest may count as 0.
+ * Arithmetic: as moda_fwd: fp32 scores and sums, P rounded to bf16 once for the second
+ * product, in every format. (moda_decode_paged holds P in more bits: two bf16 parts over
+ * bf16 pages, fp16 over MX4 ones. o of one token is right to its own rounding there, here
+ * to about 1.5 of it.) A weight below 2^-126 of the largest may count as 0. The sums of V
+ * are in fp32, of weights up to 2^8, and overflow where such sums pass 2^128. MX4 rows count
+ * with their exact values; over them, sums of up to 2^24 values, depth slots' among them, do
+ * not overflow: they are held in units of 2^32, in which products of weight and value below
+ * 2^-94 may count as 0, and V's scale bytes up to 32 (values up to 6 * 2^-95) do. (Of K, byte
+ * 0, which moda_kv_append never writes, is read as 0 as in moda_decode_paged.)
  * Supported: G = Hq/Hk from 1 to 16 (1, 2, 4, 8 and 16 use the tensor core's rows in
  * full), N <= 2^24, N*Hq <= 2^31 - 1, 0 <= L <= 1024, scale > 0 and at most 2e38.
  * Result bits depend on the batch as a whole (how it is cut) by the order of fp32 sums;

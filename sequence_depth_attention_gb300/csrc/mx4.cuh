@@ -40,6 +40,12 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t b) {
   const uint32_t x = b == 255u ? 0x7fc0u : b == 0u ? 0x0040u : b << 7;
   return x | x << 16;
 }
+// The same in units of 2^unit; 0 where that is below 2^-126. (With the subnormals a 4-bit
+// prefill of 1024 tokens at 32768 rows took 301 us, without 284.)
+__device__ __forceinline__ uint32_t scale_in_units(uint32_t b, int unit) {
+  const uint32_t x = b == 255u ? 0x7fc0u : (uint32_t)max((int)b - unit, 0) << 7;
+  return x | x << 16;
+}
 
 }  // namespace mx4
 }  // namespace moda

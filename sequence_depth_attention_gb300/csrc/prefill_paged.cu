@@ -17,7 +17,7 @@
 //     block-diagonal mask (a softmax warp has a 32-row word of it), and spread evenly
 //     among the sequence blocks.
 //   * 4-bit pages are unpacked into the bf16 tiles that the tensor core reads (exactly: a
-//     code times a power of two), once for both halves.
+//     code times a power of two), once for both halves; V in units of 2^32 (kUnitLog).
 //   * A row that a query must not see has no influence whatever it holds. Its weight is
 //     0, but 0 times an infinity or a NaN in V is NaN: in the blocks that some row of a
 //     tile sees in part (the causal border, the depth blocks), rows that no query of the
@@ -71,6 +71,11 @@ using paged::kLog2e;
 
 constexpr int BM = 128, BN = 128;  // rows of a half tile, keys of a block
 constexpr uint64_t kTimeoutNs = 2000000000ull;
+// 4-bit pages: O is held in units of 2^32, V's values unpacked in these and the depth blocks' P
+// times 2^-32. Values are up to 1.5 * 2^127, and sums of up to 2^24 of them, each times a weight
+// of up to kSumBound, stay finite. (Powers of two: no other bit changes. bf16 pages' values are what
+// the tensor core reads; their sums have fp32's range.)
+constexpr int kUnitLog = 32;
 constexpr float kSumBound = 256.0f;  // of a row's weights in a block, see the softmax warps
 // Points that are worth a CTA. Measured (us) with 1, 2, 3, 4, 6: 5 tokens at 701 rows 15.5,
 // 15.8, 15.5, 16.9, 19.0; 128 tokens at 2000 32.7, 29.0, 28.8, 29.3, 33.1; where there is more
@@ -232,8 +237,8 @@ struct Codes {
     return turn * RPT + hw * (32 / BPR) + lane / BPR;
   }
   // Into a bf16 tile, zeros from row `rows` on; `tame`: and in place of infinities and NaN.
-  // True if there were any.
-  __device__ __forceinline__ bool unpack(uint32_t tile, int hw, int lane, int rows, bool tame) {
+  // True if there were any. (Of NaN: in units no finite code is infinite.) unit: see scale_in_units.
+  __device__ __forceinline__ bool unpack(uint32_t tile, int hw, int lane, int rows, bool tame, int unit) {
     const int qtr = lane % BPR;
     // A block is four 16-byte chunks of a 64-column box from 4 (qtr & 1) on; lanes of the
     // upper box take them in another order, so that eight lanes (two rows) meet different
@@ -244,13 +249,13 @@ struct Codes {
     for (int t = 0; t < kTurns; ++t) {
       const int r = row(t, hw, lane);
       const uint32_t to = tile + (upper ? BN * 128 : 0) + r * 128;
-      const uint32_t s = r < rows ? scale_of(scale[0]) : 0u;
+      const uint32_t s = r < rows ? scale_in_units(scale[0], unit) : 0u;
 #pragma unroll 1
       for (int j = 0; j < 4; j += 2) {
         uint32_t y[2][4];
         unpack8(upper == (j == 0) ? codes[0].z : codes[0].x, s, y[0]);
         unpack8(upper == (j == 0) ? codes[0].w : codes[0].y, s, y[1]);
-        if (tame && scale[0] >= 253u) {
+        if (tame && scale[0] == 255u) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t f = not_finite(y[i >> 2][i & 3]);
@@ -727,6 +732,11 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
               slow = __any_sync(0xffffffffu, there && !(sum <= kSumBound));
               if (!slow) break;
             }
+            if constexpr (MX4) {
+              constexpr uint32_t kInUnits = (127u - kUnitLog) << 7 | (127u - kUnitLog) << 23;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) pk[i] = mul_bf16x2(pk[i], kInUnits);
+            }
             tmem_st16(scol + wl * 16, pk);
           } else {
             tmem_st16(scol + wl * 16, zeros);
@@ -813,7 +823,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       const int64_t out = (int64_t)(w.token + lp) * p.Hq + w.hk * p.G + h_off;  // the row of o and lse
       const Work wk = work_of(p.work, D);
       const int64_t part_row = (2 * (int64_t)blockIdx.x + (w.j0 > 0 ? 0 : 1)) * kRows + half * BM + row;
-      const float inv = 1.f / l;
+      const float inv = (MX4 ? (float)(1ull << kUnitLog) : 1.f) / l;
 #pragma unroll 1
       for (int c = ch; c < D / NE; c += CH) {
         uint32_t x[NE];
@@ -869,7 +879,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                   if constexpr (MX4) {
                     uint32_t z[4];
                     unpack8(*reinterpret_cast<const uint32_t*>(p.v + vr * (D / 2) + c * (NE / 2) + i * 4),
-                            scale_of(p.v_scale[vr * (D / 32) + c * NE / 32]), z);
+                            scale_in_units(p.v_scale[vr * (D / 32) + c * NE / 32], kUnitLog), z);
                     y = make_uint4(z[0], z[1], z[2], z[3]);
                   } else {
                     y = *reinterpret_cast<const uint4*>(p.v + (vr * D + c * NE + i * 8) * 2);
@@ -968,7 +978,8 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
               checks ^= 1u << s;
               if (is_v) found = tame_row<D>(tile, r, counts(r));
             } else {
-              found = c.unpack(smem_u32(tile), hw, lane, w.t_last + 1 - sch.index * BN, is_v && part);
+              found = c.unpack(smem_u32(tile), hw, lane, w.t_last + 1 - sch.index * BN, is_v && part,
+                               is_v ? kUnitLog : 0);
               fetch(sch.index + 1);
             }
             if (found) {
@@ -1040,7 +1051,7 @@ prefill_join_kernel(const __grid_constant__ Params p) {
       paged::add_partials<U, E>(M, L, acc, pm, pl, po);
     }
     const int64_t out = (int64_t)(t.token + (row >> p.lgG)) * p.Hq + t.hk * p.G + h;
-    const float inv = 1.f / L;
+    const float inv = p.unit / L;
 #pragma unroll
     for (int e = 0; e < E; e += 2)
       *reinterpret_cast<uint32_t*>(p.o + out * D + lane * E + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
@@ -1095,6 +1106,7 @@ cudaError_t launch(const PrefillPagedArgs& a, cudaStream_t stream) {
   while ((int64_t)C::kThreads << p.lg_per < c.B) ++p.lg_per;
   p.n_depth = (PW * a.L + 31) / 32;
   p.scale_log2 = a.scale * kLog2e;
+  p.unit = MX4 ? (float)(1ull << kUnitLog) : 1.f;
   p.o = (__nv_bfloat16*)a.o; p.lse = a.lse; p.work = a.work; p.err = c.err;
   p.k = (const uint8_t*)c.k; p.v = (const uint8_t*)c.v;
   p.k_scale = (const uint8_t*)c.k_scale; p.v_scale = (const uint8_t*)c.v_scale;

@@ -51,6 +51,7 @@ struct Params {
   int lgG;      // log2 of G rounded up to a power of two: rows of a position in a tile
   int n_depth;  // depth blocks of a tile
   float scale_log2;
+  float unit;  // of the partials' o
   __nv_bfloat16* o;
   float* lse;
   float* work;
