@@ -772,6 +772,14 @@ def moda_decode_paged(q, k_pages, v_pages, block_table, seq_lens, scale: float, 
     return o, lse
 
 
+def _int32(x, name):
+    """x as an int that an argument of 32 bits holds (ctypes would cut it to its low bits)."""
+    x = int(x)
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{name} = {x} does not fit 32 bits")
+    return x
+
+
 def _depth_views(dev, kd, vd, shape, what):
     """(L, kd's and vd's addresses, their strides) of depth slots kd, vd whose shape is
     `shape`, with one None where L stands; `what` names it in errors."""
@@ -892,7 +900,7 @@ def moda_select_pages(q, means, k_pages, v_pages, block_table, seq, pos, S: int,
         raise ValueError(f"q must be [N,Hq,d] with N={N}, d={d}")
     if means is None or means.shape != (k_pages.shape[0], Hk, d):
         raise ValueError(f"means must be [num_pages,Hk,d] = {(k_pages.shape[0], Hk, d)}")
-    S = int(S)
+    S, sink, recent = (_int32(x, n) for x, n in ((S, "S"), (sink, "sink"), (recent, "recent")))
     with _allocating(stream, dev):
         if pages is None:
             pages = torch.empty((N, Hk, max(S, 0)), dtype=_i32, device=q.device)
@@ -903,7 +911,7 @@ def moda_select_pages(q, means, k_pages, v_pages, block_table, seq, pos, S: int,
     if pages.shape != (N, Hk, S) or rows.shape != (N, Hk):
         raise ValueError(f"pages must be {(N, Hk, S)} and rows {(N, Hk)}")
     st = (_lib or load()).moda_select_pages(q.data_ptr(), means.data_ptr(), cache, seq.data_ptr(), pos.data_ptr(), N,
-                                            q.shape[1], S, int(sink), int(recent), pages.data_ptr(),
+                                            q.shape[1], S, sink, recent, pages.data_ptr(),
                                             rows.data_ptr(), _raw_stream(stream, dev))
     if st:
         _check(st, "moda_select_pages")
