@@ -548,7 +548,7 @@ MODA_API moda_status moda_decode_paged(const void* q, const moda_paged_kv* cache
  *             between calls. Calls that may run at the same time need one each.
  * A page index outside [0, num_pages) makes its sequence's result unspecified and is
  * latched. What a query does not see (later rows, other tokens' slots, rows past a
- * sequence's length) has no influence on its result, infinities and NaN included.
+ * sequence's length) does not count in its result, infinities and NaN included.
  * Arithmetic: as moda_fwd: fp32 scores and sums, P rounded to bf16 once for the second
  * product, in every format. (moda_decode_paged holds P in more bits: two bf16 parts over
  * bf16 pages, fp16 over MX4 ones. o of one token is right to its own rounding there, here
@@ -560,8 +560,10 @@ MODA_API moda_status moda_decode_paged(const void* q, const moda_paged_kv* cache
  * 0, which moda_kv_append never writes, is read as 0 as in moda_decode_paged.)
  * Supported: G = Hq/Hk from 1 to 16 (1, 2, 4, 8 and 16 use the tensor core's rows in
  * full), N <= 2^24, N*Hq <= 2^31 - 1, 0 <= L <= 1024, scale > 0 and at most 2e38.
- * Result bits depend on the batch as a whole (how it is cut) by the order of fp32 sums;
- * the same call on the same device gives the same bits.
+ * Result bits depend on the batch as a whole by the order of fp32 sums (how it is cut) and
+ * by the reference that weights are rounded under, which 32 rows (32 / G tokens and their
+ * heads) raise together: what one of them sees may move the rounding of the others' weights,
+ * and nothing else of them. The same call on the same device gives the same bits.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA; TIMEOUT via
  * moda_get_device_error. N == 0 or B == 0 is a no-op.
  */

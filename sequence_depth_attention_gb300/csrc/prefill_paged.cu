@@ -696,7 +696,9 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       // Every block: exponentiate against the running reference right away. Every p is
       // at most the block's sum, so a sum within kSumBound proves that no score rose more
       // than 8 (log2 units) above it, and the block needs no maximum at all. Else the
-      // reference becomes the row's maximum, and the block is weighed again.
+      // references of the warp's rows become their maxima, and the block is weighed again. (Of the
+      // rows that ask for it alone, so that no row's rounding depends on another's: 2048 tokens at
+      // 65536 1.2 % slower, 1024 over 4-bit pages 2.4 %, for each raises its own at another block.)
       const int nb = w.nb, j1 = w.j1, border0 = (w.t0 + 1) / BN;  // the first sequence block at the causal border
       bool unset = true;  // some row has no reference yet
       Sched sch(p.n_depth, nb, w.j0);

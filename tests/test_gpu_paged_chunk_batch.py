@@ -6,7 +6,6 @@ import pytest
 import torch
 
 import sequence_depth_attention_gb300 as moda
-import paged_chunk_common as cc  # noqa: F401 (what check compares with)
 from test_gpu_paged_chunk import _built, check, chunk, i32, run, settled  # noqa: F401 (_built is a fixture)
 
 pytestmark = pytest.mark.gpu
