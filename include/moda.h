@@ -609,7 +609,9 @@ MODA_API moda_status moda_page_means(const moda_paged_kv* cache, const int* seq,
  *          behind the last
  *   rows   [N, Hk] int32: the rows in them that the token sees (all but the last page's are
  *          full)
- * A page index outside [0, num_pages) is latched; it is chosen last and given as -1.
+ * A page index outside [0, num_pages) is latched; its score counts as -infinity (so it is
+ * chosen behind all pages with a finite score, and by its place among those without one),
+ * and it is given as -1.
  * Supported: G = Hq/Hk from 1 to 16, 1 <= recent, 0 <= sink, sink + recent <= S, max_pages <=
  * 32768, N <= 2^24, N*Hq <= 2^28, N*Hk*S <= 2^31 - 1.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA. N == 0 is a no-op.
