@@ -532,7 +532,9 @@ MODA_API moda_status moda_decode_paged(const void* q, const moda_paged_kv* cache
  *             Hq*d; unused when N == 1)
  *   q_starts  [B + 1] int32, device memory: 0 <= q_starts[b] <= q_starts[b+1] <= N. A
  *             sequence may have no token; o and lse of tokens that belong to no
- *             sequence (a padded batch's, behind the last) are left as they were.
+ *             sequence (a padded batch's, behind the last) are left as they were. (Where
+ *             starts fall, tokens that two sequences claim get the one's result or the
+ *             other's, or parts of both.)
  *   seq_lens  [B] int32, device memory: rows of each sequence, its tokens' own among
  *             them: q_starts[b+1] - q_starts[b] <= seq_lens[b] <= max_pages * page_size
  *             A sequence whose starts or length are outside these ranges is left out,
@@ -544,7 +546,8 @@ MODA_API moda_status moda_decode_paged(const void* q, const moda_paged_kv* cache
  *             d; one that steps along an axis of length 1 is unused). NULL when L == 0
  *   o         [N, Hq, d] bf16; lse [N, Hq] fp32 (natural log) or NULL
  *   workspace caller-owned device scratch, 16-byte aligned, of at least
- *             moda_prefill_paged_workspace_bytes(Hq, Hk, d) bytes; holds nothing
+ *             moda_prefill_paged_workspace_bytes(Hq, Hk, d) bytes (42.6 MB at d = 128, 21.6
+ *             at 64, whatever the batch: the states of tiles that CTAs share); holds nothing
  *             between calls. Calls that may run at the same time need one each.
  * A page index outside [0, num_pages) makes its sequence's result unspecified and is
  * latched. What a query does not see (later rows, other tokens' slots, rows past a

@@ -18,7 +18,7 @@
 //     among the sequence blocks.
 //   * 4-bit pages are unpacked into the bf16 tiles that the tensor core reads (exactly: a
 //     code times a power of two), once for both halves; V in units of 2^32 (kUnitLog).
-//   * A row that a query must not see has no influence whatever it holds. Its weight is
+//   * A row that a query must not see does not count whatever it holds. Its weight is
 //     0, but 0 times an infinity or a NaN in V is NaN: in the blocks that some row of a
 //     tile sees in part (the causal border, the depth blocks), rows that no query of the
 //     tile sees become 0, and an infinity or NaN among the others becomes 0 too and is
@@ -35,23 +35,30 @@
 // first 64 columns of its S, O of the halves at 256 and 256 + d. (Two threads a row: each P in
 // the first 32 of its thread's 64 columns of S, O of the threads 64 columns each from 256 on.)
 // P is rounded to bf16 once, as in the forward: the sum l keeps fp32 weights, and
-// what o is off by that is about as much as its own rounding to bf16.
+// what o is off by that is about as much as its own rounding to bf16 (0.0023 of the norm in all
+// against 0.0017 with exact weights). Two bf16 parts, which the decode takes, would make the
+// products 3/2 of what they are: 841 us and not 561 in the first case below.
 //
 // What bounds it, measured (us; the floor is that of the products or of the rows):
-//   d = 128, 2048 tokens at 65536 rows, G = 4    790 (561)   tensor pipe 72 % busy, power;
-//            700 on a cool GPU. What it is not busy is the halves' hand-over of S and P.
-//   d = 64, 7 prompts' pieces, G = 8            1330 (577)   a block's exponentials take as
-//            long as at 128, its products half. One thread a row: 1410; S ahead in columns of
-//            its own: 1418 to 1530.
-//   4-bit, 1024 tokens at 32768, G = 4           285 (140)   the unpacking warps and the softmax
-//            share the issue slots and the registers.
-//   32 drafts of up to 8 tokens, to 16000 rows    97 (80)    HBM: 82 % of the copy rate.
-//   5 tokens at 701 rows                          15 (0.3)   latencies one behind another: share
+//   d = 128, 2048 tokens at 65536 rows, G = 4    735 to 810 (561)   tensor pipe 73 % of cycles, then
+//            the clock. What the pipe is not busy is the halves' hand-over of S and P.
+//   d = 64, 7 prompts' pieces, G = 8            1350 (577)   no unit is full (tensor pipe 41 %,
+//            exponentials 37 %, issue 58 %): the softmax warps wait for TMEM and barriers, 4.1 of an
+//            instruction's 10.3 cycles, and TMEM has no room for another tile meanwhile. Where this
+//            took 1330, one thread a row took 1410, S ahead in columns of its own 1418 to 1530.
+//   4-bit, 1024 tokens at 32768, G = 4           285 (140)   issue 60 %: each CTA unpacks all of its
+//            tiles' blocks, beside the softmax. d = 64, G = 8: 772 (281), bf16 562.
+//   32 drafts of up to 8 tokens, to 16000 rows    97 (80)    HBM: 82 % of the copy rate. d = 64, G = 8
+//            136 (80): 1.45 us a block for half the bytes.
+//   the same over 4-bit rows                     150 (22), d = 64 195 (22): a block's unpacking and its
+//            softmax one behind the other, 1.9 us; to 32768 rows 278 (44) and 369 (44).
+//   5 tokens at 701 rows                          14 (0.3)   latencies one behind another: share
 //            2, first rows 3, blocks 4, the join behind the last CTA 3.
-// The softmax takes 32 scores at a time. At d = 64 with two threads a row: 1330; 16 at a time 1478, 16
-// with the next on their way 1467, 64 1563, 32 with 160 spilled bytes 1632. At d = 128: 1024 tokens
-// without a past 40.9, 128 tokens at 2000 27.9, 2048 at 65536 720 to 770; 128 at a time 42.4, 28.8
-// and 705 to 764. Over 4-bit pages 16 at a time 3 % slower, 64 5 %.
+// The softmax takes 32 scores at a time. At d = 64 with two threads a row (all before the halves had
+// flags of their own, which cost 1 %) 1330; 16 at a time 1478, 16 with the next on their way 1467, 64
+// 1563, 32 with 160 spilled bytes 1632 (some 50 are). At d = 128: 1024 tokens without a past 40.9, 128
+// tokens at 2000 27.9, 2048 at 65536 720 to 770; 128 at a time 42.4, 28.8 and 705 to 764. Over 4-bit
+// pages 16 at a time 3 % slower, 64 5 %.
 //
 // Every wait is bounded (2 s); on expiry the CTA stops issuing work, waits for its
 // copies and MMAs in flight, frees TMEM and latches MODA_ERR_TIMEOUT.
@@ -77,8 +84,8 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 // the tensor core reads; their sums have fp32's range.)
 constexpr int kUnitLog = 32;
 constexpr float kSumBound = 256.0f;  // of a row's weights in a block, see the softmax warps
-// Points that are worth a CTA. Measured (us) with 1, 2, 3, 4, 6: 5 tokens at 701 rows 15.5,
-// 15.8, 15.5, 16.9, 19.0; 128 tokens at 2000 32.7, 29.0, 28.8, 29.3, 33.1; where there is more
+// Points that are worth a CTA. Measured (us) with 1, 2, 3, 4, 6: 5 tokens at 701 rows 14.4,
+// 15.1, 15.2, 17.2, 18.9; 128 tokens at 2000 31.6, 27.9, 27.5, 28.4, 31.7; where there is more
 // work than that, no difference.
 constexpr int kLeast = 2;
 

@@ -21,8 +21,9 @@ namespace prefill {
 constexpr int kMaxCtas = 160;  // one per SM of 152; sizes the workspace
 constexpr int kRows = 256;     // rows of a tile: positions times heads
 // Points in front of a tile's blocks. Measured (us) with 2, 3, 4, 6: 16 drafts over 4-bit rows
-// 40.5, 40.5, 42.3, 44.1; 1024 tokens without a past 43.3, 42.5, 42.3, 43.1. (Blocks of a tile
-// of one half, which take 3/4 of the time, at 3 points of 4: no faster.)
+// 37.7, 37.8, 39.7, 41.8; 32 drafts over bf16 ones 97.1, 97.8, 99.0, 101.2; 7 pieces at d = 64 1372,
+// 1350, 1354, 1367; 1024 tokens without a past 41.6, 41.4, 40.9, 42.3. (Blocks of a tile of one
+// half, which take 3/4 of the time, at 3 points of 4: no faster.)
 constexpr int kTileCost = 3;
 
 // The workspace: for each CTA the cut tile whose first block is its own (parts 0:
