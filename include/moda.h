@@ -558,8 +558,8 @@ MODA_API moda_status moda_decode_paged(const void* q, const moda_paged_kv* cache
  * to about 1.5 of it.) A weight below 2^-126 of the largest may count as 0. The sums of V
  * are in fp32, of weights up to 2^8, and overflow where such sums pass 2^128. MX4 rows count
  * with their exact values; over them, sums of up to 2^24 values, depth slots' among them, do
- * not overflow: they are held in units of 2^32, in which products of weight and value below
- * 2^-94 may count as 0, and V's scale bytes up to 32 (values up to 6 * 2^-95) do. (Of K, byte
+ * not overflow: they are held in units of 2^26, in which products of weight and value below
+ * 2^-100 may count as 0, and V's scale bytes up to 26 (values up to 6 * 2^-101) do. (Of K, byte
  * 0, which moda_kv_append never writes, is read as 0 as in moda_decode_paged.)
  * Supported: G = Hq/Hk from 1 to 16 (1, 2, 4, 8 and 16 use the tensor core's rows in
  * full), N <= 2^24, N*Hq <= 2^31 - 1, 0 <= L <= 1024, scale > 0 and at most 2e38.

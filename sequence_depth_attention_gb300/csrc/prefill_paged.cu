@@ -17,7 +17,7 @@
 //     block-diagonal mask (a softmax warp has a 32-row word of it), and spread evenly
 //     among the sequence blocks.
 //   * 4-bit pages are unpacked into the bf16 tiles that the tensor core reads (exactly: a
-//     code times a power of two), once for both halves; V in units of 2^32 (kUnitLog).
+//     code times a power of two), once for both halves; V in units of 2^26 (kUnitLog).
 //   * A row that a query must not see does not count whatever it holds. Its weight is
 //     0, but 0 times an infinity or a NaN in V is NaN: in the blocks that some row of a
 //     tile sees in part (the causal border, the depth blocks), rows that no query of the
@@ -78,11 +78,11 @@ using paged::kLog2e;
 
 constexpr int BM = 128, BN = 128;  // rows of a half tile, keys of a block
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-// 4-bit pages: O is held in units of 2^32, V's values unpacked in these and the depth blocks' P
-// times 2^-32. Values are up to 1.5 * 2^127, and sums of up to 2^24 of them, each times a weight
-// of up to kSumBound, stay finite. (Powers of two: no other bit changes. bf16 pages' values are what
-// the tensor core reads; their sums have fp32's range.)
-constexpr int kUnitLog = 32;
+// 4-bit pages: O is held in units of 2^26, V's values unpacked in these and the depth blocks' P
+// times 2^-26. Values are up to 1.5 * 2^127, a block's weights add up to kSumBound at most, and 2^24
+// rows are 2^17 blocks: their sums stay finite. (Powers of two: no other bit changes. bf16 pages'
+// values are what the tensor core reads; their sums have fp32's range.)
+constexpr int kUnitLog = 26;
 constexpr float kSumBound = 256.0f;  // of a row's weights in a block, see the softmax warps
 // Points that are worth a CTA. Measured (us) with 1, 2, 3, 4, 6: 5 tokens at 701 rows 14.4,
 // 15.1, 15.2, 17.2, 18.9; 128 tokens at 2000 31.6, 27.9, 27.5, 28.4, 31.7; where there is more

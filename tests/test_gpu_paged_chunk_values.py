@@ -1,5 +1,7 @@
 """Chunks of new tokens over values at the ends of their range: sums of the largest 4-bit
 values, and the smallest ones."""
+import math
+
 import pytest
 import torch
 
@@ -61,9 +63,9 @@ def test_a_token_over_the_largest_values_is_a_decode(d):
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("low,high", [(0, 40), (20, 60), (90, 130)])
 def test_small_values(low, high, d):
-    """Scale bytes of 0 to 60 stand for 2^-127 to 2^-67. Of V those up to 32 count as 0, with which
-    an average is off by 6 * 2^-95 at most; a product of weight (the largest is at least 1) and
-    value may be lost below 2^-94."""
+    """Scale bytes of 0 to 60 stand for 2^-127 to 2^-67. Of V those up to 26 count as 0, with which
+    an average is off by 6 * 2^-101 at most; a product of weight (the largest is at least 1) and
+    value may be lost below 2^-100."""
     c, q, starts, lens, kd, vd = chunk("mx4", [5, 40, 1], [3, 700, 5000], 4, 1, d, 0, 16)
     mask = held(c, "vs")
     c.vs[mask] = torch.randint(low, high, c.vs.shape, generator=torch.Generator().manual_seed(8),
@@ -72,7 +74,7 @@ def test_small_values(low, high, d):
     wo, wl, to, tl = cc.prefill_reference(c, q, starts, lens, kd, vd, d ** -0.5)
     slack = torch.zeros_like(to)
     for b, n in enumerate(lens):
-        slack[starts[b] : starts[b + 1]] = 6 * 2.0 ** -95 + n * 2.0 ** -94
+        slack[starts[b] : starts[b + 1]] = 6 * 2.0 ** -101 + n * 2.0 ** -100
     assert ((o.double() - wo).abs() <= to + slack).all() and ((lse.double() - wl).abs() <= tl).all()
 
 
@@ -94,3 +96,24 @@ def test_bytes_from_which_on_bf16_holds_infinity(d):
     fine[5:, :, :32] = False
     err = (o.double() - want).abs() - want * (4 * pc.HALF_BF16)
     assert (err[fine.expand_as(err)] <= 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_sums_of_as_many_of_the_largest_values_as_the_header_names(d):
+    """2^24 rows (of two pages, named again and again), and 128 of smaller scores in front, whose
+    share holds blocks with weights of just under 2^8 in all."""
+    n, page = 1 << 24, 128
+    k, v = (torch.zeros(2, 1, page, d // 2, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((2, 1, page, d // 32), 127, dtype=torch.uint8, device="cuda") for _ in range(2))
+    v[:], vs[:] = 0x77, LARGEST
+    k[1, :, :, 0] = 2  # 1 in the first element
+    table = torch.ones(1, n // page, dtype=torch.int32, device="cuda")
+    table[0, 0] = 0
+    q = torch.zeros(1, 4, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1
+    scale = 0.686  # 2^0.99 as much weight as the first 128
+    o, lse = moda.moda_prefill_paged(q, k, v, table, i32([0, 1]), i32([n]), scale, k_scales=ks, v_scales=vs)
+    settled()
+    assert (o == 6 * 2.0 ** 125).all()
+    want = torch.logsumexp(torch.tensor([math.log(128.0), math.log(n - 128.0) + scale], dtype=torch.float64), 0)
+    assert (lse.double().cpu() - want).abs().max() < 2.0 ** -18 * want
