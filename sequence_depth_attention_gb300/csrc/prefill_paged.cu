@@ -55,7 +55,7 @@
 //   5 tokens at 701 rows                          14 (0.3)   latencies one behind another: share
 //            2, first rows 3, blocks 4, the join behind the last CTA 3.
 // The softmax takes 32 scores at a time. At d = 64 with two threads a row (all before the halves had
-// flags of their own, which cost 1 %) 1330; 16 at a time 1478, 16 with the next on their way 1467, 64
+// flags of their own, which cost 0.5 %) 1330; 16 at a time 1478, 16 with the next on their way 1467, 64
 // 1563, 32 with 160 spilled bytes 1632 (some 50 are). At d = 128: 1024 tokens without a past 40.9, 128
 // tokens at 2000 27.9, 2048 at 65536 720 to 770; 128 at a time 42.4, 28.8 and 705 to 764. Over 4-bit
 // pages 16 at a time 3 % slower, 64 5 %.
@@ -825,10 +825,6 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         l = l * own + o.y * other;
         m_ref = m;
       }
-      // (Any place will do. d = 64: 1353 us, 1339 without the look; by the half's place 1366, by a count of
-      // the half's tiles 1372.)
-      const bool poisoned =
-          __any_sync(0xffffffffu, ((volatile int*)&bars->poison[0][0])[lane & 15] == ((k + 1) & 0xffff));
       const int64_t out = (int64_t)(w.token + lp) * p.Hq + w.hk * p.G + h_off;  // the row of o and lse
       const Work wk = work_of(p.work, D);
       const int64_t part_row = (2 * (int64_t)blockIdx.x + (w.j0 > 0 ? 0 : 1)) * kRows + half * BM + row;
@@ -848,6 +844,10 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 #pragma unroll
           for (int i = 0; i < NE; ++i) r[i] = r[i] * own + __uint_as_float(x[i]) * other;
         }
+        // (Any place will do, and the answer is looked up for each part of O: d = 64 1336 us beside
+        // 1348 with it kept over them; from the half's own place 1366, by a count of its tiles 1372.)
+        const bool poisoned =
+            __any_sync(0xffffffffu, ((volatile int*)&bars->poison[0][0])[lane & 15] == ((k + 1) & 0xffff));
         if (poisoned && there) {
           // infinities or NaN were taken out of V rows that not all queries see: this
           // row's own are added, found again in global memory
